@@ -28,13 +28,20 @@ MOE_ERR_CUDA = 4
 MOE_ERR_BAD_INPUT = 5
 MOE_ERR_TIMEOUT = 6
 
+# moe_dtype_t
+DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
+_TORCH_DTYPE = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
 EXPORTS = ("moe_workspace_bytes", "moe_max_blocks", "moe_workspace_init", "moe_route",
            "moe_plan", "moe_expert_ffn_w4", "moe_combine", "moe_layer_w4",
            "moe_query_device_status", "moe_debug_dequant_w4", "moe_debug_dequant_w4_decode",
            "moe_status_string",
            "moe_last_error", "moe_plan_noalloc", "moe_layer_path", "moe_decode_layers",
            "moe_decoder_blocks", "moe_attn_workspace_bytes", "moe_attn_decode",
-           "moe_gdn_scan", "moe_gdn_chunked_workspace_bytes", "moe_gdn_chunked_scan")
+           "moe_gdn_scan", "moe_gdn_chunked_workspace_bytes", "moe_gdn_chunked_scan",
+           "moe_cache_workspace_bytes", "moe_cache_fork", "moe_cache_reserve", "moe_cache_write",
+           "moe_cache_compact", "moe_cache_copy_pages", "moe_verify_workspace_bytes",
+           "moe_verify_drafts")
 
 
 class MoeError(RuntimeError):
@@ -63,6 +70,19 @@ class AttnShape(C.Structure):
 class GdnShape(C.Structure):
     _fields_ = [("T", C.c_int32), ("n_k", C.c_int32), ("n_v", C.c_int32), ("dk", C.c_int32),
                 ("dv", C.c_int32)]
+
+
+class CacheShape(C.Structure):
+    _fields_ = [("n_slots", C.c_int32), ("max_blocks", C.c_int32), ("n_phys", C.c_int32),
+                ("n_kv", C.c_int32), ("D", C.c_int32), ("block", C.c_int32)]
+
+
+class CacheMetaPtrs(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("lens", C.c_void_p), ("refs", C.c_void_p)]
+
+
+class VerifyShape(C.Structure):
+    _fields_ = [("n_slots", C.c_int32), ("T", C.c_int32), ("V", C.c_int32), ("dtype", C.c_int32)]
 
 
 class W4Weights(C.Structure):
@@ -105,6 +125,12 @@ def load():
             L.moe_gdn_chunked_workspace_bytes.argtypes = [C.POINTER(GdnShape)]
             L.moe_attn_workspace_bytes.restype = SZ
             L.moe_attn_workspace_bytes.argtypes = [C.POINTER(AttnShape)]
+            pC, pM, pV = C.POINTER(CacheShape), C.POINTER(CacheMetaPtrs), C.POINTER(VerifyShape)
+            L.moe_cache_workspace_bytes.restype = SZ
+            L.moe_cache_workspace_bytes.argtypes = [pC]
+            L.moe_verify_workspace_bytes.restype = SZ
+            L.moe_verify_workspace_bytes.argtypes = [pV]
+            I64 = C.c_int64
             for name, args in (
                     ("moe_workspace_init", [P, SZ, P]),
                     ("moe_route", [pS, P, P, P, P, P, P, SZ, P]),
@@ -121,7 +147,13 @@ def load():
                     ("moe_attn_decode", [C.POINTER(AttnShape), P, P, P, P, I32, P, P, SZ, P]),
                     ("moe_gdn_scan", [C.POINTER(GdnShape), P, P, P, P, P, P, P, P, P]),
                     ("moe_gdn_chunked_scan",
-                     [C.POINTER(GdnShape), P, P, P, P, P, P, P, P, P, SZ, P])):
+                     [C.POINTER(GdnShape), P, P, P, P, P, P, P, P, P, SZ, P]),
+                    ("moe_cache_fork", [pC, pM, P, P, pM, P, SZ, P]),
+                    ("moe_cache_reserve", [pC, pM, P, pM, P, P, I32, P, SZ, P]),
+                    ("moe_cache_write", [pC, pM, P, I32, P, I64, P, I64, P, P, P, SZ, P]),
+                    ("moe_cache_compact", [pC, pM, pM, P, P, I32, P, SZ, P]),
+                    ("moe_cache_copy_pages", [pC, I32, P, P, P, P, I32, I32, P, SZ, P]),
+                    ("moe_verify_drafts", [pV, P, P, P, P, P, P, P, P, SZ, P])):
                 f = getattr(L, name)
                 f.restype = C.c_int
                 f.argtypes = args
@@ -292,6 +324,181 @@ def moe_decoder_blocks(shape, layer_table, gains, h_out, ws, h_in=None, token_id
                                    C.cast(layer_table, C.c_void_p), C.cast(gains, C.c_void_p),
                                    _p(h_in), _p(token_ids), _p(embed), vocab, _p(h_out),
                                    _p(ws), ws.numel(), _s(stream)), "moe_decoder_blocks")
+
+
+# ------------------------------------------------- batch serving calls --
+def _tensor(t, dtype, shape, what):
+    """t, checked: a contiguous CUDA tensor of this type and shape (None in
+    `shape`: any extent; bf16 and fp16 tensors may come as int16 bits)."""
+    ok = t.dtype == dtype or (dtype in (torch.bfloat16, torch.float16) and t.dtype == torch.int16)
+    if not ok:
+        raise ValueError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if len(t.shape) != len(shape) or any(n is not None and n != k for n, k in zip(shape, t.shape)):
+        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
+    return _p(t)
+
+
+def _ints(t, shape, what):
+    return None if t is None else _tensor(t, torch.int32, shape, what)
+
+
+def _tokens(t, n_slots, T, inner, what):
+    """Pointer and token stride (elements) of a 16-bit [n_slots][T][inner...]
+    tensor whose tokens lie evenly apart, each dense (a slice of a joint
+    projection is)."""
+    if not t.is_cuda or t.element_size() != 2:
+        raise ValueError("%s must be a 16-bit CUDA tensor" % what)
+    if tuple(t.shape) != (n_slots, T) + tuple(inner):
+        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape),
+                                                           (n_slots, T) + tuple(inner)))
+    dense = 1
+    for n, st in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
+        if n > 1 and st != dense:
+            raise ValueError("%s: a token's elements must be dense" % what)
+        dense *= n
+    stride = t.stride(1) if T > 1 else t.stride(0) if n_slots > 1 else dense
+    if T > 1 and n_slots > 1 and t.stride(0) != T * stride:
+        raise ValueError("%s: tokens must lie evenly apart" % what)
+    return C.c_void_p(t.data_ptr()), stride
+
+
+def _workspace(nbytes, device, stream, what):
+    if nbytes == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, what)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+def make_cache_shape(n_slots, max_blocks, n_phys, n_kv, D, block=64):
+    return CacheShape(n_slots, max_blocks, n_phys, n_kv, D, block)
+
+
+def alloc_cache_workspace(shape, device="cuda", stream=None):
+    return _workspace(load().moe_cache_workspace_bytes(C.byref(shape)), device, stream,
+                      "alloc_cache_workspace")
+
+
+class CacheMeta:
+    """State of a batch's cache (moe_cache_meta_t): table int32
+    [n_slots][max_blocks], lens int32 [n_slots], refs int32 [n_phys]. The
+    calls read one and write another; a program keeps two and swaps them."""
+
+    def __init__(self, table, lens, refs):
+        self.table, self.lens, self.refs = table, lens, refs
+        self.ptrs = CacheMetaPtrs(_ints(table, (None, None), "table"),
+                                  _ints(lens, table.shape[:1], "lens"),
+                                  _ints(refs, (None,), "refs"))
+
+    @classmethod
+    def empty(cls, shape, device="cuda"):
+        """No slot holds anything, every page is free."""
+        z = lambda *n: torch.zeros(n, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(z(shape.n_slots, shape.max_blocks).fill_(-1), z(shape.n_slots), z(shape.n_phys))
+
+    def of(self, shape):
+        if tuple(self.table.shape) != (shape.n_slots, shape.max_blocks) or \
+                self.refs.shape[0] != shape.n_phys:
+            raise ValueError("the state is not of this cache shape")
+        return C.byref(self.ptrs)
+
+
+def pool_table(pools):
+    """Host array of the pools' device pointers (16-bit [n_phys][n_kv][64][D]
+    each) for moe_cache_reserve, moe_cache_compact and moe_cache_copy_pages;
+    it keeps the tensors."""
+    arr = (C.c_void_p * max(1, len(pools)))()
+    for i, t in enumerate(pools):
+        if t.dim() != 4 or t.element_size() != 2 or t.shape != pools[0].shape:
+            raise ValueError("pools must be 16-bit [n_phys][n_kv][64][D] tensors of one shape")
+        arr[i] = _p(t)
+    arr.pools = list(pools)
+    return arr
+
+
+def _pools(shape, table, n_phys):
+    for t in table.pools[:1]:
+        if tuple(t.shape) != (n_phys, shape.n_kv, shape.block, shape.D):
+            raise ValueError("the pools are not of this cache shape")
+    return C.cast(table, C.c_void_p), len(table.pools)
+
+
+def moe_cache_fork(shape, meta, parent, out, ws, keep=None, stream=None):
+    """Slot s of `out` holds the first keep[s] positions of slot parent[s] of
+    `meta` (-1: nothing): fork, reorder, cut and free."""
+    n = (shape.n_slots,)
+    _check(load().moe_cache_fork(C.byref(shape), meta.of(shape), _ints(parent, n, "parent"),
+                                 _ints(keep, n, "keep"), out.of(shape), _p(ws), ws.numel(),
+                                 _s(stream)), "moe_cache_fork")
+
+
+def moe_cache_reserve(shape, meta, n_new, out, granted, pools, ws, stream=None):
+    """Room for n_new[s] positions more in every slot, shared last pages copied
+    in all pools (pool_table); granted[s] = n_new[s], or 0 where refused."""
+    n = (shape.n_slots,)
+    ptr, k = _pools(shape, pools, shape.n_phys)
+    _check(load().moe_cache_reserve(C.byref(shape), meta.of(shape), _ints(n_new, n, "n_new"),
+                                    out.of(shape), _ints(granted, n, "granted"), ptr, k, _p(ws),
+                                    ws.numel(), _s(stream)), "moe_cache_reserve")
+
+
+def moe_cache_write(shape, meta, n_new, k_new, v_new, k_cache, v_cache, ws, stream=None):
+    """Keys and values [n_slots][T][n_kv][D] of the last n_new[s] positions
+    (None: T) of every slot into one layer's pools."""
+    T = k_new.shape[1]
+    kp, ks = _tokens(k_new, shape.n_slots, T, (shape.n_kv, shape.D), "k_new")
+    vp, vs = _tokens(v_new, shape.n_slots, T, (shape.n_kv, shape.D), "v_new")
+    for t in (k_cache, v_cache):
+        if tuple(t.shape) != (shape.n_phys, shape.n_kv, shape.block, shape.D) or \
+                t.element_size() != 2:
+            raise ValueError("the pools are not of this cache shape")
+    _check(load().moe_cache_write(C.byref(shape), meta.of(shape),
+                                  _ints(n_new, (shape.n_slots,), "n_new"), T, kp, ks, vp, vs,
+                                  _p(k_cache), _p(v_cache), _p(ws), ws.numel(), _s(stream)),
+           "moe_cache_write")
+
+
+def moe_cache_compact(shape, meta, out, n_live, pools, ws, stream=None):
+    """Moves the held pages to the front of every pool; n_live[0] = how many."""
+    ptr, k = _pools(shape, pools, shape.n_phys)
+    _check(load().moe_cache_compact(C.byref(shape), meta.of(shape), out.of(shape),
+                                    _ints(n_live, (1,), "n_live"), ptr, k, _p(ws), ws.numel(),
+                                    _s(stream)), "moe_cache_compact")
+
+
+def moe_cache_copy_pages(shape, src, dst, from_pools, to_pools, ws, stream=None):
+    """Page src[i] of every pool of from_pools to page dst[i] of to_pools."""
+    n_to = to_pools.pools[0].shape[0]
+    a, k = _pools(shape, from_pools, shape.n_phys)
+    b, k2 = _pools(shape, to_pools, n_to)
+    if k != k2:
+        raise ValueError("as many pools on both sides")
+    _check(load().moe_cache_copy_pages(C.byref(shape), src.shape[0], _ints(src, (None,), "src"),
+                                       _ints(dst, src.shape, "dst"), a, b, k, n_to, _p(ws),
+                                       ws.numel(), _s(stream)), "moe_cache_copy_pages")
+
+
+def make_verify_shape(n_slots, T, V, dtype="fp32"):
+    return VerifyShape(n_slots, T, V, DTYPES[dtype])
+
+
+def alloc_verify_workspace(shape, device="cuda", stream=None):
+    return _workspace(load().moe_verify_workspace_bytes(C.byref(shape)), device, stream,
+                      "alloc_verify_workspace")
+
+
+def moe_verify_drafts(shape, p, q, draft, n_draft, u, tokens, n_acc, ws, stream=None):
+    """Accepts drafted tokens against the target's probabilities p
+    [n_slots][T+1][V] and the draft's q [n_slots][T][V] (None: certain) with
+    the random numbers u [n_slots][T+1], and draws the token after them."""
+    B, T, V = shape.n_slots, shape.T, shape.V
+    dt = _TORCH_DTYPE[[k for k, v in DTYPES.items() if v == shape.dtype][0]]
+    _check(load().moe_verify_drafts(
+        C.byref(shape), _tensor(p, dt, (B, T + 1, V), "p"),
+        None if q is None else _tensor(q, dt, (B, T, V), "q"), _ints(draft, (B, T), "draft"),
+        _ints(n_draft, (B,), "n_draft"), _tensor(u, torch.float32, (B, T + 1), "u"),
+        _ints(tokens, (B, T + 1), "tokens"), _ints(n_acc, (B,), "n_acc"), _p(ws), ws.numel(),
+        _s(stream)), "moe_verify_drafts")
 
 
 def moe_layer_w4(shape, x, w_router, router_bias, experts, shared, y, ws, x_next=None,

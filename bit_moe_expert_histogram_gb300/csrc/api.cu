@@ -406,6 +406,11 @@ namespace moe {
 bool shape_supported(const moe_shape_t* shape) { return shape_ok(shape); }
 void set_last_error(const char* text) { g_last_error = text; }
 void set_last_cuda_error(cudaError_t e, const char* where) { cuda_fail(e, where); }
+moe_status_t device_sm_count(int* out) { return sm_count(out); }
+moe_status_t encode_rows64(CUtensorMap* m, bool fp16, const void* base, int D, uint64_t rows) {
+  return map_2d(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                base, D, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
 }  // namespace moe
 
 extern "C" {
@@ -821,7 +826,7 @@ const char* moe_status_string(moe_status_t status) {
     case MOE_ERR_UNSUPPORTED_SHAPE: return "unsupported shape";
     case MOE_ERR_WORKSPACE: return "workspace too small";
     case MOE_ERR_CUDA: return "CUDA error";
-    case MOE_ERR_BAD_INPUT: return "bad input on device (expert id out of range)";
+    case MOE_ERR_BAD_INPUT: return "bad input on device (an id, a length or a table entry out of range)";
     case MOE_ERR_TIMEOUT: return "device wait timed out";
   }
   return "unknown status";

@@ -3,6 +3,7 @@
 // inline-PTX wrappers for mbarrier, TMA and tcgen05 (sm_103a).
 #pragma once
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -30,7 +31,8 @@ struct Ctrl {
 };
 static_assert(sizeof(Ctrl) == 256, "Ctrl must be 256 bytes");
 
-enum : int { KID_PLAN = 1, KID_FFN = 2, KID_DECODE = 3, KID_ROUTE = 4, KID_ATTN = 5, KID_GDN = 6 };
+enum : int { KID_PLAN = 1, KID_FFN = 2, KID_DECODE = 3, KID_ROUTE = 4, KID_ATTN = 5, KID_GDN = 6,
+             KID_CACHE = 7, KID_VERIFY = 8, KID_ATTNB = 9 };
 
 __device__ __forceinline__ void set_error(Ctrl* c, int code, int kid, int detail) {
   if (atomicCAS(&c->err, 0, code) == 0) {
@@ -51,6 +53,9 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ uint32_t f2bf(float f) { return pack_bf2(f, 0.0f) & 0xFFFFu; }
+__device__ __forceinline__ float half_bits_to_float(uint32_t bits) {
+  return __half2float(__ushort_as_half((unsigned short)bits));
+}
 
 // ------------------------------------------------------------- dequant --
 // Groupwise-affine 4-bit dequantisation ("Perplexity Open Sources Lily: A

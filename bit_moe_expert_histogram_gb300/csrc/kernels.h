@@ -170,10 +170,48 @@ cudaError_t launch_gdn_chunked(const moe_gdn_shape_t* s, const uint16_t* q, cons
                                const uint16_t* v, const float* alpha, const float* beta,
                                const float* s_in, float* s_out, uint16_t* o, float* ws,
                                cudaStream_t stream);
+// Pages of a block-paged cache (cache.cu). Pools: device pointers of one
+// launch's keys and values, [n_phys][n_kv][64][D] 16-bit each.
+constexpr int kMaxPools = 128;
+struct CachePools {
+  void* p[kMaxPools];
+  int n;
+};
+bool cache_supported(const moe_cache_shape_t* s);
+size_t cache_ws_bytes(const moe_cache_shape_t* s);
+cudaError_t launch_cache_fork(const moe_cache_shape_t* s, const moe_cache_meta_t& in,
+                              const moe_cache_meta_t& out, const int32_t* parent,
+                              const int32_t* keep, uint8_t* ws, cudaStream_t stream);
+cudaError_t launch_cache_reserve(const moe_cache_shape_t* s, const moe_cache_meta_t& in,
+                                 const moe_cache_meta_t& out, const int32_t* n_new,
+                                 int32_t* granted, const CachePools& pools, uint8_t* ws, int nsm,
+                                 cudaStream_t stream);
+cudaError_t launch_cache_write(const moe_cache_shape_t* s, const moe_cache_meta_t& meta,
+                               const int32_t* n_new, int T, const uint16_t* k_new,
+                               int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
+                               void* k_cache, void* v_cache, uint8_t* ws, cudaStream_t stream);
+cudaError_t launch_cache_compact(const moe_cache_shape_t* s, const moe_cache_meta_t& in,
+                                 const moe_cache_meta_t& out, int32_t* n_live,
+                                 const CachePools& pools, uint8_t* ws, int nsm,
+                                 cudaStream_t stream);
+cudaError_t launch_cache_copy_pages(const moe_cache_shape_t* s, int n, const int32_t* src,
+                                    const int32_t* dst, const CachePools& from,
+                                    const CachePools& to, int n_to, uint8_t* ws, int nsm,
+                                    cudaStream_t stream);
+// Verification of drafted tokens (verify.cu).
+bool verify_supported(const moe_verify_shape_t* s);
+size_t verify_ws_bytes(const moe_verify_shape_t* s);
+cudaError_t launch_verify(const moe_verify_shape_t* s, const void* p, const void* q,
+                          const int32_t* draft, const int32_t* n_draft, const float* u,
+                          int32_t* tokens, int32_t* n_acc, uint8_t* ws, cudaStream_t stream);
 // Host helpers shared by the C-ABI translation units (api.cu keeps the state).
 bool shape_supported(const moe_shape_t* shape);
 void set_last_error(const char* text);
 void set_last_cuda_error(cudaError_t e, const char* where);
+// SMs of the current device, and the tensor map of `rows` dense rows of D
+// 16-bit elements in boxes of 64 rows x 64 elements (128-byte swizzle)
+moe_status_t device_sm_count(int* out);
+moe_status_t encode_rows64(CUtensorMap* m, bool fp16, const void* base, int D, uint64_t rows);
 int ffn_tile_m();
 int ffn_max_tile_n();
 int ffn_stage_k();

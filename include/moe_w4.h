@@ -59,7 +59,7 @@ typedef enum moe_status {
   MOE_ERR_UNSUPPORTED_SHAPE = 2, /* shape outside the supported set above */
   MOE_ERR_WORKSPACE = 3,         /* workspace smaller than moe_workspace_bytes() */
   MOE_ERR_CUDA = 4,              /* a CUDA runtime/driver call failed */
-  MOE_ERR_BAD_INPUT = 5,         /* device: an expert id outside [0, E) */
+  MOE_ERR_BAD_INPUT = 5,         /* device: an expert id outside [0, E), a bad table entry */
   MOE_ERR_TIMEOUT = 6            /* device: a bounded wait ran out */
 } moe_status_t;
 
@@ -417,6 +417,145 @@ moe_status_t moe_gdn_chunked_scan(const moe_gdn_shape_t* shape, const void* q_de
                                   const float* beta_dev, const float* state_in_dev,
                                   float* state_out_dev, void* o_dev, void* ws_dev,
                                   size_t ws_bytes, moe_stream_t stream);
+
+/* ----------------------------------------------------------------------
+ * A batch of requests over one page pool: the pages of its cache, attention
+ * that shares a prompt, and the verification of drafted tokens. The pages
+ * name the pieces (a growing key/value cache in fixed-size blocks, decode
+ * steps that stay on the device); the batch is the form in which a server
+ * runs them.
+ *
+ * 16-bit pools [n_phys][n_kv][64][D], one per layer's keys and one per its
+ * values, share page numbers. The state of n_slots slots (requests or beams):
+ *   table_dev int32 [n_slots][max_blocks]  page of each 64-position block
+ *   lens_dev  int32 [n_slots]              positions held
+ *   refs_dev  int32 [n_phys]               table entries that hold the page;
+ *                                          0 = free (a caller may add counts
+ *                                          of its own to pin pages)
+ * A slot's entries are the first ceil(len / 64) of its row; the calls write
+ * -1 past them. Calls that change the state read `in` and write `out`, which
+ * must not share an array: the old state stays whole, so a caller can drop a
+ * result (of a reservation that was refused, say). A length, count or entry
+ * out of range is recorded as MOE_ERR_BAD_INPUT and its slot or page is left
+ * out; no such value leads to an access out of bounds. All of it is integer
+ * work and copies: deterministic.
+ * ---------------------------------------------------------------------- */
+typedef enum moe_dtype { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP16 = 1, MOE_DTYPE_FP32 = 2 } moe_dtype_t;
+
+typedef struct moe_cache_shape {
+  int32_t n_slots;    /* 1 .. 4096 */
+  int32_t max_blocks; /* entries of a table row, 1 .. 2^18 */
+  int32_t n_phys;     /* pages of every pool, 1 .. 2^20 */
+  int32_t n_kv;       /* heads of a pool, 1 .. 64 */
+  int32_t D;          /* elements of a head's row: a multiple of 8 up to 512 */
+  int32_t block;      /* positions per page: 64 */
+} moe_cache_shape_t;
+
+typedef struct moe_cache_meta {
+  int32_t* table_dev;
+  int32_t* lens_dev;
+  int32_t* refs_dev;
+} moe_cache_meta_t;
+
+/* Workspace bytes of the moe_cache_* calls, 0 for an unsupported shape.
+ * Zero-fill it once (moe_workspace_init); 256-byte aligned. */
+size_t moe_cache_workspace_bytes(const moe_cache_shape_t* shape);
+
+/* Fork, reorder, cut and free: slot s of `out` holds what slot parent_dev[s]
+ * of `in` held, the first keep_dev[s] positions of it at most (keep_dev NULL:
+ * all of them); parent -1 leaves the slot empty. Pages are shared, not
+ * copied; refs follow. parent[s] = s with keep drops the tail of a slot (its
+ * rejected drafts), beams of one request are parents of each other.
+ *  parent_dev int32 [n_slots], keep_dev int32 [n_slots] or NULL */
+moe_status_t moe_cache_fork(const moe_cache_shape_t* shape, const moe_cache_meta_t* in,
+                            const int32_t* parent_dev, const int32_t* keep_dev,
+                            const moe_cache_meta_t* out, void* ws_dev, size_t ws_bytes,
+                            moe_stream_t stream);
+
+/* Room for n_new_dev[s] more positions of every slot. A slot needs a page
+ * for each block past its last, and one more where n_new > 0 and its last
+ * page is partly filled and held more than once: that page is copied (the
+ * filled rows, in every pool) and the slot's entry points to the copy. Needs
+ * are met in slot order while the running sum of all needs so far fits the
+ * pages that `in` has free, with the lowest free pages in order (a slot's
+ * copy first); a slot that does not fit, or whose row is too short, stays as
+ * it was. A page that this call lets go of is free after it, not during it.
+ *  n_new_dev   int32 [n_slots], >= 0
+ *  granted_dev int32 [n_slots] out: n_new, or 0 where it was refused
+ *  pools_host  n_pools (0 .. 128) device pointers, 16-byte aligned */
+moe_status_t moe_cache_reserve(const moe_cache_shape_t* shape, const moe_cache_meta_t* in,
+                               const int32_t* n_new_dev, const moe_cache_meta_t* out,
+                               int32_t* granted_dev, void* const* pools_host, int32_t n_pools,
+                               void* ws_dev, size_t ws_bytes, moe_stream_t stream);
+
+/* The keys and values of new tokens into their pages: token t < n_new[s] of
+ * slot s goes to position lens[s] - n_new[s] + t (lens after the
+ * reservation). Token (s, t) of k_new_dev starts k_stride * (s * T + t)
+ * elements in, [n_kv][D], so a slice of a joint projection needs no copy.
+ *  n_new_dev int32 [n_slots] or NULL (T for every slot); reserve's granted
+ *  k_stride, v_stride elements between tokens, multiples of 8, >= n_kv * D
+ *  k_cache_dev, v_cache_dev one layer's pools
+ * Pages held more than once are the caller's to avoid (reserve copies them). */
+moe_status_t moe_cache_write(const moe_cache_shape_t* shape, const moe_cache_meta_t* meta,
+                             const int32_t* n_new_dev, int32_t T, const void* k_new_dev,
+                             int64_t k_stride, const void* v_new_dev, int64_t v_stride,
+                             void* k_cache_dev, void* v_cache_dev, void* ws_dev, size_t ws_bytes,
+                             moe_stream_t stream);
+
+/* Brings the held pages to the front: with L pages held, the i-th held page
+ * at or past L moves to the i-th free page below L, in every pool; tables and
+ * refs follow, pages from L on are free after it.
+ *  n_live_dev int32 [1] out: L */
+moe_status_t moe_cache_compact(const moe_cache_shape_t* shape, const moe_cache_meta_t* in,
+                               const moe_cache_meta_t* out, int32_t* n_live_dev,
+                               void* const* pools_host, int32_t n_pools, void* ws_dev,
+                               size_t ws_bytes, moe_stream_t stream);
+
+/* Whole pages: page src_dev[i] of every pool of from_host to page dst_dev[i]
+ * of the same pool of to_host (which may be the same pools: then no page may
+ * be both read and written, nor written twice). For swapping slots out and
+ * in.
+ *  n         pairs (>= 1); n_to: pages of the pools in to_host */
+moe_status_t moe_cache_copy_pages(const moe_cache_shape_t* shape, int32_t n,
+                                  const int32_t* src_dev, const int32_t* dst_dev,
+                                  void* const* from_host, void* const* to_host, int32_t n_pools,
+                                  int32_t n_to, void* ws_dev, size_t ws_bytes,
+                                  moe_stream_t stream);
+
+/* Verification of drafted tokens (speculative sampling: the tokens come out
+ * distributed as the target's, whatever the draft's distribution was). Slot
+ * s has n = n_draft_dev[s] drafts x_t drawn from q_t:
+ *   draft t is accepted while u_t q_t(x_t) < p_t(x_t); i = the first that is
+ *   not, n when all are;
+ *   w = max(p_i - q_i, 0) where i < n, or p_i where that is 0 everywhere;
+ *   w = p_n where i = n;
+ *   the new token is the least v with w_0 + .. + w_v > u_T (w_0 + .. + w_{V-1}).
+ * Sums carry more than 48 bits and u q is exact, so the tokens do not depend
+ * on an order of summation. Entries that are not positive and finite weigh
+ * nothing. A drafted id outside [0, V) is rejected and recorded; a row
+ * without any weight gives token -1 and is recorded.
+ *  p_dev       [n_slots][T + 1][V] target's probabilities (need not sum to 1)
+ *  q_dev       [n_slots][T][V] the draft's, same type, or NULL: the drafts
+ *              are certain (q_t(x_t) = 1, 0 elsewhere)
+ *  draft_dev   int32 [n_slots][T]; n_draft_dev int32 [n_slots] or NULL (T)
+ *  u_dev       fp32 [n_slots][T + 1] random numbers in [0, 1); u_T draws the
+ *              new token
+ *  tokens_dev  int32 [n_slots][T + 1] out: the accepted drafts, the new
+ *              token, -1
+ *  n_acc_dev   int32 [n_slots] out: i */
+typedef struct moe_verify_shape {
+  int32_t n_slots; /* 1 .. 4096 */
+  int32_t T;       /* most drafts of a slot, 1 .. 31 */
+  int32_t V;       /* vocabulary, 1 .. 2^20 */
+  int32_t dtype;   /* moe_dtype_t of p and q */
+} moe_verify_shape_t;
+
+size_t moe_verify_workspace_bytes(const moe_verify_shape_t* shape);
+moe_status_t moe_verify_drafts(const moe_verify_shape_t* shape, const void* p_dev,
+                               const void* q_dev, const int32_t* draft_dev,
+                               const int32_t* n_draft_dev, const float* u_dev,
+                               int32_t* tokens_dev, int32_t* n_acc_dev, void* ws_dev,
+                               size_t ws_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

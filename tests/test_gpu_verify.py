@@ -45,7 +45,7 @@ def check(p, q, draft, n_draft, u, dtype, want_status=0):
     got = run(p, q, draft, n_draft, u, dtype, want_status)
     B, T1, _ = p.shape
     want = ref.verify(p.double().numpy(), None if q is None else q.double().numpy(),
-                      np.asarray(draft), np.full(B, T1 - 1) if n_draft is None else n_draft,
+                      np.asarray(draft, np.int32), np.full(B, T1 - 1) if n_draft is None else n_draft,
                       np.asarray(u, np.float32).astype(np.float64))
     np.testing.assert_array_equal(got[1], want[1])
     np.testing.assert_array_equal(got[0], want[0])

@@ -41,7 +41,7 @@ EXPORTS = ("moe_workspace_bytes", "moe_max_blocks", "moe_workspace_init", "moe_r
            "moe_gdn_scan", "moe_gdn_chunked_workspace_bytes", "moe_gdn_chunked_scan",
            "moe_cache_workspace_bytes", "moe_cache_fork", "moe_cache_reserve", "moe_cache_write",
            "moe_cache_compact", "moe_cache_copy_pages", "moe_verify_workspace_bytes",
-           "moe_verify_drafts")
+           "moe_verify_drafts", "moe_attn_batch_workspace_bytes", "moe_attn_batch")
 
 
 class MoeError(RuntimeError):
@@ -79,6 +79,12 @@ class CacheShape(C.Structure):
 
 class CacheMetaPtrs(C.Structure):
     _fields_ = [("table", C.c_void_p), ("lens", C.c_void_p), ("refs", C.c_void_p)]
+
+
+class AttnBatchShape(C.Structure):
+    _fields_ = [("n_slots", C.c_int32), ("T", C.c_int32), ("n_q", C.c_int32), ("n_kv", C.c_int32),
+                ("D", C.c_int32), ("block", C.c_int32), ("max_blocks", C.c_int32),
+                ("prefix_blocks", C.c_int32), ("dtype", C.c_int32)]
 
 
 class VerifyShape(C.Structure):
@@ -130,6 +136,9 @@ def load():
             L.moe_cache_workspace_bytes.argtypes = [pC]
             L.moe_verify_workspace_bytes.restype = SZ
             L.moe_verify_workspace_bytes.argtypes = [pV]
+            pA = C.POINTER(AttnBatchShape)
+            L.moe_attn_batch_workspace_bytes.restype = SZ
+            L.moe_attn_batch_workspace_bytes.argtypes = [pA]
             I64 = C.c_int64
             for name, args in (
                     ("moe_workspace_init", [P, SZ, P]),
@@ -153,6 +162,7 @@ def load():
                     ("moe_cache_write", [pC, pM, P, I32, P, I64, P, I64, P, P, P, SZ, P]),
                     ("moe_cache_compact", [pC, pM, pM, P, P, I32, P, SZ, P]),
                     ("moe_cache_copy_pages", [pC, I32, P, P, P, P, I32, I32, P, SZ, P]),
+                    ("moe_attn_batch", [pA, P, I64, P, P, I32, P, P, P, P, P, P, SZ, P]),
                     ("moe_verify_drafts", [pV, P, P, P, P, P, P, P, P, SZ, P])):
                 f = getattr(L, name)
                 f.restype = C.c_int
@@ -476,6 +486,37 @@ def moe_cache_copy_pages(shape, src, dst, from_pools, to_pools, ws, stream=None)
     _check(load().moe_cache_copy_pages(C.byref(shape), src.shape[0], _ints(src, (None,), "src"),
                                        _ints(dst, src.shape, "dst"), a, b, k, n_to, _p(ws),
                                        ws.numel(), _s(stream)), "moe_cache_copy_pages")
+
+
+def make_attn_batch_shape(n_slots, T, n_q, n_kv, D, max_blocks, prefix_blocks=0, dtype="bf16",
+                          block=64):
+    return AttnBatchShape(n_slots, T, n_q, n_kv, D, block, max_blocks, prefix_blocks, DTYPES[dtype])
+
+
+def alloc_attn_batch_workspace(shape, device="cuda", stream=None):
+    return _workspace(load().moe_attn_batch_workspace_bytes(C.byref(shape)), device, stream,
+                      "alloc_attn_batch_workspace")
+
+
+def moe_attn_batch(shape, q, k_cache, v_cache, table, lens, o, ws, n_new=None, prefix=None,
+                   stream=None):
+    """Decode attention of every slot's last n_new[s] (None: T) tokens over its
+    pages; the first shape.prefix_blocks blocks of all slots are the pages
+    `prefix`, read once for the batch. q [n_slots][T][n_q][D] may be a slice
+    of a joint projection; o is dense."""
+    B, T, nq, D = shape.n_slots, shape.T, shape.n_q, shape.D
+    dt = torch.float16 if shape.dtype == 1 else torch.bfloat16
+    if q.dtype not in (dt, torch.int16):
+        raise ValueError("q must be %s, got %s" % (dt, q.dtype))
+    qp, qs = _tokens(q, B, T, (nq, D), "q")
+    n_phys = k_cache.shape[0]
+    cache = (n_phys, shape.n_kv, shape.block, D)
+    _check(load().moe_attn_batch(
+        C.byref(shape), qp, qs, _tensor(k_cache, dt, cache, "k_cache"),
+        _tensor(v_cache, dt, cache, "v_cache"), n_phys, _ints(table, (B, shape.max_blocks), "table"),
+        _ints(prefix, (shape.prefix_blocks,), "prefix"), _ints(lens, (B,), "lens"),
+        _ints(n_new, (B,), "n_new"), _tensor(o, dt, (B, T, nq, D), "o"), _p(ws), ws.numel(),
+        _s(stream)), "moe_attn_batch")
 
 
 def make_verify_shape(n_slots, T, V, dtype="fp32"):

@@ -140,6 +140,46 @@ moe_status_t moe_cache_copy_pages(const moe_cache_shape_t* shape, int32_t n,
               "cache page copy launch");
 }
 
+size_t moe_attn_batch_workspace_bytes(const moe_attn_batch_shape_t* shape) {
+  return attn_batch_supported(shape) ? attn_batch_ws_bytes(shape) : 0;
+}
+
+moe_status_t moe_attn_batch(const moe_attn_batch_shape_t* shape, const void* q_dev,
+                            int64_t q_stride, const void* k_cache_dev, const void* v_cache_dev,
+                            int32_t n_phys, const int32_t* table_dev, const int32_t* prefix_dev,
+                            const int32_t* lens_dev, const int32_t* n_new_dev, void* o_dev,
+                            void* ws_dev, size_t ws_bytes, moe_stream_t stream) {
+  if (!attn_batch_supported(shape)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!q_dev || !k_cache_dev || !v_cache_dev || !o_dev || !aligned(q_dev, 16) ||
+      !aligned(k_cache_dev, 16) || !aligned(v_cache_dev, 16) || !aligned(o_dev, 16) ||
+      q_stride < (int64_t)shape->n_q * shape->D || q_stride % 8 || !ints(table_dev) ||
+      !ints(lens_dev) || !aligned(n_new_dev, 4) || !aligned(prefix_dev, 4) ||
+      (shape->prefix_blocks > 0 && !prefix_dev) || n_phys < 1 ||
+      // rows of the pools, one page past the end too, are counted in 32 bits
+      ((int64_t)n_phys + 1) * shape->n_kv * shape->block > INT32_MAX)
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ws(ws_dev, ws_bytes, attn_batch_ws_bytes(shape)));
+  int nsm = 0;
+  MOE_TRY(device_sm_count(&nsm));
+  const uint64_t rows = (uint64_t)n_phys * shape->n_kv * shape->block;
+  const bool fp16 = shape->dtype == MOE_DTYPE_FP16;
+  CUtensorMap tk, tv;
+  MOE_TRY(encode_rows64(&tk, fp16, k_cache_dev, shape->D, rows));
+  MOE_TRY(encode_rows64(&tv, fp16, v_cache_dev, shape->D, rows));
+  AttnBatchArgs a{};
+  a.q = static_cast<const uint16_t*>(q_dev);
+  a.q_stride = q_stride;
+  a.table = table_dev;
+  a.prefix = prefix_dev;
+  a.lens = lens_dev;
+  a.n_new = n_new_dev;
+  a.n_phys = n_phys;
+  a.o = static_cast<uint16_t*>(o_dev);
+  return done(launch_attn_batch(shape, tk, tv, a, static_cast<uint8_t*>(ws_dev), nsm,
+                                (cudaStream_t)stream),
+              "batch attention launch");
+}
+
 size_t moe_verify_workspace_bytes(const moe_verify_shape_t* shape) {
   return verify_supported(shape) ? verify_ws_bytes(shape) : 0;
 }

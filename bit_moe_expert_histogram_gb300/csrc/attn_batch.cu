@@ -1,0 +1,506 @@
+// Grouped-query decode attention for a batch of slots over one page pool,
+// the leading pages of all slots being the same ones (a shared prompt).
+//
+// Row t of slot s sits at position p = lens[s] - n_new[s] + t:
+//   o[s][t][h] = softmax_j(q . k_j / sqrt(D)) v_j over j <= p,
+// head h reading key/value head h / (n_q / n_kv). A row with nothing to see
+// (t >= n_new, an idle slot) is 0.
+//
+// Softmax of a row split over key ranges: each range keeps its reference
+// maximum m, l = sum 2^(x - m) and O = sum 2^(x - m) v (x = log2(e) q.k /
+// sqrt(D)); ranges join as O = sum O_i 2^(m_i - M) with M = max m_i, the same
+// for l, in a fixed order.
+//
+// attn_own_kernel: each slot's own positions. The (slot, head) pairs' blocks
+// lie on one line, and CTA c takes blocks [c per, (c + 1) per) of it whatever
+// slots they belong to, so uneven lengths leave no CTA idle. The
+// T * n_q / n_kv <= 64 query rows of a pair are the M rows of mma.sync tiles
+// (16 rows; 1, 2 or 4 tiles), so each key and value is read once per slot.
+// Blocks stream through a TMA ring of three stages (64 rows x 64 elements per
+// box, 128-byte swizzle) that runs on across pairs. A pair cut by a CTA
+// border leaves (m, l, O) in the workspace and the last of its CTAs to arrive
+// joins them in CTA order.
+#include "attn_batch.cuh"
+
+namespace moe {
+
+namespace {
+constexpr int kOThr = 128;
+constexpr int kOStages = 3;
+constexpr int kOAreaFloats = 2048;  // 8 KB where the warps' O meet
+
+template <bool F16>
+__device__ __forceinline__ void mma16816t(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  if (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// byte offset of 16-byte chunk ch of row p in a [64][D] tile stored as D/64
+// TMA boxes of 64 rows x 128 bytes with the 128-byte swizzle
+__device__ __forceinline__ uint32_t swz64(int p, int ch) {
+  return (uint32_t)((ch >> 3) * (kBlk * 128) + p * 128 + (((ch & 7) ^ (p & 7)) << 4));
+}
+}  // namespace
+
+template <bool F16, int D, int MT>
+__global__ void __launch_bounds__(kOThr, 2)
+    attn_own_kernel(const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const AttnBatchArgs a) {
+  constexpr int kTile = kBlk * D * 2;  // bytes of a block's keys (or values)
+  constexpr int kNS = 4 / MT;          // warps that share a row tile, each a slice of the block
+  constexpr int kPos = kBlk / kNS;     // positions of a slice
+  constexpr int kNT = kPos / 8;        // score n-tiles of a warp
+  constexpr int kKS = D / 16, kDT = D / 8;
+  constexpr int kR = MT * 16;          // rows of the tiles
+  constexpr int kCW = kOAreaFloats / kR < D ? kOAreaFloats / kR : D;  // columns of O joined at a time
+  extern __shared__ __align__(1024) uint8_t sm_raw[];
+  __shared__ __align__(8) uint64_t full[kOStages];
+  __shared__ int s_bad[kOStages];
+  __shared__ int s_abort, s_start, s_off, s_total, s_last;
+  __shared__ int s_scan[4];
+  __shared__ float s_m[4][16], s_l[4][16];  // per warp: its rows' maximum and sum
+  __shared__ float s_M[kR], s_L[kR];        // the segment's
+  const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
+  uint8_t* sm = sm_raw + (sbase - smem_u32(sm_raw));
+  float* area = reinterpret_cast<float*>(sm + kOStages * 2 * kTile);  // [kR][kCW]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gq = lane >> 2, cq = lane & 3;
+  const int mt = warp % MT, ps = warp / MT;
+  const int G = a.n_q / a.n_kv, rows = a.T * G;
+  const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(D)
+  const uint32_t fb = smem_u32(&full[0]);
+  if (tid == 0) {
+    for (int i = 0; i < kOStages; ++i) mbar_init(fb + 8u * i, 1);
+    s_abort = 0;
+    s_start = 0;
+    s_off = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  pdl_wait();
+  pdl_trigger();
+  // ---- this CTA's part of the line of blocks
+  {
+    const int chunk = (a.n_slots + kOThr - 1) / kOThr;
+    const int s0 = min(tid * chunk, a.n_slots), s1 = min(s0 + chunk, a.n_slots);
+    int sum = 0;
+    for (int s = s0; s < s1; ++s) sum += slot_span(a, s).blocks;
+    sum *= a.n_kv;
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += s_scan[w];
+    if (tid == kOThr - 1) s_total = incl;
+    __syncthreads();
+    const int per = (s_total + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int f0 = (int)blockIdx.x * per;
+    int run = incl - sum;
+    if (f0 >= run && f0 < incl) {  // one thread's slots hold the first block
+      int s = s0;
+      for (; s < s1 - 1; ++s) {
+        const int n = slot_span(a, s).blocks * a.n_kv;
+        if (f0 < run + n) break;
+        run += n;
+      }
+      s_start = s;
+      s_off = f0 - run;
+    }
+    __syncthreads();
+  }
+  const int total = s_total;
+  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int f0 = (int)blockIdx.x * per, f1 = min(f0 + per, total);
+  if (f0 >= f1) return;
+  const uint64_t pol = policy_evict_first();  // own pages are read once
+  // ---- thread 0's cursor: the next block to load
+  int is = s_start, ig = 0, ij = s_off;
+  SlotSpan isp = slot_span(a, is);
+  ig = ij / isp.blocks;
+  ij -= ig * isp.blocks;
+  auto issue = [&](int st) {
+    const int jb = a.first + ij;
+    int phys = -1, bad = 0;
+    if (isp.n_new > 0 && jb * kBlk < isp.len) {
+      phys = jb < a.prefix_blocks ? __ldg(a.prefix + jb)
+                                  : __ldg(a.table + (int64_t)is * a.max_blocks + jb);
+      if (phys < 0 || phys >= a.n_phys) {
+        set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_ATTNB, is);
+        bad = 1;
+        phys = -1;
+      }
+    }
+    // a page that is not there reads past the pool's end: the copy fills zeros
+    const int row0 = (phys < 0 ? a.n_phys * a.n_kv : phys * a.n_kv + ig) * kBlk;
+    s_bad[st] = bad;
+    const uint32_t sk = sbase + (uint32_t)(st * 2 * kTile), sv = sk + kTile;
+    const uint32_t bar = fb + 8u * st;
+    mbar_arrive_expect_tx(bar, 2u * kTile);
+#pragma unroll
+    for (int bx = 0; bx < D / 64; ++bx) {
+      tma_load_2d(sk + bx * (kBlk * 128), &tm_k, bx * 64, row0, bar, pol);
+      tma_load_2d(sv + bx * (kBlk * 128), &tm_v, bx * 64, row0, bar, pol);
+    }
+    if (++ij == isp.blocks) {
+      ij = 0;
+      if (++ig == a.n_kv) {
+        ig = 0;
+        if (++is < a.n_slots) isp = slot_span(a, is);
+      }
+    }
+  };
+  int issued = min(kOStages - 1, f1 - f0);
+  if (tid == 0)
+    for (int i = 0; i < issued; ++i) issue(i);
+
+  // ---- the pairs of this CTA
+  int s = s_start;
+  SlotSpan sp = slot_span(a, s);
+  int g = s_off / sp.blocks;
+  int pb = f0 - (s_off - g * sp.blocks);  // where the pair starts on the line
+  int f = f0;
+  while (f < f1) {
+    const int fe = min(f1, pb + sp.blocks);
+    const bool whole = f == pb && fe == pb + sp.blocks;
+    // rows r = t * G + head in group; a row's last position, -1: sees nothing
+    const int base = sp.len - sp.n_new;  // may be negative
+    const int r0 = mt * 16 + gq, r1 = r0 + 8;
+    const int lim0 = r0 < rows && r0 / G < sp.n_new ? base + r0 / G : -1;
+    const int lim1 = r1 < rows && r1 / G < sp.n_new ? base + r1 / G : -1;
+    uint32_t qa[kKS][4];
+    {
+      const uint16_t* q0 = lim0 >= 0 ? a.q + ((int64_t)s * a.T + r0 / G) * a.q_stride + (g * G + r0 % G) * D : nullptr;
+      const uint16_t* q1 = lim1 >= 0 ? a.q + ((int64_t)s * a.T + r1 / G) * a.q_stride + (g * G + r1 % G) * D : nullptr;
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks) {
+        const int d = ks * 16 + 2 * cq;
+        qa[ks][0] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d)) : 0u;
+        qa[ks][1] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d)) : 0u;
+        qa[ks][2] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d + 8)) : 0u;
+        qa[ks][3] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d + 8)) : 0u;
+      }
+    }
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    float oacc[kDT][4];
+#pragma unroll
+    for (int j = 0; j < kDT; ++j) oacc[j][0] = oacc[j][1] = oacc[j][2] = oacc[j][3] = 0.0f;
+    for (; f < fe; ++f) {
+      const int it = f - f0, st = it % kOStages;
+      if (!mbar_wait(fb + 8u * st, (uint32_t)(it / kOStages) & 1u, &s_abort) &&
+          atomicCAS(&s_abort, 0, 1) == 0)
+        set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, s);
+      // this thread's reads of the block before are ordered before the refill
+      // of its stage, which thread 0 issues after the barrier
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (s_abort) break;
+      if (f + kOStages - 1 < f1) {
+        if (tid == 0) issue((it + kOStages - 1) % kOStages);
+        ++issued;
+      }
+      const uint32_t sk = sbase + (uint32_t)(st * 2 * kTile), sv = sk + kTile;
+      const int pos0 = (a.first + f - pb) * kBlk;
+      const bool bad = s_bad[st] != 0;
+      if (pos0 + kBlk > sp.len) {
+        // rows past the slot's end hold anything, NaN too: 0 x NaN in P V
+        // would reach the output, so they are set to 0
+        const int z0 = max(sp.len - pos0, 0);
+        for (int i = tid; i < (kBlk - z0) * (D / 8); i += kOThr) {
+          const int p = z0 + i / (D / 8);
+          *reinterpret_cast<uint4*>(sm + st * 2 * kTile + kTile + swz64(p, i % (D / 8))) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncthreads();
+      }
+      // S = Q K^T over this warp's positions
+      float sc[kNT][4];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+      const int mi = lane >> 3, rr = lane & 7;
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+        for (int n = 0; n < kNT; n += 2) {
+          uint32_t kb[4];
+          ldm_x4(sk + swz64(kPos * ps + 8 * n + ((mi & 2) ? 8 : 0) + rr, ks * 2 + (mi & 1)), kb);
+          mma16816t<F16>(sc[n], qa[ks], kb[0], kb[1]);
+          mma16816t<F16>(sc[n + 1], qa[ks], kb[2], kb[3]);
+        }
+      float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int pos = pos0 + kPos * ps + 8 * n + 2 * cq + h;
+          sc[n][h] = (!bad && pos <= lim0) ? sc[n][h] * sl2 : -INFINITY;
+          sc[n][2 + h] = (!bad && pos <= lim1) ? sc[n][2 + h] * sl2 : -INFINITY;
+          mx0 = fmaxf(mx0, sc[n][h]);
+          mx1 = fmaxf(mx1, sc[n][2 + h]);
+        }
+#pragma unroll
+      for (int d = 1; d <= 2; d <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, d));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, d));
+      }
+      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+      // all masked so far: everything stays 0 (no inf - inf)
+      const float u0 = n0 == -INFINITY ? 0.0f : n0, u1 = n1 == -INFINITY ? 0.0f : n1;
+      const float c0 = ex2(m0 - u0), c1 = ex2(m1 - u1);
+      m0 = n0;
+      m1 = n1;
+      l0 *= c0;
+      l1 *= c1;
+      const float x0 = u0 - lift<F16>(), x1 = u1 - lift<F16>();
+      uint32_t pa[kNT / 2][4];
+      // the sums take the rounded weights, the ones that the product sees
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        const uint32_t w0 = pack2<F16>(ex2(sc[n][0] - x0), ex2(sc[n][1] - x0));
+        const uint32_t w1 = pack2<F16>(ex2(sc[n][2] - x1), ex2(sc[n][3] - x1));
+        l0 += unpack_lo<F16>(w0) + unpack_hi<F16>(w0);
+        l1 += unpack_lo<F16>(w1) + unpack_hi<F16>(w1);
+        pa[n / 2][2 * (n & 1)] = w0;
+        pa[n / 2][2 * (n & 1) + 1] = w1;
+      }
+#pragma unroll
+      for (int j = 0; j < kDT; ++j) {
+        oacc[j][0] *= c0;
+        oacc[j][1] *= c0;
+        oacc[j][2] *= c1;
+        oacc[j][3] *= c1;
+      }
+#pragma unroll
+      for (int kp = 0; kp < kPos / 16; ++kp)
+#pragma unroll
+        for (int j = 0; j < kDT; j += 2) {
+          uint32_t vb[4];
+          ldm_x4_t(sv + swz64(kPos * ps + 16 * kp + ((mi & 1) ? 8 : 0) + rr, j + (mi >> 1)), vb);
+          mma16816t<F16>(oacc[j], pa[kp], vb[0], vb[1]);
+          mma16816t<F16>(oacc[j + 1], pa[kp], vb[2], vb[3]);
+        }
+    }
+    if (s_abort) break;  // the same for every thread: it was read after a barrier
+    // ---- the slices' (m, l, O) become the segment's
+#pragma unroll
+    for (int d = 1; d <= 2; d <<= 1) {
+      l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, d);
+      l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, d);
+    }
+    if (cq == 0) {
+      s_m[warp][gq] = m0;
+      s_m[warp][gq + 8] = m1;
+      s_l[warp][gq] = l0;
+      s_l[warp][gq + 8] = l1;
+    }
+    __syncthreads();
+    float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kNS; ++k) {
+      M0 = fmaxf(M0, s_m[mt + k * MT][gq]);
+      M1 = fmaxf(M1, s_m[mt + k * MT][gq + 8]);
+    }
+    const float U0 = M0 == -INFINITY ? 0.0f : M0, U1 = M1 == -INFINITY ? 0.0f : M1;
+    if (ps == 0 && cq == 0) {
+      float L0 = 0.0f, L1 = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kNS; ++k) {
+        L0 += s_l[mt + k * MT][gq] * ex2(s_m[mt + k * MT][gq] - U0);
+        L1 += s_l[mt + k * MT][gq + 8] * ex2(s_m[mt + k * MT][gq + 8] - U1);
+      }
+      s_M[r0] = M0;
+      s_M[r1] = M1;
+      s_L[r0] = L0;
+      s_L[r1] = L1;
+    }
+    const float w0 = ex2(m0 - U0), w1 = ex2(m1 - U1);
+    // a cut pair's part: place 2 c for CTA c's first pair, 2 c + 1 for a later one
+    float* part = a.part + (int64_t)(2 * (int)blockIdx.x + (f0 >= pb ? 0 : 1)) * kR * (D + 2);
+#pragma unroll
+    for (int cb = 0; cb < D; cb += kCW) {
+#pragma unroll
+      for (int k = 0; k < kNS; ++k) {
+        if (ps == k) {
+#pragma unroll
+          for (int j = 0; j < kCW / 8; ++j) {
+            const int jj = cb / 8 + j;
+            float* p0 = area + r0 * kCW + 8 * j + 2 * cq;
+            float* p1 = area + r1 * kCW + 8 * j + 2 * cq;
+            if (k == 0) {
+              p0[0] = oacc[jj][0] * w0;
+              p0[1] = oacc[jj][1] * w0;
+              p1[0] = oacc[jj][2] * w1;
+              p1[1] = oacc[jj][3] * w1;
+            } else {
+              p0[0] += oacc[jj][0] * w0;
+              p0[1] += oacc[jj][1] * w0;
+              p1[0] += oacc[jj][2] * w1;
+              p1[1] += oacc[jj][3] * w1;
+            }
+          }
+        }
+        __syncthreads();
+      }
+      for (int i = tid; i < rows * (kCW / 2); i += kOThr) {
+        const int r = i / (kCW / 2), d = 2 * (i - r * (kCW / 2));
+        const float2 o2 = *reinterpret_cast<const float2*>(area + r * kCW + d);
+        if (whole) {
+          const float inv = s_L[r] > 0.0f ? 1.0f / s_L[r] : 0.0f;
+          *reinterpret_cast<uint32_t*>(
+              a.o + (((int64_t)s * a.T + r / G) * a.n_q + g * G + r % G) * D + cb + d) =
+              pack2<F16>(o2.x * inv, o2.y * inv);
+        } else {
+          *reinterpret_cast<float2*>(part + 2 * kR + r * D + cb + d) = o2;
+        }
+      }
+      __syncthreads();
+    }
+    if (!whole) {
+      for (int r = tid; r < rows; r += kOThr) {
+        part[r] = s_M[r];
+        part[kR + r] = s_L[r];
+      }
+      __threadfence();
+      __syncthreads();
+      // the pair's CTAs: first and last to hold a block of it
+      const int c0 = pb / per, c1 = (pb + sp.blocks - 1) / per;
+      if (tid == 0) {
+        unsigned* cnt = a.count + (int64_t)s * a.n_kv + g;
+        s_last = atomicAdd(cnt, 1u) == (unsigned)(c1 - c0);
+        if (s_last) *cnt = 0u;  // ready for the next call
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_last) {
+        for (int i = tid; i < rows * (D / 2); i += kOThr) {
+          const int r = i / (D / 2), d = 2 * (i - r * (D / 2));
+          float M = -INFINITY, L = 0.0f, ox = 0.0f, oy = 0.0f;
+          for (int c = c0; c <= c1; ++c) {
+            const float* pc = a.part + (int64_t)(2 * c + (c * per >= pb ? 0 : 1)) * kR * (D + 2);
+            const float mc = __ldcg(pc + r), lc = __ldcg(pc + kR + r);
+            const float2 oc = __ldcg(reinterpret_cast<const float2*>(pc + 2 * kR + r * D + d));
+            const float nM = fmaxf(M, mc), U = nM == -INFINITY ? 0.0f : nM;
+            const float fo = ex2(M - U), fc = ex2(mc - U);
+            L = L * fo + lc * fc;
+            ox = ox * fo + oc.x * fc;
+            oy = oy * fo + oc.y * fc;
+            M = nM;
+          }
+          const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+          *reinterpret_cast<uint32_t*>(
+              a.o + (((int64_t)s * a.T + r / G) * a.n_q + g * G + r % G) * D + d) =
+              pack2<F16>(ox * inv, oy * inv);
+        }
+      }
+    }
+    // ---- the next pair
+    pb += sp.blocks;
+    if (++g == a.n_kv) {
+      g = 0;
+      if (++s < a.n_slots) sp = slot_span(a, s);
+    }
+  }
+  if (s_abort && tid == 0) {
+    // a wait ran out: wait (again bounded) for the copies that may still be
+    // in flight, so that none lands after the CTA has gone
+    volatile int never = 0;
+    for (int i = issued > kOStages ? issued - kOStages : 0; i < issued; ++i)
+      mbar_wait(fb + 8u * (i % kOStages), (uint32_t)(i / kOStages) & 1u, &never);
+  }
+}
+
+bool attn_batch_supported(const moe_attn_batch_shape_t* s) {
+  if (!s) return false;
+  if (s->n_slots < 1 || s->n_slots > 4096 || s->T < 1 || s->T > 64) return false;
+  if (s->n_q < 1 || s->n_kv < 1 || s->n_kv > 64 || s->n_q % s->n_kv) return false;
+  if ((int64_t)(s->n_q / s->n_kv) * s->T > 64) return false;
+  if (s->D != 64 && s->D != 128) return false;
+  if (s->block != kBlk || s->max_blocks < 1 || s->max_blocks > (1 << 18)) return false;
+  if (s->prefix_blocks < 0 || s->prefix_blocks > s->max_blocks) return false;
+  if (s->dtype != MOE_DTYPE_BF16 && s->dtype != MOE_DTYPE_FP16) return false;
+  // the line of blocks is counted in 32 bits
+  return (int64_t)s->n_slots * s->n_kv * s->max_blocks < (1 << 30);
+}
+
+namespace {
+int own_tiles(const moe_attn_batch_shape_t* s) {  // row tiles: 1, 2 or 4
+  const int rows = s->T * (s->n_q / s->n_kv);
+  return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+}
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+constexpr int kMostSms = 256;  // two CTAs an SM at most
+
+template <bool F16, int D, int MT>
+cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const AttnBatchArgs& a,
+                       int grid, cudaStream_t stream) {
+  const size_t smem = 1024 + (size_t)kOStages * 2 * kBlk * D * 2 + kOAreaFloats * 4;
+  const cudaError_t e = cudaFuncSetAttribute(attn_own_kernel<F16, D, MT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_own_kernel<F16, D, MT>, dim3(grid), dim3(kOThr), smem, stream, tk, tv, a);
+}
+template <bool F16, int D>
+cudaError_t launch_own_mt(int mt, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const AttnBatchArgs& a, int grid, cudaStream_t stream) {
+  if (mt == 1) return launch_own<F16, D, 1>(tk, tv, a, grid, stream);
+  if (mt == 2) return launch_own<F16, D, 2>(tk, tv, a, grid, stream);
+  return launch_own<F16, D, 4>(tk, tv, a, grid, stream);
+}
+}  // namespace
+
+// status, the pairs' counters, the cut pairs' parts (two per CTA)
+size_t attn_batch_ws_bytes(const moe_attn_batch_shape_t* s) {
+  return 256 + round256((size_t)s->n_slots * s->n_kv * 4) +
+         round256((size_t)2 * 2 * kMostSms * own_tiles(s) * 16 * (s->D + 2) * 4);
+}
+
+cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap& tk,
+                              const CUtensorMap& tv, AttnBatchArgs a, uint8_t* ws, int nsm,
+                              cudaStream_t stream) {
+  a.ctrl = reinterpret_cast<Ctrl*>(ws);
+  a.count = reinterpret_cast<unsigned*>(ws + 256);
+  a.part = reinterpret_cast<float*>(ws + 256 + round256((size_t)s->n_slots * s->n_kv * 4));
+  a.n_slots = s->n_slots;
+  a.T = s->T;
+  a.n_q = s->n_q;
+  a.n_kv = s->n_kv;
+  a.max_blocks = s->max_blocks;
+  a.prefix_blocks = s->prefix_blocks;
+  a.first = 0;
+  const int sms = nsm < kMostSms ? nsm : kMostSms;
+  // two CTAs an SM, and no more than there can be blocks
+  const int64_t most = (int64_t)s->n_slots * s->n_kv * s->max_blocks;
+  const int grid = most < 2 * sms ? (int)most : 2 * sms;
+  const int mt = own_tiles(s);
+  if (s->dtype == MOE_DTYPE_FP16)
+    return s->D == 64 ? launch_own_mt<true, 64>(mt, tk, tv, a, grid, stream)
+                      : launch_own_mt<true, 128>(mt, tk, tv, a, grid, stream);
+  return s->D == 64 ? launch_own_mt<false, 64>(mt, tk, tv, a, grid, stream)
+                    : launch_own_mt<false, 128>(mt, tk, tv, a, grid, stream);
+}
+
+}  // namespace moe

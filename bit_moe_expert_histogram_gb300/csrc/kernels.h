@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "moe_w4.h"
@@ -198,6 +199,26 @@ cudaError_t launch_cache_copy_pages(const moe_cache_shape_t* s, int n, const int
                                     const int32_t* dst, const CachePools& from,
                                     const CachePools& to, int n_to, uint8_t* ws, int nsm,
                                     cudaStream_t stream);
+// Attention of a batch of slots (attn_batch.cu).
+struct AttnBatchArgs {
+  const uint16_t* q;   // token (s, t) starts at q_stride * (s * T + t)
+  int64_t q_stride;
+  const int32_t* table;   // [n_slots][max_blocks]
+  const int32_t* prefix;  // [prefix_blocks]: pages of the first blocks of every slot
+  const int32_t* lens;    // [n_slots]
+  const int32_t* n_new;   // [n_slots] or null: T
+  int n_slots, T, n_q, n_kv, max_blocks, prefix_blocks, n_phys;
+  int first;           // the first block that attn_own_kernel takes
+  uint16_t* o;         // [n_slots][T][n_q][D]
+  float* part;         // cut pairs: per place m[R], l[R], O[R][D]
+  unsigned* count;     // [n_slots][n_kv]: CTAs of a cut pair that have arrived
+  Ctrl* ctrl;
+};
+bool attn_batch_supported(const moe_attn_batch_shape_t* s);
+size_t attn_batch_ws_bytes(const moe_attn_batch_shape_t* s);
+cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap& tk,
+                              const CUtensorMap& tv, AttnBatchArgs a, uint8_t* ws, int nsm,
+                              cudaStream_t stream);
 // Verification of drafted tokens (verify.cu).
 bool verify_supported(const moe_verify_shape_t* s);
 size_t verify_ws_bytes(const moe_verify_shape_t* s);

@@ -522,6 +522,49 @@ moe_status_t moe_cache_copy_pages(const moe_cache_shape_t* shape, int32_t n,
                                   int32_t n_to, void* ws_dev, size_t ws_bytes,
                                   moe_stream_t stream);
 
+/* Grouped-query decode attention of the batch ([Lily] "Decode": the query
+ * heads of a key/value head are packed so each cache row is loaded once, and
+ * the cache is kept in fixed-size blocks), the definition of moe_attn_decode
+ * for every slot: row t < n_new[s] of slot s sits at position
+ * p = lens[s] - n_new[s] + t (lens with the new tokens in it) and
+ *   o[s][t][h] = sum_j softmax_j( q[s][t][h] . k_j / sqrt(D) ) v_j,  j <= p,
+ * fp32 scores and sums, the softmax weights rounded to the type of V before
+ * they multiply it, o in that type. Rows with t >= n_new[s] or p < 0 are 0.
+ * With prefix_blocks > 0 the first prefix_blocks * 64 positions of every slot
+ * are those of the pages prefix_dev[0 .. prefix_blocks) - a prompt that the
+ * slots share - and are read once for the whole batch, not once per slot;
+ * the table's entries there are not read. A slot may be shorter than that.
+ * Keys and values of positions below a slot's length have to be finite; what
+ * its pages hold past it does not matter. A page number outside [0, n_phys)
+ * is recorded as MOE_ERR_BAD_INPUT and its positions are left out.
+ *  q_dev       token (s, t) starts q_stride * (s * T + t) elements in,
+ *              [n_q][D]; 16-byte aligned, q_stride >= n_q * D, a multiple of 8
+ *  k_cache_dev, v_cache_dev [n_phys][n_kv][64][D], 16-byte aligned
+ *  table_dev   int32 [n_slots][max_blocks]
+ *  prefix_dev  int32 [prefix_blocks], or NULL when prefix_blocks is 0
+ *  lens_dev    int32 [n_slots]; n_new_dev int32 [n_slots] or NULL (T)
+ *  o_dev       [n_slots][T][n_q][D] out, 16-byte aligned
+ * Deterministic. The workspace (256-byte aligned) is zero-filled once
+ * (moe_workspace_init); after MOE_ERR_TIMEOUT, again. */
+typedef struct moe_attn_batch_shape {
+  int32_t n_slots;       /* 1 .. 4096 */
+  int32_t T;             /* most new tokens of a slot; (n_q / n_kv) * T <= 64 */
+  int32_t n_q, n_kv;     /* heads; n_kv up to 64 */
+  int32_t D;             /* 64 or 128 */
+  int32_t block;         /* 64 */
+  int32_t max_blocks;    /* entries of a table row, 1 .. 2^18; n_slots * n_kv
+                            * max_blocks below 2^30 */
+  int32_t prefix_blocks; /* 0 .. max_blocks */
+  int32_t dtype;         /* MOE_DTYPE_BF16 or MOE_DTYPE_FP16 */
+} moe_attn_batch_shape_t;
+
+size_t moe_attn_batch_workspace_bytes(const moe_attn_batch_shape_t* shape);
+moe_status_t moe_attn_batch(const moe_attn_batch_shape_t* shape, const void* q_dev,
+                            int64_t q_stride, const void* k_cache_dev, const void* v_cache_dev,
+                            int32_t n_phys, const int32_t* table_dev, const int32_t* prefix_dev,
+                            const int32_t* lens_dev, const int32_t* n_new_dev, void* o_dev,
+                            void* ws_dev, size_t ws_bytes, moe_stream_t stream);
+
 /* Verification of drafted tokens (speculative sampling: the tokens come out
  * distributed as the target's, whatever the draft's distribution was). Slot
  * s has n = n_draft_dev[s] drafts x_t drawn from q_t:

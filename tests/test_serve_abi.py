@@ -112,6 +112,32 @@ def test_verify_argument_errors(lib):
     assert call(have=need - 1) == m.MOE_ERR_WORKSPACE
 
 
+def test_attention_argument_errors(lib):
+    ok = dict(n_slots=4, T=2, n_q=16, n_kv=2, D=128, block=64, max_blocks=10, prefix_blocks=3,
+              dtype=0)
+    shape = m.AttnBatchShape(**ok)
+    need = lib.moe_attn_batch_workspace_bytes(C.byref(shape))
+    assert need > 0
+
+    def call(s=shape, q=P, qs=2048, k=P, v=P, n=100, tab=P, pre=P, ln=P, nn=None, o=P, ws=P,
+             have=need):
+        return lib.moe_attn_batch(C.byref(s), q, qs, k, v, n, tab, pre, ln, nn, o, ws, have, None)
+    for bad in (dict(n_slots=0), dict(n_slots=4097), dict(T=0), dict(T=9), dict(n_q=15),
+                dict(n_kv=0), dict(D=96), dict(D=256), dict(block=32), dict(max_blocks=0),
+                dict(max_blocks=2**18 + 1), dict(prefix_blocks=-1), dict(prefix_blocks=11),
+                dict(dtype=2), dict(n_slots=4096, max_blocks=2**18)):
+        s = m.AttnBatchShape(**{**ok, **bad})
+        assert lib.moe_attn_batch_workspace_bytes(C.byref(s)) == 0, bad
+        assert call(s=s) == m.MOE_ERR_UNSUPPORTED_SHAPE, bad
+    eight = C.c_void_p(0x10008)
+    for bad in (dict(q=None), dict(q=eight), dict(qs=2047), dict(qs=2052), dict(k=None),
+                dict(v=eight), dict(n=0), dict(n=2**24), dict(tab=None), dict(pre=None),
+                dict(ln=None), dict(nn=ODD), dict(o=None), dict(o=eight), dict(ws=None),
+                dict(ws=C.c_void_p(0x10040))):
+        assert call(**bad) == m.MOE_ERR_INVALID_ARG, bad
+    assert call(have=need - 1) == m.MOE_ERR_WORKSPACE
+
+
 # ---- the references on states worked by hand
 def test_reference_fork():
     table = np.array([[3, 1, -1], [2, -1, -1]], np.int32)

@@ -30,7 +30,7 @@ MOE_ERR_TIMEOUT = 6
 
 # moe_dtype_t
 DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
-_TORCH_DTYPE = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+_DTYPE_OF = (torch.bfloat16, torch.float16, torch.float32)
 
 EXPORTS = ("moe_workspace_bytes", "moe_max_blocks", "moe_workspace_init", "moe_route",
            "moe_plan", "moe_expert_ffn_w4", "moe_combine", "moe_layer_w4",
@@ -337,39 +337,58 @@ def moe_decoder_blocks(shape, layer_table, gains, h_out, ws, h_in=None, token_id
 
 
 # ------------------------------------------------- batch serving calls --
-def _tensor(t, dtype, shape, what):
-    """t, checked: a contiguous CUDA tensor of this type and shape (None in
-    `shape`: any extent; bf16 and fp16 tensors may come as int16 bits)."""
-    ok = t.dtype == dtype or (dtype in (torch.bfloat16, torch.float16) and t.dtype == torch.int16)
-    if not ok:
-        raise ValueError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if len(t.shape) != len(shape) or any(n is not None and n != k for n, k in zip(shape, t.shape)):
-        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), tuple(shape)))
-    return _p(t)
+# A call of a few microseconds on the GPU must not wait for its checks: the
+# helpers look at each tensor once, hand plain integers to ctypes and take
+# the stream's handle without building a Stream object.
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _bad(t, what, dtype, shape):
+    raise ValueError("%s must be a contiguous CUDA tensor %s %s, got %s %s%s" % (
+        what, dtype, shape, t.dtype, tuple(t.shape), "" if t.is_cuda else " on the host"))
 
 
 def _ints(t, shape, what):
-    return None if t is None else _tensor(t, torch.int32, shape, what)
+    """Address of a contiguous int32 CUDA tensor of this shape (None: 0)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _bad(t, what, "int32", shape)
+    return t.data_ptr()
 
 
-def _tokens(t, n_slots, T, inner, what):
-    """Pointer and token stride (elements) of a 16-bit [n_slots][T][inner...]
+def _tensor(t, dtype, shape, what):
+    """Address of a contiguous CUDA tensor of this type and shape; bf16 and
+    fp16 tensors may come as int16 bits."""
+    if (t.dtype is not dtype and not (dtype.itemsize == 2 and t.dtype is torch.int16)) or \
+            t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _bad(t, what, dtype, shape)
+    return t.data_ptr()
+
+
+def _tokens(t, shape, what):
+    """Address and token stride (elements) of a 16-bit [n_slots][T][heads][D]
     tensor whose tokens lie evenly apart, each dense (a slice of a joint
     projection is)."""
-    if not t.is_cuda or t.element_size() != 2:
-        raise ValueError("%s must be a 16-bit CUDA tensor" % what)
-    if tuple(t.shape) != (n_slots, T) + tuple(inner):
-        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape),
-                                                           (n_slots, T) + tuple(inner)))
-    dense = 1
-    for n, st in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
-        if n > 1 and st != dense:
-            raise ValueError("%s: a token's elements must be dense" % what)
-        dense *= n
-    stride = t.stride(1) if T > 1 else t.stride(0) if n_slots > 1 else dense
-    if T > 1 and n_slots > 1 and t.stride(0) != T * stride:
+    if t.shape != shape or not t.is_cuda or t.element_size() != 2:
+        _bad(t, what, "of 16 bits", shape)
+    n_slots, T, heads, D = shape
+    s0, s1, s2, s3 = t.stride()
+    if (D > 1 and s3 != 1) or (heads > 1 and s2 != D):
+        raise ValueError("%s: a token's elements must be dense" % what)
+    stride = s1 if T > 1 else s0 if n_slots > 1 else heads * D
+    if T > 1 and n_slots > 1 and s0 != T * stride:
         raise ValueError("%s: tokens must lie evenly apart" % what)
-    return C.c_void_p(t.data_ptr()), stride
+    return t.data_ptr(), stride
+
+
+def _ws(ws):
+    if ws.dtype is not torch.uint8 or not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous uint8 CUDA tensor")
+    return ws.data_ptr()
 
 
 def _workspace(nbytes, device, stream, what):
@@ -395,10 +414,14 @@ class CacheMeta:
     calls read one and write another; a program keeps two and swaps them."""
 
     def __init__(self, table, lens, refs):
+        if table.dim() != 2 or refs.dim() != 1:
+            raise ValueError("table is [n_slots][max_blocks], refs [n_phys]")
         self.table, self.lens, self.refs = table, lens, refs
-        self.ptrs = CacheMetaPtrs(_ints(table, (None, None), "table"),
+        self.ptrs = CacheMetaPtrs(_ints(table, table.shape, "table"),
                                   _ints(lens, table.shape[:1], "lens"),
-                                  _ints(refs, (None,), "refs"))
+                                  _ints(refs, refs.shape, "refs"))
+        self._dims = tuple(table.shape) + tuple(refs.shape)
+        self._ref = C.byref(self.ptrs)
 
     @classmethod
     def empty(cls, shape, device="cuda"):
@@ -407,10 +430,9 @@ class CacheMeta:
         return cls(z(shape.n_slots, shape.max_blocks).fill_(-1), z(shape.n_slots), z(shape.n_phys))
 
     def of(self, shape):
-        if tuple(self.table.shape) != (shape.n_slots, shape.max_blocks) or \
-                self.refs.shape[0] != shape.n_phys:
+        if self._dims != (shape.n_slots, shape.max_blocks, shape.n_phys):
             raise ValueError("the state is not of this cache shape")
-        return C.byref(self.ptrs)
+        return self._ref
 
 
 def pool_table(pools):
@@ -419,27 +441,27 @@ def pool_table(pools):
     it keeps the tensors."""
     arr = (C.c_void_p * max(1, len(pools)))()
     for i, t in enumerate(pools):
-        if t.dim() != 4 or t.element_size() != 2 or t.shape != pools[0].shape:
-            raise ValueError("pools must be 16-bit [n_phys][n_kv][64][D] tensors of one shape")
-        arr[i] = _p(t)
+        if t.dim() != 4:
+            raise ValueError("pools are [n_phys][n_kv][64][D]")
+        arr[i] = _pool(t, pools[0].shape, "every pool")
     arr.pools = list(pools)
     return arr
 
 
 def _pools(shape, table, n_phys):
-    for t in table.pools[:1]:
-        if tuple(t.shape) != (n_phys, shape.n_kv, shape.block, shape.D):
-            raise ValueError("the pools are not of this cache shape")
-    return C.cast(table, C.c_void_p), len(table.pools)
+    n = len(table.pools)
+    if n and table.pools[0].shape != (n_phys, shape.n_kv, shape.block, shape.D):
+        raise ValueError("the pools are not of this cache shape")
+    return C.addressof(table), n
 
 
 def moe_cache_fork(shape, meta, parent, out, ws, keep=None, stream=None):
     """Slot s of `out` holds the first keep[s] positions of slot parent[s] of
     `meta` (-1: nothing): fork, reorder, cut and free."""
     n = (shape.n_slots,)
-    _check(load().moe_cache_fork(C.byref(shape), meta.of(shape), _ints(parent, n, "parent"),
-                                 _ints(keep, n, "keep"), out.of(shape), _p(ws), ws.numel(),
-                                 _s(stream)), "moe_cache_fork")
+    _check((_lib or load()).moe_cache_fork(
+        shape, meta.of(shape), _ints(parent, n, "parent"), _ints(keep, n, "keep"), out.of(shape),
+        _ws(ws), ws.numel(), _raw_stream(stream)), "moe_cache_fork")
 
 
 def moe_cache_reserve(shape, meta, n_new, out, granted, pools, ws, stream=None):
@@ -447,45 +469,51 @@ def moe_cache_reserve(shape, meta, n_new, out, granted, pools, ws, stream=None):
     in all pools (pool_table); granted[s] = n_new[s], or 0 where refused."""
     n = (shape.n_slots,)
     ptr, k = _pools(shape, pools, shape.n_phys)
-    _check(load().moe_cache_reserve(C.byref(shape), meta.of(shape), _ints(n_new, n, "n_new"),
-                                    out.of(shape), _ints(granted, n, "granted"), ptr, k, _p(ws),
-                                    ws.numel(), _s(stream)), "moe_cache_reserve")
+    _check((_lib or load()).moe_cache_reserve(
+        shape, meta.of(shape), _ints(n_new, n, "n_new"), out.of(shape),
+        _ints(granted, n, "granted"), ptr, k, _ws(ws), ws.numel(), _raw_stream(stream)),
+        "moe_cache_reserve")
 
 
 def moe_cache_write(shape, meta, n_new, k_new, v_new, k_cache, v_cache, ws, stream=None):
     """Keys and values [n_slots][T][n_kv][D] of the last n_new[s] positions
     (None: T) of every slot into one layer's pools."""
-    T = k_new.shape[1]
-    kp, ks = _tokens(k_new, shape.n_slots, T, (shape.n_kv, shape.D), "k_new")
-    vp, vs = _tokens(v_new, shape.n_slots, T, (shape.n_kv, shape.D), "v_new")
-    for t in (k_cache, v_cache):
-        if tuple(t.shape) != (shape.n_phys, shape.n_kv, shape.block, shape.D) or \
-                t.element_size() != 2:
-            raise ValueError("the pools are not of this cache shape")
-    _check(load().moe_cache_write(C.byref(shape), meta.of(shape),
-                                  _ints(n_new, (shape.n_slots,), "n_new"), T, kp, ks, vp, vs,
-                                  _p(k_cache), _p(v_cache), _p(ws), ws.numel(), _s(stream)),
-           "moe_cache_write")
+    B, n_kv, D = shape.n_slots, shape.n_kv, shape.D
+    new = (B, k_new.shape[1], n_kv, D)
+    kp, ks = _tokens(k_new, new, "k_new")
+    vp, vs = _tokens(v_new, new, "v_new")
+    cache = (shape.n_phys, n_kv, shape.block, D)
+    _check((_lib or load()).moe_cache_write(
+        shape, meta.of(shape), _ints(n_new, (B,), "n_new"), new[1], kp, ks, vp, vs,
+        _pool(k_cache, cache, "k_cache"), _pool(v_cache, cache, "v_cache"), _ws(ws), ws.numel(),
+        _raw_stream(stream)), "moe_cache_write")
+
+
+def _pool(t, shape, what):
+    if t.shape != shape or t.element_size() != 2 or not t.is_cuda or not t.is_contiguous():
+        _bad(t, what, "of 16 bits", shape)
+    return t.data_ptr()
 
 
 def moe_cache_compact(shape, meta, out, n_live, pools, ws, stream=None):
     """Moves the held pages to the front of every pool; n_live[0] = how many."""
     ptr, k = _pools(shape, pools, shape.n_phys)
-    _check(load().moe_cache_compact(C.byref(shape), meta.of(shape), out.of(shape),
-                                    _ints(n_live, (1,), "n_live"), ptr, k, _p(ws), ws.numel(),
-                                    _s(stream)), "moe_cache_compact")
+    _check((_lib or load()).moe_cache_compact(
+        shape, meta.of(shape), out.of(shape), _ints(n_live, (1,), "n_live"), ptr, k, _ws(ws),
+        ws.numel(), _raw_stream(stream)), "moe_cache_compact")
 
 
 def moe_cache_copy_pages(shape, src, dst, from_pools, to_pools, ws, stream=None):
     """Page src[i] of every pool of from_pools to page dst[i] of to_pools."""
+    if not from_pools.pools or len(from_pools.pools) != len(to_pools.pools):
+        raise ValueError("as many pools on both sides, one at least")
     n_to = to_pools.pools[0].shape[0]
     a, k = _pools(shape, from_pools, shape.n_phys)
-    b, k2 = _pools(shape, to_pools, n_to)
-    if k != k2:
-        raise ValueError("as many pools on both sides")
-    _check(load().moe_cache_copy_pages(C.byref(shape), src.shape[0], _ints(src, (None,), "src"),
-                                       _ints(dst, src.shape, "dst"), a, b, k, n_to, _p(ws),
-                                       ws.numel(), _s(stream)), "moe_cache_copy_pages")
+    b, _ = _pools(shape, to_pools, n_to)
+    n = src.shape[:1]
+    _check((_lib or load()).moe_cache_copy_pages(
+        shape, n[0], _ints(src, n, "src"), _ints(dst, n, "dst"), a, b, k, n_to, _ws(ws),
+        ws.numel(), _raw_stream(stream)), "moe_cache_copy_pages")
 
 
 def make_attn_batch_shape(n_slots, T, n_q, n_kv, D, max_blocks, prefix_blocks=0, dtype="bf16",
@@ -506,17 +534,17 @@ def moe_attn_batch(shape, q, k_cache, v_cache, table, lens, o, ws, n_new=None, p
     of a joint projection; o is dense."""
     B, T, nq, D = shape.n_slots, shape.T, shape.n_q, shape.D
     dt = torch.float16 if shape.dtype == 1 else torch.bfloat16
-    if q.dtype not in (dt, torch.int16):
+    if q.dtype is not dt and q.dtype is not torch.int16:
         raise ValueError("q must be %s, got %s" % (dt, q.dtype))
-    qp, qs = _tokens(q, B, T, (nq, D), "q")
+    qp, qs = _tokens(q, (B, T, nq, D), "q")
     n_phys = k_cache.shape[0]
     cache = (n_phys, shape.n_kv, shape.block, D)
-    _check(load().moe_attn_batch(
-        C.byref(shape), qp, qs, _tensor(k_cache, dt, cache, "k_cache"),
+    _check((_lib or load()).moe_attn_batch(
+        shape, qp, qs, _tensor(k_cache, dt, cache, "k_cache"),
         _tensor(v_cache, dt, cache, "v_cache"), n_phys, _ints(table, (B, shape.max_blocks), "table"),
         _ints(prefix, (shape.prefix_blocks,), "prefix"), _ints(lens, (B,), "lens"),
-        _ints(n_new, (B,), "n_new"), _tensor(o, dt, (B, T, nq, D), "o"), _p(ws), ws.numel(),
-        _s(stream)), "moe_attn_batch")
+        _ints(n_new, (B,), "n_new"), _tensor(o, dt, (B, T, nq, D), "o"), _ws(ws), ws.numel(),
+        _raw_stream(stream)), "moe_attn_batch")
 
 
 def make_verify_shape(n_slots, T, V, dtype="fp32"):
@@ -533,13 +561,13 @@ def moe_verify_drafts(shape, p, q, draft, n_draft, u, tokens, n_acc, ws, stream=
     [n_slots][T+1][V] and the draft's q [n_slots][T][V] (None: certain) with
     the random numbers u [n_slots][T+1], and draws the token after them."""
     B, T, V = shape.n_slots, shape.T, shape.V
-    dt = _TORCH_DTYPE[[k for k, v in DTYPES.items() if v == shape.dtype][0]]
-    _check(load().moe_verify_drafts(
-        C.byref(shape), _tensor(p, dt, (B, T + 1, V), "p"),
+    dt = _DTYPE_OF[shape.dtype]
+    _check((_lib or load()).moe_verify_drafts(
+        shape, _tensor(p, dt, (B, T + 1, V), "p"),
         None if q is None else _tensor(q, dt, (B, T, V), "q"), _ints(draft, (B, T), "draft"),
         _ints(n_draft, (B,), "n_draft"), _tensor(u, torch.float32, (B, T + 1), "u"),
-        _ints(tokens, (B, T + 1), "tokens"), _ints(n_acc, (B,), "n_acc"), _p(ws), ws.numel(),
-        _s(stream)), "moe_verify_drafts")
+        _ints(tokens, (B, T + 1), "tokens"), _ints(n_acc, (B,), "n_acc"), _ws(ws), ws.numel(),
+        _raw_stream(stream)), "moe_verify_drafts")
 
 
 def moe_layer_w4(shape, x, w_router, router_bias, experts, shared, y, ws, x_next=None,

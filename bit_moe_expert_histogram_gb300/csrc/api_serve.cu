@@ -195,8 +195,10 @@ moe_status_t moe_verify_drafts(const moe_verify_shape_t* shape, const void* p_de
       !aligned(n_draft_dev, 4) || !ints(u_dev) || !ints(tokens_dev) || !ints(n_acc_dev))
     return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_ws(ws_dev, ws_bytes, verify_ws_bytes(shape)));
+  int nsm = 0;
+  MOE_TRY(device_sm_count(&nsm));
   return done(launch_verify(shape, p_dev, q_dev, draft_dev, n_draft_dev, u_dev, tokens_dev,
-                            n_acc_dev, static_cast<uint8_t*>(ws_dev), (cudaStream_t)stream),
+                            n_acc_dev, static_cast<uint8_t*>(ws_dev), nsm, (cudaStream_t)stream),
               "draft verification launch");
 }
 

@@ -224,7 +224,8 @@ bool verify_supported(const moe_verify_shape_t* s);
 size_t verify_ws_bytes(const moe_verify_shape_t* s);
 cudaError_t launch_verify(const moe_verify_shape_t* s, const void* p, const void* q,
                           const int32_t* draft, const int32_t* n_draft, const float* u,
-                          int32_t* tokens, int32_t* n_acc, uint8_t* ws, cudaStream_t stream);
+                          int32_t* tokens, int32_t* n_acc, uint8_t* ws, int nsm,
+                          cudaStream_t stream);
 // Host helpers shared by the C-ABI translation units (api.cu keeps the state).
 bool shape_supported(const moe_shape_t* shape);
 void set_last_error(const char* text);

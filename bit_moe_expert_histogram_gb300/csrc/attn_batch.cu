@@ -19,7 +19,7 @@
 // Blocks stream through a TMA ring of three stages (64 rows x 64 elements per
 // box, 128-byte swizzle) that runs on across pairs. A pair cut by a CTA
 // border leaves (m, l, O) in the workspace and the last of its CTAs to arrive
-// joins them in CTA order.
+// joins them in CTA order, the shared part's (attn_prefix.cu) before them.
 #include "attn_batch.cuh"
 
 namespace moe {
@@ -60,6 +60,13 @@ __device__ __forceinline__ void ldm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ uint32_t swz64(int p, int ch) {
   return (uint32_t)((ch >> 3) * (kBlk * 128) + p * 128 + (((ch & 7) ^ (p & 7)) << 4));
 }
+// v / l to four 16-bit elements (0 where l is)
+template <bool F16>
+__device__ __forceinline__ void store4(uint16_t* to, const float4& v, float l) {
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  *reinterpret_cast<uint2*>(to) =
+      make_uint2(pack2<F16>(v.x * inv, v.y * inv), pack2<F16>(v.z * inv, v.w * inv));
+}
 }  // namespace
 
 template <bool F16, int D, int MT>
@@ -73,6 +80,7 @@ __global__ void __launch_bounds__(kOThr, 2)
   constexpr int kKS = D / 16, kDT = D / 8;
   constexpr int kR = MT * 16;          // rows of the tiles
   constexpr int kCW = kOAreaFloats / kR < D ? kOAreaFloats / kR : D;  // columns of O joined at a time
+  constexpr int kLd = kCW + 4;         // row stride: rows start on other banks
   extern __shared__ __align__(1024) uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t full[kOStages];
   __shared__ int s_bad[kOStages];
@@ -82,7 +90,7 @@ __global__ void __launch_bounds__(kOThr, 2)
   __shared__ float s_M[kR], s_L[kR];        // the segment's
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
   uint8_t* sm = sm_raw + (sbase - smem_u32(sm_raw));
-  float* area = reinterpret_cast<float*>(sm + kOStages * 2 * kTile);  // [kR][kCW]
+  float* area = reinterpret_cast<float*>(sm + kOStages * 2 * kTile);  // [kR][kLd]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, cq = lane & 3;
   const int mt = warp % MT, ps = warp / MT;
@@ -98,8 +106,15 @@ __global__ void __launch_bounds__(kOThr, 2)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  pdl_wait();
-  pdl_trigger();
+  // With the shared part in the kernel before, everything that comes from
+  // earlier work was complete before that kernel let this one start (it
+  // triggers after its own wait), so only its parts have to be waited for.
+  const bool shared = a.px_steps > 0;
+  if (!shared) {
+    pdl_wait();
+    pdl_trigger();
+  }
+  bool waited = !shared;
   // ---- this CTA's part of the line of blocks
   {
     const int chunk = (a.n_slots + kOThr - 1) / kOThr;
@@ -338,7 +353,12 @@ __global__ void __launch_bounds__(kOThr, 2)
       s_L[r1] = L1;
     }
     const float w0 = ex2(m0 - U0), w1 = ex2(m1 - U1);
-    // a cut pair's part: place 2 c for CTA c's first pair, 2 c + 1 for a later one
+    // a pair's result goes out at once when nothing else has a part of it
+    const bool direct = whole && !shared;
+    auto out_row = [&](int r) {
+      return a.o + (((int64_t)s * a.T + r / G) * a.n_q + g * G + r % G) * D;
+    };
+    // a pair's part: place 2 c for CTA c's first pair, 2 c + 1 for a later one
     float* part = a.part + (int64_t)(2 * (int)blockIdx.x + (f0 >= pb ? 0 : 1)) * kR * (D + 2);
 #pragma unroll
     for (int cb = 0; cb < D; cb += kCW) {
@@ -348,8 +368,8 @@ __global__ void __launch_bounds__(kOThr, 2)
 #pragma unroll
           for (int j = 0; j < kCW / 8; ++j) {
             const int jj = cb / 8 + j;
-            float* p0 = area + r0 * kCW + 8 * j + 2 * cq;
-            float* p1 = area + r1 * kCW + 8 * j + 2 * cq;
+            float* p0 = area + r0 * kLd + 8 * j + 2 * cq;
+            float* p1 = area + r1 * kLd + 8 * j + 2 * cq;
             if (k == 0) {
               p0[0] = oacc[jj][0] * w0;
               p0[1] = oacc[jj][1] * w0;
@@ -365,56 +385,73 @@ __global__ void __launch_bounds__(kOThr, 2)
         }
         __syncthreads();
       }
-      for (int i = tid; i < rows * (kCW / 2); i += kOThr) {
-        const int r = i / (kCW / 2), d = 2 * (i - r * (kCW / 2));
-        const float2 o2 = *reinterpret_cast<const float2*>(area + r * kCW + d);
-        if (whole) {
-          const float inv = s_L[r] > 0.0f ? 1.0f / s_L[r] : 0.0f;
-          *reinterpret_cast<uint32_t*>(
-              a.o + (((int64_t)s * a.T + r / G) * a.n_q + g * G + r % G) * D + cb + d) =
-              pack2<F16>(o2.x * inv, o2.y * inv);
-        } else {
-          *reinterpret_cast<float2*>(part + 2 * kR + r * D + cb + d) = o2;
-        }
+      for (int i = tid; i < rows * (kCW / 4); i += kOThr) {
+        const int d = i / rows, r = i - d * rows;
+        const float4 v = *reinterpret_cast<const float4*>(area + r * kLd + 4 * d);
+        if (direct)
+          store4<F16>(out_row(r) + cb + 4 * d, v, s_L[r]);
+        else
+          *reinterpret_cast<float4*>(part + 2 * kR + ((cb / 4 + d) * kR + r) * 4) = v;
       }
       __syncthreads();
     }
-    if (!whole) {
+    if (!direct) {
       for (int r = tid; r < rows; r += kOThr) {
         part[r] = s_M[r];
         part[kR + r] = s_L[r];
       }
-      __threadfence();
-      __syncthreads();
       // the pair's CTAs: first and last to hold a block of it
       const int c0 = pb / per, c1 = (pb + sp.blocks - 1) / per;
-      if (tid == 0) {
-        unsigned* cnt = a.count + (int64_t)s * a.n_kv + g;
-        s_last = atomicAdd(cnt, 1u) == (unsigned)(c1 - c0);
-        if (s_last) *cnt = 0u;  // ready for the next call
+      if (!whole) {
         __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          unsigned* cnt = a.count + (int64_t)s * a.n_kv + g;
+          s_last = atomicAdd(cnt, 1u) == (unsigned)(c1 - c0);
+          if (s_last) *cnt = 0u;  // ready for the next call
+          __threadfence();
+        }
+      }
+      if (!waited) {
+        pdl_wait();
+        pdl_trigger();
+        waited = true;
       }
       __syncthreads();
-      if (s_last) {
-        for (int i = tid; i < rows * (D / 2); i += kOThr) {
-          const int r = i / (D / 2), d = 2 * (i - r * (D / 2));
-          float M = -INFINITY, L = 0.0f, ox = 0.0f, oy = 0.0f;
-          for (int c = c0; c <= c1; ++c) {
-            const float* pc = a.part + (int64_t)(2 * c + (c * per >= pb ? 0 : 1)) * kR * (D + 2);
-            const float mc = __ldcg(pc + r), lc = __ldcg(pc + kR + r);
-            const float2 oc = __ldcg(reinterpret_cast<const float2*>(pc + 2 * kR + r * D + d));
+      if (whole || s_last) {
+        // join: the shared part's stretches, then the own parts, in order
+        for (int i = tid; i < rows * (D / 4); i += kOThr) {
+          const int d = i / rows, r = i - d * rows;
+          float M = -INFINITY, L = 0.0f;
+          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          auto add = [&](float mc, float lc, const float4& oc) {
             const float nM = fmaxf(M, mc), U = nM == -INFINITY ? 0.0f : nM;
             const float fo = ex2(M - U), fc = ex2(mc - U);
             L = L * fo + lc * fc;
-            ox = ox * fo + oc.x * fc;
-            oy = oy * fo + oc.y * fc;
+            o.x = o.x * fo + oc.x * fc;
+            o.y = o.y * fo + oc.y * fc;
+            o.z = o.z * fo + oc.z * fc;
+            o.w = o.w * fo + oc.w * fc;
             M = nM;
+          };
+          if (shared) {
+            const int row = s * rows + r, u = (row >> 8) * a.n_kv + g, rr = row & 255;
+            const int64_t at = (int64_t)u * a.px_steps;
+            const int e = (int)((at + a.px_steps - 1) / a.px_per);
+            for (int c = (int)(at / a.px_per); c <= e; ++c) {
+              const float* pc = a.px_part + (int64_t)(c + u) * 256 * (D + 2);
+              add(__ldcg(pc + rr), __ldcg(pc + 256 + rr),
+                  __ldcg(reinterpret_cast<const float4*>(pc + 512) + d * 256 + rr));
+            }
           }
-          const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-          *reinterpret_cast<uint32_t*>(
-              a.o + (((int64_t)s * a.T + r / G) * a.n_q + g * G + r % G) * D + d) =
-              pack2<F16>(ox * inv, oy * inv);
+          for (int c = c0; c <= c1; ++c) {
+            const float* pc = a.part + (int64_t)(2 * c + (c * per >= pb ? 0 : 1)) * kR * (D + 2);
+            add(__ldcg(pc + r), __ldcg(pc + kR + r),
+                __ldcg(reinterpret_cast<const float4*>(pc + 2 * kR) + d * kR + r));
+          }
+          store4<F16>(out_row(r) + 4 * d, o, L);
         }
+        __syncthreads();  // a whole pair's place is the next pair's too
       }
     }
     // ---- the next pair
@@ -453,11 +490,15 @@ int own_tiles(const moe_attn_batch_shape_t* s) {  // row tiles: 1, 2 or 4
 }
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr int kMostSms = 256;  // two CTAs an SM at most
+size_t own_part_bytes(const moe_attn_batch_shape_t* s) {
+  return round256((size_t)2 * 2 * kMostSms * own_tiles(s) * 16 * (s->D + 2) * 4);
+}
 
 template <bool F16, int D, int MT>
 cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const AttnBatchArgs& a,
                        int grid, cudaStream_t stream) {
-  const size_t smem = 1024 + (size_t)kOStages * 2 * kBlk * D * 2 + kOAreaFloats * 4;
+  const size_t smem = 1024 + (size_t)kOStages * 2 * kBlk * D * 2 +
+                      (kOAreaFloats + MT * 16 * 4) * 4;
   const cudaError_t e = cudaFuncSetAttribute(attn_own_kernel<F16, D, MT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -472,10 +513,11 @@ cudaError_t launch_own_mt(int mt, const CUtensorMap& tk, const CUtensorMap& tv,
 }
 }  // namespace
 
-// status, the pairs' counters, the cut pairs' parts (two per CTA)
+// status, the pairs' counters, the pairs' parts (two places per CTA), the
+// shared part's
 size_t attn_batch_ws_bytes(const moe_attn_batch_shape_t* s) {
-  return 256 + round256((size_t)s->n_slots * s->n_kv * 4) +
-         round256((size_t)2 * 2 * kMostSms * own_tiles(s) * 16 * (s->D + 2) * 4);
+  return 256 + round256((size_t)s->n_slots * s->n_kv * 4) + own_part_bytes(s) +
+         (s->prefix_blocks > 0 ? prefix_part_floats(s, kMostSms) * 4 : 0);
 }
 
 cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap& tk,
@@ -490,8 +532,19 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
   a.n_kv = s->n_kv;
   a.max_blocks = s->max_blocks;
   a.prefix_blocks = s->prefix_blocks;
-  a.first = 0;
   const int sms = nsm < kMostSms ? nsm : kMostSms;
+  a.first = 0;
+  a.px_steps = 0;
+  if (s->prefix_blocks > 0 && s->n_slots > 1) {
+    const PrefixLine line = prefix_line(s, sms);
+    a.first = s->prefix_blocks;
+    a.px_steps = line.steps;
+    a.px_per = line.per;
+    a.px_total = (int)line.total;
+    a.px_part = a.part + own_part_bytes(s) / 4;
+    const cudaError_t e = launch_attn_prefix(s, tk, tv, a, line.grid, stream);
+    if (e != cudaSuccess) return e;
+  }
   // two CTAs an SM, and no more than there can be blocks
   const int64_t most = (int64_t)s->n_slots * s->n_kv * s->max_blocks;
   const int grid = most < 2 * sms ? (int)most : 2 * sms;

@@ -1,0 +1,434 @@
+// The shared part of the batch's attention: every slot's rows against the
+// prefix pages, which are read once for all of them.
+//
+// Row (s, t, head in group) of key/value head g is row (s T + t) G + head of
+// one [n_slots T G][D] matrix, so attention over the prefix is one pair of
+// large products per key/value head, on the tensor cores (tcgen05): tiles of
+// 256 rows (two of M = 128) against steps of 128 positions (two pages),
+// S = Q K^T into TMEM, softmax weights P back into TMEM over S, O += P V.
+// The (tile, head) pairs' steps lie on one line cut evenly over one CTA per
+// SM; each stretch leaves (m, l, O) of its 256 rows in the workspace, where
+// attn_own_kernel joins them with the slots' own positions.
+//
+// Warps: 0 loads K and V (TMA, two stages each of 128 positions), 1 issues
+// the products, 2-5 and 6-9 do the softmax of the two row tiles, a row a
+// thread. While one tile's weights are formed the other's products run. The
+// running maximum is only raised when a row grows past it by 2^8 (the sums
+// are relative to it, so any reference near the maximum does): O in TMEM is
+// rescaled a few times per stretch, not at every step.
+//
+// Bounds (D = 128, per step and two tiles): products 32 MMAs of N = 128 at
+// 64 to 77 clocks, about 2256; exponentials 2 x 128 x 128 at 16 a clock,
+// 2048; a step's 64 KB at an SM's share of HBM (24 bytes a clock), 2800, but
+// only the first tile's visit comes from HBM, the others from L2.
+#include "attn_batch.cuh"
+
+namespace moe {
+
+namespace {
+constexpr int kPThr = 320;      // 2 single warps + 2 x 4 softmax warps
+constexpr int kPRows = 256;     // rows of a tile pair
+constexpr int kPStep = 128;     // positions of a step
+constexpr int kPStages = 2;
+constexpr float kSlack = 8.0f;  // growth of a row (log2) that its reference may lag behind
+
+// shared-memory descriptor of a 16-bit operand whose M or N index runs along
+// the 128-byte swizzled rows (64 elements; lbo bytes to the next 64), the
+// reduction index from row to row (8 rows = 1024 bytes)
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(lbo >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// kind::f16 instruction: fp32 D, A and B of one 16-bit type, A K-major, B
+// K-major or (bmn) N-major
+__device__ __forceinline__ constexpr uint32_t idesc16(bool f16, int M, int N, bool bmn) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (bmn ? 1u << 16 : 0u) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31, %32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* tm, int c0, int c1,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(tm), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+struct PrefixBars {
+  uint64_t k_full[kPStages], k_empty[kPStages], v_full[kPStages], v_empty[kPStages];
+  uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drain;
+};
+}  // namespace
+
+template <bool F16, int D>
+__global__ void __launch_bounds__(kPThr, 1)
+    attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const AttnBatchArgs a) {
+  constexpr int kHalves = D / 64;                     // 64-element column halves of a tile
+  constexpr uint32_t kHalf = 128 * 128;               // bytes of 128 rows of one
+  constexpr uint32_t kTile = kHalves * kHalf;         // a Q, K or V tile
+  constexpr uint32_t kO = 0, kS = 256;                // TMEM columns: O tiles, then S tiles
+  extern __shared__ __align__(1024) uint8_t sm_raw[];
+  __shared__ __align__(8) PrefixBars bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
+  uint8_t* sm = sm_raw + (sbase - smem_u32(sm_raw));
+  const uint32_t sq = sbase, sk = sq + 2 * kTile, sv = sk + kPStages * kTile;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.n_q / a.n_kv, R = a.n_slots * a.T * G;
+  const int steps = a.px_steps, per = a.px_per;
+  const int f0 = (int)blockIdx.x * per, f1 = min(f0 + per, a.px_total);
+  auto bar = [&](const uint64_t& b) { return smem_u32(&b); };
+  if (tid == 0) {
+    for (int i = 0; i < kPStages; ++i) {
+      mbar_init(bar(bars.k_full[i]), 1);
+      mbar_init(bar(bars.k_empty[i]), 1);
+      mbar_init(bar(bars.v_full[i]), 1);
+      mbar_init(bar(bars.v_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(bars.q_ready[i]), 128);
+      mbar_init(bar(bars.s_full[i]), 1);
+      mbar_init(bar(bars.p_ready[i]), 128);
+      mbar_init(bar(bars.pv_done[i]), 1);
+    }
+    mbar_init(bar(bars.drain), 1);
+    s_abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s_tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+  pdl_trigger();
+  volatile int* abort = &s_abort;
+  // a bounded wait; one that runs out is recorded and ends every role
+  auto wait = [&](const uint64_t& b, uint32_t parity) {
+    if (mbar_wait(bar(b), parity, abort)) return true;
+    if (atomicCAS(&s_abort, 0, 1) == 0) set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, -2);
+    return false;
+  };
+  // the line's stretch f .. : pair u (tile u / n_kv, head u % n_kv), steps
+  // j0 .. j1 of it
+  if (warp == 0) {
+    if (lane == 0) {
+      int n = 0;  // steps loaded
+      bool ok = true;
+      for (int f = f0; ok && f < f1; ++f, ++n) {
+        const int u = f / steps, j = f - u * steps, g = u % a.n_kv;
+        const int st = n % kPStages;
+        const uint32_t ph = (uint32_t)(n / kPStages) & 1u;
+        int row[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int jb = 2 * j + i;
+          const int phys = jb < a.prefix_blocks ? __ldg(a.prefix + jb) : -1;
+          const bool bad = phys < 0 || phys >= a.n_phys;
+          if (bad && jb < a.prefix_blocks) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_ATTNB, -1);
+          // a page that is not there reads past the pool's end: zeros
+          row[i] = (bad ? a.n_phys * a.n_kv : phys * a.n_kv + g) * kBlk;
+        }
+        ok = wait(bars.k_empty[st], ph ^ 1u);
+        if (!ok) break;
+        mbar_arrive_expect_tx(bar(bars.k_full[st]), kTile);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            tma_load_rows(sk + st * kTile + h * kHalf + i * (kBlk * 128), &tm_k, h * 64, row[i],
+                          bar(bars.k_full[st]));
+        ok = wait(bars.v_empty[st], ph ^ 1u);
+        if (!ok) {
+          // the keys just asked for must land before the CTA goes
+          volatile int never = 0;
+          mbar_wait(bar(bars.k_full[st]), ph, &never);
+          break;
+        }
+        mbar_arrive_expect_tx(bar(bars.v_full[st]), kTile);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            tma_load_rows(sv + st * kTile + h * kHalf + i * (kBlk * 128), &tm_v, h * 64, row[i],
+                          bar(bars.v_full[st]));
+      }
+      // what is still in flight lands before the CTA goes (bounded)
+      volatile int never = 0;
+      for (int i = n > kPStages ? n - kPStages : 0; i < n; ++i) {
+        mbar_wait(bar(bars.k_full[i % kPStages]), (uint32_t)(i / kPStages) & 1u, &never);
+        mbar_wait(bar(bars.v_full[i % kPStages]), (uint32_t)(i / kPStages) & 1u, &never);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id_s = idesc16(F16, 128, kPStep, false), id_o = idesc16(F16, 128, D, true);
+      auto qk = [&](int w, int st) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
+          mma_bf16_ss(tmem + kS + w * 128, smem_desc_sw128(sq + w * kTile + off),
+                      smem_desc_sw128(sk + st * kTile + off), id_s, ks > 0);
+        }
+        mma_commit(bar(bars.s_full[w]));
+      };
+      int n = 0, seg = 0, pn[2] = {0, 0}, qn[2] = {0, 0};
+      bool ok = true;
+      for (int f = f0; ok && f < f1; ++seg) {
+        const int u = f / steps, j0 = f - u * steps;
+        const int cnt = min(steps - j0, f1 - f);
+        const int tiles = (u / a.n_kv) * kPRows + 128 < R ? 2 : 1;
+        for (int w = 0; ok && w < tiles; ++w) ok = wait(bars.q_ready[w], qn[w]++ & 1u);
+        ok = ok && wait(bars.k_full[n % kPStages], (uint32_t)(n / kPStages) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        for (int w = 0; w < tiles; ++w) qk(w, n % kPStages);
+        mma_commit(bar(bars.k_empty[n % kPStages]));
+        for (int j = 0; ok && j < cnt; ++j, ++n) {
+          const int st = n % kPStages;
+          ok = wait(bars.v_full[st], (uint32_t)(n / kPStages) & 1u);
+          for (int w = 0; ok && w < tiles; ++w) {
+            ok = wait(bars.p_ready[w], pn[w]++ & 1u);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < kPStep / 16; ++ks)
+              mma_bf16_ts(tmem + kO + w * 128, tmem + kS + w * 128 + ks * 8,
+                          desc_mn_sw128(sv + st * kTile + ks * 2048, kHalf), id_o, j > 0 || ks > 0);
+            mma_commit(bar(bars.pv_done[w]));
+            if (w == tiles - 1) mma_commit(bar(bars.v_empty[st]));
+            if (j + 1 < cnt) {
+              const int nx = n + 1;
+              if (w == 0) {
+                ok = wait(bars.k_full[nx % kPStages], (uint32_t)(nx / kPStages) & 1u);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              qk(w, nx % kPStages);
+              if (w == tiles - 1) mma_commit(bar(bars.k_empty[nx % kPStages]));
+            }
+          }
+        }
+        f += cnt;
+      }
+      // every product has finished before TMEM and shared memory go (bounded)
+      volatile int never = 0;
+      mma_commit(bar(bars.drain));
+      mbar_wait(bar(bars.drain), 0, &never);
+    }
+    __syncwarp();
+  } else {
+    const int w = (warp - 2) >> 2;       // row tile
+    const int quarter = warp & 3;        // TMEM lanes 32 quarter ..
+    const int r = quarter * 32 + lane;   // row in the tile
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tS = tmem + kS + w * 128 + lanes, tO = tmem + kO + w * 128 + lanes;
+    const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(D)
+    int n = 0;  // this tile's steps so far
+    bool ok = true;
+    for (int f = f0; ok && f < f1;) {
+      const int u = f / steps, j0 = f - u * steps, g = u % a.n_kv;
+      const int cnt = min(steps - j0, f1 - f);
+      f += cnt;
+      const int row0 = (u / a.n_kv) * kPRows + w * 128;
+      if (row0 >= R) continue;  // the last tile pair has one tile only
+      // ---- this row: its query into shared memory, its last position
+      const int row = row0 + r;
+      int lim = -1;
+      {
+        const uint16_t* src = nullptr;
+        if (row < R) {
+          const int tok = row / G, hh = row - tok * G, s = tok / a.T, t = tok - s * a.T;
+          const SlotSpan sp = slot_span(a, s);
+          lim = t < sp.n_new ? sp.len - sp.n_new + t : -1;
+          if (lim >= 0) src = a.q + (int64_t)tok * a.q_stride + (g * G + hh) * D;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = src ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(sm + w * kTile + (c >> 3) * kHalf + r * 128 +
+                                    (((c & 7) ^ (r & 7)) << 4)) = v;
+        }
+      }
+      fence_proxy_async_smem();  // the tensor core reads it
+      mbar_arrive(bar(bars.q_ready[w]));
+      float ref = -INFINITY, l = 0.0f;
+      for (int j = j0; j < j0 + cnt; ++j, ++n) {
+        // what of the step this row sees
+        const int p0 = 2 * j < a.prefix_blocks ? __ldg(a.prefix + 2 * j) : -1;
+        const int p1 = 2 * j + 1 < a.prefix_blocks ? __ldg(a.prefix + 2 * j + 1) : -1;
+        const bool hole = p0 < 0 || p0 >= a.n_phys || p1 < 0 || p1 >= a.n_phys;
+        const int left = lim - j * kPStep;  // last position of the step that is seen
+        const bool plain = !__any_sync(0xFFFFFFFFu, hole || left < kPStep - 1);
+        ok = wait(bars.s_full[w], (uint32_t)n & 1u);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t x[kPStep];
+#pragma unroll
+        for (int c = 0; c < kPStep; c += 32) tmem_ld32(tS + c, x + c);
+        tmem_wait_ld();
+        if (!plain) {
+          const bool b0 = p0 < 0 || p0 >= a.n_phys, b1 = p1 < 0 || p1 >= a.n_phys;
+#pragma unroll
+          for (int c = 0; c < kPStep; ++c)
+            if (c > left || (c < kBlk ? b0 : b1)) x[c] = 0xFF800000u;  // -inf
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kPStep; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        if (j == j0) {
+          ref = top;
+        } else {
+          const bool grow = top > ref + kSlack;
+          if (__any_sync(0xFFFFFFFFu, grow)) {
+            // O of the steps before is complete, the next product waits for us
+            ok = wait(bars.pv_done[w], (uint32_t)(n - 1) & 1u);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float now = grow ? top : ref;
+            const float fac = grow ? ex2(ref - now) : 1.0f;  // 0 where nothing was seen yet
+            ref = now;
+            l *= fac;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t y[32];
+              tmem_ld32(tO + c, y);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * fac);
+              tmem_st32(tO + c, y);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float off = lift<F16>() - (ref == -INFINITY ? 0.0f : ref);
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < kPStep; c += 2) {
+          const float e0 = ex2(fmaf(__uint_as_float(x[c]), sl2, off));
+          const float e1 = ex2(fmaf(__uint_as_float(x[c + 1]), sl2, off));
+          sum[c & 2] += e0;
+          sum[(c & 2) + 1] += e1;
+          x[c >> 1] = pack2<F16>(e0, e1);
+          if ((c & 62) == 62) tmem_st32(tS + (c >> 1) - 31, x + (c >> 1) - 31);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(bars.p_ready[w]));
+      }
+      if (!ok) break;
+      // ---- the stretch's (m, l, O), rows fastest
+      ok = wait(bars.pv_done[w], (uint32_t)(n - 1) & 1u);
+      if (!__all_sync(0xFFFFFFFFu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float* part = a.px_part + (int64_t)((int)blockIdx.x + u) * kPRows * (D + 2);
+      part[w * 128 + r] = ref;
+      part[kPRows + w * 128 + r] = l;
+      float4* po = reinterpret_cast<float4*>(part + 2 * kPRows) + w * 128 + r;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t y[32];
+        tmem_ld32(tO + c, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k += 4)
+          po[(int64_t)((c + k) / 4) * kPRows] =
+              make_float4(__uint_as_float(y[k]), __uint_as_float(y[k + 1]),
+                          __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
+      }
+      tc_fence_before();  // read before the next stretch's products write it
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+namespace {
+template <bool F16, int D>
+cudaError_t launch_px(const CUtensorMap& tk, const CUtensorMap& tv, const AttnBatchArgs& a, int grid,
+                      cudaStream_t stream) {
+  const size_t smem = 1024 + (size_t)(2 + 2 * kPStages) * 128 * D * 2;
+  const cudaError_t e = cudaFuncSetAttribute(attn_prefix_kernel<F16, D>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_prefix_kernel<F16, D>, dim3(grid), dim3(kPThr), smem, stream, tk, tv, a);
+}
+}  // namespace
+
+// pairs of a row tile and a head, and the steps of each
+PrefixLine prefix_line(const moe_attn_batch_shape_t* s, int sms) {
+  PrefixLine p{};
+  const int64_t rows = (int64_t)s->n_slots * s->T * (s->n_q / s->n_kv);
+  p.pairs = (int)((rows + kPRows - 1) / kPRows) * s->n_kv;
+  p.steps = (s->prefix_blocks + 1) / 2;
+  p.total = (int64_t)p.pairs * p.steps;
+  p.grid = (int)(p.total < sms ? p.total : sms);
+  p.per = p.grid > 0 ? (int)((p.total + p.grid - 1) / p.grid) : 0;
+  return p;
+}
+// one place per stretch: CTA + pair, both of which grow along the line
+size_t prefix_part_floats(const moe_attn_batch_shape_t* s, int sms) {
+  const PrefixLine p = prefix_line(s, sms);
+  return (size_t)(p.grid + p.pairs) * kPRows * (s->D + 2);
+}
+
+cudaError_t launch_attn_prefix(const moe_attn_batch_shape_t* s, const CUtensorMap& tk,
+                               const CUtensorMap& tv, const AttnBatchArgs& a, int grid,
+                               cudaStream_t stream) {
+  if (s->dtype == MOE_DTYPE_FP16)
+    return s->D == 64 ? launch_px<true, 64>(tk, tv, a, grid, stream)
+                      : launch_px<true, 128>(tk, tv, a, grid, stream);
+  return s->D == 64 ? launch_px<false, 64>(tk, tv, a, grid, stream)
+                    : launch_px<false, 128>(tk, tv, a, grid, stream);
+}
+
+}  // namespace moe

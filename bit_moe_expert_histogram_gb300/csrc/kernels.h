@@ -210,10 +210,25 @@ struct AttnBatchArgs {
   int n_slots, T, n_q, n_kv, max_blocks, prefix_blocks, n_phys;
   int first;           // the first block that attn_own_kernel takes
   uint16_t* o;         // [n_slots][T][n_q][D]
-  float* part;         // cut pairs: per place m[R], l[R], O[R][D]
+  float* part;         // parts of pairs: per place m[R], l[R], O[D / 4][R][4]
   unsigned* count;     // [n_slots][n_kv]: CTAs of a cut pair that have arrived
+  // the shared part, when attn_prefix_kernel takes it (px_steps > 0): its
+  // line of steps and its parts, per place m[256], l[256], O[D / 4][256][4]
+  int px_steps, px_per, px_total;
+  float* px_part;
   Ctrl* ctrl;
 };
+// Steps of 128 prefix positions for each pair of 256 rows and a head, cut
+// evenly over `grid` CTAs (attn_prefix.cu).
+struct PrefixLine {
+  int pairs, steps, grid, per;
+  int64_t total;
+};
+PrefixLine prefix_line(const moe_attn_batch_shape_t* s, int sms);
+size_t prefix_part_floats(const moe_attn_batch_shape_t* s, int sms);
+cudaError_t launch_attn_prefix(const moe_attn_batch_shape_t* s, const CUtensorMap& tk,
+                               const CUtensorMap& tv, const AttnBatchArgs& a, int grid,
+                               cudaStream_t stream);
 bool attn_batch_supported(const moe_attn_batch_shape_t* s);
 size_t attn_batch_ws_bytes(const moe_attn_batch_shape_t* s);
 cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap& tk,

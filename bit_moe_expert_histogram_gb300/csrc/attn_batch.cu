@@ -15,18 +15,24 @@
 // lie on one line, and CTA c takes blocks [c per, (c + 1) per) of it whatever
 // slots they belong to, so uneven lengths leave no CTA idle. The
 // T * n_q / n_kv <= 64 query rows of a pair are the M rows of mma.sync tiles
-// (16 rows; 1, 2 or 4 tiles), so each key and value is read once per slot.
-// Blocks stream through a TMA ring of three stages (64 rows x 64 elements per
-// box, 128-byte swizzle) that runs on across pairs. A pair cut by a CTA
-// border leaves (m, l, O) in the workspace and the last of its CTAs to arrive
-// joins them in CTA order, the shared part's (attn_prefix.cu) before them.
+// (16 rows; 1, 2 or 4 tiles), so each key and value is read once per slot. A
+// warp of its own keeps a TMA ring of blocks full (64 rows x 64 elements per
+// box, 128-byte swizzle) that runs on across pairs; the four others only meet
+// at the end of a pair.
+//  - without a shared part, a pair inside one CTA goes straight to the
+//    output; one cut by a CTA border leaves (m, l, O) in the workspace and
+//    the last of its CTAs to arrive joins them in CTA order;
+//  - with one (attn_prefix.cu), every pair leaves (m, l, O), and
+//    attn_join_kernel joins them with the shared part's, a thread for four
+//    elements of the output: few threads wait long for what many threads
+//    fetch at once.
 #include "attn_batch.cuh"
 
 namespace moe {
 
 namespace {
-constexpr int kOThr = 128;
-constexpr int kOStages = 3;
+constexpr int kOThr = 128;          // the four warps that compute
+constexpr int kOAll = kOThr + 32;   // and the one that loads
 constexpr int kOAreaFloats = 2048;  // 8 KB where the warps' O meet
 
 template <bool F16>
@@ -69,36 +75,86 @@ __device__ __forceinline__ void store4(uint16_t* to, const float4& v, float l) {
 }
 }  // namespace
 
+// Joins parts in order: each batch of up to kBatch is fetched as a whole.
+struct Joined {
+  float M, L;
+  float4 o;
+};
+template <int kBatch, typename At>
+__device__ __forceinline__ void join_parts(Joined& j, int n, int rows_ld, int r, int d, At at) {
+  for (int c0 = 0; c0 < n; c0 += kBatch) {
+    float m[kBatch], l[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const bool in = c0 + k < n;
+      const float* p = at(in ? c0 + k : c0);
+      m[k] = in ? __ldcg(p + r) : -INFINITY;
+      l[k] = __ldcg(p + rows_ld + r);
+      v[k] = __ldcg(reinterpret_cast<const float4*>(p + 2 * rows_ld) + d * rows_ld + r);
+    }
+    float nM = j.M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) nM = fmaxf(nM, m[k]);
+    const float U = nM == -INFINITY ? 0.0f : nM;
+    const float f = ex2(j.M - U);
+    j.L *= f;
+    j.o.x *= f;
+    j.o.y *= f;
+    j.o.z *= f;
+    j.o.w *= f;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float w = ex2(m[k] - U);
+      j.L = fmaf(l[k], w, j.L);
+      j.o.x = fmaf(v[k].x, w, j.o.x);
+      j.o.y = fmaf(v[k].y, w, j.o.y);
+      j.o.z = fmaf(v[k].z, w, j.o.z);
+      j.o.w = fmaf(v[k].w, w, j.o.w);
+    }
+    j.M = nM;
+  }
+}
+__device__ __forceinline__ uint16_t* out_row(const AttnBatchArgs& a, int s, int g, int G, int r,
+                                             int D) {
+  return a.o + (((int64_t)s * a.T + r / G) * a.n_q + g * G + r % G) * D;
+}
+
+template <int D>
+struct OwnRing {
+  static constexpr int kTile = kBlk * D * 2;            // bytes of a block's keys (or values)
+  static constexpr int kStages = D == 64 ? 6 : 3;       // 96 KB either way: two CTAs an SM
+};
+
 template <bool F16, int D, int MT>
-__global__ void __launch_bounds__(kOThr, 2)
+__global__ void __launch_bounds__(kOAll, 2)
     attn_own_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const AttnBatchArgs a) {
-  constexpr int kTile = kBlk * D * 2;  // bytes of a block's keys (or values)
-  constexpr int kNS = 4 / MT;          // warps that share a row tile, each a slice of the block
-  constexpr int kPos = kBlk / kNS;     // positions of a slice
-  constexpr int kNT = kPos / 8;        // score n-tiles of a warp
+  constexpr int kTile = OwnRing<D>::kTile, kStages = OwnRing<D>::kStages;
+  constexpr int kNS = 4 / MT;       // warps that share a row tile, each a slice of the block
+  constexpr int kPos = kBlk / kNS;  // positions of a slice
+  constexpr int kNT = kPos / 8;     // score n-tiles of a warp
   constexpr int kKS = D / 16, kDT = D / 8;
-  constexpr int kR = MT * 16;          // rows of the tiles
+  constexpr int kR = MT * 16;       // rows of the tiles
   constexpr int kCW = kOAreaFloats / kR < D ? kOAreaFloats / kR : D;  // columns of O joined at a time
-  constexpr int kLd = kCW + 4;         // row stride: rows start on other banks
+  constexpr int kLd = kCW + 4;      // row stride: rows start on other banks
   extern __shared__ __align__(1024) uint8_t sm_raw[];
-  __shared__ __align__(8) uint64_t full[kOStages];
-  __shared__ int s_bad[kOStages];
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
+  __shared__ int s_bad[kStages];
   __shared__ int s_abort, s_start, s_off, s_total, s_last;
-  __shared__ int s_scan[4];
+  __shared__ int s_scan[kOAll / 32];
   __shared__ float s_m[4][16], s_l[4][16];  // per warp: its rows' maximum and sum
   __shared__ float s_M[kR], s_L[kR];        // the segment's
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
   uint8_t* sm = sm_raw + (sbase - smem_u32(sm_raw));
-  float* area = reinterpret_cast<float*>(sm + kOStages * 2 * kTile);  // [kR][kLd]
+  float* area = reinterpret_cast<float*>(sm + kStages * 2 * kTile);  // [kR][kLd]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int gq = lane >> 2, cq = lane & 3;
-  const int mt = warp % MT, ps = warp / MT;
-  const int G = a.n_q / a.n_kv, rows = a.T * G;
-  const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(D)
-  const uint32_t fb = smem_u32(&full[0]);
+  const uint32_t fb = smem_u32(&full[0]), eb = smem_u32(&empty[0]);
   if (tid == 0) {
-    for (int i = 0; i < kOStages; ++i) mbar_init(fb + 8u * i, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(fb + 8u * i, 1);
+      mbar_init(eb + 8u * i, 4);
+    }
     s_abort = 0;
     s_start = 0;
     s_off = 0;
@@ -108,16 +164,15 @@ __global__ void __launch_bounds__(kOThr, 2)
   }
   // With the shared part in the kernel before, everything that comes from
   // earlier work was complete before that kernel let this one start (it
-  // triggers after its own wait), so only its parts have to be waited for.
+  // triggers after its own wait), and nothing here reads its parts.
   const bool shared = a.px_steps > 0;
   if (!shared) {
     pdl_wait();
     pdl_trigger();
   }
-  bool waited = !shared;
   // ---- this CTA's part of the line of blocks
   {
-    const int chunk = (a.n_slots + kOThr - 1) / kOThr;
+    const int chunk = (a.n_slots + kOAll - 1) / kOAll;
     const int s0 = min(tid * chunk, a.n_slots), s1 = min(s0 + chunk, a.n_slots);
     int sum = 0;
     for (int s = s0; s < s1; ++s) sum += slot_span(a, s).blocks;
@@ -131,7 +186,7 @@ __global__ void __launch_bounds__(kOThr, 2)
     if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
     for (int w = 0; w < warp; ++w) incl += s_scan[w];
-    if (tid == kOThr - 1) s_total = incl;
+    if (tid == kOAll - 1) s_total = incl;
     __syncthreads();
     const int per = (s_total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int f0 = (int)blockIdx.x * per;
@@ -151,323 +206,356 @@ __global__ void __launch_bounds__(kOThr, 2)
   const int total = s_total;
   const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
   const int f0 = (int)blockIdx.x * per, f1 = min(f0 + per, total);
-  if (f0 >= f1) return;
-  const uint64_t pol = policy_evict_first();  // own pages are read once
-  // ---- thread 0's cursor: the next block to load
-  int is = s_start, ig = 0, ij = s_off;
-  SlotSpan isp = slot_span(a, is);
-  ig = ij / isp.blocks;
-  ij -= ig * isp.blocks;
-  auto issue = [&](int st) {
-    const int jb = a.first + ij;
-    int phys = -1, bad = 0;
-    if (isp.n_new > 0 && jb * kBlk < isp.len) {
-      phys = jb < a.prefix_blocks ? __ldg(a.prefix + jb)
-                                  : __ldg(a.table + (int64_t)is * a.max_blocks + jb);
-      if (phys < 0 || phys >= a.n_phys) {
-        set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_ATTNB, is);
-        bad = 1;
-        phys = -1;
-      }
-    }
-    // a page that is not there reads past the pool's end: the copy fills zeros
-    const int row0 = (phys < 0 ? a.n_phys * a.n_kv : phys * a.n_kv + ig) * kBlk;
-    s_bad[st] = bad;
-    const uint32_t sk = sbase + (uint32_t)(st * 2 * kTile), sv = sk + kTile;
-    const uint32_t bar = fb + 8u * st;
-    mbar_arrive_expect_tx(bar, 2u * kTile);
-#pragma unroll
-    for (int bx = 0; bx < D / 64; ++bx) {
-      tma_load_2d(sk + bx * (kBlk * 128), &tm_k, bx * 64, row0, bar, pol);
-      tma_load_2d(sv + bx * (kBlk * 128), &tm_v, bx * 64, row0, bar, pol);
-    }
-    if (++ij == isp.blocks) {
-      ij = 0;
-      if (++ig == a.n_kv) {
-        ig = 0;
-        if (++is < a.n_slots) isp = slot_span(a, is);
-      }
-    }
-  };
-  int issued = min(kOStages - 1, f1 - f0);
-  if (tid == 0)
-    for (int i = 0; i < issued; ++i) issue(i);
-
-  // ---- the pairs of this CTA
   int s = s_start;
   SlotSpan sp = slot_span(a, s);
   int g = s_off / sp.blocks;
   int pb = f0 - (s_off - g * sp.blocks);  // where the pair starts on the line
-  int f = f0;
-  while (f < f1) {
-    const int fe = min(f1, pb + sp.blocks);
-    const bool whole = f == pb && fe == pb + sp.blocks;
-    // rows r = t * G + head in group; a row's last position, -1: sees nothing
-    const int base = sp.len - sp.n_new;  // may be negative
-    const int r0 = mt * 16 + gq, r1 = r0 + 8;
-    const int lim0 = r0 < rows && r0 / G < sp.n_new ? base + r0 / G : -1;
-    const int lim1 = r1 < rows && r1 / G < sp.n_new ? base + r1 / G : -1;
-    uint32_t qa[kKS][4];
-    {
-      const uint16_t* q0 = lim0 >= 0 ? a.q + ((int64_t)s * a.T + r0 / G) * a.q_stride + (g * G + r0 % G) * D : nullptr;
-      const uint16_t* q1 = lim1 >= 0 ? a.q + ((int64_t)s * a.T + r1 / G) * a.q_stride + (g * G + r1 % G) * D : nullptr;
+  volatile int* abort = &s_abort;
+
+  if (warp == 4) {
+    // ---- the loader: all lanes follow the line, lane 0 issues
+    const uint64_t pol = policy_evict_first();  // own pages are read once
+    int j = f0 - pb;                            // block of the pair
+    int page = 0;                               // lane l: page of block (j & ~31) + l
+    bool fresh = true;
+    int n = 0;
+    for (int f = f0; f < f1; ++f, ++n) {
+      if (fresh || (j & 31) == 0) {
+        const int jb = a.first + (j & ~31) + lane;
+        page = -2;  // nothing there
+        if (sp.n_new > 0 && jb * kBlk < sp.len) {
+          page = jb < a.prefix_blocks ? __ldg(a.prefix + jb)
+                                      : __ldg(a.table + (int64_t)s * a.max_blocks + jb);
+          if (page < 0 || page >= a.n_phys) {
+            set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_ATTNB, s);
+            page = -1;
+          }
+        }
+        fresh = false;
+      }
+      const int phys = __shfl_sync(0xFFFFFFFFu, page, j & 31);
+      const int st = n % kStages;
+      if (lane == 0) {
+        if (!mbar_wait(eb + 8u * st, ((uint32_t)(n / kStages) & 1u) ^ 1u, abort) &&
+            atomicCAS(&s_abort, 0, 1) == 0)
+          set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, s);
+      }
+      __syncwarp();
+      if (__any_sync(0xFFFFFFFFu, *abort != 0)) break;  // the others' waits end on it too
+      if (lane == 0) {
+        // a page that is not there reads past the pool's end: the copy fills zeros
+        const int row0 = (phys < 0 ? a.n_phys * a.n_kv : phys * a.n_kv + g) * kBlk;
+        s_bad[st] = phys == -1;
+        const uint32_t sk = sbase + (uint32_t)(st * 2 * kTile), sv = sk + kTile;
+        const uint32_t bar = fb + 8u * st;
+        mbar_arrive_expect_tx(bar, 2u * kTile);
 #pragma unroll
-      for (int ks = 0; ks < kKS; ++ks) {
-        const int d = ks * 16 + 2 * cq;
-        qa[ks][0] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d)) : 0u;
-        qa[ks][1] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d)) : 0u;
-        qa[ks][2] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d + 8)) : 0u;
-        qa[ks][3] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d + 8)) : 0u;
+        for (int bx = 0; bx < D / 64; ++bx) {
+          tma_load_2d(sk + bx * (kBlk * 128), &tm_k, bx * 64, row0, bar, pol);
+          tma_load_2d(sv + bx * (kBlk * 128), &tm_v, bx * 64, row0, bar, pol);
+        }
+      }
+      if (++j == sp.blocks) {
+        j = 0;
+        if (++g == a.n_kv) {
+          g = 0;
+          if (++s < a.n_slots) sp = slot_span(a, s);
+        }
+        fresh = true;
       }
     }
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-    float oacc[kDT][4];
+    if (lane == 0) {
+      // what is still in flight lands before the CTA goes (bounded)
+      volatile int never = 0;
+      for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
+        mbar_wait(fb + 8u * (i % kStages), (uint32_t)(i / kStages) & 1u, &never);
+    }
+    __syncwarp();
+  } else {
+    // ---- the pairs of this CTA. A wait that runs out is recorded and ends
+    // all waits; the loops go on to their end over what is there.
+    const int gq = lane >> 2, cq = lane & 3;
+    const int mt = warp % MT, ps = warp / MT;
+    const int G = a.n_q / a.n_kv, rows = a.T * G;
+    const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(D)
+    const int mi = lane >> 3, rr = lane & 7;
+    auto meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    int f = f0;
+    while (f < f1) {
+      const int fe = min(f1, pb + sp.blocks);
+      const bool whole = f == pb && fe == pb + sp.blocks;
+      // rows r = t * G + head in group; a row's last position, -1: sees nothing
+      const int base = sp.len - sp.n_new;  // may be negative
+      const int r0 = mt * 16 + gq, r1 = r0 + 8;
+      const int lim0 = r0 < rows && r0 / G < sp.n_new ? base + r0 / G : -1;
+      const int lim1 = r1 < rows && r1 / G < sp.n_new ? base + r1 / G : -1;
+      uint32_t qa[kKS][4];
+      {
+        const uint16_t* q0 = lim0 >= 0 ? a.q + ((int64_t)s * a.T + r0 / G) * a.q_stride + (g * G + r0 % G) * D : nullptr;
+        const uint16_t* q1 = lim1 >= 0 ? a.q + ((int64_t)s * a.T + r1 / G) * a.q_stride + (g * G + r1 % G) * D : nullptr;
 #pragma unroll
-    for (int j = 0; j < kDT; ++j) oacc[j][0] = oacc[j][1] = oacc[j][2] = oacc[j][3] = 0.0f;
-    for (; f < fe; ++f) {
-      const int it = f - f0, st = it % kOStages;
-      if (!mbar_wait(fb + 8u * st, (uint32_t)(it / kOStages) & 1u, &s_abort) &&
-          atomicCAS(&s_abort, 0, 1) == 0)
-        set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, s);
-      // this thread's reads of the block before are ordered before the refill
-      // of its stage, which thread 0 issues after the barrier
-      fence_proxy_async_smem();
-      __syncthreads();
-      if (s_abort) break;
-      if (f + kOStages - 1 < f1) {
-        if (tid == 0) issue((it + kOStages - 1) % kOStages);
-        ++issued;
+        for (int ks = 0; ks < kKS; ++ks) {
+          const int d = ks * 16 + 2 * cq;
+          qa[ks][0] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d)) : 0u;
+          qa[ks][1] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d)) : 0u;
+          qa[ks][2] = q0 ? __ldg(reinterpret_cast<const uint32_t*>(q0 + d + 8)) : 0u;
+          qa[ks][3] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d + 8)) : 0u;
+        }
       }
-      const uint32_t sk = sbase + (uint32_t)(st * 2 * kTile), sv = sk + kTile;
-      const int pos0 = (a.first + f - pb) * kBlk;
-      const bool bad = s_bad[st] != 0;
-      if (pos0 + kBlk > sp.len) {
-        // rows past the slot's end hold anything, NaN too: 0 x NaN in P V
-        // would reach the output, so they are set to 0
-        const int z0 = max(sp.len - pos0, 0);
-        for (int i = tid; i < (kBlk - z0) * (D / 8); i += kOThr) {
-          const int p = z0 + i / (D / 8);
-          *reinterpret_cast<uint4*>(sm + st * 2 * kTile + kTile + swz64(p, i % (D / 8))) =
-              make_uint4(0u, 0u, 0u, 0u);
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      float oacc[kDT][4];
+#pragma unroll
+      for (int j = 0; j < kDT; ++j) oacc[j][0] = oacc[j][1] = oacc[j][2] = oacc[j][3] = 0.0f;
+      for (; f < fe; ++f) {
+        const int it = f - f0, st = it % kStages;
+        if (!mbar_wait(fb + 8u * st, (uint32_t)(it / kStages) & 1u, abort) &&
+            atomicCAS(&s_abort, 0, 1) == 0)
+          set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, s);
+        const uint32_t sk = sbase + (uint32_t)(st * 2 * kTile), sv = sk + kTile;
+        const int pos0 = (a.first + f - pb) * kBlk;
+        const bool bad = s_bad[st] != 0;
+        if (pos0 + kBlk > sp.len) {
+          // rows past the slot's end hold anything, NaN too: 0 x NaN in P V
+          // would reach the output, so each warp sets those it reads to 0
+          const int z0 = max(sp.len - pos0, kPos * ps), z1 = kPos * (ps + 1);
+          for (int i = lane; i < (z1 - z0) * (D / 8); i += 32)
+            *reinterpret_cast<uint4*>(sm + st * 2 * kTile + kTile +
+                                      swz64(z0 + i / (D / 8), i % (D / 8))) =
+                make_uint4(0u, 0u, 0u, 0u);
+          __syncwarp();
         }
-        __syncthreads();
+        // S = Q K^T over this warp's positions
+        float sc[kNT][4];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+          for (int n = 0; n < kNT; n += 2) {
+            uint32_t kb[4];
+            ldm_x4(sk + swz64(kPos * ps + 8 * n + ((mi & 2) ? 8 : 0) + rr, ks * 2 + (mi & 1)), kb);
+            mma16816t<F16>(sc[n], qa[ks], kb[0], kb[1]);
+            mma16816t<F16>(sc[n + 1], qa[ks], kb[2], kb[3]);
+          }
+        // every row that is in use sees positions up to base
+        if (bad || pos0 + kBlk - 1 > base) {
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int pos = pos0 + kPos * ps + 8 * n + 2 * cq + h;
+              if (bad || pos > lim0) sc[n][h] = -INFINITY;
+              if (bad || pos > lim1) sc[n][2 + h] = -INFINITY;
+            }
+        }
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+          mx0 = fmaxf(mx0, fmaxf(sc[n][0], sc[n][1]));
+          mx1 = fmaxf(mx1, fmaxf(sc[n][2], sc[n][3]));
+        }
+#pragma unroll
+        for (int d = 1; d <= 2; d <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, d));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, d));
+        }
+        const float n0 = fmaxf(m0, mx0 * sl2), n1 = fmaxf(m1, mx1 * sl2);
+        // all masked so far: everything stays 0 (no inf - inf)
+        const float u0 = n0 == -INFINITY ? 0.0f : n0, u1 = n1 == -INFINITY ? 0.0f : n1;
+        const float c0 = ex2(m0 - u0), c1 = ex2(m1 - u1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= c0;
+        l1 *= c1;
+        const float x0 = lift<F16>() - u0, x1 = lift<F16>() - u1;
+        uint32_t pa[kNT / 2][4];
+        // the sums take the rounded weights, the ones that the product sees
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+          const uint32_t w0 = pack2<F16>(ex2(fmaf(sc[n][0], sl2, x0)), ex2(fmaf(sc[n][1], sl2, x0)));
+          const uint32_t w1 = pack2<F16>(ex2(fmaf(sc[n][2], sl2, x1)), ex2(fmaf(sc[n][3], sl2, x1)));
+          l0 += unpack_lo<F16>(w0) + unpack_hi<F16>(w0);
+          l1 += unpack_lo<F16>(w1) + unpack_hi<F16>(w1);
+          pa[n / 2][2 * (n & 1)] = w0;
+          pa[n / 2][2 * (n & 1) + 1] = w1;
+        }
+#pragma unroll
+        for (int j = 0; j < kDT; ++j) {
+          oacc[j][0] *= c0;
+          oacc[j][1] *= c0;
+          oacc[j][2] *= c1;
+          oacc[j][3] *= c1;
+        }
+#pragma unroll
+        for (int kp = 0; kp < kPos / 16; ++kp)
+#pragma unroll
+          for (int j = 0; j < kDT; j += 2) {
+            uint32_t vb[4];
+            ldm_x4_t(sv + swz64(kPos * ps + 16 * kp + ((mi & 1) ? 8 : 0) + rr, j + (mi >> 1)), vb);
+            mma16816t<F16>(oacc[j], pa[kp], vb[0], vb[1]);
+            mma16816t<F16>(oacc[j + 1], pa[kp], vb[2], vb[3]);
+          }
+        // the stage goes back to the loader, after this warp's reads and writes
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(eb + 8u * st);
       }
-      // S = Q K^T over this warp's positions
-      float sc[kNT][4];
-#pragma unroll
-      for (int n = 0; n < kNT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
-      const int mi = lane >> 3, rr = lane & 7;
-#pragma unroll
-      for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-        for (int n = 0; n < kNT; n += 2) {
-          uint32_t kb[4];
-          ldm_x4(sk + swz64(kPos * ps + 8 * n + ((mi & 2) ? 8 : 0) + rr, ks * 2 + (mi & 1)), kb);
-          mma16816t<F16>(sc[n], qa[ks], kb[0], kb[1]);
-          mma16816t<F16>(sc[n + 1], qa[ks], kb[2], kb[3]);
-        }
-      float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int pos = pos0 + kPos * ps + 8 * n + 2 * cq + h;
-          sc[n][h] = (!bad && pos <= lim0) ? sc[n][h] * sl2 : -INFINITY;
-          sc[n][2 + h] = (!bad && pos <= lim1) ? sc[n][2 + h] * sl2 : -INFINITY;
-          mx0 = fmaxf(mx0, sc[n][h]);
-          mx1 = fmaxf(mx1, sc[n][2 + h]);
-        }
+      // ---- the slices' (m, l, O) become the segment's
 #pragma unroll
       for (int d = 1; d <= 2; d <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, d));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, d));
+        l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, d);
+        l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, d);
       }
-      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-      // all masked so far: everything stays 0 (no inf - inf)
-      const float u0 = n0 == -INFINITY ? 0.0f : n0, u1 = n1 == -INFINITY ? 0.0f : n1;
-      const float c0 = ex2(m0 - u0), c1 = ex2(m1 - u1);
-      m0 = n0;
-      m1 = n1;
-      l0 *= c0;
-      l1 *= c1;
-      const float x0 = u0 - lift<F16>(), x1 = u1 - lift<F16>();
-      uint32_t pa[kNT / 2][4];
-      // the sums take the rounded weights, the ones that the product sees
-#pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        const uint32_t w0 = pack2<F16>(ex2(sc[n][0] - x0), ex2(sc[n][1] - x0));
-        const uint32_t w1 = pack2<F16>(ex2(sc[n][2] - x1), ex2(sc[n][3] - x1));
-        l0 += unpack_lo<F16>(w0) + unpack_hi<F16>(w0);
-        l1 += unpack_lo<F16>(w1) + unpack_hi<F16>(w1);
-        pa[n / 2][2 * (n & 1)] = w0;
-        pa[n / 2][2 * (n & 1) + 1] = w1;
+      // a row that sees nothing weighs nothing, whatever was summed for it
+      if (lim0 < 0) {
+        m0 = -INFINITY;
+        l0 = 0.0f;
       }
-#pragma unroll
-      for (int j = 0; j < kDT; ++j) {
-        oacc[j][0] *= c0;
-        oacc[j][1] *= c0;
-        oacc[j][2] *= c1;
-        oacc[j][3] *= c1;
+      if (lim1 < 0) {
+        m1 = -INFINITY;
+        l1 = 0.0f;
       }
+      if (cq == 0) {
+        s_m[warp][gq] = m0;
+        s_m[warp][gq + 8] = m1;
+        s_l[warp][gq] = l0;
+        s_l[warp][gq + 8] = l1;
+      }
+      meet();
+      float M0 = -INFINITY, M1 = -INFINITY;
 #pragma unroll
-      for (int kp = 0; kp < kPos / 16; ++kp)
+      for (int k = 0; k < kNS; ++k) {
+        M0 = fmaxf(M0, s_m[mt + k * MT][gq]);
+        M1 = fmaxf(M1, s_m[mt + k * MT][gq + 8]);
+      }
+      const float U0 = M0 == -INFINITY ? 0.0f : M0, U1 = M1 == -INFINITY ? 0.0f : M1;
+      if (ps == 0 && cq == 0) {
+        float L0 = 0.0f, L1 = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kDT; j += 2) {
-          uint32_t vb[4];
-          ldm_x4_t(sv + swz64(kPos * ps + 16 * kp + ((mi & 1) ? 8 : 0) + rr, j + (mi >> 1)), vb);
-          mma16816t<F16>(oacc[j], pa[kp], vb[0], vb[1]);
-          mma16816t<F16>(oacc[j + 1], pa[kp], vb[2], vb[3]);
+        for (int k = 0; k < kNS; ++k) {
+          L0 += s_l[mt + k * MT][gq] * ex2(s_m[mt + k * MT][gq] - U0);
+          L1 += s_l[mt + k * MT][gq + 8] * ex2(s_m[mt + k * MT][gq + 8] - U1);
         }
-    }
-    if (s_abort) break;  // the same for every thread: it was read after a barrier
-    // ---- the slices' (m, l, O) become the segment's
-#pragma unroll
-    for (int d = 1; d <= 2; d <<= 1) {
-      l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, d);
-      l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, d);
-    }
-    if (cq == 0) {
-      s_m[warp][gq] = m0;
-      s_m[warp][gq + 8] = m1;
-      s_l[warp][gq] = l0;
-      s_l[warp][gq + 8] = l1;
-    }
-    __syncthreads();
-    float M0 = -INFINITY, M1 = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kNS; ++k) {
-      M0 = fmaxf(M0, s_m[mt + k * MT][gq]);
-      M1 = fmaxf(M1, s_m[mt + k * MT][gq + 8]);
-    }
-    const float U0 = M0 == -INFINITY ? 0.0f : M0, U1 = M1 == -INFINITY ? 0.0f : M1;
-    if (ps == 0 && cq == 0) {
-      float L0 = 0.0f, L1 = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kNS; ++k) {
-        L0 += s_l[mt + k * MT][gq] * ex2(s_m[mt + k * MT][gq] - U0);
-        L1 += s_l[mt + k * MT][gq + 8] * ex2(s_m[mt + k * MT][gq + 8] - U1);
+        s_M[r0] = M0;
+        s_M[r1] = M1;
+        s_L[r0] = L0;
+        s_L[r1] = L1;
       }
-      s_M[r0] = M0;
-      s_M[r1] = M1;
-      s_L[r0] = L0;
-      s_L[r1] = L1;
-    }
-    const float w0 = ex2(m0 - U0), w1 = ex2(m1 - U1);
-    // a pair's result goes out at once when nothing else has a part of it
-    const bool direct = whole && !shared;
-    auto out_row = [&](int r) {
-      return a.o + (((int64_t)s * a.T + r / G) * a.n_q + g * G + r % G) * D;
-    };
-    // a pair's part: place 2 c for CTA c's first pair, 2 c + 1 for a later one
-    float* part = a.part + (int64_t)(2 * (int)blockIdx.x + (f0 >= pb ? 0 : 1)) * kR * (D + 2);
+      const float w0 = ex2(m0 - U0), w1 = ex2(m1 - U1);
+      // the pair's parts: one place per CTA and pair, both of which grow
+      // along the line
+      const int pair = s * a.n_kv + g;
+      const bool direct = whole && !shared;
+      float* part = a.part + (int64_t)((int)blockIdx.x + pair) * kR * (D + 2);
 #pragma unroll
-    for (int cb = 0; cb < D; cb += kCW) {
+      for (int cb = 0; cb < D; cb += kCW) {
 #pragma unroll
-      for (int k = 0; k < kNS; ++k) {
-        if (ps == k) {
+        for (int k = 0; k < kNS; ++k) {
+          if (ps == k) {
 #pragma unroll
-          for (int j = 0; j < kCW / 8; ++j) {
-            const int jj = cb / 8 + j;
-            float* p0 = area + r0 * kLd + 8 * j + 2 * cq;
-            float* p1 = area + r1 * kLd + 8 * j + 2 * cq;
-            if (k == 0) {
-              p0[0] = oacc[jj][0] * w0;
-              p0[1] = oacc[jj][1] * w0;
-              p1[0] = oacc[jj][2] * w1;
-              p1[1] = oacc[jj][3] * w1;
-            } else {
-              p0[0] += oacc[jj][0] * w0;
-              p0[1] += oacc[jj][1] * w0;
-              p1[0] += oacc[jj][2] * w1;
-              p1[1] += oacc[jj][3] * w1;
+            for (int j = 0; j < kCW / 8; ++j) {
+              const int jj = cb / 8 + j;
+              float* p0 = area + r0 * kLd + 8 * j + 2 * cq;
+              float* p1 = area + r1 * kLd + 8 * j + 2 * cq;
+              if (k == 0) {
+                p0[0] = oacc[jj][0] * w0;
+                p0[1] = oacc[jj][1] * w0;
+                p1[0] = oacc[jj][2] * w1;
+                p1[1] = oacc[jj][3] * w1;
+              } else {
+                p0[0] += oacc[jj][0] * w0;
+                p0[1] += oacc[jj][1] * w0;
+                p1[0] += oacc[jj][2] * w1;
+                p1[1] += oacc[jj][3] * w1;
+              }
             }
           }
+          meet();
         }
-        __syncthreads();
-      }
-      for (int i = tid; i < rows * (kCW / 4); i += kOThr) {
-        const int d = i / rows, r = i - d * rows;
-        const float4 v = *reinterpret_cast<const float4*>(area + r * kLd + 4 * d);
-        if (direct)
-          store4<F16>(out_row(r) + cb + 4 * d, v, s_L[r]);
-        else
-          *reinterpret_cast<float4*>(part + 2 * kR + ((cb / 4 + d) * kR + r) * 4) = v;
-      }
-      __syncthreads();
-    }
-    if (!direct) {
-      for (int r = tid; r < rows; r += kOThr) {
-        part[r] = s_M[r];
-        part[kR + r] = s_L[r];
-      }
-      // the pair's CTAs: first and last to hold a block of it
-      const int c0 = pb / per, c1 = (pb + sp.blocks - 1) / per;
-      if (!whole) {
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-          unsigned* cnt = a.count + (int64_t)s * a.n_kv + g;
-          s_last = atomicAdd(cnt, 1u) == (unsigned)(c1 - c0);
-          if (s_last) *cnt = 0u;  // ready for the next call
-          __threadfence();
-        }
-      }
-      if (!waited) {
-        pdl_wait();
-        pdl_trigger();
-        waited = true;
-      }
-      __syncthreads();
-      if (whole || s_last) {
-        // join: the shared part's stretches, then the own parts, in order
-        for (int i = tid; i < rows * (D / 4); i += kOThr) {
+        for (int i = tid; i < rows * (kCW / 4); i += kOThr) {
           const int d = i / rows, r = i - d * rows;
-          float M = -INFINITY, L = 0.0f;
-          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          auto add = [&](float mc, float lc, const float4& oc) {
-            const float nM = fmaxf(M, mc), U = nM == -INFINITY ? 0.0f : nM;
-            const float fo = ex2(M - U), fc = ex2(mc - U);
-            L = L * fo + lc * fc;
-            o.x = o.x * fo + oc.x * fc;
-            o.y = o.y * fo + oc.y * fc;
-            o.z = o.z * fo + oc.z * fc;
-            o.w = o.w * fo + oc.w * fc;
-            M = nM;
-          };
-          if (shared) {
-            const int row = s * rows + r, u = (row >> 8) * a.n_kv + g, rr = row & 255;
-            const int64_t at = (int64_t)u * a.px_steps;
-            const int e = (int)((at + a.px_steps - 1) / a.px_per);
-            for (int c = (int)(at / a.px_per); c <= e; ++c) {
-              const float* pc = a.px_part + (int64_t)(c + u) * 256 * (D + 2);
-              add(__ldcg(pc + rr), __ldcg(pc + 256 + rr),
-                  __ldcg(reinterpret_cast<const float4*>(pc + 512) + d * 256 + rr));
+          const float4 v = *reinterpret_cast<const float4*>(area + r * kLd + 4 * d);
+          if (direct)
+            store4<F16>(out_row(a, s, g, G, r, D) + cb + 4 * d, v, s_L[r]);
+          else
+            *reinterpret_cast<float4*>(part + 2 * kR + ((cb / 4 + d) * kR + r) * 4) = v;
+        }
+        meet();
+      }
+      if (!direct) {
+        for (int r = tid; r < rows; r += kOThr) {
+          part[r] = s_M[r];
+          part[kR + r] = s_L[r];
+        }
+        if (shared) {
+          if (tid == 0 && pb >= f0) a.pair_start[pair] = pb;  // the pair's first CTA
+        } else {
+          // the pair's CTAs: first and last to hold a block of it
+          const int c0 = pb / per, c1 = (pb + sp.blocks - 1) / per;
+          __threadfence();
+          meet();
+          if (tid == 0) {
+            unsigned* cnt = a.count + pair;
+            s_last = atomicAdd(cnt, 1u) == (unsigned)(c1 - c0);
+            if (s_last) *cnt = 0u;  // ready for the next call
+            __threadfence();
+          }
+          meet();
+          if (s_last) {
+            for (int i = tid; i < rows * (D / 4); i += kOThr) {
+              const int d = i / rows, r = i - d * rows;
+              Joined jn{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+              join_parts<4>(jn, c1 - c0 + 1, kR, r, d, [&](int c) {
+                return a.part + (int64_t)(c0 + c + pair) * kR * (D + 2);
+              });
+              store4<F16>(out_row(a, s, g, G, r, D) + 4 * d, jn.o, jn.L);
             }
           }
-          for (int c = c0; c <= c1; ++c) {
-            const float* pc = a.part + (int64_t)(2 * c + (c * per >= pb ? 0 : 1)) * kR * (D + 2);
-            add(__ldcg(pc + r), __ldcg(pc + kR + r),
-                __ldcg(reinterpret_cast<const float4*>(pc + 2 * kR) + d * kR + r));
-          }
-          store4<F16>(out_row(r) + 4 * d, o, L);
         }
-        __syncthreads();  // a whole pair's place is the next pair's too
+        meet();  // s_M, s_L and s_last are the next pair's from here
+      }
+      // ---- the next pair
+      pb += sp.blocks;
+      if (++g == a.n_kv) {
+        g = 0;
+        if (++s < a.n_slots) sp = slot_span(a, s);
       }
     }
-    // ---- the next pair
-    pb += sp.blocks;
-    if (++g == a.n_kv) {
-      g = 0;
-      if (++s < a.n_slots) sp = slot_span(a, s);
-    }
+    if (shared && blockIdx.x == 0 && tid == 0) *a.own_per = per;
   }
-  if (s_abort && tid == 0) {
-    // a wait ran out: wait (again bounded) for the copies that may still be
-    // in flight, so that none lands after the CTA has gone
-    volatile int never = 0;
-    for (int i = issued > kOStages ? issued - kOStages : 0; i < issued; ++i)
-      mbar_wait(fb + 8u * (i % kOStages), (uint32_t)(i / kOStages) & 1u, &never);
+  if (shared) {
+    // the join waits for this kernel, and this one for the shared part
+    pdl_wait();
+    pdl_trigger();
   }
+}
+
+// Four elements of a row a thread: the shared part's stretches, then the own
+// parts, in order.
+template <bool F16, int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnBatchArgs a, int kR) {
+  pdl_wait();
+  pdl_trigger();
+  const int pair = blockIdx.x, s = pair / a.n_kv, g = pair - s * a.n_kv;
+  const int G = a.n_q / a.n_kv, rows = a.T * G;
+  const int i = blockIdx.y * 256 + threadIdx.x;
+  if (i >= rows * (D / 4)) return;
+  const int d = i / rows, r = i - d * rows;
+  const SlotSpan sp = slot_span(a, s);
+  Joined jn{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  if (r / G < sp.n_new && sp.len - sp.n_new + r / G >= 0) {
+    const int per = __ldg(a.own_per), pb = __ldg(a.pair_start + pair);
+    const int row = s * rows + r, u = (row >> 8) * a.n_kv + g, rr = row & 255;
+    const int x0 = u * a.px_steps / a.px_per, x1 = (u * a.px_steps + a.px_steps - 1) / a.px_per;
+    join_parts<8>(jn, x1 - x0 + 1, 256, rr, d, [&](int c) {
+      return a.px_part + (int64_t)(x0 + c + u) * 256 * (D + 2);
+    });
+    const int c0 = pb / per, c1 = (pb + sp.blocks - 1) / per;
+    join_parts<2>(jn, c1 - c0 + 1, kR, r, d, [&](int c) {
+      return a.part + (int64_t)(c0 + c + pair) * kR * (D + 2);
+    });
+  }
+  store4<F16>(out_row(a, s, g, G, r, D) + 4 * d, jn.o, jn.L);
 }
 
 bool attn_batch_supported(const moe_attn_batch_shape_t* s) {
@@ -490,19 +578,25 @@ int own_tiles(const moe_attn_batch_shape_t* s) {  // row tiles: 1, 2 or 4
 }
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr int kMostSms = 256;  // two CTAs an SM at most
+// a place per CTA and pair
 size_t own_part_bytes(const moe_attn_batch_shape_t* s) {
-  return round256((size_t)2 * 2 * kMostSms * own_tiles(s) * 16 * (s->D + 2) * 4);
+  const size_t places = 2 * kMostSms + (size_t)s->n_slots * s->n_kv;
+  return round256(places * own_tiles(s) * 16 * (s->D + 2) * 4);
 }
 
 template <bool F16, int D, int MT>
 cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const AttnBatchArgs& a,
                        int grid, cudaStream_t stream) {
-  const size_t smem = 1024 + (size_t)kOStages * 2 * kBlk * D * 2 +
+  const size_t smem = 1024 + (size_t)OwnRing<D>::kStages * 2 * OwnRing<D>::kTile +
                       (kOAreaFloats + MT * 16 * 4) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(attn_own_kernel<F16, D, MT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(attn_own_kernel<F16, D, MT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_own_kernel<F16, D, MT>, dim3(grid), dim3(kOThr), smem, stream, tk, tv, a);
+  e = launch_pdl(attn_own_kernel<F16, D, MT>, dim3(grid), dim3(kOAll), smem, stream, tk, tv, a);
+  if (e != cudaSuccess || a.px_steps == 0) return e;
+  const int items = a.T * (a.n_q / a.n_kv) * (D / 4);
+  return launch_pdl(attn_join_kernel<F16, D>, dim3(a.n_slots * a.n_kv, (items + 255) / 256),
+                    dim3(256), 0, stream, a, MT * 16);
 }
 template <bool F16, int D>
 cudaError_t launch_own_mt(int mt, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -513,10 +607,10 @@ cudaError_t launch_own_mt(int mt, const CUtensorMap& tk, const CUtensorMap& tv,
 }
 }  // namespace
 
-// status, the pairs' counters, the pairs' parts (two places per CTA), the
-// shared part's
+// status and the own line's step, the pairs' counters, their starts, their
+// parts, the shared part's
 size_t attn_batch_ws_bytes(const moe_attn_batch_shape_t* s) {
-  return 256 + round256((size_t)s->n_slots * s->n_kv * 4) + own_part_bytes(s) +
+  return 512 + 2 * round256((size_t)s->n_slots * s->n_kv * 4) + own_part_bytes(s) +
          (s->prefix_blocks > 0 ? prefix_part_floats(s, kMostSms) * 4 : 0);
 }
 
@@ -524,8 +618,11 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
                               const CUtensorMap& tv, AttnBatchArgs a, uint8_t* ws, int nsm,
                               cudaStream_t stream) {
   a.ctrl = reinterpret_cast<Ctrl*>(ws);
-  a.count = reinterpret_cast<unsigned*>(ws + 256);
-  a.part = reinterpret_cast<float*>(ws + 256 + round256((size_t)s->n_slots * s->n_kv * 4));
+  const size_t pairs = round256((size_t)s->n_slots * s->n_kv * 4);
+  a.own_per = reinterpret_cast<int32_t*>(ws + 256);
+  a.count = reinterpret_cast<unsigned*>(ws + 512);
+  a.pair_start = reinterpret_cast<int32_t*>(ws + 512 + pairs);
+  a.part = reinterpret_cast<float*>(ws + 512 + 2 * pairs);
   a.n_slots = s->n_slots;
   a.T = s->T;
   a.n_q = s->n_q;

@@ -212,6 +212,8 @@ struct AttnBatchArgs {
   uint16_t* o;         // [n_slots][T][n_q][D]
   float* part;         // parts of pairs: per place m[R], l[R], O[D / 4][R][4]
   unsigned* count;     // [n_slots][n_kv]: CTAs of a cut pair that have arrived
+  int32_t* pair_start; // [n_slots][n_kv]: where the pair starts on the own line
+  int32_t* own_per;    // blocks of that line per CTA
   // the shared part, when attn_prefix_kernel takes it (px_steps > 0): its
   // line of steps and its parts, per place m[256], l[256], O[D / 4][256][4]
   int px_steps, px_per, px_total;

@@ -14,7 +14,9 @@
 // attn_own_kernel: each slot's own positions. The (slot, head) pairs' blocks
 // lie on one line, and CTA c takes blocks [c per, (c + 1) per) of it whatever
 // slots they belong to, so uneven lengths leave no CTA idle. The
-// T * n_q / n_kv <= 64 query rows of a pair are the M rows of mma.sync tiles
+// (A pair counts pair_cost units more than its blocks: its start and end cost
+// about that many blocks' time, so a CTA of many short slots gets fewer
+// blocks.) The T * n_q / n_kv <= 64 query rows of a pair are the M rows of mma.sync tiles
 // (16 rows; 1, 2 or 4 tiles), so each key and value is read once per slot. A
 // warp of its own keeps a TMA ring of blocks full (64 rows x 64 elements per
 // box, 128-byte swizzle) that runs on across pairs; the four others only meet
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(kOAll, 2)
     const int chunk = (a.n_slots + kOAll - 1) / kOAll;
     const int s0 = min(tid * chunk, a.n_slots), s1 = min(s0 + chunk, a.n_slots);
     int sum = 0;
-    for (int s = s0; s < s1; ++s) sum += slot_span(a, s).blocks;
+    for (int s = s0; s < s1; ++s) sum += slot_span(a, s).blocks + a.pair_cost;
     sum *= a.n_kv;
     int incl = sum;
 #pragma unroll
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kOAll, 2)
     if (f0 >= run && f0 < incl) {  // one thread's slots hold the first block
       int s = s0;
       for (; s < s1 - 1; ++s) {
-        const int n = slot_span(a, s).blocks * a.n_kv;
+        const int n = (slot_span(a, s).blocks + a.pair_cost) * a.n_kv;
         if (f0 < run + n) break;
         run += n;
       }
@@ -208,18 +210,29 @@ __global__ void __launch_bounds__(kOAll, 2)
   const int f0 = (int)blockIdx.x * per, f1 = min(f0 + per, total);
   int s = s_start;
   SlotSpan sp = slot_span(a, s);
-  int g = s_off / sp.blocks;
-  int pb = f0 - (s_off - g * sp.blocks);  // where the pair starts on the line
+  int g = s_off / (sp.blocks + a.pair_cost);
+  // where the pair starts on the line; its blocks first, then its cost
+  int pb = f0 - (s_off - g * (sp.blocks + a.pair_cost));
   volatile int* abort = &s_abort;
 
   if (warp == 4) {
     // ---- the loader: all lanes follow the line, lane 0 issues
     const uint64_t pol = policy_evict_first();  // own pages are read once
-    int j = f0 - pb;                            // block of the pair
     int page = 0;                               // lane l: page of block (j & ~31) + l
     bool fresh = true;
-    int n = 0;
-    for (int f = f0; f < f1; ++f, ++n) {
+    int n = 0;  // blocks loaded
+    for (int f = f0; f < f1;) {
+      const int j = f - pb;  // block of the pair
+      if (j >= sp.blocks) {
+        pb += sp.blocks + a.pair_cost;
+        f = pb;
+        if (++g == a.n_kv) {
+          g = 0;
+          if (++s < a.n_slots) sp = slot_span(a, s);
+        }
+        fresh = true;
+        continue;
+      }
       if (fresh || (j & 31) == 0) {
         const int jb = a.first + (j & ~31) + lane;
         page = -2;  // nothing there
@@ -255,14 +268,8 @@ __global__ void __launch_bounds__(kOAll, 2)
           tma_load_2d(sv + bx * (kBlk * 128), &tm_v, bx * 64, row0, bar, pol);
         }
       }
-      if (++j == sp.blocks) {
-        j = 0;
-        if (++g == a.n_kv) {
-          g = 0;
-          if (++s < a.n_slots) sp = slot_span(a, s);
-        }
-        fresh = true;
-      }
+      ++f;
+      ++n;
     }
     if (lane == 0) {
       // what is still in flight lands before the CTA goes (bounded)
@@ -280,9 +287,18 @@ __global__ void __launch_bounds__(kOAll, 2)
     const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(D)
     const int mi = lane >> 3, rr = lane & 7;
     auto meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-    int f = f0;
+    int f = f0, it = 0;  // it: blocks done
     while (f < f1) {
       const int fe = min(f1, pb + sp.blocks);
+      if (f >= fe) {  // this CTA starts in a pair's cost
+        pb += sp.blocks + a.pair_cost;
+        f = pb;
+        if (++g == a.n_kv) {
+          g = 0;
+          if (++s < a.n_slots) sp = slot_span(a, s);
+        }
+        continue;
+      }
       const bool whole = f == pb && fe == pb + sp.blocks;
       // rows r = t * G + head in group; a row's last position, -1: sees nothing
       const int base = sp.len - sp.n_new;  // may be negative
@@ -306,8 +322,8 @@ __global__ void __launch_bounds__(kOAll, 2)
       float oacc[kDT][4];
 #pragma unroll
       for (int j = 0; j < kDT; ++j) oacc[j][0] = oacc[j][1] = oacc[j][2] = oacc[j][3] = 0.0f;
-      for (; f < fe; ++f) {
-        const int it = f - f0, st = it % kStages;
+      for (; f < fe; ++f, ++it) {
+        const int st = it % kStages;
         if (!mbar_wait(fb + 8u * st, (uint32_t)(it / kStages) & 1u, abort) &&
             atomicCAS(&s_abort, 0, 1) == 0)
           set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, s);
@@ -515,13 +531,14 @@ __global__ void __launch_bounds__(kOAll, 2)
         meet();  // s_M, s_L and s_last are the next pair's from here
       }
       // ---- the next pair
-      pb += sp.blocks;
+      pb += sp.blocks + a.pair_cost;
+      f = pb;
       if (++g == a.n_kv) {
         g = 0;
         if (++s < a.n_slots) sp = slot_span(a, s);
       }
     }
-    if (shared && blockIdx.x == 0 && tid == 0) *a.own_per = per;
+    if (shared && blockIdx.x == 0 && tid == 0) a.line[0] = per;
   }
   if (shared) {
     // the join waits for this kernel, and this one for the shared part
@@ -530,32 +547,68 @@ __global__ void __launch_bounds__(kOAll, 2)
   }
 }
 
-// Four elements of a row a thread: the shared part's stretches, then the own
-// parts, in order.
-template <bool F16, int D>
+// Joins the shared part's stretches and the own parts. kLanes threads for four
+// elements of a row, each with every kLanes-th part, so that all of a row's
+// parts are fetched at once; then the threads' results in their order.
+template <bool F16, int D, int kLanes>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnBatchArgs a, int kR) {
+  constexpr int kItems = 256 / kLanes;
+  __shared__ float4 s_o[kLanes][kItems];
+  __shared__ float2 s_ml[kLanes][kItems];
   pdl_wait();
   pdl_trigger();
   const int pair = blockIdx.x, s = pair / a.n_kv, g = pair - s * a.n_kv;
   const int G = a.n_q / a.n_kv, rows = a.T * G;
-  const int i = blockIdx.y * 256 + threadIdx.x;
-  if (i >= rows * (D / 4)) return;
-  const int d = i / rows, r = i - d * rows;
+  const int item = threadIdx.x % kItems, ln = threadIdx.x / kItems;
+  const int i = blockIdx.y * kItems + item;
+  const int d = i / rows, r = i - d * rows, t = r / G;
+  const int own_per = __ldg(a.line), px_per = __ldg(a.line + 1);
+  const int pb = __ldg(a.pair_start + pair), tok0 = __ldg(a.tok_start + s);
   const SlotSpan sp = slot_span(a, s);
   Joined jn{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-  if (r / G < sp.n_new && sp.len - sp.n_new + r / G >= 0) {
-    const int per = __ldg(a.own_per), pb = __ldg(a.pair_start + pair);
-    const int row = s * rows + r, u = (row >> 8) * a.n_kv + g, rr = row & 255;
-    const int x0 = u * a.px_steps / a.px_per, x1 = (u * a.px_steps + a.px_steps - 1) / a.px_per;
-    join_parts<8>(jn, x1 - x0 + 1, 256, rr, d, [&](int c) {
-      return a.px_part + (int64_t)(x0 + c + u) * 256 * (D + 2);
+  if (i < rows * (D / 4) && t < sp.n_new && sp.len - sp.n_new + t >= 0) {
+    const int row = tok0 * G + r, u = (row >> 8) * a.n_kv + g, rr = row & 255;
+    const int x0 = u * a.px_steps / px_per, x1 = (u * a.px_steps + a.px_steps - 1) / px_per;
+    const int nx = x1 - x0 + 1;
+    join_parts<4>(jn, (nx - ln + kLanes - 1) / kLanes, 256, rr, d, [&](int c) {
+      return a.px_part + (int64_t)(x0 + c * kLanes + ln + u) * 256 * (D + 2);
     });
-    const int c0 = pb / per, c1 = (pb + sp.blocks - 1) / per;
-    join_parts<2>(jn, c1 - c0 + 1, kR, r, d, [&](int c) {
-      return a.part + (int64_t)(c0 + c + pair) * kR * (D + 2);
+    const int c0 = pb / own_per, n = (pb + sp.blocks - 1) / own_per - c0 + 1;
+    // the own parts follow: the next lane's turn
+    const int l0 = (ln + kLanes - nx % kLanes) % kLanes;
+    join_parts<2>(jn, (n - l0 + kLanes - 1) / kLanes, kR, r, d, [&](int c) {
+      return a.part + (int64_t)(c0 + c * kLanes + l0 + pair) * kR * (D + 2);
     });
   }
-  store4<F16>(out_row(a, s, g, G, r, D) + 4 * d, jn.o, jn.L);
+  if (kLanes > 1) {
+    s_o[ln][item] = jn.o;
+    s_ml[ln][item] = make_float2(jn.M, jn.L);
+    __syncthreads();
+    if (ln > 0) return;
+    float M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kLanes; ++k) M = fmaxf(M, s_ml[k][item].x);
+    const float U = M == -INFINITY ? 0.0f : M;
+    jn = Joined{M, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+#pragma unroll
+    for (int k = 0; k < kLanes; ++k) {
+      const float w = ex2(s_ml[k][item].x - U);
+      const float4 v = s_o[k][item];
+      jn.L = fmaf(s_ml[k][item].y, w, jn.L);
+      jn.o.x = fmaf(v.x, w, jn.o.x);
+      jn.o.y = fmaf(v.y, w, jn.o.y);
+      jn.o.z = fmaf(v.z, w, jn.o.z);
+      jn.o.w = fmaf(v.w, w, jn.o.w);
+    }
+  }
+  if (i < rows * (D / 4)) store4<F16>(out_row(a, s, g, G, r, D) + 4 * d, jn.o, jn.L);
+}
+
+template <bool F16, int D, int kLanes>
+cudaError_t launch_join(const AttnBatchArgs& a, int kR, cudaStream_t stream) {
+  const int items = a.T * (a.n_q / a.n_kv) * (D / 4), per = 256 / kLanes;
+  return launch_pdl(attn_join_kernel<F16, D, kLanes>,
+                    dim3(a.n_slots * a.n_kv, (items + per - 1) / per), dim3(256), 0, stream, a, kR);
 }
 
 bool attn_batch_supported(const moe_attn_batch_shape_t* s) {
@@ -594,9 +647,10 @@ cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const AttnB
   if (e != cudaSuccess) return e;
   e = launch_pdl(attn_own_kernel<F16, D, MT>, dim3(grid), dim3(kOAll), smem, stream, tk, tv, a);
   if (e != cudaSuccess || a.px_steps == 0) return e;
-  const int items = a.T * (a.n_q / a.n_kv) * (D / 4);
-  return launch_pdl(attn_join_kernel<F16, D>, dim3(a.n_slots * a.n_kv, (items + 255) / 256),
-                    dim3(256), 0, stream, a, MT * 16);
+  // a lane for about four parts of a row
+  if (a.px_parts <= 6) return launch_join<F16, D, 1>(a, MT * 16, stream);
+  if (a.px_parts <= 16) return launch_join<F16, D, 4>(a, MT * 16, stream);
+  return launch_join<F16, D, 16>(a, MT * 16, stream);
 }
 template <bool F16, int D>
 cudaError_t launch_own_mt(int mt, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -607,10 +661,11 @@ cudaError_t launch_own_mt(int mt, const CUtensorMap& tk, const CUtensorMap& tv,
 }
 }  // namespace
 
-// status and the own line's step, the pairs' counters, their starts, their
-// parts, the shared part's
+// status and the lines' steps, the pairs' counters, their starts, the slots'
+// first tokens, the pairs' parts, the shared part's
 size_t attn_batch_ws_bytes(const moe_attn_batch_shape_t* s) {
-  return 512 + 2 * round256((size_t)s->n_slots * s->n_kv * 4) + own_part_bytes(s) +
+  return 512 + 2 * round256((size_t)s->n_slots * s->n_kv * 4) +
+         round256((size_t)s->n_slots * 4) + own_part_bytes(s) +
          (s->prefix_blocks > 0 ? prefix_part_floats(s, kMostSms) * 4 : 0);
 }
 
@@ -619,10 +674,12 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
                               cudaStream_t stream) {
   a.ctrl = reinterpret_cast<Ctrl*>(ws);
   const size_t pairs = round256((size_t)s->n_slots * s->n_kv * 4);
-  a.own_per = reinterpret_cast<int32_t*>(ws + 256);
+  a.line = reinterpret_cast<int32_t*>(ws + 256);
   a.count = reinterpret_cast<unsigned*>(ws + 512);
   a.pair_start = reinterpret_cast<int32_t*>(ws + 512 + pairs);
-  a.part = reinterpret_cast<float*>(ws + 512 + 2 * pairs);
+  a.tok_start = reinterpret_cast<int32_t*>(ws + 512 + 2 * pairs);
+  a.part = reinterpret_cast<float*>(ws + 512 + 2 * pairs + round256((size_t)s->n_slots * 4));
+  a.pair_cost = s->D == 64 ? 2 : 1;
   a.n_slots = s->n_slots;
   a.T = s->T;
   a.n_q = s->n_q;
@@ -636,8 +693,7 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
     const PrefixLine line = prefix_line(s, sms);
     a.first = s->prefix_blocks;
     a.px_steps = line.steps;
-    a.px_per = line.per;
-    a.px_total = (int)line.total;
+    a.px_parts = (line.grid + line.pairs - 1) / line.pairs + 1;
     a.px_part = a.part + own_part_bytes(s) / 4;
     const cudaError_t e = launch_attn_prefix(s, tk, tv, a, line.grid, stream);
     if (e != cudaSuccess) return e;

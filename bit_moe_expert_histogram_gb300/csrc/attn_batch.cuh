@@ -8,6 +8,11 @@ namespace moe {
 
 constexpr int kBlk = 64;  // positions per page
 
+// New tokens of a slot, brought into range.
+__device__ __forceinline__ int slot_tokens(const AttnBatchArgs& a, int s) {
+  return a.n_new ? min(max(__ldg(a.n_new + s), 0), a.T) : a.T;
+}
+
 // What a slot brings: its length, new tokens and own blocks (at least one, a
 // block of nothing where it has none, so that each slot's rows get written).
 struct SlotSpan {

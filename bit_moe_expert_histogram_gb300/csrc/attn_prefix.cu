@@ -1,21 +1,25 @@
 // The shared part of the batch's attention: every slot's rows against the
 // prefix pages, which are read once for all of them.
 //
-// Row (s, t, head in group) of key/value head g is row (s T + t) G + head of
-// one [n_slots T G][D] matrix, so attention over the prefix is one pair of
-// large products per key/value head, on the tensor cores (tcgen05): tiles of
+// The tokens that are there (t < n_new[s]) are counted through, so a batch of
+// uneven drafts has no empty rows: row tok G + head of key/value head g
+// belongs to the tok-th of them, and attention over the prefix is one pair of
+// large products per key/value head on the tensor cores (tcgen05): tiles of
 // 256 rows (two of M = 128) against steps of 128 positions (two pages),
 // S = Q K^T into TMEM, softmax weights P back into TMEM over S, O += P V.
 // The (tile, head) pairs' steps lie on one line cut evenly over one CTA per
 // SM; each stretch leaves (m, l, O) of its 256 rows in the workspace, where
-// attn_own_kernel joins them with the slots' own positions.
+// attn_join_kernel joins them with the slots' own positions.
 //
 // Warps: 0 loads K and V (TMA, two stages each of 128 positions), 1 issues
-// the products, 2-5 and 6-9 do the softmax of the two row tiles, a row a
-// thread. While one tile's weights are formed the other's products run. The
-// running maximum is only raised when a row grows past it by 2^8 (the sums
-// are relative to it, so any reference near the maximum does): O in TMEM is
-// rescaled a few times per stretch, not at every step.
+// the products, 4-11 and 12-19 do the softmax of the two row tiles, half a
+// row a thread (the halves exchange their maxima through shared memory): with
+// a whole row a thread the chain load, maximum, exponentials, store took
+// longer than the other tile's products (282 us instead of 204 on 16384 rows
+// against 32768 positions). While one tile's weights are formed the other's
+// products run. The reference that a row's weights are relative to is only
+// raised when the row grows past it by 2^8 (any reference near the maximum
+// does): O in TMEM is rescaled a few times per stretch, not at every step.
 //
 // Bounds (D = 128, per step and two tiles): products 32 MMAs of N = 128 at
 // 64 to 77 clocks, about 2256; exponentials 2 x 128 x 128 at 16 a clock,
@@ -26,7 +30,7 @@
 namespace moe {
 
 namespace {
-constexpr int kPThr = 320;      // 2 single warps + 2 x 4 softmax warps
+constexpr int kPThr = 640;      // a warpgroup of single warps, 2 x 2 of softmax warps
 constexpr int kPRows = 256;     // rows of a tile pair
 constexpr int kPStep = 128;     // positions of a step
 constexpr int kPStages = 2;
@@ -89,25 +93,54 @@ struct PrefixBars {
 };
 }  // namespace
 
+// pairs of fp32 in one instruction
+__device__ __forceinline__ uint64_t pair2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;"
+      : "=f"(r)
+      : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return r;
+}
+
 template <bool F16, int D>
 __global__ void __launch_bounds__(kPThr, 1)
     attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const AttnBatchArgs a) {
-  constexpr int kHalves = D / 64;                     // 64-element column halves of a tile
-  constexpr uint32_t kHalf = 128 * 128;               // bytes of 128 rows of one
-  constexpr uint32_t kTile = kHalves * kHalf;         // a Q, K or V tile
-  constexpr uint32_t kO = 0, kS = 256;                // TMEM columns: O tiles, then S tiles
+  constexpr int kHalves = D / 64;              // 64-element column halves of a tile
+  constexpr uint32_t kHalf = 128 * 128;        // bytes of 128 rows of one
+  constexpr uint32_t kTile = kHalves * kHalf;  // a Q, K or V tile
+  constexpr uint32_t kO = 0, kS = 256;         // TMEM columns: O tiles, then S tiles
   extern __shared__ __align__(1024) uint8_t sm_raw[];
   __shared__ __align__(8) PrefixBars bars;
+  __shared__ float s_mx[2][2][2][128];  // step parity, row tile, half, row
+  __shared__ int s_scan[kPThr / 32];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
   uint8_t* sm = sm_raw + (sbase - smem_u32(sm_raw));
   const uint32_t sq = sbase, sk = sq + 2 * kTile, sv = sk + kPStages * kTile;
+  // tokens before each slot
+  int* s_tok = reinterpret_cast<int*>(sm + (2 + 2 * kPStages) * kTile);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = a.n_q / a.n_kv, R = a.n_slots * a.T * G;
-  const int steps = a.px_steps, per = a.px_per;
-  const int f0 = (int)blockIdx.x * per, f1 = min(f0 + per, a.px_total);
+  const int G = a.n_q / a.n_kv;
   auto bar = [&](const uint64_t& b) { return smem_u32(&b); };
   if (tid == 0) {
     for (int i = 0; i < kPStages; ++i) {
@@ -117,9 +150,9 @@ __global__ void __launch_bounds__(kPThr, 1)
       mbar_init(bar(bars.v_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(bars.q_ready[i]), 128);
+      mbar_init(bar(bars.q_ready[i]), 8);  // the tile's warps
       mbar_init(bar(bars.s_full[i]), 1);
-      mbar_init(bar(bars.p_ready[i]), 128);
+      mbar_init(bar(bars.p_ready[i]), 8);
       mbar_init(bar(bars.pv_done[i]), 1);
     }
     mbar_init(bar(bars.drain), 1);
@@ -133,11 +166,45 @@ __global__ void __launch_bounds__(kPThr, 1)
     tmem_relinquish();
   }
   tc_fence_before();
+  pdl_wait();
+  pdl_trigger();
+  // ---- the tokens that are there, counted through
+  int n_tok;
+  {
+    const int chunk = (a.n_slots + kPThr - 1) / kPThr;
+    const int s0 = min(tid * chunk, a.n_slots), s1 = min(s0 + chunk, a.n_slots);
+    int sum = 0;
+    for (int s = s0; s < s1; ++s) sum += slot_tokens(a, s);
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < kPThr / 32; ++w) {
+      if (w == warp) incl += all;
+      all += s_scan[w];
+    }
+    n_tok = all;
+    int run = incl - sum;
+    for (int s = s0; s < s1; ++s) {
+      s_tok[s] = run;
+      if (blockIdx.x == 0) a.tok_start[s] = run;
+      run += slot_tokens(a, s);
+    }
+  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  pdl_wait();
-  pdl_trigger();
+  const int R = n_tok * G, steps = a.px_steps;
+  const int total = (R + kPRows - 1) / kPRows * a.n_kv * steps;
+  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int f0 = (int)blockIdx.x * per, f1 = min(f0 + per, total);
+  if (blockIdx.x == 0 && tid == 0) a.line[1] = per;
   volatile int* abort = &s_abort;
   // a bounded wait; one that runs out is recorded and ends every role
   auto wait = [&](const uint64_t& b, uint32_t parity) {
@@ -145,13 +212,11 @@ __global__ void __launch_bounds__(kPThr, 1)
     if (atomicCAS(&s_abort, 0, 1) == 0) set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, -2);
     return false;
   };
-  // the line's stretch f .. : pair u (tile u / n_kv, head u % n_kv), steps
-  // j0 .. j1 of it
+  // the line's stretch f0 .. f1: pair u (tile u / n_kv, head u % n_kv) by pair
   if (warp == 0) {
     if (lane == 0) {
       int n = 0;  // steps loaded
-      bool ok = true;
-      for (int f = f0; ok && f < f1; ++f, ++n) {
+      for (int f = f0; f < f1; ++f, ++n) {
         const int u = f / steps, j = f - u * steps, g = u % a.n_kv;
         const int st = n % kPStages;
         const uint32_t ph = (uint32_t)(n / kPStages) & 1u;
@@ -165,8 +230,7 @@ __global__ void __launch_bounds__(kPThr, 1)
           // a page that is not there reads past the pool's end: zeros
           row[i] = (bad ? a.n_phys * a.n_kv : phys * a.n_kv + g) * kBlk;
         }
-        ok = wait(bars.k_empty[st], ph ^ 1u);
-        if (!ok) break;
+        if (!wait(bars.k_empty[st], ph ^ 1u)) break;
         mbar_arrive_expect_tx(bar(bars.k_full[st]), kTile);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -174,8 +238,7 @@ __global__ void __launch_bounds__(kPThr, 1)
           for (int h = 0; h < kHalves; ++h)
             tma_load_rows(sk + st * kTile + h * kHalf + i * (kBlk * 128), &tm_k, h * 64, row[i],
                           bar(bars.k_full[st]));
-        ok = wait(bars.v_empty[st], ph ^ 1u);
-        if (!ok) {
+        if (!wait(bars.v_empty[st], ph ^ 1u)) {
           // the keys just asked for must land before the CTA goes
           volatile int never = 0;
           mbar_wait(bar(bars.k_full[st]), ph, &never);
@@ -209,9 +272,9 @@ __global__ void __launch_bounds__(kPThr, 1)
         }
         mma_commit(bar(bars.s_full[w]));
       };
-      int n = 0, seg = 0, pn[2] = {0, 0}, qn[2] = {0, 0};
+      int n = 0, pn[2] = {0, 0}, qn[2] = {0, 0};
       bool ok = true;
-      for (int f = f0; ok && f < f1; ++seg) {
+      for (int f = f0; ok && f < f1;) {
         const int u = f / steps, j0 = f - u * steps;
         const int cnt = min(steps - j0, f1 - f);
         const int tiles = (u / a.n_kv) * kPRows + 128 < R ? 2 : 1;
@@ -254,16 +317,21 @@ __global__ void __launch_bounds__(kPThr, 1)
       mbar_wait(bar(bars.drain), 0, &never);
     }
     __syncwarp();
-  } else {
-    const int w = (warp - 2) >> 2;       // row tile
-    const int quarter = warp & 3;        // TMEM lanes 32 quarter ..
-    const int r = quarter * 32 + lane;   // row in the tile
+  } else if (warp >= 4) {
+    const int w = (warp - 4) >> 3;         // row tile
+    const int hf = ((warp - 4) >> 2) & 1;  // half of the step's positions, of O's columns
+    const int quarter = warp & 3;          // TMEM lanes 32 quarter ..
+    const int r = quarter * 32 + lane;     // row in the tile
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tS = tmem + kS + w * 128 + lanes, tO = tmem + kO + w * 128 + lanes;
+    const uint32_t tS = tmem + kS + w * 128 + lanes;
+    const uint32_t tO = tmem + kO + w * 128 + hf * (D / 2) + lanes;
     const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(D)
+    const uint64_t sl22 = pair2(__float_as_uint(sl2), __float_as_uint(sl2));
+    // the tile's 256 threads; after a wait that ran out the loops go on to
+    // their end over what is there, so that all of them keep meeting
+    auto meet = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory"); };
     int n = 0;  // this tile's steps so far
-    bool ok = true;
-    for (int f = f0; ok && f < f1;) {
+    for (int f = f0; f < f1;) {
       const int u = f / steps, j0 = f - u * steps, g = u % a.n_kv;
       const int cnt = min(steps - j0, f1 - f);
       f += cnt;
@@ -275,106 +343,113 @@ __global__ void __launch_bounds__(kPThr, 1)
       {
         const uint16_t* src = nullptr;
         if (row < R) {
-          const int tok = row / G, hh = row - tok * G, s = tok / a.T, t = tok - s * a.T;
+          const int tok = row / G, hh = row - tok * G;
+          int s = 0;  // the last slot with s_tok <= tok: the one that holds it
+          for (int step = 4096; step; step >>= 1)
+            if (s + step < a.n_slots && s_tok[s + step] <= tok) s += step;
+          const int t = tok - s_tok[s];
           const SlotSpan sp = slot_span(a, s);
-          lim = t < sp.n_new ? sp.len - sp.n_new + t : -1;
-          if (lim >= 0) src = a.q + (int64_t)tok * a.q_stride + (g * G + hh) * D;
+          lim = sp.len - sp.n_new + t;
+          if (lim >= 0) src = a.q + ((int64_t)s * a.T + t) * a.q_stride + (g * G + hh) * D;
         }
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = hf * (D / 16); c < (hf + 1) * (D / 16); ++c) {
           const uint4 v = src ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4*>(sm + w * kTile + (c >> 3) * kHalf + r * 128 +
                                     (((c & 7) ^ (r & 7)) << 4)) = v;
         }
       }
       fence_proxy_async_smem();  // the tensor core reads it
-      mbar_arrive(bar(bars.q_ready[w]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars.q_ready[w]));
       float ref = -INFINITY, l = 0.0f;
       for (int j = j0; j < j0 + cnt; ++j, ++n) {
-        // what of the step this row sees
-        const int p0 = 2 * j < a.prefix_blocks ? __ldg(a.prefix + 2 * j) : -1;
-        const int p1 = 2 * j + 1 < a.prefix_blocks ? __ldg(a.prefix + 2 * j + 1) : -1;
-        const bool hole = p0 < 0 || p0 >= a.n_phys || p1 < 0 || p1 >= a.n_phys;
-        const int left = lim - j * kPStep;  // last position of the step that is seen
-        const bool plain = !__any_sync(0xFFFFFFFFu, hole || left < kPStep - 1);
-        ok = wait(bars.s_full[w], (uint32_t)n & 1u);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
+        // what of its half of the step this row sees
+        const int jb = 2 * j + hf;
+        const int page = jb < a.prefix_blocks ? __ldg(a.prefix + jb) : -1;
+        const bool bad = page < 0 || page >= a.n_phys;
+        const int left = bad ? -1 : lim - jb * kBlk;  // last position that is seen
+        const bool plain = !__any_sync(0xFFFFFFFFu, left < kBlk - 1);
+        wait(bars.s_full[w], (uint32_t)n & 1u);
         tc_fence_after();
-        uint32_t x[kPStep];
-#pragma unroll
-        for (int c = 0; c < kPStep; c += 32) tmem_ld32(tS + c, x + c);
+        uint32_t x[kBlk];
+        tmem_ld32(tS + hf * 64, x);
+        tmem_ld32(tS + hf * 64 + 32, x + 32);
         tmem_wait_ld();
         if (!plain) {
-          const bool b0 = p0 < 0 || p0 >= a.n_phys, b1 = p1 < 0 || p1 >= a.n_phys;
 #pragma unroll
-          for (int c = 0; c < kPStep; ++c)
-            if (c > left || (c < kBlk ? b0 : b1)) x[c] = 0xFF800000u;  // -inf
+          for (int c = 0; c < kBlk; ++c)
+            if (c > left) x[c] = 0xFF800000u;  // -inf
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kPStep; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        for (int c = 0; c < kBlk; c += 4) {
+          mx[0] = max3(mx[0], x[c], x[c + 1]);
+          mx[1] = max3(mx[1], x[c + 2], x[c + 3]);
+        }
+        mx[0] = fmaxf(mx[0], mx[1]);
+        s_mx[n & 1][w][hf][r] = mx[0];
+        meet();  // both halves have read S, too: P may overwrite it
+        const float top = fmaxf(mx[0], s_mx[n & 1][w][hf ^ 1][r]) * sl2;
         if (j == j0) {
           ref = top;
         } else {
           const bool grow = top > ref + kSlack;
           if (__any_sync(0xFFFFFFFFu, grow)) {
             // O of the steps before is complete, the next product waits for us
-            ok = wait(bars.pv_done[w], (uint32_t)(n - 1) & 1u);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
-              ok = false;
-              break;
-            }
+            wait(bars.pv_done[w], (uint32_t)(n - 1) & 1u);
             tc_fence_after();
             const float now = grow ? top : ref;
             const float fac = grow ? ex2(ref - now) : 1.0f;  // 0 where nothing was seen yet
             ref = now;
             l *= fac;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t y[32];
-              tmem_ld32(tO + c, y);
+            for (int c = 0; c < D / 2; c += 16) {
+              uint32_t y[16];
+              tmem_ld16r(tO + c, y);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * fac);
-              tmem_st32(tO + c, y);
+              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * fac);
+              tmem_st16(tO + c, y);
             }
             tmem_wait_st();
           }
         }
         const float off = lift<F16>() - (ref == -INFINITY ? 0.0f : ref);
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t off2 = pair2(__float_as_uint(off), __float_as_uint(off));
+        uint64_t sum = 0;  // two sums
 #pragma unroll
-        for (int c = 0; c < kPStep; c += 2) {
-          const float e0 = ex2(fmaf(__uint_as_float(x[c]), sl2, off));
-          const float e1 = ex2(fmaf(__uint_as_float(x[c + 1]), sl2, off));
-          sum[c & 2] += e0;
-          sum[(c & 2) + 1] += e1;
+        for (int c = 0; c < kBlk; c += 2) {
+          float e0, e1;
+          unpair2(fma2(pair2(x[c], x[c + 1]), sl22, off2), e0, e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          sum = add2(sum, pair2(__float_as_uint(e0), __float_as_uint(e1)));
           x[c >> 1] = pack2<F16>(e0, e1);
-          if ((c & 62) == 62) tmem_st32(tS + (c >> 1) - 31, x + (c >> 1) - 31);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st32(tS + hf * 32, x);
+        float t0, t1;
+        unpair2(sum, t0, t1);
+        l += t0 + t1;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(bars.p_ready[w]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars.p_ready[w]));
       }
-      if (!ok) break;
       // ---- the stretch's (m, l, O), rows fastest
-      ok = wait(bars.pv_done[w], (uint32_t)(n - 1) & 1u);
-      if (!__all_sync(0xFFFFFFFFu, ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
+      s_mx[n & 1][w][hf][r] = l;
+      meet();
       float* part = a.px_part + (int64_t)((int)blockIdx.x + u) * kPRows * (D + 2);
-      part[w * 128 + r] = ref;
-      part[kPRows + w * 128 + r] = l;
-      float4* po = reinterpret_cast<float4*>(part + 2 * kPRows) + w * 128 + r;
+      if (hf == 0) {
+        part[w * 128 + r] = ref;
+        part[kPRows + w * 128 + r] = l + s_mx[n & 1][w][1][r];
+      }
+      meet();  // read before the next stretch's maxima
+      wait(bars.pv_done[w], (uint32_t)(n - 1) & 1u);
+      tc_fence_after();
+      float4* po = reinterpret_cast<float4*>(part + 2 * kPRows) + (hf * (D / 8)) * kPRows + w * 128 + r;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < D / 2; c += 32) {
         uint32_t y[32];
         tmem_ld32(tO + c, y);
         tmem_wait_ld();
@@ -396,7 +471,7 @@ namespace {
 template <bool F16, int D>
 cudaError_t launch_px(const CUtensorMap& tk, const CUtensorMap& tv, const AttnBatchArgs& a, int grid,
                       cudaStream_t stream) {
-  const size_t smem = 1024 + (size_t)(2 + 2 * kPStages) * 128 * D * 2;
+  const size_t smem = 1024 + (size_t)(2 + 2 * kPStages) * 128 * D * 2 + (size_t)a.n_slots * 4;
   const cudaError_t e = cudaFuncSetAttribute(attn_prefix_kernel<F16, D>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -404,15 +479,14 @@ cudaError_t launch_px(const CUtensorMap& tk, const CUtensorMap& tv, const AttnBa
 }
 }  // namespace
 
-// pairs of a row tile and a head, and the steps of each
+// the most that there can be: every slot with T tokens
 PrefixLine prefix_line(const moe_attn_batch_shape_t* s, int sms) {
   PrefixLine p{};
   const int64_t rows = (int64_t)s->n_slots * s->T * (s->n_q / s->n_kv);
   p.pairs = (int)((rows + kPRows - 1) / kPRows) * s->n_kv;
   p.steps = (s->prefix_blocks + 1) / 2;
-  p.total = (int64_t)p.pairs * p.steps;
-  p.grid = (int)(p.total < sms ? p.total : sms);
-  p.per = p.grid > 0 ? (int)((p.total + p.grid - 1) / p.grid) : 0;
+  const int64_t total = (int64_t)p.pairs * p.steps;
+  p.grid = (int)(total < sms ? total : sms);
   return p;
 }
 // one place per stretch: CTA + pair, both of which grow along the line

@@ -212,19 +212,21 @@ struct AttnBatchArgs {
   uint16_t* o;         // [n_slots][T][n_q][D]
   float* part;         // parts of pairs: per place m[R], l[R], O[D / 4][R][4]
   unsigned* count;     // [n_slots][n_kv]: CTAs of a cut pair that have arrived
+  int pair_cost;       // units of the own line that a pair counts beside its blocks
   int32_t* pair_start; // [n_slots][n_kv]: where the pair starts on the own line
-  int32_t* own_per;    // blocks of that line per CTA
+  int32_t* line;       // [2]: units of the own line and of the shared part's per CTA
+  int32_t* tok_start;  // [n_slots]: tokens (t < n_new) of the slots before
   // the shared part, when attn_prefix_kernel takes it (px_steps > 0): its
   // line of steps and its parts, per place m[256], l[256], O[D / 4][256][4]
-  int px_steps, px_per, px_total;
+  int px_steps;
+  int px_parts;        // about the stretches that a row's steps are cut into
   float* px_part;
   Ctrl* ctrl;
 };
-// Steps of 128 prefix positions for each pair of 256 rows and a head, cut
-// evenly over `grid` CTAs (attn_prefix.cu).
+// Bounds of the shared part's line (attn_prefix.cu): pairs of 256 rows and a
+// head, steps of 128 prefix positions of each, CTAs.
 struct PrefixLine {
-  int pairs, steps, grid, per;
-  int64_t total;
+  int pairs, steps, grid;
 };
 PrefixLine prefix_line(const moe_attn_batch_shape_t* s, int sms);
 size_t prefix_part_floats(const moe_attn_batch_shape_t* s, int sms);

@@ -98,21 +98,21 @@ __device__ __forceinline__ void add_pair(float& s, float& e, float x) {
   e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
   s = t;
 }
-
 // the same of two pairs
 __device__ __forceinline__ void join_pair(float& s, float& e, float s2, float e2) {
   e = __fadd_rn(e, e2);
   add_pair(s, e, s2);
 }
-
-// a weight as a pair (hi, lo): max(p - q, 0), 0 where p - q is not finite
-__device__ __forceinline__ void weight(float p, float q, float& hi, float& lo) {
-  const float d = __fsub_rn(p, q);
-  const float z = __fsub_rn(d, p);
-  const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(d, z)), __fadd_rn(q, z));
-  const bool ok = d > 0.0f && d < INFINITY;
-  hi = ok ? d : 0.0f;
-  lo = ok ? e : 0.0f;
+// two elements at once: p - q without error as d + e, 0 where the difference
+// is not a positive finite number
+__device__ __forceinline__ void weight2(uint64_t p, uint64_t q, uint64_t& d, uint64_t& e) {
+  const uint64_t t = sub2(p, q), z = sub2(t, p);
+  const uint64_t r = sub2(sub2(p, sub2(t, z)), add2(q, z));
+  const uint32_t t0 = (uint32_t)t, t1 = (uint32_t)(t >> 32);
+  const uint32_t r0 = (uint32_t)r, r1 = (uint32_t)(r >> 32);
+  const bool k0 = t0 - 1u < 0x7F7FFFFFu, k1 = t1 - 1u < 0x7F7FFFFFu;  // 0 < bits < infinity's
+  d = pair2(k0 ? t0 : 0u, k1 ? t1 : 0u);
+  e = pair2(k0 ? r0 : 0u, k1 ? r1 : 0u);
 }
 
 // inclusive scan of one double per thread over the CTA (fixed order)
@@ -169,17 +169,23 @@ __device__ __forceinline__ void seg_load(const Rows& r, int V, int sg, float (&p
     for (int k = 0; k < kVPer; ++k) q[k] = v0 + place<DT, Walk>(k, vec) == r.cut ? p[k] : 0.0f;
   }
 }
+// the sum of 16 weights as a pair
 __device__ __forceinline__ void seg_sum(const float (&p)[kVPer], const float (&q)[kVPer], float& s,
                                         float& e) {
-  s = 0.0f;
-  e = 0.0f;
+  uint64_t s2 = 0, e2 = 0;  // even and odd elements
 #pragma unroll
-  for (int k = 0; k < kVPer; ++k) {
-    float hi, lo;
-    weight(p[k], q[k], hi, lo);
-    add_pair(s, e, hi);
-    e = __fadd_rn(e, lo);
+  for (int k = 0; k < kVPer; k += 2) {
+    uint64_t d, r;
+    weight2(pair2(__float_as_uint(p[k]), __float_as_uint(p[k + 1])),
+            pair2(__float_as_uint(q[k]), __float_as_uint(q[k + 1])), d, r);
+    const uint64_t t = add2(s2, d), z = sub2(t, s2);
+    e2 = add2(e2, add2(add2(sub2(s2, sub2(t, z)), sub2(d, z)), r));
+    s2 = t;
   }
+  float s1, e1;
+  unpair2(s2, s, s1);
+  unpair2(e2, e, e1);
+  join_pair(s, e, s1, e1);
 }
 
 template <int DT>
@@ -244,68 +250,96 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
       if (lane == 0) s_seg[k * kVWarps + warp] = make_float2(s, e);
     }
     __syncthreads();
-    for (int j = tid; j < k; j += kVThr) {
-      double sum = 0.0;
-      for (int w = 0; w < kVWarps; ++w) {
-        const float2 v = s_seg[j * kVWarps + w];
-        sum += (double)v.x + (double)v.y;
+    if (warp == 0) {
+      for (int j = lane; j < k; j += 32) {
+        float s = 0.0f, e = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kVWarps; ++w) {
+          const float2 v = s_seg[j * kVWarps + w];
+          join_pair(s, e, v.x, v.y);
+        }
+        a.part[(int64_t)b * S + (int)blockIdx.x + j * C] = (double)s + (double)e;
       }
-      a.part[(int64_t)b * S + (int)blockIdx.x + j * C] = sum;
-    }
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      s_last = atomicAdd(a.done + b, 1u) == (unsigned)C - 1u;
-      if (s_last) a.done[b] = 0u;  // ready for the next call
       __threadfence();
+      __syncwarp();
+      if (lane == 0) {
+        s_last = atomicAdd(a.done + b, 1u) == (unsigned)C - 1u;
+        if (s_last) a.done[b] = 0u;  // ready for the next call
+        __threadfence();
+      }
     }
     __syncthreads();
   }
   if (!s_last) return;
-  // ---- the slot's last CTA: first the segment (one a thread: S <= 256)
-  double mine = tid < S ? __ldcg(a.part + (int64_t)b * S + tid) : 0.0;
-  double inc = block_scan(mine, s_tot);
-  if (tid == kVThr - 1) s_base = inc;
+  // ---- the slot's last CTA: first the segment, a warp with 8 a lane
+  // (S <= 256). The first segment whose running sum passes the threshold;
+  // where none does (u_T not below 1, or a rounding), the last that weighs
+  // anything. s_first: the segment, -1 where nothing weighs anything.
+  const float u_new = __ldg(a.u + (int64_t)b * (T + 1) + T);
+  auto find_segment = [&](const double* part) {
+    double v[8], sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int sg = lane * 8 + k;
+      v[k] = sg < S ? __ldcg(part + sg) : 0.0;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += v[k];
+    double inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const double o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      if (lane >= d) inc += o;
+    }
+    const double total = __shfl_sync(0xFFFFFFFFu, inc, 31), thr = (double)u_new * total;
+    const unsigned past = __ballot_sync(0xFFFFFFFFu, sum > 0.0 && inc > thr);
+    const unsigned some = __ballot_sync(0xFFFFFFFFu, sum > 0.0);
+    if (lane == 0) s_first = -1;
+    __syncwarp();
+    if (some && lane == (past ? __ffs(past) - 1 : 31 - __clz(some))) {
+      double run = inc - sum, base = run;
+      int at = 0;
+      bool passed = false;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (v[k] > 0.0 && !passed) {
+          base = run;
+          run += v[k];
+          at = k;
+          passed = run > thr;
+        }
+      }
+      s_first = lane * 8 + at;
+      s_base = base;
+      s_thr = thr;
+    }
+    __syncwarp();
+  };
+  if (warp == 0) find_segment(a.part + (int64_t)b * S);
   __syncthreads();
-  if (!(s_base > 0.0) && rejected) {
+  if (s_first < 0 && rejected) {
     // nothing left of the difference: the target's own row, summed here (a
     // case of roundings, where q is nowhere below p)
     r.q = nullptr;
     r.cut = -1;
     r.vq = true;
-    mine = 0.0;
     for (int sg = 0; sg < S; ++sg) {
       float p[kVPer], q[kVPer], s, e;
       seg_load<DT, false>(r, V, sg, p, q);
       seg_sum(p, q, s, e);
       const double t = block_scan((double)s + (double)e, s_tot);
-      if (tid == kVThr - 1) s_base = t;
-      __syncthreads();
-      if (tid == sg) mine = s_base;
-      __syncthreads();
+      if (tid == kVThr - 1) a.part[(int64_t)b * S + sg] = t;
     }
-    inc = block_scan(mine, s_tot);
+    __threadfence();
+    __syncthreads();
+    if (warp == 0) find_segment(a.part + (int64_t)b * S);
+    __syncthreads();
   }
-  if (tid == kVThr - 1) {
-    s_thr = (double)__ldg(a.u + (int64_t)b * (T + 1) + T) * inc;
-    s_base = inc;  // the total, for now
-    s_first = kVThr;
-    s_lastpos = -1;
-  }
-  __syncthreads();
-  const double thr = s_thr, total = s_base;
-  // the first segment whose running sum passes the threshold; where none
-  // does (u_T not below 1, or a rounding), the last one that weighs anything
-  if (mine > 0.0) {
-    if (inc > thr) atomicMin(&s_first, tid);
-    atomicMax(&s_lastpos, tid);
-  }
+  const int sg = s_first;
+  const double thr = s_thr, base = s_base;
   __syncthreads();
   int token = -1;
-  if (total > 0.0) {
-    const int sg = s_first < kVThr ? s_first : s_lastpos;
-    __syncthreads();
-    if (tid == sg) s_base = inc - mine;
+  if (sg >= 0) {
     if (tid == 0) {
       s_first = kVThr;
       s_lastpos = -1;
@@ -314,8 +348,7 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
     seg_load<DT, true>(r, V, sg, p, q);
     seg_sum(p, q, s, e);
     const double own = (double)s + (double)e;
-    const double upto = block_scan(own, s_tot);  // synchronises: s_base is set
-    const double incl = s_base + upto;
+    const double incl = base + block_scan(own, s_tot);  // synchronises
     // then the thread, in the same way
     if (own > 0.0) {
       if (incl > thr) atomicMin(&s_first, tid);
@@ -330,10 +363,9 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
       bool passed = false;
 #pragma unroll
       for (int k = 0; k < kVPer; ++k) {
-        float hi, lo;
-        weight(p[k], q[k], hi, lo);
-        if (hi > 0.0f && !passed) {
-          run += (double)hi + (double)lo;
+        const double w = (double)p[k] - (double)q[k];  // exact, as the pairs are
+        if (w > 0.0 && w < INFINITY && !passed) {
+          run += w;
           at = k;
           passed = run > thr;
         }

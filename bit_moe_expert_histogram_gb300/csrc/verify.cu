@@ -10,9 +10,11 @@
 //
 // The token is a whole number that a rounding must not change, so nothing
 // here rounds where it could: u q is formed in 64 bits (two 24-bit factors,
-// exact), p - q as an fp32 pair without error, and the sums as fp32 pairs
-// (value and error term, 48 bits) that are joined in 64 bits. FP64 runs at a
-// few operations a clock per SM here, so it only joins threads.
+// exact), p - q as an fp32 pair without error, and the sums, the threshold
+// and the comparisons are fp32 pairs (value and error term, more than 46
+// bits). FP64 would be shorter to write, but an instruction of it takes a
+// warp about as long as 64 others here: with the search for the token in
+// FP64 the last CTAs of 64 slots ran for 20 us after the others were done.
 //
 // What it has to read is one row of p and one of q per slot: HBM bounds large
 // batches, a chain of dependent accesses small ones. The vocabulary is cut
@@ -98,10 +100,38 @@ __device__ __forceinline__ void add_pair(float& s, float& e, float x) {
   e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
   s = t;
 }
-// the same of two pairs
-__device__ __forceinline__ void join_pair(float& s, float& e, float s2, float e2) {
-  e = __fadd_rn(e, e2);
-  add_pair(s, e, s2);
+// A number as the sum of an fp32 value and an error term.
+struct Pair {
+  float s, e;
+};
+__device__ __forceinline__ void add(Pair& a, const Pair& b) {
+  a.e = __fadd_rn(a.e, b.e);
+  add_pair(a.s, a.e, b.s);
+}
+__device__ __forceinline__ Pair neg(const Pair& a) { return Pair{-a.s, -a.e}; }
+// the error term brought below half a step of the value
+__device__ __forceinline__ Pair tidy(const Pair& a) {
+  const float s = __fadd_rn(a.s, a.e);
+  return Pair{s, __fsub_rn(a.e, __fsub_rn(s, a.s))};
+}
+// a > b, both tidy: the values' difference is exact where it matters
+__device__ __forceinline__ bool above(const Pair& a, const Pair& b) {
+  return __fadd_rn(__fsub_rn(a.s, b.s), __fsub_rn(a.e, b.e)) > 0.0f;
+}
+__device__ __forceinline__ Pair times(float u, const Pair& t) {
+  const float s = __fmul_rn(u, t.s);
+  return tidy(Pair{s, fmaf(u, t.e, fmaf(u, t.s, -s))});
+}
+__device__ __forceinline__ Pair shfl_up(const Pair& a, int d) {
+  return Pair{__shfl_up_sync(0xFFFFFFFFu, a.s, d), __shfl_up_sync(0xFFFFFFFFu, a.e, d)};
+}
+__device__ __forceinline__ Pair warp_scan(Pair v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Pair o = shfl_up(v, d);
+    if (lane >= d) add(v, o);
+  }
+  return v;
 }
 // two elements at once: p - q without error as d + e, 0 where the difference
 // is not a positive finite number
@@ -115,20 +145,19 @@ __device__ __forceinline__ void weight2(uint64_t p, uint64_t q, uint64_t& d, uin
   e = pair2(k0 ? r0 : 0u, k1 ? r1 : 0u);
 }
 
-// inclusive scan of one double per thread over the CTA (fixed order)
-__device__ double block_scan(double v, double* warp_tot) {
+// inclusive scan of one pair per thread over the CTA (fixed order)
+__device__ __forceinline__ Pair block_scan(Pair v, float2* warp_tot) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_scan(v, lane);
+  __syncthreads();
+  if (lane == 31) warp_tot[warp] = make_float2(v.s, v.e);
+  __syncthreads();
+  Pair base{0.0f, 0.0f};
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const double o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-    if (lane >= d) v += o;
-  }
-  __syncthreads();
-  if (lane == 31) warp_tot[warp] = v;
-  __syncthreads();
-  double base = 0.0;
-  for (int w = 0; w < warp; ++w) base += warp_tot[w];
-  return base + v;
+  for (int w = 0; w < kVWarps; ++w)
+    if (w < warp) add(base, Pair{warp_tot[w].x, warp_tot[w].y});
+  add(v, base);
+  return v;
 }
 }  // namespace
 
@@ -141,7 +170,7 @@ struct VerifyArgs {
   int32_t* tokens;
   int32_t* n_acc;
   int T, V, S;     // S segments
-  double* part;    // [slot][S]: sums of the segments' weights
+  float2* part;    // [slot][S]: sums of the segments' weights
   unsigned* done;  // [slot]: CTAs finished
   Ctrl* ctrl;
 };
@@ -170,8 +199,7 @@ __device__ __forceinline__ void seg_load(const Rows& r, int V, int sg, float (&p
   }
 }
 // the sum of 16 weights as a pair
-__device__ __forceinline__ void seg_sum(const float (&p)[kVPer], const float (&q)[kVPer], float& s,
-                                        float& e) {
+__device__ __forceinline__ Pair seg_sum(const float (&p)[kVPer], const float (&q)[kVPer]) {
   uint64_t s2 = 0, e2 = 0;  // even and odd elements
 #pragma unroll
   for (int k = 0; k < kVPer; k += 2) {
@@ -182,18 +210,19 @@ __device__ __forceinline__ void seg_sum(const float (&p)[kVPer], const float (&q
     e2 = add2(e2, add2(add2(sub2(s2, sub2(t, z)), sub2(d, z)), r));
     s2 = t;
   }
-  float s1, e1;
-  unpair2(s2, s, s1);
-  unpair2(e2, e, e1);
-  join_pair(s, e, s1, e1);
+  Pair a, b;
+  unpair2(s2, a.s, b.s);
+  unpair2(e2, a.e, b.e);
+  add(a, b);
+  return a;
 }
 
 template <int DT>
 __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs a) {
   extern __shared__ float2 s_seg[];  // [this CTA's segments][warps]: sums as pairs
   __shared__ int s_i, s_n, s_bad_x, s_last, s_first, s_lastpos;
-  __shared__ double s_tot[kVWarps];
-  __shared__ double s_thr, s_base;
+  __shared__ float2 s_tot[kVWarps];
+  __shared__ Pair s_thr, s_base;
   const int b = blockIdx.y, tid = threadIdx.x, C = gridDim.x;
   const int lane = tid & 31, warp = tid >> 5;
   const int T = a.T, V = a.V, S = a.S;
@@ -241,24 +270,22 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
   {
     int k = 0;
     for (int sg = blockIdx.x; sg < S; sg += C, ++k) {
-      float p[kVPer], q[kVPer], s, e;
+      float p[kVPer], q[kVPer];
       seg_load<DT, false>(r, V, sg, p, q);
-      seg_sum(p, q, s, e);
+      Pair v = seg_sum(p, q);
 #pragma unroll
       for (int d = 16; d; d >>= 1)
-        join_pair(s, e, __shfl_xor_sync(0xFFFFFFFFu, s, d), __shfl_xor_sync(0xFFFFFFFFu, e, d));
-      if (lane == 0) s_seg[k * kVWarps + warp] = make_float2(s, e);
+        add(v, Pair{__shfl_xor_sync(0xFFFFFFFFu, v.s, d), __shfl_xor_sync(0xFFFFFFFFu, v.e, d)});
+      if (lane == 0) s_seg[k * kVWarps + warp] = make_float2(v.s, v.e);
     }
     __syncthreads();
     if (warp == 0) {
       for (int j = lane; j < k; j += 32) {
-        float s = 0.0f, e = 0.0f;
+        Pair sum{0.0f, 0.0f};
 #pragma unroll
-        for (int w = 0; w < kVWarps; ++w) {
-          const float2 v = s_seg[j * kVWarps + w];
-          join_pair(s, e, v.x, v.y);
-        }
-        a.part[(int64_t)b * S + (int)blockIdx.x + j * C] = (double)s + (double)e;
+        for (int w = 0; w < kVWarps; ++w)
+          add(sum, Pair{s_seg[j * kVWarps + w].x, s_seg[j * kVWarps + w].y});
+        a.part[(int64_t)b * S + (int)blockIdx.x + j * C] = make_float2(sum.s, sum.e);
       }
       __threadfence();
       __syncwarp();
@@ -276,37 +303,36 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
   // where none does (u_T not below 1, or a rounding), the last that weighs
   // anything. s_first: the segment, -1 where nothing weighs anything.
   const float u_new = __ldg(a.u + (int64_t)b * (T + 1) + T);
-  auto find_segment = [&](const double* part) {
-    double v[8], sum = 0.0;
+  auto find_segment = [&](const float2* part) {
+    Pair v[8], sum{0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int sg = lane * 8 + k;
-      v[k] = sg < S ? __ldcg(part + sg) : 0.0;
+      const float2 x = sg < S ? __ldcg(part + sg) : make_float2(0.0f, 0.0f);
+      v[k] = Pair{x.x, x.y};
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += v[k];
-    double inc = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const double o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-      if (lane >= d) inc += o;
-    }
-    const double total = __shfl_sync(0xFFFFFFFFu, inc, 31), thr = (double)u_new * total;
-    const unsigned past = __ballot_sync(0xFFFFFFFFu, sum > 0.0 && inc > thr);
-    const unsigned some = __ballot_sync(0xFFFFFFFFu, sum > 0.0);
+    for (int k = 0; k < 8; ++k) add(sum, v[k]);
+    const Pair inc = warp_scan(sum, lane);
+    const Pair total = tidy(Pair{__shfl_sync(0xFFFFFFFFu, inc.s, 31), __shfl_sync(0xFFFFFFFFu, inc.e, 31)});
+    const Pair thr = times(u_new, total);
+    const unsigned past = __ballot_sync(0xFFFFFFFFu, sum.s > 0.0f && above(tidy(inc), thr));
+    const unsigned some = __ballot_sync(0xFFFFFFFFu, sum.s > 0.0f);
     if (lane == 0) s_first = -1;
     __syncwarp();
     if (some && lane == (past ? __ffs(past) - 1 : 31 - __clz(some))) {
-      double run = inc - sum, base = run;
+      Pair run = inc, base;
+      add(run, neg(sum));
+      base = run;
       int at = 0;
       bool passed = false;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (v[k] > 0.0 && !passed) {
+        if (v[k].s > 0.0f && !passed) {
           base = run;
-          run += v[k];
+          add(run, v[k]);
           at = k;
-          passed = run > thr;
+          passed = above(tidy(run), thr);
         }
       }
       s_first = lane * 8 + at;
@@ -324,11 +350,10 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
     r.cut = -1;
     r.vq = true;
     for (int sg = 0; sg < S; ++sg) {
-      float p[kVPer], q[kVPer], s, e;
+      float p[kVPer], q[kVPer];
       seg_load<DT, false>(r, V, sg, p, q);
-      seg_sum(p, q, s, e);
-      const double t = block_scan((double)s + (double)e, s_tot);
-      if (tid == kVThr - 1) a.part[(int64_t)b * S + sg] = t;
+      const Pair t = block_scan(seg_sum(p, q), s_tot);
+      if (tid == kVThr - 1) a.part[(int64_t)b * S + sg] = make_float2(t.s, t.e);
     }
     __threadfence();
     __syncthreads();
@@ -336,7 +361,8 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
     __syncthreads();
   }
   const int sg = s_first;
-  const double thr = s_thr, base = s_base;
+  const Pair thr = s_thr;
+  Pair incl = s_base;
   __syncthreads();
   int token = -1;
   if (sg >= 0) {
@@ -344,30 +370,32 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
       s_first = kVThr;
       s_lastpos = -1;
     }
-    float p[kVPer], q[kVPer], s, e;
+    float p[kVPer], q[kVPer];
     seg_load<DT, true>(r, V, sg, p, q);
-    seg_sum(p, q, s, e);
-    const double own = (double)s + (double)e;
-    const double incl = base + block_scan(own, s_tot);  // synchronises
+    const Pair own = seg_sum(p, q);
+    add(incl, block_scan(own, s_tot));  // synchronises
     // then the thread, in the same way
-    if (own > 0.0) {
-      if (incl > thr) atomicMin(&s_first, tid);
+    if (own.s > 0.0f) {
+      if (above(tidy(incl), thr)) atomicMin(&s_first, tid);
       atomicMax(&s_lastpos, tid);
     }
     __syncthreads();
     if (tid == (s_first < kVThr ? s_first : s_lastpos)) {
       // then the element: the first that passes, or the thread's last that
       // weighs anything
-      double run = incl - own;
+      Pair run = incl;
+      add(run, neg(own));
       int at = 0;
       bool passed = false;
 #pragma unroll
       for (int k = 0; k < kVPer; ++k) {
-        const double w = (double)p[k] - (double)q[k];  // exact, as the pairs are
-        if (w > 0.0 && w < INFINITY && !passed) {
-          run += w;
+        uint64_t d, e;
+        weight2(pair2(__float_as_uint(p[k]), 0u), pair2(__float_as_uint(q[k]), 0u), d, e);
+        const Pair w{__uint_as_float((uint32_t)d), __uint_as_float((uint32_t)e)};
+        if (w.s > 0.0f && !passed) {
+          add(run, w);
           at = k;
-          passed = run > thr;
+          passed = above(tidy(run), thr);
         }
       }
       s_i = sg * kVSeg + tid * kVPer + at;
@@ -413,7 +441,7 @@ cudaError_t launch_verify(const moe_verify_shape_t* s, const void* p, const void
   a.S = (s->V + kVSeg - 1) / kVSeg;
   a.ctrl = reinterpret_cast<Ctrl*>(ws);
   a.done = reinterpret_cast<unsigned*>(ws + 256);
-  a.part = reinterpret_cast<double*>(ws + 256 + (((size_t)s->n_slots * 4 + 255) & ~(size_t)255));
+  a.part = reinterpret_cast<float2*>(ws + 256 + (((size_t)s->n_slots * 4 + 255) & ~(size_t)255));
   // each CTA with as many segments as four CTAs an SM leave it
   const int per_slot = (kVCtas * nsm + s->n_slots - 1) / s->n_slots;
   const int C = per_slot < a.S ? per_slot : a.S;

@@ -18,8 +18,8 @@
 //
 // What it has to read is one row of p and one of q per slot: HBM bounds large
 // batches, a chain of dependent accesses small ones. The vocabulary is cut
-// into segments of 4096; a slot's C CTAs (four per SM over the batch, at most
-// one per segment) each find i by themselves (a warp, one draft a lane: two
+// into segments of 4096; a slot's C CTAs (four or five per SM over the batch,
+// at most one per segment) each find i by themselves (a warp, one draft a lane: two
 // dependent loads), sum their segments and leave the sums in the workspace.
 // The slot's last CTA scans the segments' sums, re-reads the one segment that
 // the threshold falls into (it is in L2) and walks it. A thread's sixteen
@@ -35,7 +35,9 @@ constexpr int kVThr = 256;
 constexpr int kVPer = 16;             // elements per thread
 constexpr int kVSeg = kVThr * kVPer;  // elements per segment
 constexpr int kVWarps = kVThr / 32;
-constexpr int kVCtas = 4;             // CTAs an SM
+// CTAs an SM: as many as the registers of a thread's values allow
+template <int DT>
+constexpr int kVCtas = DT == MOE_DTYPE_FP32 ? 4 : 5;
 
 template <int DT>
 __device__ __forceinline__ float elem(const void* p, int64_t i) {
@@ -52,45 +54,73 @@ __device__ __forceinline__ int place(int k, bool vec) {
   constexpr int kPiece = DT == MOE_DTYPE_FP32 ? 4 : 8;
   return vec ? ((k / kPiece) * kVThr + threadIdx.x) * kPiece + k % kPiece : k * kVThr + threadIdx.x;
 }
+// They stay as they were read (a 16-bit word holds elements k, k + 1) until
+// they are used.
 template <int DT>
-__device__ __forceinline__ void load_piece(const void* p, float* x) {
-  if (DT == MOE_DTYPE_FP32) {
-    const float4 v = __ldg(static_cast<const float4*>(p));
-    x[0] = v.x;
-    x[1] = v.y;
-    x[2] = v.z;
-    x[3] = v.w;
-  } else {
-    const uint4 v = __ldg(static_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = DT == MOE_DTYPE_BF16 ? bf_lo(w[j]) : half_bits_to_float(w[j] & 0xFFFFu);
-      x[2 * j + 1] = DT == MOE_DTYPE_BF16 ? bf_hi(w[j]) : half_bits_to_float(w[j] >> 16);
-    }
-  }
+struct Raw {
+  uint32_t w[DT == MOE_DTYPE_FP32 ? kVPer : kVPer / 2];
+};
+template <int DT>
+__device__ __forceinline__ uint32_t bits(const char* seg, int i) {
+  return DT == MOE_DTYPE_FP32 ? __ldg(reinterpret_cast<const uint32_t*>(seg) + i)
+                              : (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(seg) + i);
 }
 template <int DT, bool Walk>
-__device__ __forceinline__ void load16(const char* seg, int n, bool vec, float (&x)[kVPer]) {
+__device__ __forceinline__ void load16(const char* seg, int n, bool vec, Raw<DT>& x) {
   constexpr int kE = DT == MOE_DTYPE_FP32 ? 4 : 2, kPiece = 16 / kE;
+  const bool full = n >= kVSeg;  // the same for every thread
   if (vec) {
 #pragma unroll
-    for (int k = 0; k < kVPer; k += kPiece) {
-      const int at = place<DT, Walk>(k, true);
-      if (at + kPiece <= n) {
-        load_piece<DT>(seg + (int64_t)at * kE, x + k);
+    for (int k = 0; k < kVPer / kPiece; ++k) {
+      const int at = place<DT, Walk>(k * kPiece, true);
+      if (full || at + kPiece <= n) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(seg + (int64_t)at * kE));
+        x.w[4 * k] = v.x;
+        x.w[4 * k + 1] = v.y;
+        x.w[4 * k + 2] = v.z;
+        x.w[4 * k + 3] = v.w;
       } else {
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) x[k + j] = at + j < n ? elem<DT>(seg, at + j) : 0.0f;
+        for (int j = 0; j < 4; ++j) {
+          if (DT == MOE_DTYPE_FP32) {
+            x.w[4 * k + j] = at + j < n ? bits<DT>(seg, at + j) : 0u;
+          } else {
+            const uint32_t lo = at + 2 * j < n ? bits<DT>(seg, at + 2 * j) : 0u;
+            const uint32_t hi = at + 2 * j + 1 < n ? bits<DT>(seg, at + 2 * j + 1) : 0u;
+            x.w[4 * k + j] = lo | hi << 16;
+          }
+        }
       }
     }
   } else {
+    uint32_t e[kVPer];
+    if (full) {
+#pragma unroll
+      for (int k = 0; k < kVPer; ++k) e[k] = bits<DT>(seg, place<DT, Walk>(k, false));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kVPer; ++k) {
+        const int at = place<DT, Walk>(k, false);
+        e[k] = at < n ? bits<DT>(seg, at) : 0u;
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kVPer; ++k) {
-      const int at = place<DT, Walk>(k, false);
-      x[k] = at < n ? elem<DT>(seg, at) : 0.0f;
+      if (DT == MOE_DTYPE_FP32)
+        x.w[k] = e[k];
+      else if (k & 1)
+        x.w[k / 2] = e[k - 1] | e[k] << 16;
     }
   }
+}
+// elements k and k + 1 (k even) as fp32 numbers
+template <int DT>
+__device__ __forceinline__ uint64_t two(const Raw<DT>& x, int k) {
+  if (DT == MOE_DTYPE_FP32) return pair2(x.w[k], x.w[k + 1]);
+  const uint32_t w = x.w[k / 2];
+  if (DT == MOE_DTYPE_BF16) return pair2(w << 16, w & 0xFFFF0000u);
+  return pair2(__float_as_uint(half_bits_to_float(w & 0xFFFFu)),
+               __float_as_uint(half_bits_to_float(w >> 16)));
 }
 
 // s + e += x without error but for e's own rounding
@@ -133,16 +163,19 @@ __device__ __forceinline__ Pair warp_scan(Pair v, int lane) {
   }
   return v;
 }
-// two elements at once: p - q without error as d + e, 0 where the difference
-// is not a positive finite number
+// two elements at once, 0 where they are not positive finite numbers
+__device__ __forceinline__ uint64_t clean2(uint64_t t) {
+  const uint32_t t0 = (uint32_t)t, t1 = (uint32_t)(t >> 32);
+  // 0 < bits < infinity's
+  return pair2(t0 - 1u < 0x7F7FFFFFu ? t0 : 0u, t1 - 1u < 0x7F7FFFFFu ? t1 : 0u);
+}
+// p - q without error as d + e, 0 where the difference is not a positive
+// finite number
 __device__ __forceinline__ void weight2(uint64_t p, uint64_t q, uint64_t& d, uint64_t& e) {
   const uint64_t t = sub2(p, q), z = sub2(t, p);
   const uint64_t r = sub2(sub2(p, sub2(t, z)), add2(q, z));
-  const uint32_t t0 = (uint32_t)t, t1 = (uint32_t)(t >> 32);
-  const uint32_t r0 = (uint32_t)r, r1 = (uint32_t)(r >> 32);
-  const bool k0 = t0 - 1u < 0x7F7FFFFFu, k1 = t1 - 1u < 0x7F7FFFFFu;  // 0 < bits < infinity's
-  d = pair2(k0 ? t0 : 0u, k1 ? t1 : 0u);
-  e = pair2(k0 ? r0 : 0u, k1 ? r1 : 0u);
+  d = clean2(t);
+  e = pair2((uint32_t)d ? (uint32_t)r : 0u, (uint32_t)(d >> 32) ? (uint32_t)(r >> 32) : 0u);
 }
 
 // inclusive scan of one pair per thread over the CTA (fixed order)
@@ -182,33 +215,48 @@ struct Rows {
   int cut;        // the certain draft's token, which has no weight left; -1: none
   bool vp, vq;    // 16-byte aligned
 };
-// weights (value and error term) of this thread's 16 elements of segment sg
+// this thread's 16 elements of segment sg
 template <int DT, bool Walk>
-__device__ __forceinline__ void seg_load(const Rows& r, int V, int sg, float (&p)[kVPer],
-                                         float (&q)[kVPer]) {
+__device__ __forceinline__ void seg_load(const Rows& r, int V, int sg, Raw<DT>& p, Raw<DT>& q) {
   constexpr int kE = DT == MOE_DTYPE_FP32 ? 4 : 2;
-  const int v0 = sg * kVSeg, n = min(kVSeg, V - v0);
+  const int v0 = sg * kVSeg, n = V - v0;
   // one arrangement for both rows: pieces only where both allow them
   const bool vec = r.vp && r.vq;
   load16<DT, Walk>(r.p + (int64_t)v0 * kE, n, vec, p);
   if (r.q) {
     load16<DT, Walk>(r.q + (int64_t)v0 * kE, n, vec, q);
-  } else {
+  } else if (r.cut >= v0 && r.cut - v0 < kVSeg) {
 #pragma unroll
-    for (int k = 0; k < kVPer; ++k) q[k] = v0 + place<DT, Walk>(k, vec) == r.cut ? p[k] : 0.0f;
+    for (int k = 0; k < kVPer; ++k)
+      if (v0 + place<DT, Walk>(k, vec) == r.cut) {
+        if (DT == MOE_DTYPE_FP32)
+          p.w[k] = 0u;
+        else
+          p.w[k / 2] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+      }
   }
 }
-// the sum of 16 weights as a pair
-__device__ __forceinline__ Pair seg_sum(const float (&p)[kVPer], const float (&q)[kVPer]) {
+// the sum of their weights
+template <int DT>
+__device__ __forceinline__ Pair seg_sum(bool has_q, const Raw<DT>& p, const Raw<DT>& q) {
   uint64_t s2 = 0, e2 = 0;  // even and odd elements
+  if (has_q) {
 #pragma unroll
-  for (int k = 0; k < kVPer; k += 2) {
-    uint64_t d, r;
-    weight2(pair2(__float_as_uint(p[k]), __float_as_uint(p[k + 1])),
-            pair2(__float_as_uint(q[k]), __float_as_uint(q[k + 1])), d, r);
-    const uint64_t t = add2(s2, d), z = sub2(t, s2);
-    e2 = add2(e2, add2(add2(sub2(s2, sub2(t, z)), sub2(d, z)), r));
-    s2 = t;
+    for (int k = 0; k < kVPer; k += 2) {
+      uint64_t d, r;
+      weight2(two<DT>(p, k), two<DT>(q, k), d, r);
+      const uint64_t t = add2(s2, d), z = sub2(t, s2);
+      e2 = add2(e2, add2(add2(sub2(s2, sub2(t, z)), sub2(d, z)), r));
+      s2 = t;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kVPer; k += 2) {
+      const uint64_t d = clean2(two<DT>(p, k));
+      const uint64_t t = add2(s2, d), z = sub2(t, s2);
+      e2 = add2(e2, add2(sub2(s2, sub2(t, z)), sub2(d, z)));
+      s2 = t;
+    }
   }
   Pair a, b;
   unpair2(s2, a.s, b.s);
@@ -218,7 +266,7 @@ __device__ __forceinline__ Pair seg_sum(const float (&p)[kVPer], const float (&q
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVThr, kVCtas<DT>) verify_kernel(const VerifyArgs a) {
   extern __shared__ float2 s_seg[];  // [this CTA's segments][warps]: sums as pairs
   __shared__ int s_i, s_n, s_bad_x, s_last, s_first, s_lastpos;
   __shared__ float2 s_tot[kVWarps];
@@ -270,9 +318,9 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
   {
     int k = 0;
     for (int sg = blockIdx.x; sg < S; sg += C, ++k) {
-      float p[kVPer], q[kVPer];
+      Raw<DT> p, q;
       seg_load<DT, false>(r, V, sg, p, q);
-      Pair v = seg_sum(p, q);
+      Pair v = seg_sum<DT>(r.q != nullptr, p, q);
 #pragma unroll
       for (int d = 16; d; d >>= 1)
         add(v, Pair{__shfl_xor_sync(0xFFFFFFFFu, v.s, d), __shfl_xor_sync(0xFFFFFFFFu, v.e, d)});
@@ -350,9 +398,9 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
     r.cut = -1;
     r.vq = true;
     for (int sg = 0; sg < S; ++sg) {
-      float p[kVPer], q[kVPer];
+      Raw<DT> p, q;
       seg_load<DT, false>(r, V, sg, p, q);
-      const Pair t = block_scan(seg_sum(p, q), s_tot);
+      const Pair t = block_scan(seg_sum<DT>(false, p, q), s_tot);
       if (tid == kVThr - 1) a.part[(int64_t)b * S + sg] = make_float2(t.s, t.e);
     }
     __threadfence();
@@ -370,9 +418,9 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
       s_first = kVThr;
       s_lastpos = -1;
     }
-    float p[kVPer], q[kVPer];
+    Raw<DT> p, q;
     seg_load<DT, true>(r, V, sg, p, q);
-    const Pair own = seg_sum(p, q);
+    const Pair own = seg_sum<DT>(r.q != nullptr, p, q);
     add(incl, block_scan(own, s_tot));  // synchronises
     // then the thread, in the same way
     if (own.s > 0.0f) {
@@ -389,9 +437,13 @@ __global__ void __launch_bounds__(kVThr, kVCtas) verify_kernel(const VerifyArgs 
       bool passed = false;
 #pragma unroll
       for (int k = 0; k < kVPer; ++k) {
-        uint64_t d, e;
-        weight2(pair2(__float_as_uint(p[k]), 0u), pair2(__float_as_uint(q[k]), 0u), d, e);
-        const Pair w{__uint_as_float((uint32_t)d), __uint_as_float((uint32_t)e)};
+        uint64_t d = two<DT>(p, k & ~1), e = 0;
+        if (r.q)
+          weight2(d, two<DT>(q, k & ~1), d, e);
+        else
+          d = clean2(d);
+        const Pair w{__uint_as_float((uint32_t)(d >> (k & 1 ? 32 : 0))),
+                     __uint_as_float((uint32_t)(e >> (k & 1 ? 32 : 0)))};
         if (w.s > 0.0f && !passed) {
           add(run, w);
           at = k;
@@ -442,8 +494,9 @@ cudaError_t launch_verify(const moe_verify_shape_t* s, const void* p, const void
   a.ctrl = reinterpret_cast<Ctrl*>(ws);
   a.done = reinterpret_cast<unsigned*>(ws + 256);
   a.part = reinterpret_cast<float2*>(ws + 256 + (((size_t)s->n_slots * 4 + 255) & ~(size_t)255));
-  // each CTA with as many segments as four CTAs an SM leave it
-  const int per_slot = (kVCtas * nsm + s->n_slots - 1) / s->n_slots;
+  // each CTA with as many segments as the CTAs that fit at once leave it
+  const int ctas = s->dtype == MOE_DTYPE_FP32 ? kVCtas<MOE_DTYPE_FP32> : kVCtas<MOE_DTYPE_BF16>;
+  const int per_slot = (ctas * nsm + s->n_slots - 1) / s->n_slots;
   const int C = per_slot < a.S ? per_slot : a.S;
   const dim3 grid(C, s->n_slots);
   const size_t smem = (size_t)((a.S + C - 1) / C) * kVWarps * sizeof(float2);

@@ -496,7 +496,7 @@ cudaError_t launch_verify(const moe_verify_shape_t* s, const void* p, const void
   a.part = reinterpret_cast<float2*>(ws + 256 + (((size_t)s->n_slots * 4 + 255) & ~(size_t)255));
   // each CTA with as many segments as the CTAs that fit at once leave it
   const int ctas = s->dtype == MOE_DTYPE_FP32 ? kVCtas<MOE_DTYPE_FP32> : kVCtas<MOE_DTYPE_BF16>;
-  const int per_slot = (ctas * nsm + s->n_slots - 1) / s->n_slots;
+  const int per_slot = ctas * nsm / s->n_slots > 1 ? ctas * nsm / s->n_slots : 1;
   const int C = per_slot < a.S ? per_slot : a.S;
   const dim3 grid(C, s->n_slots);
   const size_t smem = (size_t)((a.S + C - 1) / C) * kVWarps * sizeof(float2);

@@ -87,6 +87,15 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* t
       : "memory");
 }
 
+// true in one lane of the warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 struct PrefixBars {
   uint64_t k_full[kPStages], k_empty[kPStages], v_full[kPStages], v_empty[kPStages];
   uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drain;
@@ -242,57 +251,79 @@ __global__ void __launch_bounds__(kPThr, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t id_s = idesc16(F16, 128, kPStep, false), id_o = idesc16(F16, 128, D, true);
-      auto qk = [&](int w, int st) {
+    // The whole warp follows the line and waits; one elected lane issues. Its
+    // descriptors differ by constants, so an instruction costs an addition.
+    constexpr uint32_t id_s = idesc16(F16, 128, kPStep, false), id_o = idesc16(F16, 128, D, true);
+    const uint64_t dq[2] = {smem_desc_sw128(sq), smem_desc_sw128(sq + kTile)};
+    const uint64_t dk[2] = {smem_desc_sw128(sk), smem_desc_sw128(sk + kTile)};
+    const uint64_t dv[2] = {desc_mn_sw128(sv, kHalf), desc_mn_sw128(sv + kTile, kHalf)};
+    const uint32_t b_k_empty[2] = {bar(bars.k_empty[0]), bar(bars.k_empty[1])};
+    const uint32_t b_v_empty[2] = {bar(bars.v_empty[0]), bar(bars.v_empty[1])};
+    auto qk = [&](int w, int st, bool last) {
+      if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-          mma_bf16_ss(tmem + kS + w * 128, smem_desc_sw128(sq + w * kTile + off),
-                      smem_desc_sw128(sk + st * kTile + off), id_s, ks > 0);
+          const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+          mma_bf16_ss(tmem + kS + w * 128, dq[w] + off, dk[st] + off, id_s, ks > 0);
         }
         mma_commit(bar(bars.s_full[w]));
-      };
-      int n = 0, pn[2] = {0, 0}, qn[2] = {0, 0};
-      bool ok = true;
-      for (int f = f0; ok && f < f1;) {
-        const int u = f / steps, j0 = f - u * steps;
-        const int cnt = min(steps - j0, f1 - f);
-        const int tiles = (u / a.n_kv) * kPRows + 128 < R ? 2 : 1;
-        for (int w = 0; ok && w < tiles; ++w) ok = wait(bars.q_ready[w], qn[w]++ & 1u);
-        ok = ok && wait(bars.k_full[n % kPStages], (uint32_t)(n / kPStages) & 1u);
-        if (!ok) break;
-        tc_fence_after();
-        for (int w = 0; w < tiles; ++w) qk(w, n % kPStages);
-        mma_commit(bar(bars.k_empty[n % kPStages]));
-        for (int j = 0; ok && j < cnt; ++j, ++n) {
-          const int st = n % kPStages;
-          ok = wait(bars.v_full[st], (uint32_t)(n / kPStages) & 1u);
-          for (int w = 0; ok && w < tiles; ++w) {
-            ok = wait(bars.p_ready[w], pn[w]++ & 1u);
-            if (!ok) break;
-            tc_fence_after();
+        if (last) mma_commit(b_k_empty[st]);
+      }
+      __syncwarp();
+    };
+    auto pv = [&](int w, int st, bool fresh, bool last) {
+      if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < kPStep / 16; ++ks)
-              mma_bf16_ts(tmem + kO + w * 128, tmem + kS + w * 128 + ks * 8,
-                          desc_mn_sw128(sv + st * kTile + ks * 2048, kHalf), id_o, j > 0 || ks > 0);
-            mma_commit(bar(bars.pv_done[w]));
-            if (w == tiles - 1) mma_commit(bar(bars.v_empty[st]));
-            if (j + 1 < cnt) {
-              const int nx = n + 1;
-              if (w == 0) {
-                ok = wait(bars.k_full[nx % kPStages], (uint32_t)(nx / kPStages) & 1u);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              qk(w, nx % kPStages);
-              if (w == tiles - 1) mma_commit(bar(bars.k_empty[nx % kPStages]));
+        for (int ks = 0; ks < kPStep / 16; ++ks)
+          mma_bf16_ts(tmem + kO + w * 128, tmem + kS + w * 128 + ks * 8, dv[st] + ks * (2048 >> 4),
+                      id_o, ks > 0 || !fresh);
+        mma_commit(bar(bars.pv_done[w]));
+        if (last) mma_commit(b_v_empty[st]);
+      }
+      __syncwarp();
+    };
+    auto wait_all = [&](const uint64_t& b, uint32_t parity) {
+      return __all_sync(0xFFFFFFFFu, wait(b, parity)) != 0;
+    };
+    int n = 0, pn[2] = {0, 0}, qn[2] = {0, 0};
+    bool ok = true;
+    for (int f = f0; ok && f < f1;) {
+      const int u = f / steps, j0 = f - u * steps;
+      const int cnt = min(steps - j0, f1 - f);
+      const int tiles = (u / a.n_kv) * kPRows + 128 < R ? 2 : 1;
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (ok && w < tiles) ok = wait_all(bars.q_ready[w], qn[w]++ & 1u);
+      ok = ok && wait_all(bars.k_full[n & 1], (uint32_t)(n >> 1) & 1u);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (w < tiles) qk(w, n & 1, w == tiles - 1);
+      for (int j = 0; ok && j < cnt; ++j, ++n) {
+        const int st = n & 1, nx = n + 1;
+        ok = wait_all(bars.v_full[st], (uint32_t)(n >> 1) & 1u);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (!ok || w >= tiles) break;
+          ok = wait_all(bars.p_ready[w], pn[w]++ & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          pv(w, st, j == 0, w == tiles - 1);
+          if (j + 1 < cnt) {
+            if (w == 0) {
+              ok = wait_all(bars.k_full[nx & 1], (uint32_t)(nx >> 1) & 1u);
+              if (!ok) break;
+              tc_fence_after();
             }
+            qk(w, nx & 1, w == tiles - 1);
           }
         }
-        f += cnt;
       }
-      // every product has finished before TMEM and shared memory go (bounded)
+      f += cnt;
+    }
+    // every product has finished before TMEM and shared memory go (bounded)
+    if (elect_one()) {
       volatile int never = 0;
       mma_commit(bar(bars.drain));
       mbar_wait(bar(bars.drain), 0, &never);
@@ -308,9 +339,9 @@ __global__ void __launch_bounds__(kPThr, 1)
     const uint32_t tO = tmem + kO + w * 128 + hf * (D / 2) + lanes;
     const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(D)
     const uint64_t sl22 = pair2(__float_as_uint(sl2), __float_as_uint(sl2));
-    // the tile's 256 threads; after a wait that ran out the loops go on to
-    // their end over what is there, so that all of them keep meeting
-    auto meet = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory"); };
+    // the two warps that share 32 rows; after a wait that ran out the loops go
+    // on to their end over what is there, so that both keep meeting
+    auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + w * 4 + quarter) : "memory"); };
     int n = 0;  // this tile's steps so far
     for (int f = f0; f < f1;) {
       const int u = f / steps, j0 = f - u * steps, g = u % a.n_kv;
@@ -398,19 +429,19 @@ __global__ void __launch_bounds__(kPThr, 1)
         }
         const float off = lift<F16>() - (ref == -INFINITY ? 0.0f : ref);
         const uint64_t off2 = pair2(__float_as_uint(off), __float_as_uint(off));
-        uint64_t sum = 0;  // two sums
+        uint64_t sum[2] = {0, 0};  // four sums
 #pragma unroll
         for (int c = 0; c < kBlk; c += 2) {
           float e0, e1;
           unpair2(fma2(pair2(x[c], x[c + 1]), sl22, off2), e0, e1);
           e0 = ex2(e0);
           e1 = ex2(e1);
-          sum = add2(sum, pair2(__float_as_uint(e0), __float_as_uint(e1)));
+          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair2(__float_as_uint(e0), __float_as_uint(e1)));
           x[c >> 1] = pack2<F16>(e0, e1);
         }
         tmem_st32(tS + hf * 32, x);
         float t0, t1;
-        unpair2(sum, t0, t1);
+        unpair2(add2(sum[0], sum[1]), t0, t1);
         l += t0 + t1;
         tmem_wait_st();
         tc_fence_before();

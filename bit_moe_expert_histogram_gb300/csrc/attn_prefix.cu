@@ -254,20 +254,18 @@ __global__ void __launch_bounds__(kPThr, 1)
     // The whole warp follows the line and waits; one elected lane issues. Its
     // descriptors differ by constants, so an instruction costs an addition.
     constexpr uint32_t id_s = idesc16(F16, 128, kPStep, false), id_o = idesc16(F16, 128, D, true);
-    const uint64_t dq[2] = {smem_desc_sw128(sq), smem_desc_sw128(sq + kTile)};
-    const uint64_t dk[2] = {smem_desc_sw128(sk), smem_desc_sw128(sk + kTile)};
-    const uint64_t dv[2] = {desc_mn_sw128(sv, kHalf), desc_mn_sw128(sv + kTile, kHalf)};
-    const uint32_t b_k_empty[2] = {bar(bars.k_empty[0]), bar(bars.k_empty[1])};
-    const uint32_t b_v_empty[2] = {bar(bars.v_empty[0]), bar(bars.v_empty[1])};
+    constexpr uint32_t kTileD = kTile >> 4;  // in a descriptor's address units
+    const uint64_t dq = smem_desc_sw128(sq), dk = smem_desc_sw128(sk), dv = desc_mn_sw128(sv, kHalf);
+    const uint32_t b_k_empty = bar(bars.k_empty[0]), b_v_empty = bar(bars.v_empty[0]);
     auto qk = [&](int w, int st, bool last) {
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
-          mma_bf16_ss(tmem + kS + w * 128, dq[w] + off, dk[st] + off, id_s, ks > 0);
+          mma_bf16_ss(tmem + kS + w * 128, dq + w * kTileD + off, dk + st * kTileD + off, id_s, ks > 0);
         }
         mma_commit(bar(bars.s_full[w]));
-        if (last) mma_commit(b_k_empty[st]);
+        if (last) mma_commit(b_k_empty + 8 * st);
       }
       __syncwarp();
     };
@@ -275,10 +273,10 @@ __global__ void __launch_bounds__(kPThr, 1)
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < kPStep / 16; ++ks)
-          mma_bf16_ts(tmem + kO + w * 128, tmem + kS + w * 128 + ks * 8, dv[st] + ks * (2048 >> 4),
+          mma_bf16_ts(tmem + kO + w * 128, tmem + kS + w * 128 + ks * 8, dv + st * kTileD + ks * (2048 >> 4),
                       id_o, ks > 0 || !fresh);
         mma_commit(bar(bars.pv_done[w]));
-        if (last) mma_commit(b_v_empty[st]);
+        if (last) mma_commit(b_v_empty + 8 * st);
       }
       __syncwarp();
     };

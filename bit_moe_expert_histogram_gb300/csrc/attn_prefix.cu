@@ -11,8 +11,8 @@
 // SM; each stretch leaves (m, l, O) of its 256 rows in the workspace, where
 // attn_join_kernel joins them with the slots' own positions.
 //
-// Warps: 0 loads K and V (TMA, two stages each of 128 positions), 1 issues
-// the products, 4-11 and 12-19 do the softmax of the two row tiles, half a
+// Warps: 0 loads K and V (TMA, two stages each of 128 positions), 1 and 2
+// issue the products of the two row tiles, 4-11 and 12-19 do the softmax of the two row tiles, half a
 // row a thread (the halves exchange their maxima through shared memory): with
 // a whole row a thread the chain load, maximum, exponentials, store took
 // longer than the other tile's products (282 us instead of 204 on 16384 rows
@@ -98,7 +98,7 @@ __device__ __forceinline__ bool elect_one() {
 
 struct PrefixBars {
   uint64_t k_full[kPStages], k_empty[kPStages], v_full[kPStages], v_empty[kPStages];
-  uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drain;
+  uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], turn[2], drain[2];
 };
 }  // namespace
 
@@ -135,17 +135,18 @@ __global__ void __launch_bounds__(kPThr, 1)
   if (tid == 0) {
     for (int i = 0; i < kPStages; ++i) {
       mbar_init(bar(bars.k_full[i]), 1);
-      mbar_init(bar(bars.k_empty[i]), 1);
+      mbar_init(bar(bars.k_empty[i]), 2);  // both tiles' products
       mbar_init(bar(bars.v_full[i]), 1);
-      mbar_init(bar(bars.v_empty[i]), 1);
+      mbar_init(bar(bars.v_empty[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(bars.q_ready[i]), 8);  // the tile's warps
       mbar_init(bar(bars.s_full[i]), 1);
       mbar_init(bar(bars.p_ready[i]), 8);
       mbar_init(bar(bars.pv_done[i]), 1);
+      mbar_init(bar(bars.turn[i]), 1);
+      mbar_init(bar(bars.drain[i]), 1);
     }
-    mbar_init(bar(bars.drain), 1);
     s_abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
@@ -250,81 +251,94 @@ __global__ void __launch_bounds__(kPThr, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // The whole warp follows the line and waits; one elected lane issues. Its
-    // descriptors differ by constants, so an instruction costs an addition.
+  } else if (warp == 1 || warp == 2) {
+    // The products of row tile w. The whole warp follows the line and waits;
+    // one elected lane issues. Its descriptors differ by constants, so an
+    // instruction costs an addition. The two warps take turns: with the
+    // tiles' products mixed both tiles would wait for all of them, then both
+    // do their softmax at once. (One warp for both tiles adds its waits to the
+    // tensor core's time.)
+    const int w = warp - 1;
     constexpr uint32_t id_s = idesc16(F16, 128, kPStep, false), id_o = idesc16(F16, 128, D, true);
     constexpr uint32_t kTileD = kTile >> 4;  // in a descriptor's address units
-    const uint64_t dq = smem_desc_sw128(sq), dk = smem_desc_sw128(sk), dv = desc_mn_sw128(sv, kHalf);
+    const uint64_t dq = smem_desc_sw128(sq + w * kTile), dk = smem_desc_sw128(sk);
+    const uint64_t dv = desc_mn_sw128(sv, kHalf);
+    const uint32_t tS = tmem + kS + w * 128, tO = tmem + kO + w * 128;
     const uint32_t b_k_empty = bar(bars.k_empty[0]), b_v_empty = bar(bars.v_empty[0]);
-    auto qk = [&](int w, int st, bool last) {
+    auto qk = [&](int st) {
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
-          mma_bf16_ss(tmem + kS + w * 128, dq + w * kTileD + off, dk + st * kTileD + off, id_s, ks > 0);
+          mma_bf16_ss(tS, dq + off, dk + st * kTileD + off, id_s, ks > 0);
         }
         mma_commit(bar(bars.s_full[w]));
-        if (last) mma_commit(b_k_empty + 8 * st);
+        mma_commit(b_k_empty + 8 * st);
       }
       __syncwarp();
     };
-    auto pv = [&](int w, int st, bool fresh, bool last) {
+    auto pv = [&](int st, bool fresh) {
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < kPStep / 16; ++ks)
-          mma_bf16_ts(tmem + kO + w * 128, tmem + kS + w * 128 + ks * 8, dv + st * kTileD + ks * (2048 >> 4),
-                      id_o, ks > 0 || !fresh);
+          mma_bf16_ts(tO, tS + ks * 8, dv + st * kTileD + ks * (2048 >> 4), id_o,
+                      ks > 0 || !fresh);
         mma_commit(bar(bars.pv_done[w]));
-        if (last) mma_commit(b_v_empty + 8 * st);
+        mma_commit(b_v_empty + 8 * st);
       }
       __syncwarp();
     };
     auto wait_all = [&](const uint64_t& b, uint32_t parity) {
       return __all_sync(0xFFFFFFFFu, wait(b, parity)) != 0;
     };
-    int n = 0, pn[2] = {0, 0}, qn[2] = {0, 0};
+    int n = 0, pn = 0, qn = 0, tn = 0;
     bool ok = true;
     for (int f = f0; ok && f < f1;) {
       const int u = f / steps, j0 = f - u * steps;
       const int cnt = min(steps - j0, f1 - f);
-      const int tiles = (u / a.n_kv) * kPRows + 128 < R ? 2 : 1;
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-        if (ok && w < tiles) ok = wait_all(bars.q_ready[w], qn[w]++ & 1u);
-      ok = ok && wait_all(bars.k_full[n & 1], (uint32_t)(n >> 1) & 1u);
+      f += cnt;
+      const bool both = (u / a.n_kv) * kPRows + 128 < R;
+      auto take = [&] {  // tile 0 has the first turn
+        return !both || wait_all(bars.turn[w], (uint32_t)(tn++ & 1) ^ (w == 0 ? 1u : 0u));
+      };
+      auto pass = [&] {
+        if (both && lane == 0) mbar_arrive(bar(bars.turn[1 - w]));
+        __syncwarp();
+      };
+      if (w == 1 && !both) {
+        // no such tile in the last pair: its stages go back as they come
+        for (int j = 0; ok && j < cnt; ++j, ++n) {
+          ok = wait_all(bars.k_full[n & 1], (uint32_t)(n >> 1) & 1u);
+          if (ok && lane == 0) mbar_arrive(b_k_empty + 8 * (n & 1));
+          ok = ok && wait_all(bars.v_full[n & 1], (uint32_t)(n >> 1) & 1u);
+          if (ok && lane == 0) mbar_arrive(b_v_empty + 8 * (n & 1));
+          __syncwarp();
+        }
+        continue;
+      }
+      ok = wait_all(bars.q_ready[w], qn++ & 1u) &&
+           wait_all(bars.k_full[n & 1], (uint32_t)(n >> 1) & 1u) && take();
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-        if (w < tiles) qk(w, n & 1, w == tiles - 1);
+      qk(n & 1);
+      pass();
       for (int j = 0; ok && j < cnt; ++j, ++n) {
-        const int st = n & 1, nx = n + 1;
-        ok = wait_all(bars.v_full[st], (uint32_t)(n >> 1) & 1u);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (!ok || w >= tiles) break;
-          ok = wait_all(bars.p_ready[w], pn[w]++ & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          pv(w, st, j == 0, w == tiles - 1);
-          if (j + 1 < cnt) {
-            if (w == 0) {
-              ok = wait_all(bars.k_full[nx & 1], (uint32_t)(nx >> 1) & 1u);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            qk(w, nx & 1, w == tiles - 1);
-          }
-        }
+        const int nx = n + 1;
+        ok = wait_all(bars.v_full[n & 1], (uint32_t)(n >> 1) & 1u) &&
+             (j + 1 == cnt || wait_all(bars.k_full[nx & 1], (uint32_t)(nx >> 1) & 1u)) &&
+             wait_all(bars.p_ready[w], pn++ & 1u) && take();
+        if (!ok) break;
+        tc_fence_after();
+        pv(n & 1, j == 0);
+        if (j + 1 < cnt) qk(nx & 1);
+        pass();
       }
-      f += cnt;
     }
     // every product has finished before TMEM and shared memory go (bounded)
     if (elect_one()) {
       volatile int never = 0;
-      mma_commit(bar(bars.drain));
-      mbar_wait(bar(bars.drain), 0, &never);
+      mma_commit(bar(bars.drain[w]));
+      mbar_wait(bar(bars.drain[w]), 0, &never);
     }
     __syncwarp();
   } else if (warp >= 4) {

@@ -16,7 +16,10 @@
 // slots they belong to, so uneven lengths leave no CTA idle. The
 // (A pair counts pair_cost units more than its blocks: its start and end cost
 // about that many blocks' time, so a CTA of many short slots gets fewer
-// blocks.) The T * n_q / n_kv <= 64 query rows of a pair are the M rows of mma.sync tiles
+// blocks. Measured with 0, 1, 2, 3, 4, 6: 32.5, 29.7, 24.4, 21.9, 22.7, 21.7
+// us for 33 slots of up to 5000 positions with D = 64; 205, 196, 189, 186,
+// 184, 186 for 256 slots of up to 1500 with D = 128 and 32 rows a pair; 32.9,
+// 30.8, 30.5, 30.8, 31.1, 31.3 for 48 slots of up to 777 with 8 rows.) The T * n_q / n_kv <= 64 query rows of a pair are the M rows of mma.sync tiles
 // (16 rows; 1, 2 or 4 tiles), so each key and value is read once per slot. A
 // warp of its own keeps a TMA ring of blocks full (64 rows x 64 elements per
 // box, 128-byte swizzle) that runs on across pairs; the four others only meet
@@ -77,23 +80,31 @@ __device__ __forceinline__ void store4(uint16_t* to, const float4& v, float l) {
 }
 }  // namespace
 
-// Joins parts in order: each batch of up to kBatch is fetched as a whole.
+// Joins parts 0 .. n - 1 in order: each batch of up to kBatch is fetched as a
+// whole. at(c, base, ld, row): where part c lies (m at base[row], l at
+// base[ld + row], O[d][row] from base + 2 ld on).
 struct Joined {
   float M, L;
   float4 o;
 };
 template <int kBatch, typename At>
-__device__ __forceinline__ void join_parts(Joined& j, int n, int rows_ld, int r, int d, At at) {
+__device__ __forceinline__ void join_parts(Joined& j, int n, int d, At at) {
   for (int c0 = 0; c0 < n; c0 += kBatch) {
     float m[kBatch], l[kBatch];
     float4 v[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const bool in = c0 + k < n;
-      const float* p = at(in ? c0 + k : c0);
-      m[k] = in ? __ldcg(p + r) : -INFINITY;
-      l[k] = __ldcg(p + rows_ld + r);
-      v[k] = __ldcg(reinterpret_cast<const float4*>(p + 2 * rows_ld) + d * rows_ld + r);
+      m[k] = -INFINITY;
+      l[k] = 0.0f;
+      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (c0 + k < n) {
+        const float* p;
+        int ld, row;
+        at(c0 + k, p, ld, row);
+        m[k] = __ldcg(p + row);
+        l[k] = __ldcg(p + ld + row);
+        v[k] = __ldcg(reinterpret_cast<const float4*>(p + 2 * ld) + d * ld + row);
+      }
     }
     float nM = j.M;
 #pragma unroll
@@ -521,8 +532,10 @@ __global__ void __launch_bounds__(kOAll, 2)
             for (int i = tid; i < rows * (D / 4); i += kOThr) {
               const int d = i / rows, r = i - d * rows;
               Joined jn{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-              join_parts<4>(jn, c1 - c0 + 1, kR, r, d, [&](int c) {
-                return a.part + (int64_t)(c0 + c + pair) * kR * (D + 2);
+              join_parts<4>(jn, c1 - c0 + 1, d, [&](int c, const float*& p, int& ld, int& row) {
+                p = a.part + (int64_t)(c0 + c + pair) * kR * (D + 2);
+                ld = kR;
+                row = r;
               });
               store4<F16>(out_row(a, s, g, G, r, D) + 4 * d, jn.o, jn.L);
             }
@@ -570,15 +583,16 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnBatchArgs a, i
     const int row = tok0 * G + r, u = (row >> 8) * a.n_kv + g, rr = row & 255;
     const int x0 = u * a.px_steps / px_per, x1 = (u * a.px_steps + a.px_steps - 1) / px_per;
     const int nx = x1 - x0 + 1;
-    join_parts<4>(jn, (nx - ln + kLanes - 1) / kLanes, 256, rr, d, [&](int c) {
-      return a.px_part + (int64_t)(x0 + c * kLanes + ln + u) * 256 * (D + 2);
-    });
-    const int c0 = pb / own_per, n = (pb + sp.blocks - 1) / own_per - c0 + 1;
-    // the own parts follow: the next lane's turn
-    const int l0 = (ln + kLanes - nx % kLanes) % kLanes;
-    join_parts<2>(jn, (n - l0 + kLanes - 1) / kLanes, kR, r, d, [&](int c) {
-      return a.part + (int64_t)(c0 + c * kLanes + l0 + pair) * kR * (D + 2);
-    });
+    const int c0 = pb / own_per, n = nx + (pb + sp.blocks - 1) / own_per - c0 + 1;
+    join_parts<kLanes == 1 ? 6 : 3>(jn, (n - ln + kLanes - 1) / kLanes, d,
+                  [&](int c, const float*& p, int& ld, int& prow) {
+                    const int k = c * kLanes + ln;
+                    const bool px = k < nx;
+                    ld = px ? 256 : kR;
+                    prow = px ? rr : r;
+                    p = px ? a.px_part + (int64_t)(x0 + k + u) * 256 * (D + 2)
+                           : a.part + (int64_t)(c0 + k - nx + pair) * kR * (D + 2);
+                  });
   }
   if (kLanes > 1) {
     s_o[ln][item] = jn.o;
@@ -679,7 +693,7 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
   a.pair_start = reinterpret_cast<int32_t*>(ws + 512 + pairs);
   a.tok_start = reinterpret_cast<int32_t*>(ws + 512 + 2 * pairs);
   a.part = reinterpret_cast<float*>(ws + 512 + 2 * pairs + round256((size_t)s->n_slots * 4));
-  a.pair_cost = s->D == 64 ? 2 : 1;
+  a.pair_cost = s->D == 64 || own_tiles(s) > 1 ? 4 : 2;
   a.n_slots = s->n_slots;
   a.T = s->T;
   a.n_q = s->n_q;

@@ -575,16 +575,16 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnBatchArgs a, i
   const int item = threadIdx.x % kItems, ln = threadIdx.x / kItems;
   const int i = blockIdx.y * kItems + item;
   const int d = i / rows, r = i - d * rows, t = r / G;
-  const int own_per = __ldg(a.line), px_per = __ldg(a.line + 1);
+  const int own_per = __ldg(a.line), px_per = __ldg(a.line + 1), px_len = __ldg(a.line + 2);
   const int pb = __ldg(a.pair_start + pair), tok0 = __ldg(a.tok_start + s);
   const SlotSpan sp = slot_span(a, s);
   Joined jn{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   if (i < rows * (D / 4) && t < sp.n_new && sp.len - sp.n_new + t >= 0) {
     const int row = tok0 * G + r, u = (row >> 8) * a.n_kv + g, rr = row & 255;
-    const int x0 = u * a.px_steps / px_per, x1 = (u * a.px_steps + a.px_steps - 1) / px_per;
+    const int x0 = u * px_len / px_per, x1 = (u * px_len + a.px_steps - 1) / px_per;
     const int nx = x1 - x0 + 1;
     const int c0 = pb / own_per, n = nx + (pb + sp.blocks - 1) / own_per - c0 + 1;
-    join_parts<kLanes == 1 ? 6 : 3>(jn, (n - ln + kLanes - 1) / kLanes, d,
+    join_parts<6>(jn, (n - ln + kLanes - 1) / kLanes, d,
                   [&](int c, const float*& p, int& ld, int& prow) {
                     const int k = c * kLanes + ln;
                     const bool px = k < nx;
@@ -661,9 +661,9 @@ cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const AttnB
   if (e != cudaSuccess) return e;
   e = launch_pdl(attn_own_kernel<F16, D, MT>, dim3(grid), dim3(kOAll), smem, stream, tk, tv, a);
   if (e != cudaSuccess || a.px_steps == 0) return e;
-  // a lane for about four parts of a row
+  // a thread fetches six parts at once
   if (a.px_parts <= 6) return launch_join<F16, D, 1>(a, MT * 16, stream);
-  if (a.px_parts <= 16) return launch_join<F16, D, 4>(a, MT * 16, stream);
+  if (a.px_parts <= 48) return launch_join<F16, D, 4>(a, MT * 16, stream);
   return launch_join<F16, D, 16>(a, MT * 16, stream);
 }
 template <bool F16, int D>
@@ -701,20 +701,24 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
   a.max_blocks = s->max_blocks;
   a.prefix_blocks = s->prefix_blocks;
   const int sms = nsm < kMostSms ? nsm : kMostSms;
+  int px_grid = 0;
   a.first = 0;
   a.px_steps = 0;
   if (s->prefix_blocks > 0 && s->n_slots > 1) {
     const PrefixLine line = prefix_line(s, sms);
     a.first = s->prefix_blocks;
     a.px_steps = line.steps;
-    a.px_parts = (line.grid + line.pairs - 1) / line.pairs + 1;
+    a.px_parts = (line.steps + line.per - 1) / line.per + 1;
+    px_grid = line.grid;
     a.px_part = a.part + own_part_bytes(s) / 4;
     const cudaError_t e = launch_attn_prefix(s, tk, tv, a, line.grid, stream);
     if (e != cudaSuccess) return e;
   }
-  // two CTAs an SM, and no more than there can be blocks
+  // two CTAs an SM, and no more than there can be blocks; beside a shared part
+  // that leaves SMs over, as many as fit beside it, so that both run at once
   const int64_t most = (int64_t)s->n_slots * s->n_kv * s->max_blocks;
-  const int grid = most < 2 * sms ? (int)most : 2 * sms;
+  const int beside = 2 * (px_grid * 5 <= sms * 3 ? sms - px_grid : sms);
+  const int grid = most < beside ? (int)most : beside;
   const int mt = own_tiles(s);
   if (s->dtype == MOE_DTYPE_FP16)
     return s->D == 64 ? launch_own_mt<true, 64>(mt, tk, tv, a, grid, stream)

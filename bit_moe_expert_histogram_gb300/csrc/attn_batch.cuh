@@ -8,6 +8,33 @@ namespace moe {
 
 constexpr int kBlk = 64;  // positions per page
 
+// How `pairs` pairs of `steps` steps go over `ctas` CTAs. Cut evenly, most
+// CTAs get the end of one pair and the start of the next, and a stretch costs
+// about kStretch steps beside its own (queries in, O out); cut pair by pair
+// every CTA has one stretch but some CTAs may be left over. The shorter way
+// is taken; a stretch of fewer than two steps would be mostly cost.
+__host__ __device__ inline PrefixLine prefix_cut(int pairs, int steps, int ctas) {
+  constexpr int kStretch = 3;
+  PrefixLine p;
+  p.pairs = pairs;
+  p.steps = steps;
+  p.len = steps;
+  p.per = (int)(((int64_t)pairs * steps + ctas - 1) / ctas);
+  p.grid = ctas;
+  if (pairs > 0 && pairs <= ctas) {
+    int per = (steps + ctas / pairs - 1) / (ctas / pairs);
+    per = per < 2 ? 2 : per;
+    if (per <= p.per + kStretch) {
+      const int cuts = (steps + per - 1) / per;
+      p.per = per;
+      p.len = cuts * per;
+      p.grid = pairs * cuts;
+    }
+  }
+  if (p.per < 1) p.per = 1;
+  return p;
+}
+
 // New tokens of a slot, brought into range.
 __device__ __forceinline__ int slot_tokens(const AttnBatchArgs& a, int s) {
   return a.n_new ? min(max(__ldg(a.n_new + s), 0), a.T) : a.T;

@@ -7,8 +7,8 @@
 // large products per key/value head on the tensor cores (tcgen05): tiles of
 // 256 rows (two of M = 128) against steps of 128 positions (two pages),
 // S = Q K^T into TMEM, softmax weights P back into TMEM over S, O += P V.
-// The (tile, head) pairs' steps lie on one line cut evenly over one CTA per
-// SM; each stretch leaves (m, l, O) of its 256 rows in the workspace, where
+// The (tile, head) pairs' steps lie on one line cut over one CTA per SM
+// (prefix_cut); each stretch leaves (m, l, O) of its 256 rows in the workspace, where
 // attn_join_kernel joins them with the slots' own positions.
 //
 // Warps: 0 loads K and V (TMA, two stages each of 128 positions), 1 and 2
@@ -192,10 +192,13 @@ __global__ void __launch_bounds__(kPThr, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const int R = n_tok * G, steps = a.px_steps;
-  const int total = (R + kPRows - 1) / kPRows * a.n_kv * steps;
-  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-  const int f0 = (int)blockIdx.x * per, f1 = min(f0 + per, total);
-  if (blockIdx.x == 0 && tid == 0) a.line[1] = per;
+  const PrefixLine line = prefix_cut((R + kPRows - 1) / kPRows * a.n_kv, steps, (int)gridDim.x);
+  const int plen = line.len;
+  const int f0 = (int)blockIdx.x * line.per, f1 = min(f0 + line.per, line.pairs * plen);
+  if (blockIdx.x == 0 && tid == 0) {
+    a.line[1] = line.per;
+    a.line[2] = plen;
+  }
   volatile int* abort = &s_abort;
   // a bounded wait; one that runs out is recorded and ends every role
   auto wait = [&](const uint64_t& b, uint32_t parity) {
@@ -203,12 +206,14 @@ __global__ void __launch_bounds__(kPThr, 1)
     if (atomicCAS(&s_abort, 0, 1) == 0) set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, -2);
     return false;
   };
-  // the line's stretch f0 .. f1: pair u (tile u / n_kv, head u % n_kv) by pair
+  // the line's stretch f0 .. f1, pair u (tile u / n_kv, head u % n_kv) by
+  // pair; a pair's units from `steps` on are nothing
   if (warp == 0) {
     if (lane == 0) {
       int n = 0;  // steps loaded
-      for (int f = f0; f < f1; ++f, ++n) {
-        const int u = f / steps, j = f - u * steps, g = u % a.n_kv;
+      for (int f = f0; f < f1; ++f) {
+        const int u = f / plen, j = f - u * plen, g = u % a.n_kv;
+        if (j >= steps) continue;
         const int st = n % kPStages;
         const uint32_t ph = (uint32_t)(n / kPStages) & 1u;
         int row[2];
@@ -242,6 +247,7 @@ __global__ void __launch_bounds__(kPThr, 1)
           for (int h = 0; h < kHalves; ++h)
             tma_load_rows(sv + st * kTile + h * kHalf + i * (kBlk * 128), &tm_v, h * 64, row[i],
                           bar(bars.v_full[st]));
+        ++n;
       }
       // what is still in flight lands before the CTA goes (bounded)
       volatile int never = 0;
@@ -294,9 +300,10 @@ __global__ void __launch_bounds__(kPThr, 1)
     int n = 0, pn = 0, qn = 0, tn = 0;
     bool ok = true;
     for (int f = f0; ok && f < f1;) {
-      const int u = f / steps, j0 = f - u * steps;
+      const int u = f / plen, j0 = f - u * plen;
       const int cnt = min(steps - j0, f1 - f);
-      f += cnt;
+      f = cnt < 1 || j0 + cnt == steps ? (u + 1) * plen : f + cnt;
+      if (cnt < 1) continue;
       const bool both = (u / a.n_kv) * kPRows + 128 < R;
       auto take = [&] {  // tile 0 has the first turn
         return !both || wait_all(bars.turn[w], (uint32_t)(tn++ & 1) ^ (w == 0 ? 1u : 0u));
@@ -356,9 +363,10 @@ __global__ void __launch_bounds__(kPThr, 1)
     auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + w * 4 + quarter) : "memory"); };
     int n = 0;  // this tile's steps so far
     for (int f = f0; f < f1;) {
-      const int u = f / steps, j0 = f - u * steps, g = u % a.n_kv;
+      const int u = f / plen, j0 = f - u * plen, g = u % a.n_kv;
       const int cnt = min(steps - j0, f1 - f);
-      f += cnt;
+      f = cnt < 1 || j0 + cnt == steps ? (u + 1) * plen : f + cnt;
+      if (cnt < 1) continue;
       const int row0 = (u / a.n_kv) * kPRows + w * 128;
       if (row0 >= R) continue;  // the last tile pair has one tile only
       // ---- this row: its query into shared memory, its last position
@@ -505,18 +513,12 @@ cudaError_t launch_px(const CUtensorMap& tk, const CUtensorMap& tv, const AttnBa
 
 // the most that there can be: every slot with T tokens
 PrefixLine prefix_line(const moe_attn_batch_shape_t* s, int sms) {
-  PrefixLine p{};
   const int64_t rows = (int64_t)s->n_slots * s->T * (s->n_q / s->n_kv);
-  p.pairs = (int)((rows + kPRows - 1) / kPRows) * s->n_kv;
-  p.steps = (s->prefix_blocks + 1) / 2;
-  const int64_t total = (int64_t)p.pairs * p.steps;
-  p.grid = (int)(total < sms ? total : sms);
-  return p;
+  return prefix_cut((int)((rows + kPRows - 1) / kPRows) * s->n_kv, (s->prefix_blocks + 1) / 2, sms);
 }
 // one place per stretch: CTA + pair, both of which grow along the line
 size_t prefix_part_floats(const moe_attn_batch_shape_t* s, int sms) {
-  const PrefixLine p = prefix_line(s, sms);
-  return (size_t)(p.grid + p.pairs) * kPRows * (s->D + 2);
+  return (size_t)(sms + prefix_line(s, sms).pairs) * kPRows * (s->D + 2);
 }
 
 cudaError_t launch_attn_prefix(const moe_attn_batch_shape_t* s, const CUtensorMap& tk,

@@ -214,19 +214,20 @@ struct AttnBatchArgs {
   unsigned* count;     // [n_slots][n_kv]: CTAs of a cut pair that have arrived
   int pair_cost;       // units of the own line that a pair counts beside its blocks
   int32_t* pair_start; // [n_slots][n_kv]: where the pair starts on the own line
-  int32_t* line;       // [2]: units of the own line and of the shared part's per CTA
+  int32_t* line;       // [3]: units per CTA of the own line and of the shared part's, and a
+                       // pair's length on that
   int32_t* tok_start;  // [n_slots]: tokens (t < n_new) of the slots before
   // the shared part, when attn_prefix_kernel takes it (px_steps > 0): its
   // line of steps and its parts, per place m[256], l[256], O[D / 4][256][4]
   int px_steps;
-  int px_parts;        // about the stretches that a row's steps are cut into
+  int px_parts;        // the stretches that a row's steps are cut into, at most about
   float* px_part;
   Ctrl* ctrl;
 };
-// Bounds of the shared part's line (attn_prefix.cu): pairs of 256 rows and a
-// head, steps of 128 prefix positions of each, CTAs.
+// The shared part's line (attn_prefix.cu): pairs of 256 rows and a head, each
+// with `steps` steps of 128 prefix positions on `len` units; `per` units a CTA.
 struct PrefixLine {
-  int pairs, steps, grid;
+  int pairs, steps, len, per, grid;
 };
 PrefixLine prefix_line(const moe_attn_batch_shape_t* s, int sms);
 size_t prefix_part_floats(const moe_attn_batch_shape_t* s, int sms);

@@ -24,13 +24,13 @@
 // warp of its own keeps a TMA ring of blocks full (64 rows x 64 elements per
 // box, 128-byte swizzle) that runs on across pairs; the four others only meet
 // at the end of a pair.
-//  - without a shared part, a pair inside one CTA goes straight to the
-//    output; one cut by a CTA border leaves (m, l, O) in the workspace and
-//    the last of its CTAs to arrive joins them in CTA order;
-//  - with one (attn_prefix.cu), every pair leaves (m, l, O), and
-//    attn_join_kernel joins them with the shared part's, a thread for four
+//  - where a pair has few parts, one inside a CTA goes straight to the output,
+//    and one cut by a CTA border leaves (m, l, O) in the workspace and the
+//    last of its CTAs to arrive joins them in CTA order;
+//  - where it has many, or a shared part (attn_prefix.cu), every pair leaves
+//    (m, l, O), and attn_join_kernel joins them all, a thread for four
 //    elements of the output: few threads wait long for what many threads
-//    fetch at once.
+//    fetch at once (one slot of 32768 positions: 28 us against 16).
 #include "attn_batch.cuh"
 
 namespace moe {
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kOAll, 2)
       // the pair's parts: one place per CTA and pair, both of which grow
       // along the line
       const int pair = s * a.n_kv + g;
-      const bool direct = whole && !shared;
+      const bool direct = whole && !a.join;
       float* part = a.part + (int64_t)((int)blockIdx.x + pair) * kR * (D + 2);
 #pragma unroll
       for (int cb = 0; cb < D; cb += kCW) {
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kOAll, 2)
           part[r] = s_M[r];
           part[kR + r] = s_L[r];
         }
-        if (shared) {
+        if (a.join) {
           if (tid == 0 && pb >= f0) a.pair_start[pair] = pb;  // the pair's first CTA
         } else {
           // the pair's CTAs: first and last to hold a block of it
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kOAll, 2)
         if (++s < a.n_slots) sp = slot_span(a, s);
       }
     }
-    if (shared && blockIdx.x == 0 && tid == 0) a.line[0] = per;
+    if (a.join && blockIdx.x == 0 && tid == 0) a.line[0] = per;
   }
   if (shared) {
     // the join waits for this kernel, and this one for the shared part
@@ -575,14 +575,16 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnBatchArgs a, i
   const int item = threadIdx.x % kItems, ln = threadIdx.x / kItems;
   const int i = blockIdx.y * kItems + item;
   const int d = i / rows, r = i - d * rows, t = r / G;
-  const int own_per = __ldg(a.line), px_per = __ldg(a.line + 1), px_len = __ldg(a.line + 2);
-  const int pb = __ldg(a.pair_start + pair), tok0 = __ldg(a.tok_start + s);
+  const int own_per = __ldg(a.line), pb = __ldg(a.pair_start + pair);
+  const bool shared = a.px_steps > 0;
+  const int px_per = shared ? __ldg(a.line + 1) : 1, px_len = shared ? __ldg(a.line + 2) : 0;
+  const int tok0 = shared ? __ldg(a.tok_start + s) : 0;
   const SlotSpan sp = slot_span(a, s);
   Joined jn{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   if (i < rows * (D / 4) && t < sp.n_new && sp.len - sp.n_new + t >= 0) {
     const int row = tok0 * G + r, u = (row >> 8) * a.n_kv + g, rr = row & 255;
-    const int x0 = u * px_len / px_per, x1 = (u * px_len + a.px_steps - 1) / px_per;
-    const int nx = x1 - x0 + 1;
+    const int x0 = u * px_len / px_per;
+    const int nx = shared ? (u * px_len + a.px_steps - 1) / px_per - x0 + 1 : 0;
     const int c0 = pb / own_per, n = nx + (pb + sp.blocks - 1) / own_per - c0 + 1;
     join_parts<6>(jn, (n - ln + kLanes - 1) / kLanes, d,
                   [&](int c, const float*& p, int& ld, int& prow) {
@@ -645,6 +647,19 @@ int own_tiles(const moe_attn_batch_shape_t* s) {  // row tiles: 1, 2 or 4
 }
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr int kMostSms = 256;  // two CTAs an SM at most
+// Whether the prefix is read once for all slots. Otherwise each slot's own line
+// reads it, in one or two launches instead of three, which is shorter while
+// the slots' prefix blocks together are few. Measured, per slot against
+// shared (D = 128, 8 rows a pair): 12.2 and 12.6 us at 512 blocks over all
+// slots and heads, 15.4 and 15.9 at 1024, 17.4 and 16.5 at 2048; with 32 rows
+// 19.1 and 20.1 at 512, 20.3 and 18.8 at 1024; with 64 rows even at 256 to
+// 512; with D = 64, half the bytes a block, 12.0 and 12.2 at 1024, 13.5 and
+// 12.6 at 2048, where the calls from the host still favour one launch.
+bool share(const moe_attn_batch_shape_t* s) {
+  if (s->prefix_blocks == 0 || s->n_slots == 1) return false;
+  const int64_t blocks = (int64_t)s->n_slots * s->n_kv * s->prefix_blocks;
+  return blocks * s->D / 128 * own_tiles(s) > 1024;
+}
 // a place per CTA and pair
 size_t own_part_bytes(const moe_attn_batch_shape_t* s) {
   const size_t places = 2 * kMostSms + (size_t)s->n_slots * s->n_kv;
@@ -660,10 +675,10 @@ cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const AttnB
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(attn_own_kernel<F16, D, MT>, dim3(grid), dim3(kOAll), smem, stream, tk, tv, a);
-  if (e != cudaSuccess || a.px_steps == 0) return e;
+  if (e != cudaSuccess || !a.join) return e;
   // a thread fetches six parts at once
-  if (a.px_parts <= 6) return launch_join<F16, D, 1>(a, MT * 16, stream);
-  if (a.px_parts <= 48) return launch_join<F16, D, 4>(a, MT * 16, stream);
+  if (a.parts <= 6) return launch_join<F16, D, 1>(a, MT * 16, stream);
+  if (a.parts <= 48) return launch_join<F16, D, 4>(a, MT * 16, stream);
   return launch_join<F16, D, 16>(a, MT * 16, stream);
 }
 template <bool F16, int D>
@@ -701,14 +716,16 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
   a.max_blocks = s->max_blocks;
   a.prefix_blocks = s->prefix_blocks;
   const int sms = nsm < kMostSms ? nsm : kMostSms;
+  const int mt = own_tiles(s);
   int px_grid = 0;
   a.first = 0;
   a.px_steps = 0;
-  if (s->prefix_blocks > 0 && s->n_slots > 1) {
+  a.parts = 0;
+  if (share(s)) {
     const PrefixLine line = prefix_line(s, sms);
     a.first = s->prefix_blocks;
     a.px_steps = line.steps;
-    a.px_parts = (line.steps + line.per - 1) / line.per + 1;
+    a.parts = (line.steps + line.per - 1) / line.per + 1;
     px_grid = line.grid;
     a.px_part = a.part + own_part_bytes(s) / 4;
     const cudaError_t e = launch_attn_prefix(s, tk, tv, a, line.grid, stream);
@@ -719,7 +736,12 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
   const int64_t most = (int64_t)s->n_slots * s->n_kv * s->max_blocks;
   const int beside = 2 * (px_grid * 5 <= sms * 3 ? sms - px_grid : sms);
   const int grid = most < beside ? (int)most : beside;
-  const int mt = own_tiles(s);
+  // the parts of a pair's own blocks, were all pairs as long as they can be
+  const int64_t pairs_n = (int64_t)s->n_slots * s->n_kv;
+  a.parts += (int)(grid / pairs_n < s->max_blocks - a.first ? grid / pairs_n : s->max_blocks - a.first);
+  // few parts of few rows are joined by the last CTA: 8.6 and 8.1 us at 5 or
+  // 6 parts of 8 rows, 13.9 and 9.4 of 32 rows, 19.4 and 12.1 of 64
+  a.join = a.px_steps > 0 || a.parts * mt > 6;
   if (s->dtype == MOE_DTYPE_FP16)
     return s->D == 64 ? launch_own_mt<true, 64>(mt, tk, tv, a, grid, stream)
                       : launch_own_mt<true, 128>(mt, tk, tv, a, grid, stream);

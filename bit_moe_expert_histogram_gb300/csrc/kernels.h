@@ -220,7 +220,8 @@ struct AttnBatchArgs {
   // the shared part, when attn_prefix_kernel takes it (px_steps > 0): its
   // line of steps and its parts, per place m[256], l[256], O[D / 4][256][4]
   int px_steps;
-  int px_parts;        // the stretches that a row's steps are cut into, at most about
+  int join;            // attn_join_kernel follows
+  int parts;           // about how many parts a row then has
   float* px_part;
   Ctrl* ctrl;
 };

@@ -15,9 +15,12 @@
 // changed, and a caller can drop the result). Copies read only pages that
 // are held and write only pages that are free, so none of them overlap.
 //
-// Bound: the copies by HBM (each byte once in, once out); fork and reserve
-// by launch and L2 latency, so they are two or three short kernels chained
-// by programmatic dependent launch.
+// Bound: the copies by HBM (each byte once in, once out); fork and reserve by
+// launch and L2 latency. A small state is one CTA's work, one launch; a large
+// one takes two and three short kernels chained by programmatic dependent
+// launch. (One cooperative launch whose CTAs meet in the workspace takes the
+// host 1.3 us less than two, but the GPU 6.4 us instead of 4.1 for 1000 slots
+// and 4.5 instead of 2.9 for 16.)
 #include "common.cuh"
 #include "kernels.h"
 
@@ -25,7 +28,7 @@ namespace moe {
 
 namespace {
 constexpr int kPage = 64;         // positions per page
-constexpr int kPlanThr = 1024;    // the reserve plan's one CTA
+constexpr int kOneCta = 1024;     // threads of a CTA that plans alone
 constexpr int kRankChunk = 1024;  // pages per CTA of the compaction's count and rank
 
 __device__ __forceinline__ int blocks_of(int len) { return (len + kPage - 1) / kPage; }
@@ -76,88 +79,150 @@ __global__ void __launch_bounds__(256)
     if (i0 + k * 256 < n) out[i0 + k * 256] = __ldg(in + i0 + k * 256);
 }
 
-// One CTA per slot: the row of its parent cut to the new length, and the
-// difference in the pages' counts (none where the page stays in its place).
-__global__ void __launch_bounds__(128)
+// Four warps per slot: the row of its parent cut to the new length, and the
+// difference in the pages' counts (none where a page stays in its place).
+// refs: the counts are not in the new state yet, and this CTA is the only one.
+__global__ void __launch_bounds__(kOneCta)
     cache_fork_kernel(const moe_cache_meta_t in, const moe_cache_meta_t out,
                       const int32_t* __restrict__ parent, const int32_t* __restrict__ keep,
-                      int n_slots, int max_blocks, int n_phys, Ctrl* ctrl) {
+                      int n_slots, int max_blocks, int n_phys, bool refs, Ctrl* ctrl) {
   pdl_wait();
   pdl_trigger();
-  const int s = blockIdx.x;
-  const int a = __ldg(parent + s);
-  const bool live = a >= 0 && a < n_slots;
-  if (threadIdx.x == 0 && a >= n_slots) set_error(ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
-  int len = 0;
-  if (live) {
-    len = len_of(in.lens_dev, a, max_blocks, ctrl);
-    if (keep) len = min(len, max(0, __ldg(keep + s)));
+  if (refs) {
+    for (int i = threadIdx.x; i < n_phys; i += blockDim.x) out.refs_dev[i] = __ldg(in.refs_dev + i);
+    __syncthreads();
   }
-  const int nb_old = blocks_of(len_of(in.lens_dev, s, max_blocks, ctrl)), nb_new = blocks_of(len);
-  const int32_t* row_old = in.table_dev + (int64_t)s * max_blocks;
-  const int32_t* row_new = in.table_dev + (int64_t)(live ? a : s) * max_blocks;
-  int32_t* row = out.table_dev + (int64_t)s * max_blocks;
-  for (int j = threadIdx.x; j < max_blocks; j += 128) {
-    int po = j < nb_old ? __ldg(row_old + j) : -1, pn = j < nb_new ? __ldg(row_new + j) : -1;
-    if ((j < nb_old && (po < 0 || po >= n_phys)) || (j < nb_new && (pn < 0 || pn >= n_phys)))
-      set_error(ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
-    if (po < 0 || po >= n_phys) po = -1;
-    if (pn < 0 || pn >= n_phys) pn = -1;
-    row[j] = pn;
-    if (po != pn) {
-      if (pn >= 0) atomicAdd(out.refs_dev + pn, 1);
-      if (po >= 0) atomicAdd(out.refs_dev + po, -1);
+  const int per = blockDim.x >> 7, j0 = threadIdx.x & 127;
+  for (int s = blockIdx.x * per + (threadIdx.x >> 7); s < n_slots; s += gridDim.x * per) {
+    const int a = __ldg(parent + s);
+    const bool live = a >= 0 && a < n_slots;
+    if (j0 == 0 && a >= n_slots) set_error(ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
+    int len = 0;
+    if (live) {
+      len = len_of(in.lens_dev, a, max_blocks, ctrl);
+      if (keep) len = min(len, max(0, __ldg(keep + s)));
+    }
+    const int nb_old = blocks_of(len_of(in.lens_dev, s, max_blocks, ctrl)), nb_new = blocks_of(len);
+    const int32_t* row_old = in.table_dev + (int64_t)s * max_blocks;
+    const int32_t* row_new = in.table_dev + (int64_t)(live ? a : s) * max_blocks;
+    int32_t* row = out.table_dev + (int64_t)s * max_blocks;
+    for (int j = j0; j < max_blocks; j += 128) {
+      int po = j < nb_old ? __ldg(row_old + j) : -1, pn = j < nb_new ? __ldg(row_new + j) : -1;
+      if ((j < nb_old && (po < 0 || po >= n_phys)) || (j < nb_new && (pn < 0 || pn >= n_phys)))
+        set_error(ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
+      if (po < 0 || po >= n_phys) po = -1;
+      if (pn < 0 || pn >= n_phys) pn = -1;
+      row[j] = pn;
+      if (po != pn) {
+        if (pn >= 0) atomicAdd(out.refs_dev + pn, 1);
+        if (po >= 0) atomicAdd(out.refs_dev + po, -1);
+      }
+    }
+    if (j0 == 0) out.lens_dev[s] = len;
+  }
+}
+
+// ---------------------------------------------------------------- copies --
+// The first `rows` rows of every head of a page to another; row_u4: 16-byte
+// words of a row, D * 2 / 16.
+__device__ __forceinline__ void copy_page(const uint4* __restrict__ from, uint4* __restrict__ to,
+                                          int n_kv, int rows, int row_u4) {
+  const int per = rows * row_u4, page = kPage * row_u4;
+  for (int h = 0; h < n_kv; ++h) {
+    const uint4* f = from + (int64_t)h * page;
+    uint4* t = to + (int64_t)h * page;
+    for (int i0 = threadIdx.x; i0 < per; i0 += 256 * 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k * 256 < per) v[k] = __ldcs(f + i0 + k * 256);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k * 256 < per) __stcs(t + i0 + k * 256, v[k]);
     }
   }
-  if (threadIdx.x == 0) out.lens_dev[s] = len;
+}
+
+// The listed copies, (source, destination, rows) each, in every pool: chunk q
+// of head h of pool k of copy c, 4 KB a warp at a time, all of it in flight.
+__device__ __forceinline__ void copy_list(const CachePools& pools, const int32_t* list, int copies,
+                                          int n_kv, int row_u4) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int head = kPage * row_u4, chunks = (head + 255) / 256;
+  // at most 4096 copies in 128 pools of 64 heads of 16 chunks: 32 bits
+  const unsigned n = (unsigned)copies * pools.n * n_kv * chunks;
+  for (unsigned w = blockIdx.x * warps + (threadIdx.x >> 5); w < n; w += gridDim.x * warps) {
+    const unsigned hk = w / chunks, kc = hk / n_kv;
+    const int q = w - hk * chunks, h = hk - kc * n_kv, c = kc / pools.n, k = kc - c * pools.n;
+    const int32_t* it = list + 3 * c;
+    const int end = min(__ldcg(it + 2) * row_u4, q * 256 + 256);
+    uint4* pool = static_cast<uint4*>(pools.p[k]);
+    const uint4* from = pool + ((int64_t)__ldcg(it) * n_kv + h) * head;
+    uint4* to = pool + ((int64_t)__ldcg(it + 1) * n_kv + h) * head;
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = q * 256 + i * 32 + lane;
+      if (at < end) v[i] = __ldcs(from + at);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = q * 256 + i * 32 + lane;
+      if (at < end) __stcs(to + at, v[i]);
+    }
+  }
+}
+__global__ void __launch_bounds__(256)
+    cache_copy_list_kernel(const __grid_constant__ CachePools pools, const int32_t* list,
+                           const int32_t* n_copies, int n_kv, int row_u4) {
+  pdl_wait();
+  pdl_trigger();
+  copy_list(pools, list, __ldg(n_copies), n_kv, row_u4);
 }
 
 // --------------------------------------------------------------- reserve --
-// List of page copies in the workspace: (source, destination, rows).
-struct CopyList {
-  int32_t* count;  // [1]
-  int32_t* item;   // [n][3]
-};
-
-// Table and refs into the new state; a row's entries past its slot's blocks
-// become -1.
-__global__ void __launch_bounds__(256)
-    cache_reserve_state_kernel(const moe_cache_meta_t in, const moe_cache_meta_t out, int n_slots,
-                               int max_blocks, int n_phys, Ctrl* ctrl) {
-  pdl_wait();
-  pdl_trigger();
-  if ((int)blockIdx.x < n_slots) {
-    const int s = blockIdx.x;
+// Table and refs into the new state, rows s0, s0 + n, .. and pages likewise by
+// CTA; a row's entries past its slot's blocks become -1.
+__device__ __forceinline__ void bring_state(const moe_cache_meta_t& in, const moe_cache_meta_t& out,
+                                            int n_slots, int max_blocks, int n_phys, Ctrl* ctrl) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_phys; i += gridDim.x * blockDim.x)
+    out.refs_dev[i] = __ldg(in.refs_dev + i);
+  for (int s = blockIdx.x * warps + (threadIdx.x >> 5); s < n_slots; s += gridDim.x * warps) {
     const int nb = blocks_of(len_of(in.lens_dev, s, max_blocks, ctrl));
     const int64_t r0 = (int64_t)s * max_blocks;
-    for (int j = threadIdx.x; j < max_blocks; j += 256)
+#pragma unroll 4
+    for (int j = lane; j < max_blocks; j += 32)
       out.table_dev[r0 + j] = j < nb ? __ldg(in.table_dev + r0 + j) : -1;
-  } else {
-    const int i0 = ((int)blockIdx.x - n_slots) * 1024 + threadIdx.x;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k * 256;
-      if (i < n_phys) out.refs_dev[i] = __ldg(in.refs_dev + i);
-    }
   }
 }
+__global__ void __launch_bounds__(256)
+    cache_state_kernel(const moe_cache_meta_t in, const moe_cache_meta_t out, int n_slots,
+                       int max_blocks, int n_phys, Ctrl* ctrl) {
+  pdl_wait();
+  pdl_trigger();
+  bring_state(in, out, n_slots, max_blocks, n_phys, ctrl);
+}
 
-// One CTA. Needs of the slots and their running sum; the lowest free pages,
-// as many as are needed; then each granted slot's entries, counts and copy.
-__global__ void __launch_bounds__(kPlanThr)
-    cache_reserve_kernel(const moe_cache_meta_t in, const moe_cache_meta_t out,
-                         const int32_t* __restrict__ n_new, int32_t* __restrict__ granted,
-                         int n_slots, int max_blocks, int n_phys, int32_t* __restrict__ before,
-                         int32_t* __restrict__ free_page, CopyList list, Ctrl* ctrl) {
+// One CTA. The slots' needs and their running sum, the lowest free pages, as
+// many as are needed; then each granted slot's entries, counts and page copy.
+// all: the state is not in `out` yet, and no kernel for the copies follows.
+__global__ void __launch_bounds__(kOneCta)
+    cache_reserve_kernel(const __grid_constant__ CachePools pools, const moe_cache_meta_t in,
+                         const moe_cache_meta_t out, const int32_t* __restrict__ n_new,
+                         int32_t* __restrict__ granted, int n_slots, int max_blocks, int n_phys,
+                         int n_kv, int row_u4, bool all, int32_t* before, int32_t* free_page,
+                         int32_t* list, int32_t* n_copies, Ctrl* ctrl) {
   __shared__ int s_tot[32];
   __shared__ int s_sum;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  // what slot s asks for: its length, the new positions, its blocks, the page
-  // to copy (-1: none); returns the pages that this takes. A request that is
-  // wider than the row counts in full here, so that the slots after it see
-  // the same running sum either way.
+  if (all) bring_state(in, out, n_slots, max_blocks, n_phys, ctrl);
+  // what slot s asks for: its length, the new positions, its blocks, the
+  // page to copy (-1: none); returns the pages that this takes. A request
+  // that is wider than the row counts in full here, so that the slots after
+  // it see the same running sum either way.
   auto ask = [&](int s, int& len, int& n, int& nb0, int& cow) {
     len = len_of(in.lens_dev, s, max_blocks, ctrl);
     n = __ldg(n_new + s);
@@ -182,20 +247,20 @@ __global__ void __launch_bounds__(kPlanThr)
   };
   // running sum of the needs, in slot order, kept below 2^30
   int sum = 0;
-  for (int s0 = 0; s0 < n_slots; s0 += kPlanThr) {
+  for (int s0 = 0; s0 < n_slots; s0 += kOneCta) {
     const int s = s0 + tid;
     int len, n, nb0, cow;
     const int need = s < n_slots ? ask(s, len, n, nb0, cow) : 0;
     const int incl = block_scan_i(need, s_tot);  // below 2^31: a need is at most 2^20 + 1
     if (s < n_slots) before[s] = (int)min((int64_t)sum + incl - need, (int64_t)1 << 30);
-    if (tid == kPlanThr - 1) s_sum = incl;
+    if (tid == kOneCta - 1) s_sum = incl;
     __syncthreads();
     sum = (int)min((int64_t)sum + s_sum, (int64_t)1 << 30);
     __syncthreads();
   }
   // the lowest `sum` free pages (or all there are), in order
   int found = 0;
-  for (int p0 = 0; p0 < n_phys && found < sum; p0 += kPlanThr * 4) {
+  for (int p0 = 0; p0 < n_phys && found < sum; p0 += kOneCta * 4) {
     int f[4], c = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -208,14 +273,14 @@ __global__ void __launch_bounds__(kPlanThr)
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (f[k]) free_page[at++] = p0 + tid * 4 + k;
-    if (tid == kPlanThr - 1) s_sum = incl;
+    if (tid == kOneCta - 1) s_sum = incl;
     __syncthreads();
     found += s_sum;
     __syncthreads();
   }
-  // each slot's pages; the copies are listed in slot order
+  // each slot's pages
   int copies = 0;
-  for (int s0 = 0; s0 < n_slots; s0 += kPlanThr) {
+  for (int s0 = 0; s0 < n_slots; s0 += kOneCta) {
     const int s = s0 + tid;
     int len = 0, n = 0, nb0 = 0, cow = -1, at = 0;
     if (s < n_slots) {
@@ -243,54 +308,18 @@ __global__ void __launch_bounds__(kPlanThr)
     }
     const int incl = block_scan_i(cow >= 0 ? 1 : 0, s_tot);
     if (cow >= 0) {
-      int32_t* it = list.item + 3 * (copies + incl - 1);
+      int32_t* it = list + 3 * (copies + incl - 1);
       it[0] = cow;
       it[1] = free_page[at];
       it[2] = len % kPage;
     }
-    if (tid == kPlanThr - 1) s_sum = incl;
+    if (tid == kOneCta - 1) s_sum = incl;
     __syncthreads();
     copies += s_sum;
     __syncthreads();
   }
-  if (tid == 0) *list.count = copies;
-}
-
-// ---------------------------------------------------------------- copies --
-// The first `rows` rows of every head of a page to another; row_u4: 16-byte
-// words of a row, D * 2 / 16.
-__device__ __forceinline__ void copy_page(const uint4* __restrict__ from, uint4* __restrict__ to,
-                                          int n_kv, int rows, int row_u4) {
-  const int per = rows * row_u4, page = kPage * row_u4;
-  for (int h = 0; h < n_kv; ++h) {
-    const uint4* f = from + (int64_t)h * page;
-    uint4* t = to + (int64_t)h * page;
-    for (int i0 = threadIdx.x; i0 < per; i0 += 256 * 4) {
-      uint4 v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i0 + k * 256 < per) v[k] = __ldcs(f + i0 + k * 256);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i0 + k * 256 < per) __stcs(t + i0 + k * 256, v[k]);
-    }
-  }
-}
-
-// The listed copies in every pool.
-__global__ void __launch_bounds__(256)
-    cache_copy_list_kernel(const __grid_constant__ CachePools pools, CopyList list, int n_kv,
-                           int row_u4) {
-  pdl_wait();
-  pdl_trigger();
-  const int n = __ldg(list.count) * pools.n;
-  const int64_t page = (int64_t)n_kv * kPage * row_u4;
-  for (int w = blockIdx.x; w < n; w += gridDim.x) {
-    const int c = w / pools.n, k = w - c * pools.n;
-    const int32_t* it = list.item + 3 * c;
-    uint4* pool = static_cast<uint4*>(pools.p[k]);
-    copy_page(pool + __ldg(it) * page, pool + __ldg(it + 1) * page, n_kv, __ldg(it + 2), row_u4);
-  }
+  if (tid == 0) *n_copies = copies;
+  if (all) copy_list(pools, list, copies, n_kv, row_u4);  // the list is complete: a scan ended it
 }
 
 // Whole pages from one set of pools to another by two caller-given lists.
@@ -494,14 +523,25 @@ int copy_ctas(int64_t pages, int nsm) { return (int)(pages < nsm * 8 ? pages : n
 
 size_t cache_ws_bytes(const moe_cache_shape_t* s) { return cache_ws(s).total; }
 
+// Few enough words that one CTA brings them over in the time of a launch.
+namespace {
+bool small_state(const moe_cache_shape_t* s) {
+  return (int64_t)s->n_slots * s->max_blocks + s->n_phys <= 16384;
+}
+}  // namespace
+
 cudaError_t launch_cache_fork(const moe_cache_shape_t* s, const moe_cache_meta_t& in,
                               const moe_cache_meta_t& out, const int32_t* parent,
                               const int32_t* keep, uint8_t* ws, cudaStream_t stream) {
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(ws);
+  if (small_state(s))
+    return launch_pdl(cache_fork_kernel, dim3(1), dim3(kOneCta), 0, stream, in, out, parent, keep,
+                      s->n_slots, s->max_blocks, s->n_phys, true, ctrl);
   const cudaError_t e = launch_pdl(cache_copy_refs_kernel, dim3(ceil_div(s->n_phys, 1024)),
                                    dim3(256), 0, stream, in.refs_dev, out.refs_dev, s->n_phys);
   if (e != cudaSuccess) return e;
   return launch_pdl(cache_fork_kernel, dim3(s->n_slots), dim3(128), 0, stream, in, out, parent,
-                    keep, s->n_slots, s->max_blocks, s->n_phys, reinterpret_cast<Ctrl*>(ws));
+                    keep, s->n_slots, s->max_blocks, s->n_phys, false, ctrl);
 }
 
 cudaError_t launch_cache_reserve(const moe_cache_shape_t* s, const moe_cache_meta_t& in,
@@ -510,17 +550,23 @@ cudaError_t launch_cache_reserve(const moe_cache_shape_t* s, const moe_cache_met
                                  cudaStream_t stream) {
   const CacheWs w = cache_ws(s);
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(ws);
-  cudaError_t e = launch_pdl(cache_reserve_state_kernel,
-                             dim3(s->n_slots + ceil_div(s->n_phys, 1024)), dim3(256), 0, stream,
-                             in, out, s->n_slots, s->max_blocks, s->n_phys, ctrl);
-  if (e != cudaSuccess) return e;
-  const CopyList list{at(ws, w.count), at(ws, w.item)};
-  e = launch_pdl(cache_reserve_kernel, dim3(1), dim3(kPlanThr), 0, stream, in, out, n_new, granted,
-                 s->n_slots, s->max_blocks, s->n_phys, at(ws, w.before), at(ws, w.free_page), list,
-                 ctrl);
-  if (e != cudaSuccess || pools.n == 0) return e;
-  return launch_pdl(cache_copy_list_kernel, dim3(copy_ctas((int64_t)s->n_slots * pools.n, nsm)),
-                    dim3(256), 0, stream, pools, list, s->n_kv, s->D / 8);
+  // one CTA copies a few pages in a few microseconds, should every slot need it
+  const int64_t copies = (int64_t)s->n_slots * pools.n;
+  const bool all = small_state(s) && copies * s->n_kv * s->D <= 8192;
+  if (!all) {
+    const int ctas = ceil_div((int64_t)s->n_slots * s->max_blocks + s->n_phys, 2048);
+    const cudaError_t e =
+        launch_pdl(cache_state_kernel, dim3(ctas < 8 * nsm ? ctas : 8 * nsm), dim3(256), 0, stream,
+                   in, out, s->n_slots, s->max_blocks, s->n_phys, ctrl);
+    if (e != cudaSuccess) return e;
+  }
+  const cudaError_t e = launch_pdl(
+      cache_reserve_kernel, dim3(1), dim3(kOneCta), 0, stream, pools, in, out, n_new, granted,
+      s->n_slots, s->max_blocks, s->n_phys, s->n_kv, s->D / 8, all, at(ws, w.before),
+      at(ws, w.free_page), at(ws, w.item), at(ws, w.count), ctrl);
+  if (e != cudaSuccess || all || pools.n == 0) return e;
+  return launch_pdl(cache_copy_list_kernel, dim3(copy_ctas(copies, nsm)), dim3(256), 0, stream,
+                    pools, at(ws, w.item), at(ws, w.count), s->n_kv, s->D / 8);
 }
 
 cudaError_t launch_cache_write(const moe_cache_shape_t* s, const moe_cache_meta_t& meta,

@@ -71,12 +71,14 @@ __device__ __forceinline__ void ldm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ uint32_t swz64(int p, int ch) {
   return (uint32_t)((ch >> 3) * (kBlk * 128) + p * 128 + (((ch & 7) ^ (p & 7)) << 4));
 }
-// v / l to four 16-bit elements (0 where l is)
+// v / l to four 16-bit elements, 0 where l is (a row that sees nothing), even
+// if what was summed for it is not finite; a NaN sum stays one
 template <bool F16>
 __device__ __forceinline__ void store4(uint16_t* to, const float4& v, float l) {
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = 1.0f / l;
   *reinterpret_cast<uint2*>(to) =
-      make_uint2(pack2<F16>(v.x * inv, v.y * inv), pack2<F16>(v.z * inv, v.w * inv));
+      l == 0.0f ? make_uint2(0u, 0u)
+                : make_uint2(pack2<F16>(v.x * inv, v.y * inv), pack2<F16>(v.z * inv, v.w * inv));
 }
 }  // namespace
 
@@ -135,12 +137,15 @@ __device__ __forceinline__ uint16_t* out_row(const AttnBatchArgs& a, int s, int 
 
 template <int D>
 struct OwnRing {
-  static constexpr int kTile = kBlk * D * 2;            // bytes of a block's keys (or values)
-  static constexpr int kStages = D == 64 ? 6 : 3;       // 96 KB either way: two CTAs an SM
+  static constexpr int kTile = kBlk * D * 2;       // bytes of a block's keys (or values)
+  static constexpr int kStages = D == 64 ? 4 : 3;  // 64 and 96 KB
 };
+// CTAs an SM: two, or three where registers and stages allow (19.1 us instead
+// of 20.2 for 33 slots of up to 5000 positions)
+__host__ __device__ constexpr int own_ctas(int D, int MT) { return D == 64 && MT == 1 ? 3 : 2; }
 
 template <bool F16, int D, int MT>
-__global__ void __launch_bounds__(kOAll, 2)
+__global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
     attn_own_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const AttnBatchArgs a) {
   constexpr int kTile = OwnRing<D>::kTile, kStages = OwnRing<D>::kStages;
@@ -229,9 +234,18 @@ __global__ void __launch_bounds__(kOAll, 2)
   if (warp == 4) {
     // ---- the loader: all lanes follow the line, lane 0 issues
     const uint64_t pol = policy_evict_first();  // own pages are read once
-    int page = 0;                               // lane l: page of block (j & ~31) + l
-    bool fresh = true;
-    int n = 0;  // blocks loaded
+    // lane l: the pages of the slot's first 32 own blocks and of the next
+    // slot's, with that slot's span: a short pair does not wait for them
+    auto page_of = [&](int slot, int j) {
+      const int jb = a.first + j + lane;
+      if (slot >= a.n_slots || jb >= a.max_blocks) return -1;
+      return jb < a.prefix_blocks ? __ldg(a.prefix + jb)
+                                  : __ldg(a.table + (int64_t)slot * a.max_blocks + jb);
+    };
+    int first32 = page_of(s, 0), next32 = page_of(s + 1, 0);
+    SlotSpan next_sp = s + 1 < a.n_slots ? slot_span(a, s + 1) : sp;
+    int page = first32, base = 0;  // page: of blocks base + lane
+    int n = 0;                     // blocks loaded
     for (int f = f0; f < f1;) {
       const int j = f - pb;  // block of the pair
       if (j >= sp.blocks) {
@@ -239,25 +253,27 @@ __global__ void __launch_bounds__(kOAll, 2)
         f = pb;
         if (++g == a.n_kv) {
           g = 0;
-          if (++s < a.n_slots) sp = slot_span(a, s);
+          ++s;
+          sp = next_sp;
+          first32 = next32;
+          next32 = page_of(s + 1, 0);
+          if (s + 1 < a.n_slots) next_sp = slot_span(a, s + 1);
         }
-        fresh = true;
+        page = first32;
+        base = 0;
         continue;
       }
-      if (fresh || (j & 31) == 0) {
-        const int jb = a.first + (j & ~31) + lane;
-        page = -2;  // nothing there
-        if (sp.n_new > 0 && jb * kBlk < sp.len) {
-          page = jb < a.prefix_blocks ? __ldg(a.prefix + jb)
-                                      : __ldg(a.table + (int64_t)s * a.max_blocks + jb);
-          if (page < 0 || page >= a.n_phys) {
-            set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_ATTNB, s);
-            page = -1;
-          }
-        }
-        fresh = false;
+      if ((j & ~31) != base) {
+        base = j & ~31;
+        page = page_of(s, base);
       }
-      const int phys = __shfl_sync(0xFFFFFFFFu, page, j & 31);
+      int phys = __shfl_sync(0xFFFFFFFFu, page, j & 31);
+      if (sp.n_new == 0 || (a.first + j) * kBlk >= sp.len) {
+        phys = -2;  // nothing there
+      } else if (phys < 0 || phys >= a.n_phys) {
+        if (lane == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_ATTNB, s);
+        phys = -1;
+      }
       const int st = n % kStages;
       if (lane == 0) {
         if (!mbar_wait(eb + 8u * st, ((uint32_t)(n / kStages) & 1u) ^ 1u, abort) &&
@@ -646,7 +662,7 @@ int own_tiles(const moe_attn_batch_shape_t* s) {  // row tiles: 1, 2 or 4
   return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
 }
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
-constexpr int kMostSms = 256;  // two CTAs an SM at most
+constexpr int kMostSms = 256;  // three CTAs an SM at most
 // Whether the prefix is read once for all slots. Otherwise each slot's own line
 // reads it, in one or two launches instead of three, which is shorter while
 // the slots' prefix blocks together are few. Measured, per slot against
@@ -662,7 +678,7 @@ bool share(const moe_attn_batch_shape_t* s) {
 }
 // a place per CTA and pair
 size_t own_part_bytes(const moe_attn_batch_shape_t* s) {
-  const size_t places = 2 * kMostSms + (size_t)s->n_slots * s->n_kv;
+  const size_t places = 3 * kMostSms + (size_t)s->n_slots * s->n_kv;
   return round256(places * own_tiles(s) * 16 * (s->D + 2) * 4);
 }
 
@@ -731,10 +747,10 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
     const cudaError_t e = launch_attn_prefix(s, tk, tv, a, line.grid, stream);
     if (e != cudaSuccess) return e;
   }
-  // two CTAs an SM, and no more than there can be blocks; beside a shared part
-  // that leaves SMs over, as many as fit beside it, so that both run at once
+  // as many CTAs as fit, and no more than there can be blocks; beside a shared
+  // part that leaves SMs over, as many as fit there, so that both run at once
   const int64_t most = (int64_t)s->n_slots * s->n_kv * s->max_blocks;
-  const int beside = 2 * (px_grid * 5 <= sms * 3 ? sms - px_grid : sms);
+  const int beside = own_ctas(s->D, mt) * (px_grid * 5 <= sms * 3 ? sms - px_grid : sms);
   const int grid = most < beside ? (int)most : beside;
   // the parts of a pair's own blocks, were all pairs as long as they can be
   const int64_t pairs_n = (int64_t)s->n_slots * s->n_kv;

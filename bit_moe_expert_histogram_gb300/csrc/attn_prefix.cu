@@ -8,23 +8,36 @@
 // 256 rows (two of M = 128) against steps of 128 positions (two pages),
 // S = Q K^T into TMEM, softmax weights P back into TMEM over S, O += P V.
 // The (tile, head) pairs' steps lie on one line cut over one CTA per SM
-// (prefix_cut); each stretch leaves (m, l, O) of its 256 rows in the workspace, where
-// attn_join_kernel joins them with the slots' own positions.
+// (prefix_cut); each stretch leaves (m, l, O) of its 256 rows in the
+// workspace, where attn_join_kernel joins them with the slots' own positions.
 //
 // Warps: 0 loads K and V (TMA, two stages each of 128 positions), 1 and 2
-// issue the products of the two row tiles, 4-11 and 12-19 do the softmax of the two row tiles, half a
-// row a thread (the halves exchange their maxima through shared memory): with
-// a whole row a thread the chain load, maximum, exponentials, store took
-// longer than the other tile's products (282 us instead of 204 on 16384 rows
-// against 32768 positions). While one tile's weights are formed the other's
-// products run. The reference that a row's weights are relative to is only
-// raised when the row grows past it by 2^8 (any reference near the maximum
-// does): O in TMEM is rescaled a few times per stretch, not at every step.
+// issue the products of the two row tiles, 4-11 and 12-19 do the softmax of
+// the two row tiles, half a row a thread (the two warps of 32 rows exchange
+// the halves' maxima through shared memory). While one tile's weights are
+// formed the other's products run. The reference that a row's weights are
+// relative to is only raised when the row grows past it by 2^8 (any reference
+// near the maximum does): O in TMEM is rescaled a few times per stretch, not
+// at every step.
 //
-// Bounds (D = 128, per step and two tiles): products 32 MMAs of N = 128 at
-// 64 to 77 clocks, about 2256; exponentials 2 x 128 x 128 at 16 a clock,
-// 2048; a step's 64 KB at an SM's share of HBM (24 bytes a clock), 2800, but
-// only the first tile's visit comes from HBM, the others from L2.
+// Measured at 256 slots of up to 4 tokens (12288 query rows a key/value head
+// of 2 in all, D = 128, bf16) under 32768 positions, this kernel alone:
+//   282 us  four warps a tile, a row a thread, one lane issuing with
+//           descriptors built per product, rows of absent tokens computed
+//   162 us  eight warps a tile, half a row a thread; absent tokens left out
+//   141 us  one elected lane of a uniform warp issues, descriptors by
+//           addition, a warp a tile, in turns
+// and the whole call 181 us, then 174 us with the line cut pair by pair.
+// Leaving parts out for timing: without the exponentials the call takes as
+// long as with them, without the maxima and their exchange 13 us less, without
+// any softmax 23 us less, and then without the loads still as long: the rest
+// is the products' own time and hand-over. 1.5 PFLOP/s, 0.78 of the burst rate
+// of a plain bf16 product.
+//
+// Per step and two tiles (D = 128) the products take 32 MMAs of N = 128 at 64
+// to 77 clocks, about 2256, and their operands, the TMA writes among them,
+// about as much of shared memory's 128 bytes a clock; the exponentials 1024
+// to 2048. A step's 64 KB come from HBM for the first tile, from L2 after.
 #include "attn_batch.cuh"
 
 namespace moe {

@@ -20,7 +20,9 @@
 // one takes two and three short kernels chained by programmatic dependent
 // launch. (One cooperative launch whose CTAs meet in the workspace takes the
 // host 1.3 us less than two, but the GPU 6.4 us instead of 4.1 for 1000 slots
-// and 4.5 instead of 2.9 for 16.)
+// and 4.5 instead of 2.9 for 16.) Fork of 16 and of 1000 slots: 3.1 and 4.1 us
+// in a graph, 5.3 and 6.9 from the host; 2500 pages of a pool of 8192 brought
+// together in 4 pools: 75.5 us, 6.0 TB/s, 0.89 of a plain copy's rate.
 #include "common.cuh"
 #include "kernels.h"
 

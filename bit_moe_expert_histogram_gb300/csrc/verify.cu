@@ -12,19 +12,27 @@
 // here rounds where it could: u q is formed in 64 bits (two 24-bit factors,
 // exact), p - q as an fp32 pair without error, and the sums, the threshold
 // and the comparisons are fp32 pairs (value and error term, more than 46
-// bits). FP64 would be shorter to write, but an instruction of it takes a
-// warp about as long as 64 others here: with the search for the token in
-// FP64 the last CTAs of 64 slots ran for 20 us after the others were done.
+// bits). FP64 does the same in fewer lines, but its rate here is a small
+// fraction of fp32's: joining the threads in fp32 pairs instead took 57.5 us
+// to 28.2 (64 slots of 131072 in bf16), the search for the token too 26.6 to
+// 22.5, and 11.9 to 7.1 for one slot of 32000.
 //
 // What it has to read is one row of p and one of q per slot: HBM bounds large
 // batches, a chain of dependent accesses small ones. The vocabulary is cut
-// into segments of 4096; a slot's C CTAs (four or five per SM over the batch,
-// at most one per segment) each find i by themselves (a warp, one draft a lane: two
-// dependent loads), sum their segments and leave the sums in the workspace.
-// The slot's last CTA scans the segments' sums, re-reads the one segment that
-// the threshold falls into (it is in L2) and walks it. A thread's sixteen
-// values come in 16-byte loads, or in single ones, a warp's neighbours each,
-// where a row is not 16-byte aligned (an odd vocabulary).
+// into segments of 4096; a slot's C CTAs (one wave of four or five per SM over
+// the batch, at most one per segment) each find i by themselves (a warp, one
+// draft a lane: two dependent loads), sum their segments and leave the sums in
+// the workspace. The slot's last CTA scans the segments' sums, re-reads the
+// one segment that the threshold falls into (it is in L2) and walks it. A
+// thread's sixteen values come in 16-byte loads, or in single ones, a warp's
+// neighbours each, where a row is not 16-byte aligned (an odd vocabulary).
+//
+// 64 slots of 131072 in bf16: 17.5 us, 1.9 TB/s; 256 slots of 128001 in fp32
+// with certain drafts: 38 us, 3.5 TB/s, 0.51 of a plain copy's rate. With the
+// sums left out these take 11.6 and 31 us: the exact sums, some 20 to 29
+// instructions an element, are what is left over the loads. (A ring in shared
+// memory filled by bulk copies whatever a row's alignment read no faster: 19.9
+// and 37.8 us.)
 #include "common.cuh"
 #include "kernels.h"
 

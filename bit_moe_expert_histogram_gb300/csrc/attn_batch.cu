@@ -86,15 +86,18 @@ __device__ __forceinline__ void store4(uint16_t* to, const float4& v, float l) {
 }
 }  // namespace
 
-// Joins parts 0 .. n - 1 in order: each batch of up to kBatch is fetched as a
-// whole. at(c, base, ld, row): where part c lies (m at base[row], l at
-// base[ld + row], O[d][row] from base + 2 ld on).
+// Joins parts 0 .. n - 1 in order, each batch of up to kBatch fetched as a
+// whole: part k has m at p, l at p + l_at and O at p + o_at for its p.
 struct Joined {
   float M, L;
   float4 o;
 };
+struct PartRef {
+  const float* p;
+  int l_at, o_at;
+};
 template <int kBatch, typename At>
-__device__ __forceinline__ void join_parts(Joined& j, int n, int d, At at) {
+__device__ __forceinline__ void join_parts(Joined& j, int n, At at) {
   for (int c0 = 0; c0 < n; c0 += kBatch) {
     float m[kBatch], l[kBatch];
     float4 v[kBatch];
@@ -104,12 +107,10 @@ __device__ __forceinline__ void join_parts(Joined& j, int n, int d, At at) {
       l[k] = 0.0f;
       v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (c0 + k < n) {
-        const float* p;
-        int ld, row;
-        at(c0 + k, p, ld, row);
-        m[k] = __ldcg(p + row);
-        l[k] = __ldcg(p + ld + row);
-        v[k] = __ldcg(reinterpret_cast<const float4*>(p + 2 * ld) + d * ld + row);
+        const PartRef r = at(c0 + k);
+        m[k] = __ldcg(r.p);
+        l[k] = __ldcg(r.p + r.l_at);
+        v[k] = __ldcg(reinterpret_cast<const float4*>(r.p + r.o_at));
       }
     }
     float nM = j.M;
@@ -133,6 +134,10 @@ __device__ __forceinline__ void join_parts(Joined& j, int n, int d, At at) {
     }
     j.M = nM;
   }
+}
+// where row r, columns 4 d .. of a part of ld rows lie: m[ld], l[ld], O[d][ld][4]
+__device__ __forceinline__ PartRef part_ref(const float* part, int ld, int r, int d) {
+  return PartRef{part + r, ld, 2 * ld + 4 * (d * ld + r) - r};
 }
 __device__ __forceinline__ uint16_t* out_row(const AttnBatchArgs& a, int s, int g, int G, int r,
                                              int D) {
@@ -552,10 +557,9 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
             for (int i = tid; i < rows * (D / 4); i += kOThr) {
               const int d = i / rows, r = i - d * rows;
               Joined jn{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-              join_parts<4>(jn, c1 - c0 + 1, d, [&](int c, const float*& p, int& ld, int& row) {
-                p = a.part + (int64_t)(c0 + c + pair) * kR * (D + 2);
-                ld = kR;
-                row = r;
+              const PartRef own = part_ref(a.part + (int64_t)(c0 + pair) * kR * (D + 2), kR, r, d);
+              join_parts<4>(jn, c1 - c0 + 1, [&](int c) {
+                return PartRef{own.p + c * (kR * (D + 2)), own.l_at, own.o_at};
               });
               store4<F16>(out_row(a, s, g, G, r, D) + 4 * d, jn.o, jn.L);
             }
@@ -582,39 +586,55 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
 
 // Joins the shared part's stretches and the own parts. kLanes threads for four
 // elements of a row, each with every kLanes-th part, so that all of a row's
-// parts are fetched at once; then the threads' results in their order.
+// parts are fetched at once; then the threads' results in their order. A CTA
+// has items of one pair, rows (1 << row_bits of them, the pair's and none)
+// fastest; divisions by what the kernel is given are done once a CTA. Latency
+// bounds it: 14 us of 175 for 720 tokens of 16 heads with about five parts a
+// row, 34 MB from L2, and as long with batches of three to six parts.
 template <bool F16, int D, int kLanes>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnBatchArgs a, int kR) {
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnBatchArgs a, int kR, int row_bits) {
   constexpr int kItems = 256 / kLanes;
   __shared__ float4 s_o[kLanes][kItems];
   __shared__ float2 s_ml[kLanes][kItems];
+  __shared__ int s_cut[2][2];  // for the two tiles that a pair's rows can lie in: first stretch, how many
+  __shared__ int s_own[2];     // first own part, how many
   pdl_wait();
   pdl_trigger();
-  const int pair = blockIdx.x, s = pair / a.n_kv, g = pair - s * a.n_kv;
+  const int s = blockIdx.x, g = blockIdx.z, pair = s * a.n_kv + g;
   const int G = a.n_q / a.n_kv, rows = a.T * G;
+  const bool shared = a.px_steps > 0;
+  const SlotSpan sp = slot_span(a, s);
+  const int row0 = shared ? __ldg(a.tok_start + s) * G : 0;
+  if (threadIdx.x < 2 && shared) {
+    const int per = __ldg(a.line + 1), len = __ldg(a.line + 2);
+    const int u = ((row0 >> 8) + (int)threadIdx.x) * a.n_kv + g;
+    const int x0 = u * len / per;
+    s_cut[threadIdx.x][0] = x0;
+    s_cut[threadIdx.x][1] = (u * len + a.px_steps - 1) / per - x0 + 1;
+  } else if (threadIdx.x == 2) {
+    const int per = __ldg(a.line), pb = __ldg(a.pair_start + pair);
+    s_own[0] = pb / per;
+    s_own[1] = (pb + sp.blocks - 1) / per - s_own[0] + 1;
+  }
+  __syncthreads();
   const int item = threadIdx.x % kItems, ln = threadIdx.x / kItems;
   const int i = blockIdx.y * kItems + item;
-  const int d = i / rows, r = i - d * rows, t = r / G;
-  const int own_per = __ldg(a.line), pb = __ldg(a.pair_start + pair);
-  const bool shared = a.px_steps > 0;
-  const int px_per = shared ? __ldg(a.line + 1) : 1, px_len = shared ? __ldg(a.line + 2) : 0;
-  const int tok0 = shared ? __ldg(a.tok_start + s) : 0;
-  const SlotSpan sp = slot_span(a, s);
+  const int d = i >> row_bits, r = i & ((1 << row_bits) - 1);
+  // r / G for r < 64: the product is off by less than 1/2 G steps of 2^-24
+  const int t = (int)(((float)r + 0.5f) * (1.0f / (float)G));
   Joined jn{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-  if (i < rows * (D / 4) && t < sp.n_new && sp.len - sp.n_new + t >= 0) {
-    const int row = tok0 * G + r, u = (row >> 8) * a.n_kv + g, rr = row & 255;
-    const int x0 = u * px_len / px_per;
-    const int nx = shared ? (u * px_len + a.px_steps - 1) / px_per - x0 + 1 : 0;
-    const int c0 = pb / own_per, n = nx + (pb + sp.blocks - 1) / own_per - c0 + 1;
-    join_parts<6>(jn, (n - ln + kLanes - 1) / kLanes, d,
-                  [&](int c, const float*& p, int& ld, int& prow) {
-                    const int k = c * kLanes + ln;
-                    const bool px = k < nx;
-                    ld = px ? 256 : kR;
-                    prow = px ? rr : r;
-                    p = px ? a.px_part + (int64_t)(x0 + k + u) * 256 * (D + 2)
-                           : a.part + (int64_t)(c0 + k - nx + pair) * kR * (D + 2);
-                  });
+  const bool here = r < rows && d < D / 4;
+  if (here && t < sp.n_new && sp.len - sp.n_new + t >= 0) {
+    const int row = row0 + r, tile = (row >> 8) - (row0 >> 8), u = (row >> 8) * a.n_kv + g;
+    const int nx = shared ? s_cut[tile][1] : 0, n = nx + s_own[1];
+    const PartRef px = part_ref(a.px_part + (int64_t)(shared ? s_cut[tile][0] + u : 0) * 256 * (D + 2),
+                                256, row & 255, d);
+    const PartRef own = part_ref(a.part + (int64_t)(s_own[0] + pair) * kR * (D + 2), kR, r, d);
+    join_parts<6>(jn, (n - ln + kLanes - 1) / kLanes, [&](int c) {
+      const int k = c * kLanes + ln;
+      return k < nx ? PartRef{px.p + k * (256 * (D + 2)), px.l_at, px.o_at}
+                    : PartRef{own.p + (k - nx) * (kR * (D + 2)), own.l_at, own.o_at};
+    });
   }
   if (kLanes > 1) {
     s_o[ln][item] = jn.o;
@@ -637,14 +657,18 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnBatchArgs a, i
       jn.o.w = fmaf(v.w, w, jn.o.w);
     }
   }
-  if (i < rows * (D / 4)) store4<F16>(out_row(a, s, g, G, r, D) + 4 * d, jn.o, jn.L);
+  if (here)
+    store4<F16>(a.o + (((int64_t)s * a.T + t) * a.n_q + g * G + r - t * G) * D + 4 * d, jn.o, jn.L);
 }
 
 template <bool F16, int D, int kLanes>
 cudaError_t launch_join(const AttnBatchArgs& a, int kR, cudaStream_t stream) {
-  const int items = a.T * (a.n_q / a.n_kv) * (D / 4), per = 256 / kLanes;
+  const int rows = a.T * (a.n_q / a.n_kv), per = 256 / kLanes;
+  int bits = 0;
+  while (1 << bits < rows) ++bits;
   return launch_pdl(attn_join_kernel<F16, D, kLanes>,
-                    dim3(a.n_slots * a.n_kv, (items + per - 1) / per), dim3(256), 0, stream, a, kR);
+                    dim3(a.n_slots, (((D / 4) << bits) + per - 1) / per, a.n_kv), dim3(256), 0,
+                    stream, a, kR, bits);
 }
 
 bool attn_batch_supported(const moe_attn_batch_shape_t* s) {

@@ -9,7 +9,10 @@ library has not been built, load() raises.
 Names follow the C ABI: moe_route, moe_plan, moe_expert_ffn_w4,
 moe_combine, moe_layer_w4, moe_workspace_bytes, moe_max_blocks,
 moe_workspace_init, moe_query_device_status, moe_debug_dequant_w4,
-moe_debug_dequant_w4_decode.
+moe_debug_dequant_w4_decode; for one sequence moe_attn_decode, moe_gdn_scan,
+moe_gdn_chunked_scan; for a batch of requests over one page pool
+moe_cache_fork, moe_cache_reserve, moe_cache_write, moe_cache_compact,
+moe_cache_copy_pages, moe_attn_batch, moe_verify_drafts.
 """
 import ctypes as C
 import os

@@ -216,6 +216,69 @@ def test_joint_projection_slices():
     c.check(q=qkv.to(DEV)[:, :, :n_q])
 
 
+def test_absent_rows_are_zero_whatever_lies_there():
+    """Queries of tokens that are not there hold NaN; a slot whose values are
+    infinite gives infinities to its own row only, and zeros to absent ones."""
+    for prefix in (0, 40):
+        P = 64 * prefix
+        c = Case(20 + prefix, [(P + 100, 1), (P + 70, 2), (0, 0), (P + 5, 3)] * 8, 3, 16, 2, 128,
+                 prefix=prefix)
+        for s in range(32):
+            c.q[s, c.n_new[s]:] = float("nan")
+        got = c.check()
+        page = c.table[0, prefix]
+        c.v[page, 0, 3, 5] = float("inf")
+        again = c.run()
+        assert np.isposinf(again[0, 0, :8, 5]).all()
+        again[0, 0, :8, 5] = got[0, 0, :8, 5]
+        np.testing.assert_array_equal(again, got)
+
+
+def test_pages_past_32_bits_of_elements():
+    """A pool of 150000 pages of 2 heads: 2.5e9 elements, the pages used at its
+    end, in a per-slot call and in one with a shared part."""
+    n_phys, n_kv, D = 150000, 2, 128
+    for prefix in (0, 60):
+        c = Case(31, [(64 * prefix + 200, 1)] * 12, 1, 16, n_kv, D, prefix=prefix)
+        small = c.k.shape[0]
+        big = torch.zeros((n_phys, n_kv, 64, D), dtype=c.k.dtype, device=DEV)
+        bigv = torch.zeros_like(big)
+        big[n_phys - small:] = c.k.to(DEV)
+        bigv[n_phys - small:] = c.v.to(DEV)
+        off = n_phys - small
+        up = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(DEV)  # noqa: E731
+        shape = m.make_attn_batch_shape(12, 1, 16, n_kv, D, c.table.shape[1], prefix)
+        ws = m.alloc_attn_batch_workspace(shape, DEV)
+        o = torch.empty((12, 1, 16, D), dtype=c.k.dtype, device=DEV)
+        m.moe_attn_batch(shape, c.q.to(DEV), big, bigv, up(np.where(c.table < 0, -1, c.table + off)),
+                         up(c.lens), o, ws, prefix=up(c.prefix + off) if prefix else None)
+        assert m.moe_query_device_status(ws) == 0
+        np.testing.assert_array_equal(o.cpu().double().numpy(), c.run())
+        del big, bigv
+
+
+def test_two_streams_with_their_own_workspaces():
+    cases = [Case(41, [(64 * 30 + 90, 2)] * 40, 2, 16, 2, 128, prefix=30),
+             Case(42, [(700, 1)] * 30, 1, 8, 8, 64)]
+    want = [c.run() for c in cases]
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(DEV)  # noqa: E731
+    work = []
+    for c in cases:
+        B, T, n_q, n_kv, D, P, dtype = c.dims
+        shape = m.make_attn_batch_shape(B, T, n_q, n_kv, D, c.table.shape[1], P, dtype)
+        work.append((shape, c.q.to(DEV), c.k.to(DEV), c.v.to(DEV), up(c.table), up(c.lens),
+                     torch.empty_like(c.q, device=DEV), m.alloc_attn_batch_workspace(shape, DEV),
+                     up(c.n_new), up(c.prefix) if P else None, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for shape, q, k, v, tab, ln, o, ws, nn, pre, st in work:
+            with torch.cuda.stream(st):
+                m.moe_attn_batch(shape, q, k, v, tab, ln, o, ws, n_new=nn, prefix=pre)
+    torch.cuda.synchronize()
+    for w, x in zip(want, work):
+        np.testing.assert_array_equal(x[6].cpu().double().numpy(), w)
+
+
 def test_bad_pages_are_recorded_and_left_out():
     c = Case(14, [(64 * 3 + 250, 1), (64 * 3 + 10, 1)], 1, 16, 2, 128, prefix=3)
     t = c.table.copy()

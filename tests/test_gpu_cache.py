@@ -250,6 +250,49 @@ def test_copy_pages_out_and_in():
     assert m.moe_query_device_status(c.ws) == m.MOE_ERR_BAD_INPUT
 
 
+def test_pages_past_32_bits_of_elements():
+    """Pools of 150000 pages of 2 heads of 128: 2.5e9 elements. Copy-on-write
+    and write at their end, then everything brought to the front."""
+    n_phys, n_kv, D = 150000, 2, 128
+    shape = m.make_cache_shape(3, 2, n_phys, n_kv, D)
+    ws = m.alloc_cache_workspace(shape, DEV)
+    pools = [torch.zeros((n_phys, n_kv, 64, D), dtype=torch.int16, device=DEV) for _ in range(2)]
+    table = np.full((3, 2), -1, np.int32)
+    table[:, 0] = (n_phys - 1, n_phys - 1, n_phys - 7)
+    lens = np.array([10, 10, 64], np.int32)
+    refs = np.ones(n_phys, np.int32)  # all pinned but a few at the end
+    refs[n_phys - 1], refs[[n_phys - 3, n_phys - 2, n_phys - 9]] = 2, 0
+    g = torch.Generator(device=DEV).manual_seed(0)
+    for p in pools:
+        p[n_phys - 10:] = torch.randint(-99, 99, (10, n_kv, 64, D), generator=g, device=DEV,
+                                        dtype=torch.int16)
+    before = [p[n_phys - 10:].clone() for p in pools]
+    meta = m.CacheMeta(dev(table), dev(lens), dev(refs))
+    out, granted = m.CacheMeta.empty(shape, DEV), torch.empty(3, dtype=torch.int32, device=DEV)
+    ptable = m.pool_table(pools)
+    m.moe_cache_reserve(shape, meta, dev(np.array([2, 2, 2], np.int32)), out, granted, ptable, ws)
+    new = torch.randint(100, 200, (3, 2, n_kv, D), generator=g, device=DEV, dtype=torch.int16)
+    m.moe_cache_write(shape, out, granted, new, new, pools[0], pools[1], ws)
+    assert m.moe_query_device_status(ws) == 0 and granted.tolist() == [2, 2, 2]
+    assert out.table.tolist() == [[n_phys - 9, -1], [n_phys - 3, -1], [n_phys - 7, n_phys - 2]]
+    for p, b in zip(pools, before):
+        for s, page in ((0, 1), (1, 7)):
+            torch.testing.assert_close(p[n_phys - 10 + page, :, :10], b[9, :, :10], rtol=0, atol=0)
+            torch.testing.assert_close(p[n_phys - 10 + page, :, 10:12], new[s].transpose(0, 1),
+                                       rtol=0, atol=0)
+        torch.testing.assert_close(p[n_phys - 2, :, :2], new[2].transpose(0, 1), rtol=0, atol=0)
+    # free everything but the slots' pages, and compact
+    out.refs.zero_()
+    out.refs[out.table[out.table >= 0].long()] = 1
+    want = [p[out.table[2, 1].long()].clone() for p in pools]
+    n_live = torch.empty(1, dtype=torch.int32, device=DEV)
+    m.moe_cache_compact(shape, out, meta, n_live, ptable, ws)
+    assert m.moe_query_device_status(ws) == 0 and n_live.item() == 4
+    assert meta.table.tolist() == [[0, -1], [2, -1], [1, 3]]
+    for p, w in zip(pools, want):
+        torch.testing.assert_close(p[3], w, rtol=0, atol=0)
+
+
 def test_step_in_a_graph_on_a_side_stream():
     """Reserve and write captured once and replayed over a state that moves
     on: the graph's calls read what the buffers hold at the time."""

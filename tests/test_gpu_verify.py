@@ -167,6 +167,30 @@ def test_rows_at_odd_addresses():
     np.testing.assert_array_equal(acc.cpu().numpy(), want[1])
 
 
+def test_graph_replays_with_new_numbers():
+    """Captured once; the random numbers of the time decide."""
+    p, q, draft, n, u = draws(9, 40, 4, 20000, "fp32")
+    shape = m.make_verify_shape(40, 4, 20000, "fp32")
+    ws = m.alloc_verify_workspace(shape, DEV)
+    tokens = torch.empty((40, 5), dtype=torch.int32, device=DEV)
+    acc = torch.empty(40, dtype=torch.int32, device=DEV)
+    dp, dq, dd, dn = p.to(DEV), q.to(DEV), torch.from_numpy(draft).to(DEV), torch.from_numpy(n).to(DEV)
+    du = torch.from_numpy(u).to(DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        m.moe_verify_drafts(shape, dp, dq, dd, dn, du, tokens, acc, ws)
+    for seed in range(4):
+        u = np.random.default_rng(seed).random((40, 5), np.float32)
+        du.copy_(torch.from_numpy(u))
+        g.replay()
+        torch.cuda.synchronize()
+        want = ref.verify(p.double().numpy(), q.double().numpy(), draft, n, u.astype(np.float64))
+        np.testing.assert_array_equal(tokens.cpu().numpy(), want[0])
+        np.testing.assert_array_equal(acc.cpu().numpy(), want[1])
+
+
 def test_binding_refuses_wrong_tensors():
     shape = m.make_verify_shape(2, 2, 100, "fp32")
     ws = m.alloc_verify_workspace(shape, DEV)

@@ -81,21 +81,22 @@ __global__ void __launch_bounds__(256)
     if (i0 + k * 256 < n) out[i0 + k * 256] = __ldg(in + i0 + k * 256);
 }
 
-// Four warps per slot: the row of its parent cut to the new length, and the
-// difference in the pages' counts (none where a page stays in its place).
-// refs: the counts are not in the new state yet, and this CTA is the only one.
+// `per` threads per slot (a warp or four): the row of its parent cut to the new
+// length, and the difference in the pages' counts (none where a page stays in
+// its place). refs: the counts are not in the new state yet, and this CTA is
+// the only one.
 __global__ void __launch_bounds__(kOneCta)
     cache_fork_kernel(const moe_cache_meta_t in, const moe_cache_meta_t out,
                       const int32_t* __restrict__ parent, const int32_t* __restrict__ keep,
-                      int n_slots, int max_blocks, int n_phys, bool refs, Ctrl* ctrl) {
+                      int n_slots, int max_blocks, int n_phys, int per, bool refs, Ctrl* ctrl) {
   pdl_wait();
   pdl_trigger();
   if (refs) {
     for (int i = threadIdx.x; i < n_phys; i += blockDim.x) out.refs_dev[i] = __ldg(in.refs_dev + i);
     __syncthreads();
   }
-  const int per = blockDim.x >> 7, j0 = threadIdx.x & 127;
-  for (int s = blockIdx.x * per + (threadIdx.x >> 7); s < n_slots; s += gridDim.x * per) {
+  const int j0 = threadIdx.x & (per - 1), slots = blockDim.x / per;
+  for (int s = blockIdx.x * slots + threadIdx.x / per; s < n_slots; s += gridDim.x * slots) {
     const int a = __ldg(parent + s);
     const bool live = a >= 0 && a < n_slots;
     if (j0 == 0 && a >= n_slots) set_error(ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kOneCta)
     const int32_t* row_old = in.table_dev + (int64_t)s * max_blocks;
     const int32_t* row_new = in.table_dev + (int64_t)(live ? a : s) * max_blocks;
     int32_t* row = out.table_dev + (int64_t)s * max_blocks;
-    for (int j = j0; j < max_blocks; j += 128) {
+    for (int j = j0; j < max_blocks; j += per) {
       int po = j < nb_old ? __ldg(row_old + j) : -1, pn = j < nb_new ? __ldg(row_new + j) : -1;
       if ((j < nb_old && (po < 0 || po >= n_phys)) || (j < nb_new && (pn < 0 || pn >= n_phys)))
         set_error(ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
@@ -525,10 +526,16 @@ int copy_ctas(int64_t pages, int nsm) { return (int)(pages < nsm * 8 ? pages : n
 
 size_t cache_ws_bytes(const moe_cache_shape_t* s) { return cache_ws(s).total; }
 
-// Few enough words that one CTA brings them over in the time of a launch.
+// Few enough that one CTA, with four warps or one for a row, is done in the
+// time of a launch: 2.8 us for a round or two of 32 rows x 32 entries, 4.7 for
+// three, against 3.3 of a CTA a slot after a launch for the counts (one CTA
+// that was given 461 slots took 40 us).
 namespace {
-bool small_state(const moe_cache_shape_t* s) {
-  return (int64_t)s->n_slots * s->max_blocks + s->n_phys <= 16384;
+int row_threads(const moe_cache_shape_t* s) { return s->n_slots <= kOneCta / 128 ? 128 : 32; }
+bool small_fork(const moe_cache_shape_t* s) {
+  const int per = row_threads(s);
+  return (int64_t)ceil_div(s->n_slots, kOneCta / per) * ceil_div(s->max_blocks, per) <= 2 &&
+         s->n_phys <= 8192;
 }
 }  // namespace
 
@@ -536,14 +543,14 @@ cudaError_t launch_cache_fork(const moe_cache_shape_t* s, const moe_cache_meta_t
                               const moe_cache_meta_t& out, const int32_t* parent,
                               const int32_t* keep, uint8_t* ws, cudaStream_t stream) {
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(ws);
-  if (small_state(s))
+  if (small_fork(s))
     return launch_pdl(cache_fork_kernel, dim3(1), dim3(kOneCta), 0, stream, in, out, parent, keep,
-                      s->n_slots, s->max_blocks, s->n_phys, true, ctrl);
+                      s->n_slots, s->max_blocks, s->n_phys, row_threads(s), true, ctrl);
   const cudaError_t e = launch_pdl(cache_copy_refs_kernel, dim3(ceil_div(s->n_phys, 1024)),
                                    dim3(256), 0, stream, in.refs_dev, out.refs_dev, s->n_phys);
   if (e != cudaSuccess) return e;
   return launch_pdl(cache_fork_kernel, dim3(s->n_slots), dim3(128), 0, stream, in, out, parent,
-                    keep, s->n_slots, s->max_blocks, s->n_phys, false, ctrl);
+                    keep, s->n_slots, s->max_blocks, s->n_phys, 128, false, ctrl);
 }
 
 cudaError_t launch_cache_reserve(const moe_cache_shape_t* s, const moe_cache_meta_t& in,
@@ -552,9 +559,10 @@ cudaError_t launch_cache_reserve(const moe_cache_shape_t* s, const moe_cache_met
                                  cudaStream_t stream) {
   const CacheWs w = cache_ws(s);
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(ws);
-  // one CTA copies a few pages in a few microseconds, should every slot need it
+  // one CTA brings a small state over, 4096 words at a time, and copies a few
+  // pages, should every slot need it, in a few microseconds
   const int64_t copies = (int64_t)s->n_slots * pools.n;
-  const bool all = small_state(s) && copies * s->n_kv * s->D <= 8192;
+  const bool all = (int64_t)s->n_slots * s->max_blocks + s->n_phys <= 16384 && copies * s->n_kv * s->D <= 8192;
   if (!all) {
     const int ctas = ceil_div((int64_t)s->n_slots * s->max_blocks + s->n_phys, 2048);
     const cudaError_t e =

@@ -40,9 +40,8 @@
 namespace moe {
 
 namespace {
-constexpr int kOThr = 128;          // the four warps that compute
-constexpr int kOAll = kOThr + 32;   // and the one that loads
-constexpr int kOAreaFloats = 2048;  // 8 KB where the warps' O meet
+constexpr int kOThr = 128;         // the four warps that compute
+constexpr int kOAll = kOThr + 32;  // and the one that loads
 
 template <bool F16>
 __device__ __forceinline__ void mma16816t(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -57,6 +56,12 @@ __device__ __forceinline__ void mma16816t(float (&d)[4], const uint32_t (&a)[4],
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 __device__ __forceinline__ void ldm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -139,16 +144,16 @@ __device__ __forceinline__ void join_parts(Joined& j, int n, At at) {
 __device__ __forceinline__ PartRef part_ref(const float* part, int ld, int r, int d) {
   return PartRef{part + r, ld, 2 * ld + 4 * (d * ld + r) - r};
 }
-__device__ __forceinline__ uint16_t* out_row(const AttnBatchArgs& a, int s, int g, int G, int r,
-                                             int D) {
-  return a.o + (((int64_t)s * a.T + r / G) * a.n_q + g * G + r % G) * D;
-}
-
 template <int D>
 struct OwnRing {
   static constexpr int kTile = kBlk * D * 2;       // bytes of a block's keys (or values)
   static constexpr int kStages = D == 64 ? 4 : 3;  // 64 and 96 KB
 };
+// Two places for a pair's queries, so that the next pair's come while one is
+// computed (they took a seventh of a short pair); with more rows there is no
+// room for them beside the ring.
+template <int D, int MT>
+constexpr int kQTile = MT * 16 * D * 2 <= 4096 ? MT * 16 * D * 2 : 0;
 // CTAs an SM: two, or three where registers and stages allow (19.1 us instead
 // of 20.2 for 33 slots of up to 5000 positions)
 __host__ __device__ constexpr int own_ctas(int D, int MT) { return D == 64 && MT == 1 ? 3 : 2; }
@@ -163,8 +168,9 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
   constexpr int kNT = kPos / 8;     // score n-tiles of a warp
   constexpr int kKS = D / 16, kDT = D / 8;
   constexpr int kR = MT * 16;       // rows of the tiles
-  constexpr int kCW = kOAreaFloats / kR < D ? kOAreaFloats / kR : D;  // columns of O joined at a time
-  constexpr int kLd = kCW + 4;      // row stride: rows start on other banks
+  constexpr int kQB = kQTile<D, MT>;
+  constexpr int kQPass = kQB / 16 / kOThr;     // 16-byte pieces of queries a thread fetches
+  constexpr int kCols = kR * D / 4 / kOThr;    // float4 of the pair's output a thread has
   extern __shared__ __align__(1024) uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
   __shared__ int s_bad[kStages];
@@ -174,7 +180,6 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
   __shared__ float s_M[kR], s_L[kR];        // the segment's
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
   uint8_t* sm = sm_raw + (sbase - smem_u32(sm_raw));
-  float* area = reinterpret_cast<float*>(sm + kStages * 2 * kTile);  // [kR][kLd]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t fb = smem_u32(&full[0]), eb = smem_u32(&empty[0]);
   if (tid == 0) {
@@ -323,6 +328,30 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
     const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(D)
     const int mi = lane >> 3, rr = lane & 7;
     auto meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    // rows r = t * G + head in group, of the products ...
+    const int r0 = mt * 16 + gq, r1 = r0 + 8;
+    const int t0 = r0 < rows ? r0 / G : a.T, t1 = r1 < rows ? r1 / G : a.T;
+    // ... of the output: one a thread, every 128 / kR-th float4 of it ...
+    const int ro = tid % kR, co = tid / kR, to = ro / G;
+    const int64_t o_off = ((int64_t)to * a.n_q + ro - to * G) * D + 4 * co;
+    // ... and of the queries to fetch
+    const uint32_t sq = sbase + kStages * 2 * kTile;
+    int64_t q_off[kQPass > 0 ? kQPass : 1];
+#pragma unroll
+    for (int k = 0; k < kQPass; ++k) {
+      const int r = tid / (D / 8) + k * (kOThr * 8 / D), t = r / G;
+      q_off[k] = r < rows ? t * a.q_stride + (r - t * G) * D + tid % (D / 8) * 8 : -1;
+    }
+    auto fetch_q = [&](int slot, int head, int place) {
+      const uint16_t* q0 = a.q + (int64_t)slot * a.T * a.q_stride + head * G * D;
+#pragma unroll
+      for (int k = 0; k < kQPass; ++k) {
+        const int r = tid / (D / 8) + k * (kOThr * 8 / D);
+        if (q_off[k] >= 0)
+          cp_async16(sq + place * kQB + r * (D * 2) + ((tid % (D / 8)) ^ (r & 7)) * 16, q0 + q_off[k]);
+      }
+    };
+    int place = -1;  // of the pair's queries, -1: not asked for yet
     int f = f0, it = 0;  // it: blocks done
     while (f < f1) {
       const int fe = min(f1, pb + sp.blocks);
@@ -336,15 +365,30 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
         continue;
       }
       const bool whole = f == pb && fe == pb + sp.blocks;
-      // rows r = t * G + head in group; a row's last position, -1: sees nothing
+      // where the pair after this one starts, whose span and queries are on
+      // their way from here on
+      const int next_pb = pb + sp.blocks + a.pair_cost;
+      const int next_g = g + 1 == a.n_kv ? 0 : g + 1, next_s = next_g == 0 ? s + 1 : s;
+      // a row's last position, -1: sees nothing
       const int base = sp.len - sp.n_new;  // may be negative
-      const int r0 = mt * 16 + gq, r1 = r0 + 8;
-      const int lim0 = r0 < rows && r0 / G < sp.n_new ? base + r0 / G : -1;
-      const int lim1 = r1 < rows && r1 / G < sp.n_new ? base + r1 / G : -1;
+      const int lim0 = t0 < sp.n_new ? base + t0 : -1;
+      const int lim1 = t1 < sp.n_new ? base + t1 : -1;
       uint32_t qa[kKS][4];
-      {
-        const uint16_t* q0 = lim0 >= 0 ? a.q + ((int64_t)s * a.T + r0 / G) * a.q_stride + (g * G + r0 % G) * D : nullptr;
-        const uint16_t* q1 = lim1 >= 0 ? a.q + ((int64_t)s * a.T + r1 / G) * a.q_stride + (g * G + r1 % G) * D : nullptr;
+      if (kQB > 0) {
+        if (place < 0) fetch_q(s, g, place = 0);
+        cp_async_wait();
+        meet();  // what warps share is this pair's from here
+        // rows that see nothing hold anything, which reaches nothing but them
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks)
+          ldm_x4(sq + place * kQB + (mt * 16 + (mi & 1) * 8 + rr) * (D * 2) +
+                     ((ks * 2 + (mi >> 1)) ^ rr) * 16,
+                 qa[ks]);
+        place ^= 1;
+        if (next_pb < f1) fetch_q(next_s, next_g, place);
+      } else {
+        const uint16_t* q0 = lim0 >= 0 ? a.q + ((int64_t)s * a.T + t0) * a.q_stride + (g * G + r0 - t0 * G) * D : nullptr;
+        const uint16_t* q1 = lim1 >= 0 ? a.q + ((int64_t)s * a.T + t1) * a.q_stride + (g * G + r1 - t1 * G) * D : nullptr;
 #pragma unroll
         for (int ks = 0; ks < kKS; ++ks) {
           const int d = ks * 16 + 2 * cq;
@@ -354,6 +398,8 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
           qa[ks][3] = q1 ? __ldg(reinterpret_cast<const uint32_t*>(q1 + d + 8)) : 0u;
         }
       }
+      SlotSpan next_sp = sp;
+      if (next_pb < f1 && next_s != s) next_sp = slot_span(a, next_s);
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
       float oacc[kDT][4];
 #pragma unroll
@@ -369,11 +415,13 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
         if (pos0 + kBlk > sp.len) {
           // rows past the slot's end hold anything, NaN too: 0 x NaN in P V
           // would reach the output, so each warp sets those it reads to 0
-          const int z0 = max(sp.len - pos0, kPos * ps), z1 = kPos * (ps + 1);
-          for (int i = lane; i < (z1 - z0) * (D / 8); i += 32)
-            *reinterpret_cast<uint4*>(sm + st * 2 * kTile + kTile +
-                                      swz64(z0 + i / (D / 8), i % (D / 8))) =
-                make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int k = 0; k < kPos * (D / 8) / 32; ++k) {
+            const int z = kPos * ps + (k * 32 + lane) / (D / 8);
+            if (pos0 + z >= sp.len)
+              *reinterpret_cast<uint4*>(sm + st * 2 * kTile + kTile + swz64(z, lane % (D / 8))) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
           __syncwarp();
         }
         // S = Q K^T over this warp's positions
@@ -447,12 +495,18 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
             mma16816t<F16>(oacc[j], pa[kp], vb[0], vb[1]);
             mma16816t<F16>(oacc[j + 1], pa[kp], vb[2], vb[3]);
           }
+        if (f + 1 == fe) break;  // the last block's stage is kept for what follows
         // the stage goes back to the loader, after this warp's reads and writes
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(eb + 8u * st);
       }
-      // ---- the slices' (m, l, O) become the segment's
+      // ---- the slices' (m, l, O) become the segment's. Each warp's O, weighed,
+      // goes to a quarter of the stage whose keys and values all are done with
+      // ([16][D] floats, 16-byte pieces in an order that spreads the banks), and
+      // a thread then adds up what the slices have for it. (One place of 8 KB
+      // that the warps added to in turn, and rows by division, took three times
+      // as long: 1.5 of a short pair's 3.6 us.)
 #pragma unroll
       for (int d = 1; d <= 2; d <<= 1) {
         l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, d);
@@ -494,50 +548,57 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
         s_L[r1] = L1;
       }
       const float w0 = ex2(m0 - U0), w1 = ex2(m1 - U1);
+      const int st = it % kStages;
+      float* area = reinterpret_cast<float*>(sm + st * 2 * kTile);
+      auto piece = [](int r) { return ((r & 3) << 1) | ((r >> 2) & 1); };
+      {
+        float* mine = area + warp * (16 * D) + gq * D + 2 * (cq & 1);
+        const int x = piece(gq);  // and of row gq + 8
+#pragma unroll
+        for (int j = 0; j < kDT; ++j) {
+          float* p0 = mine + ((2 * j + (cq >> 1)) ^ x) * 4;
+          *reinterpret_cast<float2*>(p0) = make_float2(oacc[j][0] * w0, oacc[j][1] * w0);
+          *reinterpret_cast<float2*>(p0 + 8 * D) = make_float2(oacc[j][2] * w1, oacc[j][3] * w1);
+        }
+      }
+      meet();
       // the pair's parts: one place per CTA and pair, both of which grow
       // along the line
       const int pair = s * a.n_kv + g;
       const bool direct = whole && !a.join;
       float* part = a.part + (int64_t)((int)blockIdx.x + pair) * kR * (D + 2);
+      uint16_t* out = a.o + ((int64_t)s * a.T * a.n_q + g * G) * D + o_off;
+      if (ro < rows) {
+        const float* from = area + (ro >> 4) * (16 * D) + (ro & 15) * D;
+        const int x = piece(ro);
 #pragma unroll
-      for (int cb = 0; cb < D; cb += kCW) {
+        for (int k = 0; k < kCols; ++k) {
+          const int d = co + k * (kOThr / kR);
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int k = 0; k < kNS; ++k) {
-          if (ps == k) {
-#pragma unroll
-            for (int j = 0; j < kCW / 8; ++j) {
-              const int jj = cb / 8 + j;
-              float* p0 = area + r0 * kLd + 8 * j + 2 * cq;
-              float* p1 = area + r1 * kLd + 8 * j + 2 * cq;
-              if (k == 0) {
-                p0[0] = oacc[jj][0] * w0;
-                p0[1] = oacc[jj][1] * w0;
-                p1[0] = oacc[jj][2] * w1;
-                p1[1] = oacc[jj][3] * w1;
-              } else {
-                p0[0] += oacc[jj][0] * w0;
-                p0[1] += oacc[jj][1] * w0;
-                p1[0] += oacc[jj][2] * w1;
-                p1[1] += oacc[jj][3] * w1;
-              }
-            }
+          for (int i = 0; i < kNS; ++i) {
+            const float4 u = *reinterpret_cast<const float4*>(from + i * MT * (16 * D) + (d ^ x) * 4);
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
           }
-          meet();
-        }
-        for (int i = tid; i < rows * (kCW / 4); i += kOThr) {
-          const int d = i / rows, r = i - d * rows;
-          const float4 v = *reinterpret_cast<const float4*>(area + r * kLd + 4 * d);
           if (direct)
-            store4<F16>(out_row(a, s, g, G, r, D) + cb + 4 * d, v, s_L[r]);
+            store4<F16>(out + k * (kOThr / kR * 4), v, s_L[ro]);
           else
-            *reinterpret_cast<float4*>(part + 2 * kR + ((cb / 4 + d) * kR + r) * 4) = v;
+            *reinterpret_cast<float4*>(part + 2 * kR + (d * kR + ro) * 4) = v;
         }
-        meet();
       }
+      // the stage goes back to the loader
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(eb + 8u * st);
+      ++f;
+      ++it;
       if (!direct) {
-        for (int r = tid; r < rows; r += kOThr) {
-          part[r] = s_M[r];
-          part[kR + r] = s_L[r];
+        if (tid < rows) {
+          part[tid] = s_M[tid];
+          part[kR + tid] = s_L[tid];
         }
         if (a.join) {
           if (tid == 0 && pb >= f0) a.pair_start[pair] = pb;  // the pair's first CTA
@@ -553,27 +614,27 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
             __threadfence();
           }
           meet();
-          if (s_last) {
-            for (int i = tid; i < rows * (D / 4); i += kOThr) {
-              const int d = i / rows, r = i - d * rows;
+          if (s_last && ro < rows) {
+#pragma unroll 1
+            for (int k = 0; k < kCols; ++k) {
               Joined jn{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-              const PartRef own = part_ref(a.part + (int64_t)(c0 + pair) * kR * (D + 2), kR, r, d);
+              const PartRef own = part_ref(a.part + (int64_t)(c0 + pair) * kR * (D + 2), kR, ro,
+                                           co + k * (kOThr / kR));
               join_parts<4>(jn, c1 - c0 + 1, [&](int c) {
                 return PartRef{own.p + c * (kR * (D + 2)), own.l_at, own.o_at};
               });
-              store4<F16>(out_row(a, s, g, G, r, D) + 4 * d, jn.o, jn.L);
+              store4<F16>(out + k * (kOThr / kR * 4), jn.o, jn.L);
             }
           }
         }
-        meet();  // s_M, s_L and s_last are the next pair's from here
       }
+      if (kQB == 0) meet();  // what warps share is the next pair's from here
       // ---- the next pair
-      pb += sp.blocks + a.pair_cost;
+      pb = next_pb;
       f = pb;
-      if (++g == a.n_kv) {
-        g = 0;
-        if (++s < a.n_slots) sp = slot_span(a, s);
-      }
+      g = next_g;
+      s = next_s;
+      sp = next_sp;
     }
     if (a.join && blockIdx.x == 0 && tid == 0) a.line[0] = per;
   }
@@ -713,8 +774,8 @@ size_t own_part_bytes(const moe_attn_batch_shape_t* s) {
 template <bool F16, int D, int MT>
 cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const AttnBatchArgs& a,
                        int grid, cudaStream_t stream) {
-  const size_t smem = 1024 + (size_t)OwnRing<D>::kStages * 2 * OwnRing<D>::kTile +
-                      (kOAreaFloats + MT * 16 * 4) * 4;
+  const size_t smem =
+      1024 + (size_t)OwnRing<D>::kStages * 2 * OwnRing<D>::kTile + 2 * kQTile<D, MT>;
   cudaError_t e = cudaFuncSetAttribute(attn_own_kernel<F16, D, MT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

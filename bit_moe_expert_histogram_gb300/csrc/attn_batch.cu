@@ -57,12 +57,6 @@ __device__ __forceinline__ void mma16816t(float (&d)[4], const uint32_t (&a)[4],
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
 __device__ __forceinline__ void ldm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -348,7 +342,8 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
       for (int k = 0; k < kQPass; ++k) {
         const int r = tid / (D / 8) + k * (kOThr * 8 / D);
         if (q_off[k] >= 0)
-          cp_async16(sq + place * kQB + r * (D * 2) + ((tid % (D / 8)) ^ (r & 7)) * 16, q0 + q_off[k]);
+          cp_async16(sq + place * kQB + r * (D * 2) + ((tid % (D / 8)) ^ (r & 7)) * 16,
+                     q0 + q_off[k], 16);
       }
     };
     int place = -1;  // of the pair's queries, -1: not asked for yet
@@ -830,6 +825,7 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
     const PrefixLine line = prefix_line(s, sms);
     a.first = s->prefix_blocks;
     a.px_steps = line.steps;
+    a.px_line = line;
     a.parts = (line.steps + line.per - 1) / line.per + 1;
     px_grid = line.grid;
     a.px_part = a.part + own_part_bytes(s) / 4;

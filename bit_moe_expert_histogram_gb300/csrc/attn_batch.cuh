@@ -19,13 +19,15 @@ __host__ __device__ inline PrefixLine prefix_cut(int pairs, int steps, int ctas)
   p.pairs = pairs;
   p.steps = steps;
   p.len = steps;
-  p.per = (int)(((int64_t)pairs * steps + ctas - 1) / ctas);
+  // below 2^31: the calls' 2^30 blocks in all, and ctas
+  p.per = (int)(((unsigned)pairs * (unsigned)steps + ctas - 1) / (unsigned)ctas);
   p.grid = ctas;
   if (pairs > 0 && pairs <= ctas) {
-    int per = (steps + ctas / pairs - 1) / (ctas / pairs);
+    const unsigned each = (unsigned)ctas / (unsigned)pairs;
+    int per = (int)((steps + each - 1) / each);
     per = per < 2 ? 2 : per;
     if (per <= p.per + kStretch) {
-      const int cuts = (steps + per - 1) / per;
+      const int cuts = (int)((unsigned)(steps + per - 1) / (unsigned)per);
       p.per = per;
       p.len = cuts * per;
       p.grid = pairs * cuts;
@@ -58,6 +60,15 @@ __device__ __forceinline__ SlotSpan slot_span(const AttnBatchArgs& a, int s) {
   const int nb = (r.len + kBlk - 1) / kBlk - a.first;
   r.blocks = r.n_new == 0 || nb < 1 ? 1 : nb;
   return r;
+}
+
+// 16 bytes to shared memory, past the first `bytes` (0 or 16) zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {

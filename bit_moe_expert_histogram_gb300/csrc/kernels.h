@@ -199,6 +199,11 @@ cudaError_t launch_cache_copy_pages(const moe_cache_shape_t* s, int n, const int
                                     const int32_t* dst, const CachePools& from,
                                     const CachePools& to, int n_to, uint8_t* ws, int nsm,
                                     cudaStream_t stream);
+// The shared part's line (attn_prefix.cu): pairs of 256 rows and a head, each
+// with `steps` steps of 128 prefix positions on `len` units; `per` units a CTA.
+struct PrefixLine {
+  int pairs, steps, len, per, grid;
+};
 // Attention of a batch of slots (attn_batch.cu).
 struct AttnBatchArgs {
   const uint16_t* q;   // token (s, t) starts at q_stride * (s * T + t)
@@ -220,15 +225,11 @@ struct AttnBatchArgs {
   // the shared part, when attn_prefix_kernel takes it (px_steps > 0): its
   // line of steps and its parts, per place m[256], l[256], O[D / 4][256][4]
   int px_steps;
+  PrefixLine px_line;  // that line where every slot has all T tokens
   int join;            // attn_join_kernel follows
   int parts;           // about how many parts a row then has
   float* px_part;
   Ctrl* ctrl;
-};
-// The shared part's line (attn_prefix.cu): pairs of 256 rows and a head, each
-// with `steps` steps of 128 prefix positions on `len` units; `per` units a CTA.
-struct PrefixLine {
-  int pairs, steps, len, per, grid;
 };
 PrefixLine prefix_line(const moe_attn_batch_shape_t* s, int sms);
 size_t prefix_part_floats(const moe_attn_batch_shape_t* s, int sms);

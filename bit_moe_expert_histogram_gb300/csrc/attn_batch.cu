@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
   extern __shared__ __align__(1024) uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
   __shared__ int s_bad[kStages];
-  __shared__ int s_abort, s_start, s_off, s_total, s_last;
-  __shared__ int s_scan[kOAll / 32];
+  __shared__ int s_abort, s_start, s_off, s_total, s_per, s_last;
+  __shared__ int s_scan[kOAll / 32], s_tok[kOAll / 32];
   __shared__ float s_m[4][16], s_l[4][16];  // per warp: its rows' maximum and sum
   __shared__ float s_M[kR], s_L[kR];        // the segment's
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
@@ -200,22 +200,44 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
   {
     const int chunk = (a.n_slots + kOAll - 1) / kOAll;
     const int s0 = min(tid * chunk, a.n_slots), s1 = min(s0 + chunk, a.n_slots);
-    int sum = 0;
-    for (int s = s0; s < s1; ++s) sum += slot_span(a, s).blocks + a.pair_cost;
+    int sum = 0, tok = 0;
+    for (int s = s0; s < s1; ++s) {
+      const SlotSpan sp = slot_span(a, s);
+      sum += sp.blocks + a.pair_cost;
+      tok += sp.n_new;
+    }
     sum *= a.n_kv;
+    tok = __reduce_add_sync(0xFFFFFFFFu, tok);
     int incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
       if (lane >= d) incl += o;
     }
-    if (lane == 31) s_scan[warp] = incl;
+    if (lane == 31) {
+      s_scan[warp] = incl;
+      s_tok[warp] = tok;
+    }
     __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += s_scan[w];
-    if (tid == kOAll - 1) s_total = incl;
+    int all = 0;
+    tok = 0;
+    for (int w = 0; w < kOAll / 32; ++w) {
+      if (w == warp) incl += all;
+      all += s_scan[w];
+      tok += s_tok[w];
+    }
+    if (warp == kOAll / 32 - 1) {
+      // with a shared part, as many CTAs as there is room for beside it
+      int n = (int)gridDim.x;
+      if (shared && !a.px_fixed) n = max(min((a.sms - best_line(a, tok, all).grid) * own_ctas(D, MT), n), 1);
+      if (lane == 0) {
+        s_total = all;
+        s_per = (int)((unsigned)(all + n - 1) / (unsigned)n);
+      }
+    }
     __syncthreads();
-    const int per = (s_total + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int f0 = (int)blockIdx.x * per;
+    const int per = s_per;
+    const int f0 = (int)min((int64_t)blockIdx.x * per, (int64_t)s_total);
     int run = incl - sum;
     if (f0 >= run && f0 < incl) {  // one thread's slots hold the first block
       int s = s0;
@@ -230,8 +252,8 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
     __syncthreads();
   }
   const int total = s_total;
-  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-  const int f0 = (int)blockIdx.x * per, f1 = min(f0 + per, total);
+  const int per = s_per;
+  const int f0 = (int)min((int64_t)blockIdx.x * per, (int64_t)total), f1 = min(f0 + per, total);
   int s = s_start;
   SlotSpan sp = slot_span(a, s);
   int g = s_off / (sp.blocks + a.pair_cost);
@@ -776,9 +798,12 @@ cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const AttnB
   if (e != cudaSuccess) return e;
   e = launch_pdl(attn_own_kernel<F16, D, MT>, dim3(grid), dim3(kOAll), smem, stream, tk, tv, a);
   if (e != cudaSuccess || !a.join) return e;
-  // a thread fetches six parts at once
-  if (a.parts <= 6) return launch_join<F16, D, 1>(a, MT * 16, stream);
-  if (a.parts <= 48) return launch_join<F16, D, 4>(a, MT * 16, stream);
+  // A thread fetches six parts at once; with more of them several threads
+  // share an output while all of them run at once (30 parts, 25000 outputs:
+  // 18.8 us the call with four, 20.3 with one; 70000 outputs: 36.2 and 33.4).
+  const int64_t outs = (int64_t)a.n_slots * a.T * a.n_q * (D / 4);
+  if (a.parts <= 6 || outs > 32768) return launch_join<F16, D, 1>(a, MT * 16, stream);
+  if (a.parts <= 48 || outs > 8192) return launch_join<F16, D, 4>(a, MT * 16, stream);
   return launch_join<F16, D, 16>(a, MT * 16, stream);
 }
 template <bool F16, int D>
@@ -817,26 +842,47 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
   a.prefix_blocks = s->prefix_blocks;
   const int sms = nsm < kMostSms ? nsm : kMostSms;
   const int mt = own_tiles(s);
-  int px_grid = 0;
   a.first = 0;
   a.px_steps = 0;
+  int room = sms;  // SMs that the slots' own lines can have
+  a.sms = sms;
+  // about 0.35 us of an SM for a unit (two of them at a time; 0.16, three at a
+  // time, with D = 64) and 1.3 for a step of the shared part
+  a.unit_weight = s->D == 64 ? (mt == 1 ? 0.13f : 0.18f) : (mt == 1 ? 0.27f : 0.3f);
   a.parts = 0;
   if (share(s)) {
-    const PrefixLine line = prefix_line(s, sms);
+    // What the kernel gets of the SMs if every token is there and the slots'
+    // own lines are as short as they can be, and as long: the most that it is
+    // launched with, and what it leaves is the most for the own lines. (CTAs
+    // for nothing cost 2 to 3 us where they stand in the way.) Where the own
+    // lines are over in two steps anyway, nothing depends on the lengths.
+    const PrefixLine whole = prefix_line(s, sms);
+    const int64_t own_pairs = (int64_t)s->n_slots * s->n_kv;
+    auto plan = [&](int64_t units) {
+      PrefixWay best{};
+      for (int i = 0; i < kWays; ++i) {
+        const PrefixWay w =
+            prefix_way(i, whole.pairs, whole.steps, (int)units, a.unit_weight, sms, sms - 1);
+        if (i == 0 || w.time < best.time) best = w;
+      }
+      return best;
+    };
+    const int own_most = s->max_blocks - s->prefix_blocks > 1 ? s->max_blocks - s->prefix_blocks : 1;
+    const PrefixLine line = plan(own_pairs * (1 + a.pair_cost)).line;
+    const PrefixWay least = plan(own_pairs * (own_most + a.pair_cost));
+    a.px_fixed = least.line.grid == line.grid && least.time <= 2.0f;
+    room = sms - least.line.grid;
     a.first = s->prefix_blocks;
     a.px_steps = line.steps;
-    a.px_line = line;
+    a.px_most = line.grid;
     a.parts = (line.steps + line.per - 1) / line.per + 1;
-    px_grid = line.grid;
     a.px_part = a.part + own_part_bytes(s) / 4;
     const cudaError_t e = launch_attn_prefix(s, tk, tv, a, line.grid, stream);
     if (e != cudaSuccess) return e;
   }
-  // as many CTAs as fit, and no more than there can be blocks; beside a shared
-  // part that leaves SMs over, as many as fit there, so that both run at once
+  // as many CTAs as fit there, and no more than there can be blocks
   const int64_t most = (int64_t)s->n_slots * s->n_kv * s->max_blocks;
-  const int beside = own_ctas(s->D, mt) * (px_grid * 5 <= sms * 3 ? sms - px_grid : sms);
-  const int grid = most < beside ? (int)most : beside;
+  const int grid = (int)(most < own_ctas(s->D, mt) * room ? most : own_ctas(s->D, mt) * room);
   // the parts of a pair's own blocks, were all pairs as long as they can be
   const int64_t pairs_n = (int64_t)s->n_slots * s->n_kv;
   a.parts += (int)(grid / pairs_n < s->max_blocks - a.first ? grid / pairs_n : s->max_blocks - a.first);

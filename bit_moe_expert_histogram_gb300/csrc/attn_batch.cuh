@@ -13,21 +13,36 @@ constexpr int kBlk = 64;  // positions per page
 // about kStretch steps beside its own (queries in, O out); cut pair by pair
 // every CTA has one stretch but some CTAs may be left over. The shorter way
 // is taken; a stretch of fewer than two steps would be mostly cost.
+__host__ __device__ inline int cut_up(unsigned n, unsigned d) {  // ceil(n / d)
+#ifdef __CUDA_ARCH__
+  // five of these in a row keep the shared part's kernel waiting: a float
+  // quotient put right takes a third of a division's time (n < 2^31: off by
+  // less than 2^8, by one or less where the quotient is below 2^23)
+  unsigned q = __float2uint_rd(__fdividef((float)n, (float)d));
+  if (q >= (1u << 22)) return (int)((n + d - 1) / d);
+  if (q * d > n) --q;
+  while (q * d < n) ++q;
+  return (int)q;
+#else
+  return (int)((n + d - 1) / d);
+#endif
+}
+constexpr int kStretch = 3;
 __host__ __device__ inline PrefixLine prefix_cut(int pairs, int steps, int ctas) {
-  constexpr int kStretch = 3;
   PrefixLine p;
   p.pairs = pairs;
   p.steps = steps;
   p.len = steps;
   // below 2^31: the calls' 2^30 blocks in all, and ctas
-  p.per = (int)(((unsigned)pairs * (unsigned)steps + ctas - 1) / (unsigned)ctas);
+  p.per = cut_up((unsigned)pairs * (unsigned)steps, ctas);
   p.grid = ctas;
   if (pairs > 0 && pairs <= ctas) {
-    const unsigned each = (unsigned)ctas / (unsigned)pairs;
-    int per = (int)((steps + each - 1) / each);
+    int each = cut_up(ctas, pairs);  // rounded down from here on
+    each -= each * pairs > ctas;
+    int per = cut_up(steps, each);
     per = per < 2 ? 2 : per;
     if (per <= p.per + kStretch) {
-      const int cuts = (int)((unsigned)(steps + per - 1) / (unsigned)per);
+      const int cuts = cut_up(steps, per);
       p.per = per;
       p.len = cuts * per;
       p.grid = pairs * cuts;
@@ -36,6 +51,57 @@ __host__ __device__ inline PrefixLine prefix_cut(int pairs, int steps, int ctas)
   if (p.per < 1) p.per = 1;
   return p;
 }
+
+// How the SMs are divided between the shared part (one CTA each) and the slots'
+// own line of `units`, which only the lengths tell: the i-th of 32 ways, and
+// how long the longer of both then takes, in steps. The last way cuts evenly,
+// the others pair by pair. weight: of a unit on one SM, against a step; most:
+// CTAs that the shared part can have.
+constexpr int kPRows = 256;  // rows of a tile pair of the shared part
+constexpr int kWays = 32;
+struct PrefixWay {
+  PrefixLine line;
+  float time;
+};
+__host__ __device__ inline PrefixWay prefix_way(int i, int pairs, int steps, int units,
+                                                float weight, int sms, int most) {
+  const bool even = i == kWays - 1;
+  const float own = (float)units * weight, px = (float)pairs * (float)steps;
+  int ctas = (int)((float)sms * px / (px + own) + 0.5f);
+  ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
+  int cuts = cut_up(most + 1, pairs) - 1;  // most / pairs
+  cuts = (i + 1) * cuts / (kWays - 1);
+  PrefixWay r;
+  r.line.pairs = pairs;
+  r.line.steps = steps;
+  int per = cut_up(even ? (unsigned)pairs * (unsigned)steps : steps, even ? ctas : cuts > 0 ? cuts : 1);
+  per = per < 2 ? 2 : per;
+  cuts = cut_up(steps, per);
+  r.line.per = per;
+  r.line.len = even ? steps : cuts * per;
+  r.line.grid = even ? ctas : pairs * cuts;
+  const float t = own / (float)(sms - r.line.grid), p = (float)(even ? per + kStretch : per);
+  r.time = r.line.grid > most ? INFINITY : t > p ? t : p;
+  return r;
+}
+#ifdef __CUDACC__
+// The best way, asked by a whole warp, a way a lane. (Both kernels ask, each
+// for itself; did they not agree, the balance alone would suffer.)
+__device__ __forceinline__ PrefixLine best_line(const AttnBatchArgs& a, int n_tok, int units) {
+  const int pairs = (n_tok * (a.n_q / a.n_kv) + kPRows - 1) / kPRows * a.n_kv, lane = threadIdx.x & 31;
+  if (a.px_fixed || pairs == 0) return prefix_cut(pairs, a.px_steps, a.px_most);
+  const PrefixWay w = prefix_way(lane, pairs, a.px_steps, units, a.unit_weight, a.sms, a.px_most);
+  const unsigned key = (__float_as_uint(w.time) & ~31u) | lane;
+  const int best = (int)(__reduce_min_sync(0xFFFFFFFFu, key) & 31u);
+  PrefixLine p;
+  p.pairs = pairs;
+  p.steps = a.px_steps;
+  p.len = __shfl_sync(0xFFFFFFFFu, w.line.len, best);
+  p.per = __shfl_sync(0xFFFFFFFFu, w.line.per, best);
+  p.grid = __shfl_sync(0xFFFFFFFFu, w.line.grid, best);
+  return p;
+}
+#endif
 
 // New tokens of a slot, brought into range.
 __device__ __forceinline__ int slot_tokens(const AttnBatchArgs& a, int s) {

@@ -10,6 +10,9 @@
 // The (tile, head) pairs' steps lie on one line cut over one CTA per SM
 // (prefix_cut); each stretch leaves (m, l, O) of its 256 rows in the
 // workspace, where attn_join_kernel joins them with the slots' own positions.
+// Both parts run at once, on SMs of their own (best_line): a CTA without a
+// stretch goes as soon as it has read the lengths, and leaves its SM to the
+// slots' own line.
 //
 // Warps: 0 loads K and V (TMA, two stages each of 128 positions), 1 and 2
 // issue the products of the two row tiles, 4-11 and 12-19 do the softmax of
@@ -44,7 +47,6 @@ namespace moe {
 
 namespace {
 constexpr int kPThr = 640;      // a warpgroup of single warps, 2 x 2 of softmax warps
-constexpr int kPRows = 256;     // rows of a tile pair
 constexpr int kPStep = 128;     // positions of a step
 constexpr int kPStages = 2;
 constexpr float kSlack = 8.0f;  // growth of a row (log2) that its reference may lag behind
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kPThr, 1)
   extern __shared__ __align__(1024) uint8_t sm_raw[];
   __shared__ __align__(8) PrefixBars bars;
   __shared__ float s_mx[2][2][2][128];  // step parity, row tile, half, row
-  __shared__ int s_scan[kPThr / 32];
+  __shared__ int s_scan[kPThr / 32], s_units[kPThr / 32], s_line[4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
@@ -172,48 +174,60 @@ __global__ void __launch_bounds__(kPThr, 1)
   tc_fence_before();
   pdl_wait();
   pdl_trigger();
-  // ---- the tokens that are there, counted through
-  int n_tok;
+  // ---- the tokens that are there, counted through, and the units of the
+  // slots' own line; one warp finds the shared part's
   {
     const int chunk = (a.n_slots + kPThr - 1) / kPThr;
     const int s0 = min(tid * chunk, a.n_slots), s1 = min(s0 + chunk, a.n_slots);
-    int sum = 0;
+    int sum = 0, units = 0;
     // the whole span: its length is read again for the rows, out of L1 then
-    for (int s = s0; s < s1; ++s) sum += slot_span(a, s).n_new;
+    for (int s = s0; s < s1; ++s) {
+      const SlotSpan sp = slot_span(a, s);
+      sum += sp.n_new;
+      units += sp.blocks + a.pair_cost;
+    }
     int incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
       if (lane >= d) incl += o;
     }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    int all = 0;
-#pragma unroll
-    for (int w = 0; w < kPThr / 32; ++w) {
-      if (w == warp) incl += all;
-      all += s_scan[w];
+    units = __reduce_add_sync(0xFFFFFFFFu, units);
+    if (lane == 31) {
+      s_scan[warp] = incl;
+      s_units[warp] = units;
     }
-    n_tok = all;
-    int run = incl - sum;
-    for (int s = s0; s < s1; ++s) {
-      s_tok[s] = run;
-      if (blockIdx.x == 0) a.tok_start[s] = run;
-      run += slot_tokens(a, s);
+    __syncthreads();
+    if (warp == 3) {
+      constexpr int kWarps = kPThr / 32;
+      const int all = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? s_scan[lane] : 0);
+      units = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? s_units[lane] : 0) * a.n_kv;
+      const PrefixLine line = best_line(a, all, units);
+      if (lane == 0) {
+        s_line[0] = line.per;
+        s_line[1] = line.len;
+        s_line[2] = line.pairs * line.len;
+        s_line[3] = all;
+      }
+    }
+    if (s0 < s1) {
+      int run = incl - sum;
+      for (int w = 0; w < warp; ++w) run += s_scan[w];
+      for (int s = s0; s < s1; ++s) {
+        s_tok[s] = run;
+        if (blockIdx.x == 0) a.tok_start[s] = run;
+        run += slot_tokens(a, s);
+      }
     }
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const int R = n_tok * G, steps = a.px_steps;
-  // (the divisions take a microsecond: only where tiles are missing)
-  const int pairs = (R + kPRows - 1) / kPRows * a.n_kv;
-  const PrefixLine line =
-      pairs == a.px_line.pairs ? a.px_line : prefix_cut(pairs, steps, (int)gridDim.x);
-  const int plen = line.len;
-  const int f0 = (int)blockIdx.x * line.per, f1 = min(f0 + line.per, line.pairs * plen);
+  const int R = s_line[3] * G, steps = a.px_steps, plen = s_line[1];
+  const int f0 = (int)min((int64_t)blockIdx.x * s_line[0], (int64_t)s_line[2]);
+  const int f1 = min(f0 + s_line[0], s_line[2]);
   if (blockIdx.x == 0 && tid == 0) {
-    a.line[1] = line.per;
+    a.line[1] = s_line[0];
     a.line[2] = plen;
   }
   volatile int* abort = &s_abort;

@@ -225,7 +225,10 @@ struct AttnBatchArgs {
   // the shared part, when attn_prefix_kernel takes it (px_steps > 0): its
   // line of steps and its parts, per place m[256], l[256], O[D / 4][256][4]
   int px_steps;
-  PrefixLine px_line;  // that line where every slot has all T tokens
+  int sms;             // that the shared part and the own one divide between them
+  int px_most;         // CTAs that the shared part was launched with
+  int px_fixed;        // that is the size, whatever the lengths
+  float unit_weight;   // a unit of the own line, against a step of the shared part's
   int join;            // attn_join_kernel follows
   int parts;           // about how many parts a row then has
   float* px_part;

@@ -846,9 +846,10 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
   a.px_steps = 0;
   int room = sms;  // SMs that the slots' own lines can have
   a.sms = sms;
-  // about 0.35 us of an SM for a unit (two of them at a time; 0.16, three at a
-  // time, with D = 64) and 1.3 for a step of the shared part
-  a.unit_weight = s->D == 64 ? (mt == 1 ? 0.13f : 0.18f) : (mt == 1 ? 0.27f : 0.3f);
+  // fitted over twenty shapes; 0.15 more or less costs 2 to 8 us where the
+  // next cut is another one, nothing elsewhere (a step takes 1.3 to 1.7 us, a
+  // unit 0.15 to 0.4 us of an SM's two or three CTAs)
+  a.unit_weight = s->D == 64 ? (mt == 1 ? 0.115f : 0.23f) : (mt == 1 ? 0.23f : 0.36f);
   a.parts = 0;
   if (share(s)) {
     // What the kernel gets of the SMs if every token is there and the slots'

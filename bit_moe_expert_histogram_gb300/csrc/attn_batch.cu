@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
   extern __shared__ __align__(1024) uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
   __shared__ int s_bad[kStages];
-  __shared__ int s_abort, s_start, s_off, s_total, s_per, s_last;
+  __shared__ int s_abort, s_start, s_off, s_ctas, s_last;
   __shared__ int s_scan[kOAll / 32], s_tok[kOAll / 32];
   __shared__ float s_m[4][16], s_l[4][16];  // per warp: its rows' maximum and sum
   __shared__ float s_M[kR], s_L[kR];        // the segment's
@@ -197,6 +197,8 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
     pdl_trigger();
   }
   // ---- this CTA's part of the line of blocks
+  const bool plan = shared && !a.px_fixed;
+  int total = 0, ctas = (int)gridDim.x, per, f0;
   {
     const int chunk = (a.n_slots + kOAll - 1) / kOAll;
     const int s0 = min(tid * chunk, a.n_slots), s1 = min(s0 + chunk, a.n_slots);
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
       tok += sp.n_new;
     }
     sum *= a.n_kv;
-    tok = __reduce_add_sync(0xFFFFFFFFu, tok);
+    if (plan) tok = __reduce_add_sync(0xFFFFFFFFu, tok);
     int incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -219,25 +221,21 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
       s_tok[warp] = tok;
     }
     __syncthreads();
-    int all = 0;
-    tok = 0;
     for (int w = 0; w < kOAll / 32; ++w) {
-      if (w == warp) incl += all;
-      all += s_scan[w];
-      tok += s_tok[w];
+      if (w < warp) incl += s_scan[w];
+      total += s_scan[w];
     }
-    if (warp == kOAll / 32 - 1) {
-      // with a shared part, as many CTAs as there is room for beside it
-      int n = (int)gridDim.x;
-      if (shared && !a.px_fixed) n = max(min((a.sms - best_line(a, tok, all).grid) * own_ctas(D, MT), n), 1);
-      if (lane == 0) {
-        s_total = all;
-        s_per = (int)((unsigned)(all + n - 1) / (unsigned)n);
+    if (plan) {  // as many CTAs as there is room for beside the shared part
+      if (warp == kOAll / 32 - 1) {
+        tok = __reduce_add_sync(0xFFFFFFFFu, lane < kOAll / 32 ? s_tok[lane] : 0);
+        const int room = (a.sms - best_line(a, tok, total).grid) * own_ctas(D, MT);
+        if (lane == 0) s_ctas = max(min(room, ctas), 1);
       }
+      __syncthreads();
+      ctas = s_ctas;
     }
-    __syncthreads();
-    const int per = s_per;
-    const int f0 = (int)min((int64_t)blockIdx.x * per, (int64_t)s_total);
+    per = (int)((unsigned)(total + ctas - 1) / (unsigned)ctas);
+    f0 = (int)blockIdx.x < ctas ? min((int)blockIdx.x * per, total) : total;
     int run = incl - sum;
     if (f0 >= run && f0 < incl) {  // one thread's slots hold the first block
       int s = s0;
@@ -251,9 +249,7 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
     }
     __syncthreads();
   }
-  const int total = s_total;
-  const int per = s_per;
-  const int f0 = (int)min((int64_t)blockIdx.x * per, (int64_t)total), f1 = min(f0 + per, total);
+  const int f1 = min(f0 + per, total);
   int s = s_start;
   SlotSpan sp = slot_span(a, s);
   int g = s_off / (sp.blocks + a.pair_cost);

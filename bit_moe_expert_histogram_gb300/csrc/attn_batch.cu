@@ -767,16 +767,17 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr int kMostSms = 256;  // three CTAs an SM at most
 // Whether the prefix is read once for all slots. Otherwise each slot's own line
 // reads it, in one or two launches instead of three, which is shorter while
-// the slots' prefix blocks together are few. Measured, per slot against
-// shared (D = 128, 8 rows a pair): 12.2 and 12.6 us at 512 blocks over all
-// slots and heads, 15.4 and 15.9 at 1024, 17.4 and 16.5 at 2048; with 32 rows
-// 19.1 and 20.1 at 512, 20.3 and 18.8 at 1024; with 64 rows even at 256 to
-// 512; with D = 64, half the bytes a block, 12.0 and 12.2 at 1024, 13.5 and
-// 12.6 at 2048, where the calls from the host still favour one launch.
+// the slots' prefix blocks together are few. Measured, per slot against shared
+// (blocks over all slots and heads, those of D = 64 as halves): rows of one
+// tile 9.7 and 12.5 us at 512, 10.8 and 12.7, 13.4 and 13.4 at 1024, 16.1 and
+// 15.2, 17.6 and 15.2 at 2048; of more tiles, blocks times tiles, 15.2 and
+// 16.5, 19.1 and 17.0 at 2048 (13.3 and 15.2 with D = 64), 18.6 and 16.6, 25.8
+// and 22.7 at 4096.
 bool share(const moe_attn_batch_shape_t* s) {
   if (s->prefix_blocks == 0 || s->n_slots == 1) return false;
   const int64_t blocks = (int64_t)s->n_slots * s->n_kv * s->prefix_blocks;
-  return blocks * s->D / 128 * own_tiles(s) > 1024;
+  const int mt = own_tiles(s);
+  return blocks * s->D / 128 * mt > (mt > 1 ? 2048 : 1024);
 }
 // a place per CTA and pair
 size_t own_part_bytes(const moe_attn_batch_shape_t* s) {

@@ -80,7 +80,9 @@ __host__ __device__ inline PrefixWay prefix_way(int i, int pairs, int steps, int
   r.line.per = per;
   r.line.len = even ? steps : cuts * per;
   r.line.grid = even ? ctas : pairs * cuts;
-  const float t = own / (float)(sms - r.line.grid), p = (float)(even ? per + kStretch : per);
+  // an even cut has the ends of per / steps pairs more in a CTA
+  const float ends = even ? kStretch * (1.0f + (float)per / (float)steps) : 0.0f;
+  const float t = own / (float)(sms - r.line.grid), p = (float)per + ends;
   r.time = r.line.grid > most ? INFINITY : t > p ? t : p;
   return r;
 }

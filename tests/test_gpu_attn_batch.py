@@ -158,6 +158,24 @@ def test_many_slots_on_a_prefix(B, T, n_q, n_kv, D, prefix):
     Case(B + 1, pairs, T, n_q, n_kv, D, prefix=prefix).check()
 
 
+@pytest.mark.parametrize("B,T,n_q,n_kv,D,prefix,extra,new", [
+    (130, 4, 32, 4, 128, 4, 200, "few"), (130, 4, 32, 4, 128, 4, 0, "some"),
+    (64, 8, 8, 8, 64, 20, 0, "one"), (64, 8, 8, 8, 64, 20, 40, "none"),
+    (300, 4, 16, 2, 64, 30, 3, "all"), (90, 1, 8, 8, 128, 17, 0, "some")])
+def test_shared_part_beside_the_own_lines(B, T, n_q, n_kv, D, prefix, extra, new):
+    """The SMs are divided by what there is of both: few and many tokens,
+    short and long own lines, tables wider than any length, nothing at all."""
+    rng = np.random.default_rng(B + extra)
+    n_new = {"few": rng.integers(0, T + 1, B) * (rng.random(B) < 0.1),
+             "some": rng.integers(0, T + 1, B), "one": (np.arange(B) == 41) * T,
+             "none": np.zeros(B), "all": np.full(B, T)}[new].astype(int)
+    own = rng.integers(1, 100, B)
+    own[B // 2] = 2000  # one slot goes on long after the others
+    own[3] = -100  # and one ends inside the prefix
+    Case(B, [(prefix * 64 + int(a), int(t)) for a, t in zip(own, n_new)], T, n_q, n_kv, D,
+         prefix=prefix, extra=extra).check()
+
+
 def test_long_and_short_slots_together():
     pairs = [(9000, 1), (3, 1), (0, 0), (64 * 90, 1), (1, 1), (4097, 1)]
     Case(17, pairs, 1, 16, 2, 128).check()

@@ -662,9 +662,11 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
 // elements of a row, each with every kLanes-th part, so that all of a row's
 // parts are fetched at once; then the threads' results in their order. A CTA
 // has items of one pair, rows (1 << row_bits of them, the pair's and none)
-// fastest; divisions by what the kernel is given are done once a CTA. Latency
-// bounds it: 14 us of 175 for 720 tokens of 16 heads with about five parts a
-// row, 34 MB from L2, and as long with batches of three to six parts.
+// fastest, of which it takes one batch after the other (a CTA a batch took 22
+// us of 53 for 32000 rows, one after the other 19); divisions by what the
+// kernel is given are done once a CTA. Latency bounds it: 14 us of 175 for 720
+// tokens of 16 heads with about five parts a row, 34 MB from L2, and as long
+// with batches of three to six parts.
 template <bool F16, int D, int kLanes>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnBatchArgs a, int kR, int row_bits) {
   constexpr int kItems = 256 / kLanes;
@@ -692,47 +694,50 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnBatchArgs a, i
   }
   __syncthreads();
   const int item = threadIdx.x % kItems, ln = threadIdx.x / kItems;
-  const int i = blockIdx.y * kItems + item;
-  const int d = i >> row_bits, r = i & ((1 << row_bits) - 1);
-  // r / G for r < 64: the product is off by less than 1/2 G steps of 2^-24
-  const int t = (int)(((float)r + 0.5f) * (1.0f / (float)G));
-  Joined jn{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-  const bool here = r < rows && d < D / 4;
-  if (here && t < sp.n_new && sp.len - sp.n_new + t >= 0) {
-    const int row = row0 + r, tile = (row >> 8) - (row0 >> 8), u = (row >> 8) * a.n_kv + g;
-    const int nx = shared ? s_cut[tile][1] : 0, n = nx + s_own[1];
-    const PartRef px = part_ref(a.px_part + (int64_t)(shared ? s_cut[tile][0] + u : 0) * 256 * (D + 2),
-                                256, row & 255, d);
-    const PartRef own = part_ref(a.part + (int64_t)(s_own[0] + pair) * kR * (D + 2), kR, r, d);
-    join_parts<6>(jn, (n - ln + kLanes - 1) / kLanes, [&](int c) {
-      const int k = c * kLanes + ln;
-      return k < nx ? PartRef{px.p + k * (256 * (D + 2)), px.l_at, px.o_at}
-                    : PartRef{own.p + (k - nx) * (kR * (D + 2)), own.l_at, own.o_at};
-    });
-  }
-  if (kLanes > 1) {
-    s_o[ln][item] = jn.o;
-    s_ml[ln][item] = make_float2(jn.M, jn.L);
-    __syncthreads();
-    if (ln > 0) return;
-    float M = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kLanes; ++k) M = fmaxf(M, s_ml[k][item].x);
-    const float U = M == -INFINITY ? 0.0f : M;
-    jn = Joined{M, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-#pragma unroll
-    for (int k = 0; k < kLanes; ++k) {
-      const float w = ex2(s_ml[k][item].x - U);
-      const float4 v = s_o[k][item];
-      jn.L = fmaf(s_ml[k][item].y, w, jn.L);
-      jn.o.x = fmaf(v.x, w, jn.o.x);
-      jn.o.y = fmaf(v.y, w, jn.o.y);
-      jn.o.z = fmaf(v.z, w, jn.o.z);
-      jn.o.w = fmaf(v.w, w, jn.o.w);
+  for (int i0 = blockIdx.y * kItems; i0 < (D / 4) << row_bits; i0 += gridDim.y * kItems) {
+    const int i = i0 + item;
+    const int d = i >> row_bits, r = i & ((1 << row_bits) - 1);
+    // r / G for r < 64: the product is off by less than 1/2 G steps of 2^-24
+    const int t = (int)(((float)r + 0.5f) * (1.0f / (float)G));
+    if (kLanes > 1) __syncthreads();  // the threads' results of the items before are read
+    Joined jn{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+    const bool here = r < rows && d < D / 4;
+    if (here && t < sp.n_new && sp.len - sp.n_new + t >= 0) {
+      const int row = row0 + r, tile = (row >> 8) - (row0 >> 8), u = (row >> 8) * a.n_kv + g;
+      const int nx = shared ? s_cut[tile][1] : 0, n = nx + s_own[1];
+      const PartRef px = part_ref(a.px_part + (int64_t)(shared ? s_cut[tile][0] + u : 0) * 256 * (D + 2),
+                                  256, row & 255, d);
+      const PartRef own = part_ref(a.part + (int64_t)(s_own[0] + pair) * kR * (D + 2), kR, r, d);
+      join_parts<6>(jn, (n - ln + kLanes - 1) / kLanes, [&](int c) {
+        const int k = c * kLanes + ln;
+        return k < nx ? PartRef{px.p + k * (256 * (D + 2)), px.l_at, px.o_at}
+                      : PartRef{own.p + (k - nx) * (kR * (D + 2)), own.l_at, own.o_at};
+      });
     }
+    if (kLanes > 1) {
+      s_o[ln][item] = jn.o;
+      s_ml[ln][item] = make_float2(jn.M, jn.L);
+      __syncthreads();
+      if (ln > 0) continue;
+      float M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kLanes; ++k) M = fmaxf(M, s_ml[k][item].x);
+      const float U = M == -INFINITY ? 0.0f : M;
+      jn = Joined{M, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+#pragma unroll
+      for (int k = 0; k < kLanes; ++k) {
+        const float w = ex2(s_ml[k][item].x - U);
+        const float4 v = s_o[k][item];
+        jn.L = fmaf(s_ml[k][item].y, w, jn.L);
+        jn.o.x = fmaf(v.x, w, jn.o.x);
+        jn.o.y = fmaf(v.y, w, jn.o.y);
+        jn.o.z = fmaf(v.z, w, jn.o.z);
+        jn.o.w = fmaf(v.w, w, jn.o.w);
+      }
+    }
+    if (here)
+      store4<F16>(a.o + (((int64_t)s * a.T + t) * a.n_q + g * G + r - t * G) * D + 4 * d, jn.o, jn.L);
   }
-  if (here)
-    store4<F16>(a.o + (((int64_t)s * a.T + t) * a.n_q + g * G + r - t * G) * D + 4 * d, jn.o, jn.L);
 }
 
 template <bool F16, int D, int kLanes>
@@ -740,8 +745,11 @@ cudaError_t launch_join(const AttnBatchArgs& a, int kR, cudaStream_t stream) {
   const int rows = a.T * (a.n_q / a.n_kv), per = 256 / kLanes;
   int bits = 0;
   while (1 << bits < rows) ++bits;
-  return launch_pdl(attn_join_kernel<F16, D, kLanes>,
-                    dim3(a.n_slots, (((D / 4) << bits) + per - 1) / per, a.n_kv), dim3(256), 0,
+  // about as many CTAs as there is room for at once, four an SM
+  const int items = (((D / 4) << bits) + per - 1) / per;
+  const int64_t pairs = (int64_t)a.n_slots * a.n_kv, fit = (4 * a.sms + pairs - 1) / pairs;
+  const int y = items < fit ? items : (int)fit;
+  return launch_pdl(attn_join_kernel<F16, D, kLanes>, dim3(a.n_slots, y, a.n_kv), dim3(256), 0,
                     stream, a, kR, bits);
 }
 

@@ -66,7 +66,7 @@ struct PrefixWay {
 __host__ __device__ inline PrefixWay prefix_way(int i, int pairs, int steps, int units,
                                                 float weight, int sms, int most) {
   const bool even = i == kWays - 1;
-  const float own = (float)units * weight, px = (float)pairs * (float)steps;
+  const float own = (float)units * weight, px = (float)pairs * (float)(steps + kStretch);
   int ctas = (int)((float)sms * px / (px + own) + 0.5f);
   ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
   int cuts = cut_up(most + 1, pairs) - 1;  // most / pairs

@@ -16,16 +16,19 @@
 // slots they belong to, so uneven lengths leave no CTA idle. (A pair counts
 // pair_cost units more than its blocks: its start and end cost about that many
 // blocks' time, so a CTA of many short slots gets fewer blocks. Measured with
-// 0, 1, 2, 3, 4, 6: 32.5, 29.7, 24.4, 21.9, 22.7, 21.7 us for 33 slots of up
-// to 5000 positions with D = 64; 205, 196, 189, 186, 184, 186 for 256 slots of
-// up to 1500 with D = 128 and 32 rows a pair; 32.9, 30.8, 30.5, 30.8, 31.1,
-// 31.3 for 48 slots of up to 777 with 8 rows.) The T * n_q / n_kv <= 64 query
+// 1, 2, 3, 4, 6: 28.0, 25.4, 25.4, 25.4, 25.8 us for 64 slots of 8 + 5 pages
+// and 8 heads, D = 128, 16 rows a pair; 26.8, 24.8, 23.7, 22.8, 22.9 for 64 of
+// 16 + 5 and 2 heads, 32 rows; 12.5, 12.0, 11.5, 11.5, 11.2 for 16 of 16 + 5
+// and 8 heads, D = 64.) The T * n_q / n_kv <= 64 query
 // rows of a pair are the M rows of mma.sync tiles (16 rows; 1, 2 or 4 tiles),
 // so each key and value is read once per slot: HBM bounds it, and the tensor
 // core's own instructions, whose M is 128, would mostly multiply nothing. A
 // warp of its own keeps a TMA ring of blocks full (64 rows x 64 elements per
 // box, 128-byte swizzle) that runs on across pairs, knowing the next slot's
-// pages before it gets there; the four others only meet at the end of a pair.
+// pages before it gets there; the four others only meet at a pair's ends,
+// where their results meet in the stage of its last block while the next
+// pair's queries, span and blocks are on their way. A pair of one block takes
+// 2.6 us (D = 128, 5 rows), no one wait of which is more than a seventh.
 //  - where a pair has few parts, one inside a CTA goes straight to the output,
 //    and one cut by a CTA border leaves (m, l, O) in the workspace and the
 //    last of its CTAs to arrive joins them in CTA order;
@@ -33,8 +36,8 @@
 //    (m, l, O), and attn_join_kernel joins them all, a thread for four
 //    elements of the output: few threads wait long for what many threads
 //    fetch at once (one slot of 32768 positions: 28 us against 12.4).
-// 33 slots of up to 5000 positions, D = 64, fp16, 65 MB: 17.2 us in a graph,
-// 3.8 TB/s, 0.56 of a plain copy's rate.
+// 33 slots of up to 5000 positions, D = 64, fp16, 65 MB: 15.0 us in a graph,
+// 4.3 TB/s, 0.64 of a plain copy's rate (the next call's reads partly from L2).
 #include "attn_batch.cuh"
 
 namespace moe {

@@ -8,25 +8,25 @@ namespace moe {
 
 constexpr int kBlk = 64;  // positions per page
 
-// How `pairs` pairs of `steps` steps go over `ctas` CTAs. Cut evenly, most
-// CTAs get the end of one pair and the start of the next, and a stretch costs
-// about kStretch steps beside its own (queries in, O out); cut pair by pair
-// every CTA has one stretch but some CTAs may be left over. The shorter way
-// is taken; a stretch of fewer than two steps would be mostly cost.
 __host__ __device__ inline int cut_up(unsigned n, unsigned d) {  // ceil(n / d)
 #ifdef __CUDA_ARCH__
-  // five of these in a row keep the shared part's kernel waiting: a float
-  // quotient put right takes a third of a division's time (n < 2^31: off by
-  // less than 2^8, by one or less where the quotient is below 2^23)
+  // several of these in a row keep the shared part's kernel waiting, and a
+  // float quotient put right takes a third of a division's time (below 2^22
+  // it is off by two at most)
   unsigned q = __float2uint_rd(__fdividef((float)n, (float)d));
   if (q >= (1u << 22)) return (int)((n + d - 1) / d);
-  if (q * d > n) --q;
+  while (q * d > n) --q;
   while (q * d < n) ++q;
   return (int)q;
 #else
   return (int)((n + d - 1) / d);
 #endif
 }
+// How `pairs` pairs of `steps` steps go over `ctas` CTAs. Cut evenly, most
+// CTAs get the end of one pair and the start of the next, and a stretch costs
+// about kStretch steps beside its own (queries in, O out); cut pair by pair
+// every CTA has one stretch but some CTAs may be left over. The shorter way
+// is taken; a stretch of fewer than two steps would be mostly cost.
 constexpr int kStretch = 3;
 __host__ __device__ inline PrefixLine prefix_cut(int pairs, int steps, int ctas) {
   PrefixLine p;

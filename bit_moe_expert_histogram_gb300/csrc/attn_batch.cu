@@ -895,9 +895,18 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
   // the parts of a pair's own blocks, were all pairs as long as they can be
   const int64_t pairs_n = (int64_t)s->n_slots * s->n_kv;
   a.parts += (int)(grid / pairs_n < s->max_blocks - a.first ? grid / pairs_n : s->max_blocks - a.first);
-  // few parts of few rows are joined by the last CTA: 8.6 and 8.1 us at 5 or
-  // 6 parts of 8 rows, 13.9 and 9.4 of 32 rows, 19.4 and 12.1 of 64
-  a.join = a.px_steps > 0 || a.parts * mt > 6;
+  // Parts are joined by a pair's last CTA where few pairs are cut: 5.7 us
+  // against 7.6 by a kernel of its own for pairs of two blocks (D = 128, 8 rows;
+  // 9.6 and 12.1 for 512 such pairs, 67 and 70 for 1024 of up to 32), but 12.5
+  // and 10.7 for 128 pairs of up to 16, 24.4 and 21.9 for 512, 11.9 and 8.6 for
+  // 32 with nine parts each; with 64 rows 11.1 and 11.2 for two blocks, 16.6
+  // and 12.2 for eight. In between, 8.2 and 7.5 for three to five blocks, the
+  // second launch costs the host the 1.7 us that such a call cannot hide. A
+  // pair of `longest` is cut if a border, `per` units apart, falls into it.
+  const int longest = s->max_blocks - a.first;
+  const int64_t per = (pairs_n * (longest + a.pair_cost) + grid - 1) / grid;
+  const bool cut = longest >= (mt == 4 && s->D == 128 ? 2 : 3) && 2 * longest > per;
+  a.join = a.px_steps > 0 || a.parts > 6 || (cut && (mt > 1 || per >= 6));
   if (s->dtype == MOE_DTYPE_FP16)
     return s->D == 64 ? launch_own_mt<true, 64>(mt, tk, tv, a, grid, stream)
                       : launch_own_mt<true, 128>(mt, tk, tv, a, grid, stream);

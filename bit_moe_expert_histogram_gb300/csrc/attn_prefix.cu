@@ -117,6 +117,7 @@ __device__ __forceinline__ bool elect_one() {
 struct PrefixBars {
   uint64_t k_full[kPStages], k_empty[kPStages], v_full[kPStages], v_empty[kPStages];
   uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], turn[2], drain[2];
+  uint64_t v_end;  // values of the step in which the longest slot ends
 };
 }  // namespace
 
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kPThr, 1)
   extern __shared__ __align__(1024) uint8_t sm_raw[];
   __shared__ __align__(8) PrefixBars bars;
   __shared__ float s_mx[2][2][2][128];  // step parity, row tile, half, row
-  __shared__ int s_scan[kPThr / 32], s_units[kPThr / 32], s_line[4];
+  __shared__ int s_scan[kPThr / 32], s_units[kPThr / 32], s_long[kPThr / 32], s_line[5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(kPThr, 1)
       mbar_init(bar(bars.turn[i]), 1);
       mbar_init(bar(bars.drain[i]), 1);
     }
+    mbar_init(bar(bars.v_end), 1);
     s_abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
@@ -182,12 +184,13 @@ __global__ void __launch_bounds__(kPThr, 1)
   {
     const int chunk = (a.n_slots + kPThr - 1) / kPThr;
     const int s0 = min(tid * chunk, a.n_slots), s1 = min(s0 + chunk, a.n_slots);
-    int sum = 0, units = 0;
+    int sum = 0, units = 0, longest = 0;
     // the whole span: its length is read again for the rows, out of L1 then
     for (int s = s0; s < s1; ++s) {
       const SlotSpan sp = slot_span(a, s);
       sum += sp.n_new;
       units += sp.blocks + a.pair_cost;
+      longest = max(longest, sp.n_new > 0 ? sp.len : 0);
     }
     int incl = sum;
 #pragma unroll
@@ -196,21 +199,25 @@ __global__ void __launch_bounds__(kPThr, 1)
       if (lane >= d) incl += o;
     }
     units = __reduce_add_sync(0xFFFFFFFFu, units);
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     if (lane == 31) {
       s_scan[warp] = incl;
       s_units[warp] = units;
+      s_long[warp] = longest;
     }
     __syncthreads();
     if (warp == 3) {
       constexpr int kWarps = kPThr / 32;
       const int all = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? s_scan[lane] : 0);
       units = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? s_units[lane] : 0) * a.n_kv;
+      longest = __reduce_max_sync(0xFFFFFFFFu, lane < kWarps ? s_long[lane] : 0);
       const PrefixLine line = best_line(a, all, units);
       if (lane == 0) {
         s_line[0] = line.per;
         s_line[1] = line.len;
         s_line[2] = line.pairs * line.len;
         s_line[3] = all;
+        s_line[4] = longest;
       }
     }
     if (s0 < s1) {
@@ -243,8 +250,14 @@ __global__ void __launch_bounds__(kPThr, 1)
   // the line's stretch f0 .. f1, pair u (tile u / n_kv, head u % n_kv) by
   // pair; a pair's units from `steps` on are nothing
   if (warp == 0) {
+    // ---- the loader, one lane. Positions from `longest` on belong to no slot
+    // and may hold anything, NaN too: 0 x NaN in P V would reach the output.
+    // Pages past it are read as pages that are not there are; the page that it
+    // ends in has the rest of its values set to 0 before the step goes on.
     if (lane == 0) {
-      int n = 0;  // steps loaded
+      const int longest = s_line[4];
+      volatile int never = 0;
+      int n = 0, ends = 0;  // steps loaded, those among them in which longest lies
       for (int f = f0; f < f1; ++f) {
         const int u = f / plen, j = f - u * plen, g = u % a.n_kv;
         if (j >= steps) continue;
@@ -258,8 +271,11 @@ __global__ void __launch_bounds__(kPThr, 1)
           const bool bad = phys < 0 || phys >= a.n_phys;
           if (bad && jb < a.prefix_blocks) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_ATTNB, -1);
           // a page that is not there reads past the pool's end: zeros
-          row[i] = (bad ? a.n_phys * a.n_kv : phys * a.n_kv + g) * kBlk;
+          row[i] = (bad || jb * kBlk >= longest ? a.n_phys * a.n_kv : phys * a.n_kv + g) * kBlk;
         }
+        const int end = longest - j * kPStep;  // of what is anyone's, in the step
+        const bool inside = end > 0 && end < kPStep && end % kBlk != 0;
+        const uint32_t b_v = bar(inside ? bars.v_end : bars.v_full[st]);
         if (!wait(bars.k_empty[st], ph ^ 1u)) break;
         mbar_arrive_expect_tx(bar(bars.k_full[st]), kTile);
 #pragma unroll
@@ -270,21 +286,34 @@ __global__ void __launch_bounds__(kPThr, 1)
                           bar(bars.k_full[st]));
         if (!wait(bars.v_empty[st], ph ^ 1u)) {
           // the keys just asked for must land before the CTA goes
-          volatile int never = 0;
           mbar_wait(bar(bars.k_full[st]), ph, &never);
           break;
         }
-        mbar_arrive_expect_tx(bar(bars.v_full[st]), kTile);
+        mbar_arrive_expect_tx(b_v, kTile);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int h = 0; h < kHalves; ++h)
             tma_load_rows(sv + st * kTile + h * kHalf + i * (kBlk * 128), &tm_v, h * 64, row[i],
-                          bar(bars.v_full[st]));
+                          b_v);
+        if (inside) {
+          // bounded, and the copies land whatever the other roles do
+          if (!mbar_wait(b_v, (uint32_t)ends++ & 1u, &never) && atomicCAS(&s_abort, 0, 1) == 0)
+            set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, -2);
+#pragma unroll 1
+          for (int r = end; r % kBlk != 0; ++r)  // to its page's last row
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                               sv + st * kTile + (c >> 3) * kHalf + r * 128 + (c & 7) * 16),
+                           "r"(0)
+                           : "memory");
+          fence_proxy_async_smem();  // the tensor core reads it
+          mbar_arrive(bar(bars.v_full[st]));
+        }
         ++n;
       }
       // what is still in flight lands before the CTA goes (bounded)
-      volatile int never = 0;
       for (int i = n > kPStages ? n - kPStages : 0; i < n; ++i) {
         mbar_wait(bar(bars.k_full[i % kPStages]), (uint32_t)(i / kPStages) & 1u, &never);
         mbar_wait(bar(bars.v_full[i % kPStages]), (uint32_t)(i / kPStages) & 1u, &never);

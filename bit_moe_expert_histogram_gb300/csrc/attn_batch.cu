@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kOAll, own_ctas(D, MT))
           __threadfence();
           meet();
           if (tid == 0) {
-            unsigned* cnt = a.count + pair;
+            unsigned* cnt = a.count + c0;  // whose end cuts this pair and no other
             s_last = atomicAdd(cnt, 1u) == (unsigned)(c1 - c0);
             if (s_last) *cnt = 0u;  // ready for the next call
             __threadfence();
@@ -775,7 +775,8 @@ int own_tiles(const moe_attn_batch_shape_t* s) {  // row tiles: 1, 2 or 4
   return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
 }
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
-constexpr int kMostSms = 256;  // three CTAs an SM at most
+constexpr int kMostSms = 256;
+constexpr int kMostCtas = 3 * kMostSms;  // of attn_own_kernel
 // Whether the prefix is read once for all slots. Otherwise each slot's own line
 // reads it, in one or two launches instead of three, which is shorter while
 // the slots' prefix blocks together are few. Measured, per slot against shared
@@ -792,7 +793,7 @@ bool share(const moe_attn_batch_shape_t* s) {
 }
 // a place per CTA and pair
 size_t own_part_bytes(const moe_attn_batch_shape_t* s) {
-  const size_t places = 3 * kMostSms + (size_t)s->n_slots * s->n_kv;
+  const size_t places = kMostCtas + (size_t)s->n_slots * s->n_kv;
   return round256(places * own_tiles(s) * 16 * (s->D + 2) * 4);
 }
 
@@ -823,10 +824,14 @@ cudaError_t launch_own_mt(int mt, const CUtensorMap& tk, const CUtensorMap& tv,
 }
 }  // namespace
 
-// status and the lines' steps, the pairs' counters, their starts, the slots'
-// first tokens, the pairs' parts, the shared part's
+// status and the lines' steps, the CTAs' counters, the pairs' starts, the
+// slots' first tokens, the pairs' parts, the shared part's. The counters are
+// all that one call leaves to the next (zeros), so their place and extent are
+// the same for every shape: a server's batch grows and shrinks in one
+// workspace.
+constexpr size_t kCountAt = 512, kStartAt = kCountAt + kMostCtas * 4;
 size_t attn_batch_ws_bytes(const moe_attn_batch_shape_t* s) {
-  return 512 + 2 * round256((size_t)s->n_slots * s->n_kv * 4) +
+  return kStartAt + round256((size_t)s->n_slots * s->n_kv * 4) +
          round256((size_t)s->n_slots * 4) + own_part_bytes(s) +
          (s->prefix_blocks > 0 ? prefix_part_floats(s, kMostSms) * 4 : 0);
 }
@@ -837,10 +842,10 @@ cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap
   a.ctrl = reinterpret_cast<Ctrl*>(ws);
   const size_t pairs = round256((size_t)s->n_slots * s->n_kv * 4);
   a.line = reinterpret_cast<int32_t*>(ws + 256);
-  a.count = reinterpret_cast<unsigned*>(ws + 512);
-  a.pair_start = reinterpret_cast<int32_t*>(ws + 512 + pairs);
-  a.tok_start = reinterpret_cast<int32_t*>(ws + 512 + 2 * pairs);
-  a.part = reinterpret_cast<float*>(ws + 512 + 2 * pairs + round256((size_t)s->n_slots * 4));
+  a.count = reinterpret_cast<unsigned*>(ws + kCountAt);
+  a.pair_start = reinterpret_cast<int32_t*>(ws + kStartAt);
+  a.tok_start = reinterpret_cast<int32_t*>(ws + kStartAt + pairs);
+  a.part = reinterpret_cast<float*>(ws + kStartAt + pairs + round256((size_t)s->n_slots * 4));
   a.pair_cost = s->D == 64 || own_tiles(s) > 1 ? 4 : 2;
   a.n_slots = s->n_slots;
   a.T = s->T;

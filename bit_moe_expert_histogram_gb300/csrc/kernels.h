@@ -216,7 +216,7 @@ struct AttnBatchArgs {
   int first;           // the first block that attn_own_kernel takes
   uint16_t* o;         // [n_slots][T][n_q][D]
   float* part;         // parts of pairs: per place m[R], l[R], O[D / 4][R][4]
-  unsigned* count;     // [n_slots][n_kv]: CTAs of a cut pair that have arrived
+  unsigned* count;     // [CTAs of the own line]: arrivals at the pair that the CTA's end cuts
   int pair_cost;       // units of the own line that a pair counts beside its blocks
   int32_t* pair_start; // [n_slots][n_kv]: where the pair starts on the own line
   int32_t* line;       // [3]: units per CTA of the own line and of the shared part's, and a

@@ -545,7 +545,9 @@ moe_status_t moe_cache_copy_pages(const moe_cache_shape_t* shape, int32_t n,
  *  lens_dev    int32 [n_slots]; n_new_dev int32 [n_slots] or NULL (T)
  *  o_dev       [n_slots][T][n_q][D] out, 16-byte aligned
  * Deterministic. The workspace (256-byte aligned) is zero-filled once
- * (moe_workspace_init); after MOE_ERR_TIMEOUT, again. */
+ * (moe_workspace_init); after MOE_ERR_TIMEOUT, again. Calls of any shape that
+ * it is large enough for can use it in turn, but no other call of this
+ * library: it keeps counters past its status word. */
 typedef struct moe_attn_batch_shape {
   int32_t n_slots;       /* 1 .. 4096 */
   int32_t T;             /* most new tokens of a slot; (n_q / n_kv) * T <= 64 */

@@ -119,6 +119,23 @@ struct PrefixBars {
   uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], turn[2], drain[2];
   uint64_t v_end;  // values of the step in which the longest slot ends
 };
+// The values of the step in which the longest slot ends, once they are there:
+// rows from `end` to the end of its page become 0. Out of line: it is rare.
+template <int D>
+__device__ __noinline__ bool end_values(uint32_t sv, int end, uint32_t landed, uint32_t parity) {
+  volatile int never = 0;  // bounded, and the copies land whatever the other roles do
+  const bool ok = mbar_wait(landed, parity, &never);
+#pragma unroll 1
+  for (int r = end; r % kBlk != 0; ++r)
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                       sv + (c >> 3) * (128 * 128) + r * 128 + (c & 7) * 16),
+                   "r"(0)
+                   : "memory");
+  fence_proxy_async_smem();  // the tensor core reads it
+  return ok;
+}
 }  // namespace
 
 __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
@@ -297,18 +314,9 @@ __global__ void __launch_bounds__(kPThr, 1)
             tma_load_rows(sv + st * kTile + h * kHalf + i * (kBlk * 128), &tm_v, h * 64, row[i],
                           b_v);
         if (inside) {
-          // bounded, and the copies land whatever the other roles do
-          if (!mbar_wait(b_v, (uint32_t)ends++ & 1u, &never) && atomicCAS(&s_abort, 0, 1) == 0)
+          if (!end_values<D>(sv + st * kTile, end, b_v, (uint32_t)ends++ & 1u) &&
+              atomicCAS(&s_abort, 0, 1) == 0)
             set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, -2);
-#pragma unroll 1
-          for (int r = end; r % kBlk != 0; ++r)  // to its page's last row
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                               sv + st * kTile + (c >> 3) * kHalf + r * 128 + (c & 7) * 16),
-                           "r"(0)
-                           : "memory");
-          fence_proxy_async_smem();  // the tensor core reads it
           mbar_arrive(bar(bars.v_full[st]));
         }
         ++n;

@@ -472,17 +472,24 @@ __global__ void __launch_bounds__(kVThr, kVCtas<DT>) verify_kernel(const VerifyA
   }
 }
 
+namespace {
+constexpr int kMostSlots = 4096;
+// The slots' counters (zeros between calls) lie at one place and have one
+// extent, whatever the shape: a server's batch grows and shrinks in one
+// workspace. The segments' sums follow, which no call leaves to the next.
+constexpr size_t kDoneAt = 256, kPartAt = kDoneAt + kMostSlots * 4;
+}  // namespace
+
 bool verify_supported(const moe_verify_shape_t* s) {
   if (!s) return false;
-  if (s->n_slots < 1 || s->n_slots > 4096 || s->T < 1 || s->T > 31) return false;
+  if (s->n_slots < 1 || s->n_slots > kMostSlots || s->T < 1 || s->T > 31) return false;
   if (s->V < 1 || s->V > kVSeg * kVThr) return false;
   return s->dtype == MOE_DTYPE_BF16 || s->dtype == MOE_DTYPE_FP16 || s->dtype == MOE_DTYPE_FP32;
 }
 
-// 256 bytes of status, the slots' counters, the segments' sums
 size_t verify_ws_bytes(const moe_verify_shape_t* s) {
   const size_t S = (s->V + kVSeg - 1) / kVSeg;
-  return 256 + (((size_t)s->n_slots * 4 + 255) & ~(size_t)255) + (size_t)s->n_slots * S * 8;
+  return kPartAt + (size_t)s->n_slots * S * 8;
 }
 
 cudaError_t launch_verify(const moe_verify_shape_t* s, const void* p, const void* q,
@@ -500,8 +507,8 @@ cudaError_t launch_verify(const moe_verify_shape_t* s, const void* p, const void
   a.V = s->V;
   a.S = (s->V + kVSeg - 1) / kVSeg;
   a.ctrl = reinterpret_cast<Ctrl*>(ws);
-  a.done = reinterpret_cast<unsigned*>(ws + 256);
-  a.part = reinterpret_cast<float2*>(ws + 256 + (((size_t)s->n_slots * 4 + 255) & ~(size_t)255));
+  a.done = reinterpret_cast<unsigned*>(ws + kDoneAt);
+  a.part = reinterpret_cast<float2*>(ws + kPartAt);
   // each CTA with as many segments as the CTAs that fit at once leave it
   const int ctas = s->dtype == MOE_DTYPE_FP32 ? kVCtas<MOE_DTYPE_FP32> : kVCtas<MOE_DTYPE_BF16>;
   const int per_slot = ctas * nsm / s->n_slots > 1 ? ctas * nsm / s->n_slots : 1;

@@ -587,7 +587,10 @@ moe_status_t moe_attn_batch(const moe_attn_batch_shape_t* shape, const void* q_d
  *              new token
  *  tokens_dev  int32 [n_slots][T + 1] out: the accepted drafts, the new
  *              token, -1
- *  n_acc_dev   int32 [n_slots] out: i */
+ *  n_acc_dev   int32 [n_slots] out: i
+ * The workspace (256-byte aligned) is zero-filled once (moe_workspace_init).
+ * Calls of any shape that it is large enough for can use it in turn, but no
+ * other call of this library: it keeps counters past its status word. */
 typedef struct moe_verify_shape {
   int32_t n_slots; /* 1 .. 4096 */
   int32_t T;       /* most drafts of a slot, 1 .. 31 */

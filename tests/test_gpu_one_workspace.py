@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import bit_moe_expert_histogram_gb300 as m
+import serve_ref as ref
 from test_gpu_attn_batch import DEV, Case
 
 pytestmark = pytest.mark.gpu
@@ -49,3 +50,36 @@ def test_attention():
     assert m.moe_query_device_status(ws) == 0
     for i, o in zip(order, outs):
         np.testing.assert_array_equal(o.cpu().double().numpy(), want[i], err_msg=str(i))
+
+
+def test_verification():
+    """Segments' sums of a small batch with a large vocabulary could lie where
+    a large batch has its counters. Every output is written and right, however
+    the batch changes."""
+    g = torch.Generator().manual_seed(60)
+    work, want = [], []
+    for B, T, V, dtype in ((4, 2, 90000, "fp32"), (512, 3, 9000, "fp32"), (40, 1, 40000, "bf16"),
+                           (1, 31, 5, "fp16"), (2000, 1, 300, "bf16")):
+        dt = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+        p = torch.softmax(3 * torch.randn((B, T + 1, V), generator=g), -1).to(dt)
+        draft = p[:, :T].float().argmax(-1).to(torch.int32)
+        n = torch.randint(0, T + 1, (B,), generator=g, dtype=torch.int32)
+        u = torch.rand((B, T + 1), generator=g)
+        want.append(ref.verify(p.double().numpy(), None, draft.numpy(), n.numpy(),
+                               u.double().numpy()))
+        work.append((m.make_verify_shape(B, T, V, dtype), p.to(DEV), draft.to(DEV), n.to(DEV),
+                     u.to(DEV)))
+    need = [m.load().moe_verify_workspace_bytes(w[0]) for w in work]
+    ws = torch.empty(max(need), dtype=torch.uint8, device=DEV)
+    m.moe_workspace_init(ws)
+    order, outs = [0, 1, 0, 1, 2, 1, 4, 0, 4, 3, 1, 2, 4, 1, 0], []
+    for i in order:
+        shape, p, draft, n, u = work[i]
+        tokens = torch.full(u.shape, -7, dtype=torch.int32, device=DEV)
+        acc = torch.full(n.shape, -7, dtype=torch.int32, device=DEV)
+        m.moe_verify_drafts(shape, p, None, draft, n, u, tokens, acc, ws)
+        outs.append((tokens, acc))
+    assert m.moe_query_device_status(ws) == 0
+    for i, (tokens, acc) in zip(order, outs):
+        np.testing.assert_array_equal(tokens.cpu().numpy(), want[i][0], err_msg=str(i))
+        np.testing.assert_array_equal(acc.cpu().numpy(), want[i][1], err_msg=str(i))

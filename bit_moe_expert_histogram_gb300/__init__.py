@@ -11,8 +11,9 @@ moe_combine, moe_layer_w4, moe_workspace_bytes, moe_max_blocks,
 moe_workspace_init, moe_query_device_status, moe_debug_dequant_w4,
 moe_debug_dequant_w4_decode; for one sequence moe_attn_decode, moe_gdn_scan,
 moe_gdn_chunked_scan; for a batch of requests over one page pool
-moe_cache_fork, moe_cache_reserve, moe_cache_write, moe_cache_compact,
-moe_cache_copy_pages, moe_attn_batch, moe_verify_drafts.
+moe_cache_fork, moe_cache_reserve, moe_cache_write, moe_cache_compact (with
+moved: moe_cache_compact_map), moe_cache_copy_pages, moe_attn_batch,
+moe_verify_drafts.
 """
 import ctypes as C
 import os
@@ -43,8 +44,8 @@ EXPORTS = ("moe_workspace_bytes", "moe_max_blocks", "moe_workspace_init", "moe_r
            "moe_decoder_blocks", "moe_attn_workspace_bytes", "moe_attn_decode",
            "moe_gdn_scan", "moe_gdn_chunked_workspace_bytes", "moe_gdn_chunked_scan",
            "moe_cache_workspace_bytes", "moe_cache_fork", "moe_cache_reserve", "moe_cache_write",
-           "moe_cache_compact", "moe_cache_copy_pages", "moe_verify_workspace_bytes",
-           "moe_verify_drafts", "moe_attn_batch_workspace_bytes", "moe_attn_batch")
+           "moe_cache_compact", "moe_cache_compact_map", "moe_cache_copy_pages",
+           "moe_verify_workspace_bytes", "moe_verify_drafts", "moe_attn_batch_workspace_bytes", "moe_attn_batch")
 
 
 class MoeError(RuntimeError):
@@ -164,6 +165,7 @@ def load():
                     ("moe_cache_reserve", [pC, pM, P, pM, P, P, I32, P, SZ, P]),
                     ("moe_cache_write", [pC, pM, P, I32, P, I64, P, I64, P, P, P, SZ, P]),
                     ("moe_cache_compact", [pC, pM, pM, P, P, I32, P, SZ, P]),
+                    ("moe_cache_compact_map", [pC, pM, pM, P, P, P, I32, P, SZ, P]),
                     ("moe_cache_copy_pages", [pC, I32, P, P, P, P, I32, I32, P, SZ, P]),
                     ("moe_attn_batch", [pA, P, I64, P, P, I32, P, P, P, P, P, P, SZ, P]),
                     ("moe_verify_drafts", [pV, P, P, P, P, P, P, P, P, SZ, P])):
@@ -498,12 +500,16 @@ def _pool(t, shape, what):
     return t.data_ptr()
 
 
-def moe_cache_compact(shape, meta, out, n_live, pools, ws, stream=None):
-    """Moves the held pages to the front of every pool; n_live[0] = how many."""
+def moe_cache_compact(shape, meta, out, n_live, pools, ws, stream=None, moved=None):
+    """Moves the held pages to the front of every pool; n_live[0] = how many.
+    moved (int32 [n_phys], or None): each held page's new number, -1 for a free
+    one. Page numbers kept outside the tables (a `prefix` of moe_attn_batch,
+    pinned pages) are moved[old] from here on."""
     ptr, k = _pools(shape, pools, shape.n_phys)
-    _check((_lib or load()).moe_cache_compact(
-        shape, meta.of(shape), out.of(shape), _ints(n_live, (1,), "n_live"), ptr, k, _ws(ws),
-        ws.numel(), _raw_stream(stream)), "moe_cache_compact")
+    _check((_lib or load()).moe_cache_compact_map(
+        shape, meta.of(shape), out.of(shape), _ints(n_live, (1,), "n_live"),
+        _ints(moved, (shape.n_phys,), "moved"), ptr, k, _ws(ws), ws.numel(), _raw_stream(stream)),
+        "moe_cache_compact")
 
 
 def moe_cache_copy_pages(shape, src, dst, from_pools, to_pools, ws, stream=None):

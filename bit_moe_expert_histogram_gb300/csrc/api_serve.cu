@@ -110,14 +110,23 @@ moe_status_t moe_cache_compact(const moe_cache_shape_t* shape, const moe_cache_m
                                const moe_cache_meta_t* out, int32_t* n_live_dev,
                                void* const* pools_host, int32_t n_pools, void* ws_dev,
                                size_t ws_bytes, moe_stream_t stream) {
+  return moe_cache_compact_map(shape, in, out, n_live_dev, nullptr, pools_host, n_pools, ws_dev,
+                               ws_bytes, stream);
+}
+
+moe_status_t moe_cache_compact_map(const moe_cache_shape_t* shape, const moe_cache_meta_t* in,
+                                   const moe_cache_meta_t* out, int32_t* n_live_dev,
+                                   int32_t* moved_dev, void* const* pools_host, int32_t n_pools,
+                                   void* ws_dev, size_t ws_bytes, moe_stream_t stream) {
   if (!cache_supported(shape)) return MOE_ERR_UNSUPPORTED_SHAPE;
   CachePools pools;
-  if (!metas_ok(in, out) || !ints(n_live_dev) || !pools_ok(pools_host, n_pools, &pools))
+  if (!metas_ok(in, out) || !ints(n_live_dev) || !aligned(moved_dev, 4) ||
+      !pools_ok(pools_host, n_pools, &pools))
     return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_ws(ws_dev, ws_bytes, cache_ws_bytes(shape)));
   int nsm = 0;
   MOE_TRY(device_sm_count(&nsm));
-  return done(launch_cache_compact(shape, *in, *out, n_live_dev, pools,
+  return done(launch_cache_compact(shape, *in, *out, n_live_dev, moved_dev, pools,
                                    static_cast<uint8_t*>(ws_dev), nsm, (cudaStream_t)stream),
               "cache compact launch");
 }

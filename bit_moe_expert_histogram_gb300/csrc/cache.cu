@@ -436,14 +436,16 @@ __global__ void __launch_bounds__(kRankChunk)
   }
 }
 
-// The moves in every pool, the tables and the counts. The first meta_ctas
-// CTAs take the state, the others the pages.
+// The moves in every pool, the tables and the counts, and where each page went
+// (moved, or null). The first meta_ctas CTAs take the state, the others the
+// pages.
 __global__ void __launch_bounds__(256)
     cache_move_kernel(const __grid_constant__ CachePools pools, const moe_cache_meta_t in,
                       const moe_cache_meta_t out, int n_slots, int max_blocks, int n_phys, int n_kv,
                       int row_u4, const int32_t* __restrict__ rank, const int32_t* __restrict__ src,
                       const int32_t* __restrict__ dst, const int32_t* __restrict__ n_live,
-                      const int32_t* __restrict__ n_moves, int meta_ctas, Ctrl* ctrl) {
+                      const int32_t* __restrict__ n_moves, int32_t* __restrict__ moved,
+                      int meta_ctas, Ctrl* ctrl) {
   pdl_wait();
   pdl_trigger();
   if ((int)blockIdx.x >= meta_ctas) {
@@ -482,6 +484,8 @@ __global__ void __launch_bounds__(256)
       if (r == 0) r = __ldg(in.refs_dev + __ldg(src + __ldg(rank + p)));
     }
     out.refs_dev[p] = r;
+    if (moved)
+      moved[p] = __ldg(in.refs_dev + p) == 0 ? -1 : p < L ? p : __ldg(dst + __ldg(rank + p));
   }
 }
 
@@ -591,7 +595,7 @@ cudaError_t launch_cache_write(const moe_cache_shape_t* s, const moe_cache_meta_
 }
 
 cudaError_t launch_cache_compact(const moe_cache_shape_t* s, const moe_cache_meta_t& in,
-                                 const moe_cache_meta_t& out, int32_t* n_live,
+                                 const moe_cache_meta_t& out, int32_t* n_live, int32_t* moved,
                                  const CachePools& pools, uint8_t* ws, int nsm,
                                  cudaStream_t stream) {
   const CacheWs w = cache_ws(s);
@@ -609,7 +613,7 @@ cudaError_t launch_cache_compact(const moe_cache_shape_t* s, const moe_cache_met
   const int ctas = copy_ctas((int64_t)(s->n_phys / 2) * pools.n, nsm);
   return launch_pdl(cache_move_kernel, dim3(meta + ctas), dim3(256), 0, stream, pools, in, out,
                     s->n_slots, s->max_blocks, s->n_phys, s->n_kv, s->D / 8, at(ws, w.rank),
-                    at(ws, w.src), at(ws, w.dst), n_live, at(ws, w.moves), meta, ctrl);
+                    at(ws, w.src), at(ws, w.dst), n_live, at(ws, w.moves), moved, meta, ctrl);
 }
 
 cudaError_t launch_cache_copy_pages(const moe_cache_shape_t* s, int n, const int32_t* src,

@@ -192,7 +192,7 @@ cudaError_t launch_cache_write(const moe_cache_shape_t* s, const moe_cache_meta_
                                int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
                                void* k_cache, void* v_cache, uint8_t* ws, cudaStream_t stream);
 cudaError_t launch_cache_compact(const moe_cache_shape_t* s, const moe_cache_meta_t& in,
-                                 const moe_cache_meta_t& out, int32_t* n_live,
+                                 const moe_cache_meta_t& out, int32_t* n_live, int32_t* moved,
                                  const CachePools& pools, uint8_t* ws, int nsm,
                                  cudaStream_t stream);
 cudaError_t launch_cache_copy_pages(const moe_cache_shape_t* s, int n, const int32_t* src,

@@ -504,12 +504,23 @@ moe_status_t moe_cache_write(const moe_cache_shape_t* shape, const moe_cache_met
 
 /* Brings the held pages to the front: with L pages held, the i-th held page
  * at or past L moves to the i-th free page below L, in every pool; tables and
- * refs follow, pages from L on are free after it.
+ * refs follow, pages from L on are free after it. Pages that are held by a
+ * caller's own counts move like the others: page numbers kept outside the
+ * tables (pinned pages, the prefix_dev of moe_attn_batch) have to be taken
+ * through the map of moe_cache_compact_map.
  *  n_live_dev int32 [1] out: L */
 moe_status_t moe_cache_compact(const moe_cache_shape_t* shape, const moe_cache_meta_t* in,
                                const moe_cache_meta_t* out, int32_t* n_live_dev,
                                void* const* pools_host, int32_t n_pools, void* ws_dev,
                                size_t ws_bytes, moe_stream_t stream);
+
+/* moe_cache_compact, saying where the pages went.
+ *  moved_dev int32 [n_phys] out, or NULL: the new number of each held page
+ *            (its own where it stayed), -1 for a free one */
+moe_status_t moe_cache_compact_map(const moe_cache_shape_t* shape, const moe_cache_meta_t* in,
+                                   const moe_cache_meta_t* out, int32_t* n_live_dev,
+                                   int32_t* moved_dev, void* const* pools_host, int32_t n_pools,
+                                   void* ws_dev, size_t ws_bytes, moe_stream_t stream);
 
 /* Whole pages: page src_dev[i] of every pool of from_host to page dst_dev[i]
  * of the same pool of to_host (which may be the same pools: then no page may

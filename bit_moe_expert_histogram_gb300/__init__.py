@@ -482,16 +482,24 @@ def moe_cache_reserve(shape, meta, n_new, out, granted, pools, ws, stream=None):
 
 def moe_cache_write(shape, meta, n_new, k_new, v_new, k_cache, v_cache, ws, stream=None):
     """Keys and values [n_slots][T][n_kv][D] of the last n_new[s] positions
-    (None: T) of every slot into one layer's pools."""
+    (None: T) of every slot into one layer's pools of their type."""
     B, n_kv, D = shape.n_slots, shape.n_kv, shape.D
     new = (B, k_new.shape[1], n_kv, D)
     kp, ks = _tokens(k_new, new, "k_new")
     vp, vs = _tokens(v_new, new, "v_new")
     cache = (shape.n_phys, n_kv, shape.block, D)
+    _alike(k_new, k_cache, "k_new and k_cache")
+    _alike(v_new, v_cache, "v_new and v_cache")
     _check((_lib or load()).moe_cache_write(
         shape, meta.of(shape), _ints(n_new, (B,), "n_new"), new[1], kp, ks, vp, vs,
         _pool(k_cache, cache, "k_cache"), _pool(v_cache, cache, "v_cache"), _ws(ws), ws.numel(),
         _raw_stream(stream)), "moe_cache_write")
+
+
+def _alike(a, b, what):
+    """Rows are copied as they are: one type, or int16 bits on either side."""
+    if a.dtype is not b.dtype and torch.int16 not in (a.dtype, b.dtype):
+        raise ValueError("%s must be of one type, got %s and %s" % (what, a.dtype, b.dtype))
 
 
 def _pool(t, shape, what):
@@ -516,6 +524,8 @@ def moe_cache_copy_pages(shape, src, dst, from_pools, to_pools, ws, stream=None)
     """Page src[i] of every pool of from_pools to page dst[i] of to_pools."""
     if not from_pools.pools or len(from_pools.pools) != len(to_pools.pools):
         raise ValueError("as many pools on both sides, one at least")
+    for a, b in zip(from_pools.pools, to_pools.pools):
+        _alike(a, b, "a pool and the one it is copied to")
     n_to = to_pools.pools[0].shape[0]
     a, k = _pools(shape, from_pools, shape.n_phys)
     b, _ = _pools(shape, to_pools, n_to)

@@ -416,17 +416,23 @@ def alloc_cache_workspace(shape, device="cuda", stream=None):
 class CacheMeta:
     """State of a batch's cache (moe_cache_meta_t): table int32
     [n_slots][max_blocks], lens int32 [n_slots], refs int32 [n_phys]. The
-    calls read one and write another; a program keeps two and swaps them."""
+    calls read one and write another; a program keeps two and swaps them.
+    The addresses are taken once, so the tensors can be changed in place but
+    not exchanged for others."""
 
     def __init__(self, table, lens, refs):
         if table.dim() != 2 or refs.dim() != 1:
             raise ValueError("table is [n_slots][max_blocks], refs [n_phys]")
-        self.table, self.lens, self.refs = table, lens, refs
+        self._tensors = table, lens, refs
         self.ptrs = CacheMetaPtrs(_ints(table, table.shape, "table"),
                                   _ints(lens, table.shape[:1], "lens"),
                                   _ints(refs, refs.shape, "refs"))
         self._dims = tuple(table.shape) + tuple(refs.shape)
         self._ref = C.byref(self.ptrs)
+
+    table = property(lambda self: self._tensors[0])
+    lens = property(lambda self: self._tensors[1])
+    refs = property(lambda self: self._tensors[2])
 
     @classmethod
     def empty(cls, shape, device="cuda"):
@@ -443,13 +449,13 @@ class CacheMeta:
 def pool_table(pools):
     """Host array of the pools' device pointers (16-bit [n_phys][n_kv][64][D]
     each) for moe_cache_reserve, moe_cache_compact and moe_cache_copy_pages;
-    it keeps the tensors."""
+    it keeps the tensors, whose addresses it has taken."""
     arr = (C.c_void_p * max(1, len(pools)))()
     for i, t in enumerate(pools):
         if t.dim() != 4:
             raise ValueError("pools are [n_phys][n_kv][64][D]")
         arr[i] = _pool(t, pools[0].shape, "every pool")
-    arr.pools = list(pools)
+    arr.pools = tuple(pools)
     return arr
 
 

@@ -33,3 +33,12 @@ def test_compaction_with_a_map(lib):
     assert call(k=129) == m.MOE_ERR_INVALID_ARG
     assert call(have=need - 1) == m.MOE_ERR_WORKSPACE
     assert call(s=m.CacheShape(8, 16, 0, 2, 128, 64)) == m.MOE_ERR_UNSUPPORTED_SHAPE
+
+
+def test_a_states_tensors_cannot_be_exchanged():
+    """The addresses were taken when the state was made: another tensor put in
+    a tensor's place would not be read, and the old one's memory would be."""
+    state = m.CacheMeta.__new__(m.CacheMeta)
+    for name in ("table", "lens", "refs"):
+        with pytest.raises(AttributeError):
+            setattr(state, name, None)

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kOneCta)
   for (int s = blockIdx.x * slots + threadIdx.x / per; s < n_slots; s += gridDim.x * slots) {
     const int a = __ldg(parent + s);
     const bool live = a >= 0 && a < n_slots;
-    if (j0 == 0 && a >= n_slots) set_error(ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
+    if (j0 == 0 && (a >= n_slots || a < -1)) set_error(ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
     int len = 0;
     if (live) {
       len = len_of(in.lens_dev, a, max_blocks, ctrl);

@@ -435,10 +435,12 @@ moe_status_t moe_gdn_chunked_scan(const moe_gdn_shape_t* shape, const void* q_de
  * A slot's entries are the first ceil(len / 64) of its row; the calls write
  * -1 past them. Calls that change the state read `in` and write `out`, which
  * must not share an array: the old state stays whole, so a caller can drop a
- * result (of a reservation that was refused, say). A length, count or entry
- * out of range is recorded as MOE_ERR_BAD_INPUT and its slot or page is left
- * out; no such value leads to an access out of bounds. All of it is integer
- * work and copies: deterministic.
+ * result (of a reservation that was refused, say). A slot number, request,
+ * count or entry out of range is recorded as MOE_ERR_BAD_INPUT and its slot or
+ * page is left out; a length out of range is recorded and counts as 0 or as
+ * the row's whole width (moe_cache_write leaves its slot out). No such value
+ * leads to an access out of bounds. All of it is integer work and copies:
+ * deterministic.
  * ---------------------------------------------------------------------- */
 typedef enum moe_dtype { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP16 = 1, MOE_DTYPE_FP32 = 2 } moe_dtype_t;
 
@@ -463,7 +465,8 @@ size_t moe_cache_workspace_bytes(const moe_cache_shape_t* shape);
 
 /* Fork, reorder, cut and free: slot s of `out` holds what slot parent_dev[s]
  * of `in` held, the first keep_dev[s] positions of it at most (keep_dev NULL:
- * all of them); parent -1 leaves the slot empty. Pages are shared, not
+ * all of them; below 0: none); parent -1 leaves the slot empty, as any other
+ * number that is no slot does, which is recorded. Pages are shared, not
  * copied; refs follow. parent[s] = s with keep drops the tail of a slot (its
  * rejected drafts), beams of one request are parents of each other.
  *  parent_dev int32 [n_slots], keep_dev int32 [n_slots] or NULL */

@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(kVThr, kVCtas<DT>) verify_kernel(const VerifyA
   // ---- the slot's last CTA: first the segment, a warp with 8 a lane
   // (S <= 256). The first segment whose running sum passes the threshold;
   // where none does (u_T not below 1, or a rounding), the last that weighs
-  // anything. s_first: the segment, -1 where nothing weighs anything.
+  // anything. s_first: the segment, -1 where nothing weighs anything, -2 where
+  // the sum is past fp32's largest number (the thresholds mean nothing then).
   const float u_new = __ldg(a.u + (int64_t)b * (T + 1) + T);
   auto find_segment = [&](const float2* part) {
     Pair v[8], sum{0.0f, 0.0f};
@@ -374,9 +375,10 @@ __global__ void __launch_bounds__(kVThr, kVCtas<DT>) verify_kernel(const VerifyA
     const Pair thr = times(u_new, total);
     const unsigned past = __ballot_sync(0xFFFFFFFFu, sum.s > 0.0f && above(tidy(inc), thr));
     const unsigned some = __ballot_sync(0xFFFFFFFFu, sum.s > 0.0f);
-    if (lane == 0) s_first = -1;
+    const bool finite = fabsf(total.s) < INFINITY;  // a NaN is not
+    if (lane == 0) s_first = finite ? -1 : -2;
     __syncwarp();
-    if (some && lane == (past ? __ffs(past) - 1 : 31 - __clz(some))) {
+    if (finite && some && lane == (past ? __ffs(past) - 1 : 31 - __clz(some))) {
       Pair run = inc, base;
       add(run, neg(sum));
       base = run;
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kVThr, kVCtas<DT>) verify_kernel(const VerifyA
   };
   if (warp == 0) find_segment(a.part + (int64_t)b * S);
   __syncthreads();
-  if (s_first < 0 && rejected) {
+  if (s_first == -1 && rejected) {
     // nothing left of the difference: the target's own row, summed here (a
     // case of roundings, where q is nowhere below p)
     r.q = nullptr;
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kVThr, kVCtas<DT>) verify_kernel(const VerifyA
     __syncthreads();
     token = s_i;
   } else if (tid == 0) {
-    set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_VERIFY, b);  // a row without any weight
+    set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_VERIFY, b);  // no weight, or past all numbers
   }
   if (tid <= T) {
     const int64_t at = (int64_t)b * (T + 1) + tid;

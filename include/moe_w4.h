@@ -592,7 +592,8 @@ moe_status_t moe_attn_batch(const moe_attn_batch_shape_t* shape, const void* q_d
  * Sums carry more than 48 bits and u q is exact, so the tokens do not depend
  * on an order of summation. Entries that are not positive and finite weigh
  * nothing. A drafted id outside [0, V) is rejected and recorded; a row
- * without any weight gives token -1 and is recorded.
+ * without any weight, or whose weights' sum is past fp32's largest number,
+ * gives token -1 and is recorded.
  *  p_dev       [n_slots][T + 1][V] target's probabilities (need not sum to 1)
  *  q_dev       [n_slots][T][V] the draft's, same type, or NULL: the drafts
  *              are certain (q_t(x_t) = 1, 0 elsewhere)

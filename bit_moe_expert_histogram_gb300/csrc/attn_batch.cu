@@ -36,8 +36,9 @@
 //    (m, l, O), and attn_join_kernel joins them all, a thread for four
 //    elements of the output: few threads wait long for what many threads
 //    fetch at once (one slot of 32768 positions: 28 us against 12.4).
-// 33 slots of up to 5000 positions, D = 64, fp16, 65 MB: 15.0 us in a graph,
-// 4.3 TB/s, 0.64 of a plain copy's rate (the next call's reads partly from L2).
+// 33 slots of up to 5000 positions, D = 64, fp16, 65 MB: 14.5 us in a graph,
+// 4.5 TB/s, 0.66 of a plain copy's rate (the next call's reads partly from L2;
+// 17 us where the pages lie badly).
 #include "attn_batch.cuh"
 
 namespace moe {

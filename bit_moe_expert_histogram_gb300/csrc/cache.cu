@@ -20,9 +20,9 @@
 // one takes two and three short kernels chained by programmatic dependent
 // launch. (One cooperative launch whose CTAs meet in the workspace takes the
 // host 1.3 us less than two, but the GPU 6.4 us instead of 4.1 for 1000 slots
-// and 4.5 instead of 2.9 for 16.) Fork of 16 and of 1000 slots: 3.1 and 4.1 us
-// in a graph, 5.3 and 6.9 from the host; 2500 pages of a pool of 8192 brought
-// together in 4 pools: 75.5 us, 6.0 TB/s, 0.89 of a plain copy's rate.
+// and 4.5 instead of 2.9 for 16.) Fork of 16 and of 1000 slots: 2.6 and 4.1 us
+// in a graph, 5.3 and 6.9 from the host; 1740 pages of 4 pools of 8192 brought
+// together: 75.3 us, 6.05 TB/s, 0.89 of a plain copy's rate.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -531,7 +531,7 @@ int copy_ctas(int64_t pages, int nsm) { return (int)(pages < nsm * 8 ? pages : n
 size_t cache_ws_bytes(const moe_cache_shape_t* s) { return cache_ws(s).total; }
 
 // Few enough that one CTA, with four warps or one for a row, is done in the
-// time of a launch: 2.8 us for a round or two of 32 rows x 32 entries, 4.7 for
+// time of a launch: 2.6 us for a round or two of 32 rows x 32 entries, 4.7 for
 // three, against 3.3 of a CTA a slot after a launch for the counts (one CTA
 // that was given 461 slots took 40 us).
 namespace {

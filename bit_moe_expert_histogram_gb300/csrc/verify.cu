@@ -11,11 +11,16 @@
 // The token is a whole number that a rounding must not change, so nothing
 // here rounds where it could: u q is formed in 64 bits (two 24-bit factors,
 // exact), p - q as an fp32 pair without error, and the sums, the threshold
-// and the comparisons are fp32 pairs (value and error term, more than 46
-// bits). FP64 does the same in fewer lines, but its rate here is a small
-// fraction of fp32's: joining the threads in fp32 pairs instead took 57.5 us
-// to 28.2 (64 slots of 131072 in bf16), the search for the token too 26.6 to
-// 22.5, and 11.9 to 7.1 for one slot of 32000.
+// and the comparisons are fp32 pairs (value and error term). An addition adds
+// at most 2^-24 of its sum to the error terms, so after k of them these hold
+// (k + 1) 2^-24 of it, and their own two roundings an addition less than
+// k (k + 2) 2^-48: 2^-37.9 for a total (32 additions deep), 2^-36.6 for a
+// running sum (50), together below 2^-36 of the total on a threshold's way to
+// a border. Restated on the host, totals of random rows were off by less than
+// 2^-43 (vocabularies of 32000 to 2^20). FP64 does the same in fewer lines,
+// but its rate here is a small fraction of fp32's: joining the threads in fp32
+// pairs instead took 57.5 us to 28.2 (64 slots of 131072 in bf16), the search
+// for the token too 26.6 to 22.5, and 11.9 to 7.1 for one slot of 32000.
 //
 // What it has to read is one row of p and one of q per slot: HBM bounds large
 // batches, a chain of dependent accesses small ones. The vocabulary is cut

@@ -550,10 +550,12 @@ moe_status_t moe_cache_copy_pages(const moe_cache_shape_t* shape, int32_t n,
  * the table's entries there are not read. A slot may be shorter than that.
  * Keys and values of positions below a slot's length have to be finite; what
  * its pages hold past it does not matter. A page number outside [0, n_phys)
- * is recorded as MOE_ERR_BAD_INPUT and its positions are left out.
+ * is recorded as MOE_ERR_BAD_INPUT and its positions are left out; a length or
+ * count out of range is recorded and brought into it.
  *  q_dev       token (s, t) starts q_stride * (s * T + t) elements in,
  *              [n_q][D]; 16-byte aligned, q_stride >= n_q * D, a multiple of 8
- *  k_cache_dev, v_cache_dev [n_phys][n_kv][64][D], 16-byte aligned
+ *  k_cache_dev, v_cache_dev [n_phys][n_kv][64][D], 16-byte aligned;
+ *              (n_phys + 1) * n_kv * 64 below 2^31
  *  table_dev   int32 [n_slots][max_blocks]
  *  prefix_dev  int32 [prefix_blocks], or NULL when prefix_blocks is 0
  *  lens_dev    int32 [n_slots]; n_new_dev int32 [n_slots] or NULL (T)
@@ -581,20 +583,25 @@ moe_status_t moe_attn_batch(const moe_attn_batch_shape_t* shape, const void* q_d
                             const int32_t* lens_dev, const int32_t* n_new_dev, void* o_dev,
                             void* ws_dev, size_t ws_bytes, moe_stream_t stream);
 
-/* Verification of drafted tokens (speculative sampling: the tokens come out
- * distributed as the target's, whatever the draft's distribution was). Slot
- * s has n = n_draft_dev[s] drafts x_t drawn from q_t:
+/* Verification of drafted tokens (speculative sampling: where rows sum to 1,
+ * or p_t and q_t to the same number, the tokens come out distributed as the
+ * target's, whatever the draft's distribution was). Slot s has n = n_draft_dev[s] drafts x_t drawn from q_t:
  *   draft t is accepted while u_t q_t(x_t) < p_t(x_t); i = the first that is
  *   not, n when all are;
  *   w = max(p_i - q_i, 0) where i < n, or p_i where that is 0 everywhere;
  *   w = p_n where i = n;
  *   the new token is the least v with w_0 + .. + w_v > u_T (w_0 + .. + w_{V-1}).
- * Sums carry more than 48 bits and u q is exact, so the tokens do not depend
- * on an order of summation. Entries that are not positive and finite weigh
+ * The first test is exact. Sums are fp32 pairs (a value and an error term)
+ * added in an order that V and the rows' alignment fix: deterministic, and a
+ * threshold u_T (w_0 + ..) of a row that sums to 2^-100 or more falls to its
+ * side of every border that is 2^-36 of the sum or more away (the worst that
+ * roundings could add up to; totals of random rows were off by less than
+ * 2^-43). Entries that are not positive and finite weigh
  * nothing. A drafted id outside [0, V) is rejected and recorded; a row
  * without any weight, or whose weights' sum is past fp32's largest number,
  * gives token -1 and is recorded.
- *  p_dev       [n_slots][T + 1][V] target's probabilities (need not sum to 1)
+ *  p_dev       [n_slots][T + 1][V] target's probabilities (need not sum to 1,
+ *              but p_t is compared with q_t as it is)
  *  q_dev       [n_slots][T][V] the draft's, same type, or NULL: the drafts
  *              are certain (q_t(x_t) = 1, 0 elsewhere)
  *  draft_dev   int32 [n_slots][T]; n_draft_dev int32 [n_slots] or NULL (T)

@@ -13,7 +13,8 @@ moe_debug_dequant_w4_decode; for one sequence moe_attn_decode, moe_gdn_scan,
 moe_gdn_chunked_scan; for a batch of requests over one page pool
 moe_cache_fork, moe_cache_reserve, moe_cache_write, moe_cache_compact (with
 moved: moe_cache_compact_map), moe_cache_copy_pages, moe_attn_batch,
-moe_verify_drafts.
+moe_verify_drafts, moe_token_logprobs; over a cache held in 4 bits
+moe_cache_write_q4, moe_cache_read_q4, moe_attn_batch_q4.
 """
 import ctypes as C
 import os
@@ -45,7 +46,10 @@ EXPORTS = ("moe_workspace_bytes", "moe_max_blocks", "moe_workspace_init", "moe_r
            "moe_gdn_scan", "moe_gdn_chunked_workspace_bytes", "moe_gdn_chunked_scan",
            "moe_cache_workspace_bytes", "moe_cache_fork", "moe_cache_reserve", "moe_cache_write",
            "moe_cache_compact", "moe_cache_compact_map", "moe_cache_copy_pages",
-           "moe_verify_workspace_bytes", "moe_verify_drafts", "moe_attn_batch_workspace_bytes", "moe_attn_batch")
+           "moe_verify_workspace_bytes", "moe_verify_drafts", "moe_attn_batch_workspace_bytes", "moe_attn_batch",
+           "moe_cache_q4_units", "moe_cache_write_q4", "moe_cache_read_q4",
+           "moe_attn_batch_q4_workspace_bytes", "moe_attn_batch_q4",
+           "moe_logprobs_workspace_bytes", "moe_token_logprobs")
 
 
 class MoeError(RuntimeError):
@@ -93,6 +97,10 @@ class AttnBatchShape(C.Structure):
 
 class VerifyShape(C.Structure):
     _fields_ = [("n_slots", C.c_int32), ("T", C.c_int32), ("V", C.c_int32), ("dtype", C.c_int32)]
+
+
+class LogprobsShape(C.Structure):
+    _fields_ = [("n_rows", C.c_int32), ("V", C.c_int32), ("k", C.c_int32), ("dtype", C.c_int32)]
 
 
 class W4Weights(C.Structure):
@@ -143,6 +151,13 @@ def load():
             pA = C.POINTER(AttnBatchShape)
             L.moe_attn_batch_workspace_bytes.restype = SZ
             L.moe_attn_batch_workspace_bytes.argtypes = [pA]
+            L.moe_attn_batch_q4_workspace_bytes.restype = SZ
+            L.moe_attn_batch_q4_workspace_bytes.argtypes = [pA]
+            pL = C.POINTER(LogprobsShape)
+            L.moe_logprobs_workspace_bytes.restype = SZ
+            L.moe_logprobs_workspace_bytes.argtypes = [pL]
+            L.moe_cache_q4_units.restype = I32
+            L.moe_cache_q4_units.argtypes = [I32]
             I64 = C.c_int64
             for name, args in (
                     ("moe_workspace_init", [P, SZ, P]),
@@ -168,6 +183,12 @@ def load():
                     ("moe_cache_compact_map", [pC, pM, pM, P, P, P, I32, P, SZ, P]),
                     ("moe_cache_copy_pages", [pC, I32, P, P, P, P, I32, I32, P, SZ, P]),
                     ("moe_attn_batch", [pA, P, I64, P, P, I32, P, P, P, P, P, P, SZ, P]),
+                    ("moe_cache_write_q4",
+                     [pC, pM, P, I32, I32, P, I64, P, I64, P, P, P, SZ, P]),
+                    ("moe_cache_read_q4",
+                     [pC, pM, P, P, I32, P, P, I32, P, I64, P, I64, P, SZ, P]),
+                    ("moe_attn_batch_q4", [pA, P, I64, P, P, I32, P, P, P, P, P, SZ, P]),
+                    ("moe_token_logprobs", [pL, P, I64, P, P, P, P, P, P, SZ, P]),
                     ("moe_verify_drafts", [pV, P, P, P, P, P, P, P, P, SZ, P])):
                 f = getattr(L, name)
                 f.restype = C.c_int
@@ -593,6 +614,136 @@ def moe_verify_drafts(shape, p, q, draft, n_draft, u, tokens, n_acc, ws, stream=
         _ints(n_draft, (B,), "n_draft"), _tensor(u, torch.float32, (B, T + 1), "u"),
         _ints(tokens, (B, T + 1), "tokens"), _ints(n_acc, (B,), "n_acc"), _ws(ws), ws.numel(),
         _raw_stream(stream)), "moe_verify_drafts")
+
+
+# --------------------------------------------------- a cache held in 4 bits --
+def moe_cache_q4_units(D):
+    """16-bit units of a head's 4-bit row: 40 for D = 128, 24 for D = 64."""
+    n = (_lib or load()).moe_cache_q4_units(D)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_cache_q4_units")
+    return n
+
+
+def q4_page_shape(shape):
+    """The cache shape under which the page calls (moe_cache_reserve,
+    moe_cache_compact, moe_cache_copy_pages) move the 4-bit pools of `shape`."""
+    return CacheShape(shape.n_slots, shape.max_blocks, shape.n_phys, shape.n_kv,
+                      moe_cache_q4_units(shape.D), shape.block)
+
+
+def alloc_q4_pool(shape, device="cuda"):
+    """A pool of 4-bit rows, int16 [n_phys][n_kv][64][units] (uninitialised)."""
+    return torch.empty((shape.n_phys, shape.n_kv, shape.block, moe_cache_q4_units(shape.D)),
+                       dtype=torch.int16, device=device)
+
+
+def _q4_pool(t, shape, what):
+    if t.dtype is not torch.int16 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _bad(t, what, "int16", shape)
+    return t.data_ptr()
+
+
+def _rows_of(t, shape, dtype, what):
+    """As _tokens, for outputs and rows of any element size."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        _bad(t, what, dtype, shape)
+    n_slots, T, heads, D = shape
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 or (heads > 1 and s2 != D):
+        raise ValueError("%s: a token's elements must be dense" % what)
+    stride = s1 if T > 1 else s0 if n_slots > 1 else heads * D
+    if T > 1 and n_slots > 1 and s0 != T * stride:
+        raise ValueError("%s: tokens must lie evenly apart" % what)
+    return t.data_ptr(), stride
+
+
+def moe_cache_write_q4(shape, meta, n_new, k_new, v_new, k_cache, v_cache, ws, stream=None):
+    """moe_cache_write into 4-bit pools (alloc_q4_pool): bf16 or fp16 rows
+    [n_slots][T][n_kv][D] are quantised as they are written."""
+    B, n_kv, D = shape.n_slots, shape.n_kv, shape.D
+    dt = k_new.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise ValueError("k_new must be bfloat16 or float16, got %s" % dt)
+    new = (B, k_new.shape[1], n_kv, D)
+    kp, ks = _rows_of(k_new, new, dt, "k_new")
+    vp, vs = _rows_of(v_new, new, dt, "v_new")
+    cache = (shape.n_phys, n_kv, shape.block, moe_cache_q4_units(D))
+    _check((_lib or load()).moe_cache_write_q4(
+        shape, meta.of(shape), _ints(n_new, (B,), "n_new"), new[1], _DTYPE_OF.index(dt), kp, ks,
+        vp, vs, _q4_pool(k_cache, cache, "k_cache"), _q4_pool(v_cache, cache, "v_cache"), _ws(ws),
+        ws.numel(), _raw_stream(stream)), "moe_cache_write_q4")
+
+
+def moe_cache_read_q4(shape, meta, first, n, k_cache, v_cache, k_out, v_out, ws, stream=None):
+    """What positions first[s] .. first[s] + n[s] - 1 (None: from 0; T of them)
+    of every slot stand for, to k_out and v_out [n_slots][T][n_kv][D] (bf16,
+    fp16 or fp32); tokens from n[s] on stay as they were."""
+    B, n_kv, D = shape.n_slots, shape.n_kv, shape.D
+    dt = k_out.dtype
+    if dt not in _DTYPE_OF:
+        raise ValueError("k_out must be bfloat16, float16 or float32, got %s" % dt)
+    out = (B, k_out.shape[1], n_kv, D)
+    kp, ks = _rows_of(k_out, out, dt, "k_out")
+    vp, vs = _rows_of(v_out, out, dt, "v_out")
+    cache = (shape.n_phys, n_kv, shape.block, moe_cache_q4_units(D))
+    _check((_lib or load()).moe_cache_read_q4(
+        shape, meta.of(shape), _ints(first, (B,), "first"), _ints(n, (B,), "n"), out[1],
+        _q4_pool(k_cache, cache, "k_cache"), _q4_pool(v_cache, cache, "v_cache"),
+        _DTYPE_OF.index(dt), kp, ks, vp, vs, _ws(ws), ws.numel(), _raw_stream(stream)),
+        "moe_cache_read_q4")
+
+
+def alloc_attn_batch_q4_workspace(shape, device="cuda", stream=None):
+    return _workspace(load().moe_attn_batch_q4_workspace_bytes(C.byref(shape)), device, stream,
+                      "alloc_attn_batch_q4_workspace")
+
+
+def moe_attn_batch_q4(shape, q, k_cache, v_cache, table, lens, o, ws, n_new=None, stream=None):
+    """moe_attn_batch over 4-bit pools (shape.prefix_blocks is 0)."""
+    B, T, nq, D = shape.n_slots, shape.T, shape.n_q, shape.D
+    dt = torch.float16 if shape.dtype == 1 else torch.bfloat16
+    if q.dtype is not dt and q.dtype is not torch.int16:
+        raise ValueError("q must be %s, got %s" % (dt, q.dtype))
+    qp, qs = _tokens(q, (B, T, nq, D), "q")
+    n_phys = k_cache.shape[0]
+    cache = (n_phys, shape.n_kv, shape.block, moe_cache_q4_units(D))
+    _check((_lib or load()).moe_attn_batch_q4(
+        shape, qp, qs, _q4_pool(k_cache, cache, "k_cache"), _q4_pool(v_cache, cache, "v_cache"),
+        n_phys, _ints(table, (B, shape.max_blocks), "table"), _ints(lens, (B,), "lens"),
+        _ints(n_new, (B,), "n_new"), _tensor(o, dt, (B, T, nq, D), "o"), _ws(ws), ws.numel(),
+        _raw_stream(stream)), "moe_attn_batch_q4")
+
+
+# ----------------------------------------------------- log probabilities --
+def make_logprobs_shape(n_rows, V, k=0, dtype="fp32"):
+    return LogprobsShape(n_rows, V, k, DTYPES[dtype])
+
+
+def alloc_logprobs_workspace(shape, device="cuda", stream=None):
+    return _workspace(load().moe_logprobs_workspace_bytes(C.byref(shape)), device, stream,
+                      "alloc_logprobs_workspace")
+
+
+def moe_token_logprobs(shape, logits, tokens, logp, ws, entropy=None, top_ids=None, top_logp=None,
+                       stream=None):
+    """Log probabilities of tokens [n_rows] (-1: none) under logits
+    [n_rows][V] (rows may lie apart), the rows' entropies and their shape.k
+    likeliest ids with log probabilities [n_rows][k]."""
+    n, V, k = shape.n_rows, shape.V, shape.k
+    dt, f32 = _DTYPE_OF[shape.dtype], torch.float32
+    if logits.dtype is not dt or logits.shape != (n, V) or not logits.is_cuda or \
+            (V > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA tensor %s %s with dense rows, got %s %s" % (
+            dt, (n, V), logits.dtype, tuple(logits.shape)))
+    stride = logits.stride(0) if n > 1 else V
+    _check((_lib or load()).moe_token_logprobs(
+        shape, logits.data_ptr(), stride, _ints(tokens, (n,), "tokens"),
+        _tensor(logp, f32, (n,), "logp"),
+        None if entropy is None else _tensor(entropy, f32, (n,), "entropy"),
+        _ints(top_ids, (n, k), "top_ids"),
+        None if top_logp is None else _tensor(top_logp, f32, (n, k), "top_logp"), _ws(ws),
+        ws.numel(), _raw_stream(stream)), "moe_token_logprobs")
 
 
 def moe_layer_w4(shape, x, w_router, router_bias, experts, shared, y, ws, x_next=None,

@@ -4,6 +4,7 @@
 // throws.
 #include <climits>
 
+#include "attn_q4.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -209,6 +210,107 @@ moe_status_t moe_verify_drafts(const moe_verify_shape_t* shape, const void* p_de
   return done(launch_verify(shape, p_dev, q_dev, draft_dev, n_draft_dev, u_dev, tokens_dev,
                             n_acc_dev, static_cast<uint8_t*>(ws_dev), nsm, (cudaStream_t)stream),
               "draft verification launch");
+}
+
+int32_t moe_cache_q4_units(int32_t D) { return q4_units(D); }
+
+moe_status_t moe_cache_write_q4(const moe_cache_shape_t* shape, const moe_cache_meta_t* meta,
+                                const int32_t* n_new_dev, int32_t T, int32_t dtype,
+                                const void* k_new_dev, int64_t k_stride, const void* v_new_dev,
+                                int64_t v_stride, void* k_cache_dev, void* v_cache_dev,
+                                void* ws_dev, size_t ws_bytes, moe_stream_t stream) {
+  if (!cache_q4_supported(shape) || T < 1 || T > (1 << 18)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP16) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const int64_t row = (int64_t)shape->n_kv * shape->D;
+  if (!meta_ok(meta) || !aligned(n_new_dev, 4) || !k_new_dev || !v_new_dev || !k_cache_dev ||
+      !v_cache_dev || !aligned(k_new_dev, 16) || !aligned(v_new_dev, 16) ||
+      !aligned(k_cache_dev, 16) || !aligned(v_cache_dev, 16) || k_stride < row || v_stride < row ||
+      k_stride % 8 || v_stride % 8)
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ws(ws_dev, ws_bytes, cache_ws_bytes(shape)));
+  return done(launch_cache_write_q4(shape, *meta, n_new_dev, T,
+                                    static_cast<const uint16_t*>(k_new_dev), k_stride,
+                                    static_cast<const uint16_t*>(v_new_dev), v_stride,
+                                    dtype == MOE_DTYPE_FP16, k_cache_dev, v_cache_dev,
+                                    static_cast<uint8_t*>(ws_dev), (cudaStream_t)stream),
+              "4-bit cache write launch");
+}
+
+moe_status_t moe_cache_read_q4(const moe_cache_shape_t* shape, const moe_cache_meta_t* meta,
+                               const int32_t* first_dev, const int32_t* n_dev, int32_t T,
+                               const void* k_cache_dev, const void* v_cache_dev, int32_t dtype,
+                               void* k_out_dev, int64_t k_stride, void* v_out_dev,
+                               int64_t v_stride, void* ws_dev, size_t ws_bytes,
+                               moe_stream_t stream) {
+  if (!cache_q4_supported(shape) || T < 1 || T > (1 << 18)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (dtype < MOE_DTYPE_BF16 || dtype > MOE_DTYPE_FP32) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const int64_t row = (int64_t)shape->n_kv * shape->D;
+  const int64_t per = dtype == MOE_DTYPE_FP32 ? 4 : 8;  // elements of 16 bytes
+  if (!meta_ok(meta) || !aligned(first_dev, 4) || !aligned(n_dev, 4) || !k_cache_dev ||
+      !v_cache_dev || !k_out_dev || !v_out_dev || !aligned(k_cache_dev, 16) ||
+      !aligned(v_cache_dev, 16) || !aligned(k_out_dev, 16) || !aligned(v_out_dev, 16) ||
+      k_stride < row || v_stride < row || k_stride % per || v_stride % per)
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ws(ws_dev, ws_bytes, cache_ws_bytes(shape)));
+  return done(launch_cache_read_q4(shape, *meta, first_dev, n_dev, T, k_cache_dev, v_cache_dev,
+                                   k_out_dev, k_stride, v_out_dev, v_stride, dtype,
+                                   static_cast<uint8_t*>(ws_dev), (cudaStream_t)stream),
+              "4-bit cache read launch");
+}
+
+size_t moe_attn_batch_q4_workspace_bytes(const moe_attn_batch_shape_t* shape) {
+  return attn_q4_supported(shape) ? attn_q4_ws_bytes(shape) : 0;
+}
+
+moe_status_t moe_attn_batch_q4(const moe_attn_batch_shape_t* shape, const void* q_dev,
+                               int64_t q_stride, const void* k_cache_dev, const void* v_cache_dev,
+                               int32_t n_phys, const int32_t* table_dev, const int32_t* lens_dev,
+                               const int32_t* n_new_dev, void* o_dev, void* ws_dev,
+                               size_t ws_bytes, moe_stream_t stream) {
+  if (!attn_q4_supported(shape)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!q_dev || !k_cache_dev || !v_cache_dev || !o_dev || !aligned(q_dev, 16) ||
+      !aligned(k_cache_dev, 16) || !aligned(v_cache_dev, 16) || !aligned(o_dev, 16) ||
+      q_stride < (int64_t)shape->n_q * shape->D || q_stride % 8 || !ints(table_dev) ||
+      !ints(lens_dev) || !aligned(n_new_dev, 4) || n_phys < 1)
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ws(ws_dev, ws_bytes, attn_q4_ws_bytes(shape)));
+  int nsm = 0;
+  MOE_TRY(device_sm_count(&nsm));
+  AttnQ4Args a{};
+  a.q = static_cast<const uint16_t*>(q_dev);
+  a.q_stride = q_stride;
+  a.k = static_cast<const char*>(k_cache_dev);
+  a.v = static_cast<const char*>(v_cache_dev);
+  a.table = table_dev;
+  a.lens = lens_dev;
+  a.n_new = n_new_dev;
+  a.n_phys = n_phys;
+  a.o = static_cast<uint16_t*>(o_dev);
+  return done(launch_attn_q4(shape, a, static_cast<uint8_t*>(ws_dev), nsm, (cudaStream_t)stream),
+              "4-bit batch attention launch");
+}
+
+size_t moe_logprobs_workspace_bytes(const moe_logprobs_shape_t* shape) {
+  return logprobs_supported(shape) ? logprobs_ws_bytes(shape) : 0;
+}
+
+moe_status_t moe_token_logprobs(const moe_logprobs_shape_t* shape, const void* logits_dev,
+                                int64_t stride, const int32_t* tokens_dev, float* logp_dev,
+                                float* entropy_dev, int32_t* top_ids_dev, float* top_logp_dev,
+                                void* ws_dev, size_t ws_bytes, moe_stream_t stream) {
+  if (!logprobs_supported(shape)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const uintptr_t e = shape->dtype == MOE_DTYPE_FP32 ? 4 : 2;
+  if (!logits_dev || !aligned(logits_dev, e) || stride < shape->V || !ints(tokens_dev) ||
+      !ints(logp_dev) || !aligned(entropy_dev, 4) || !aligned(top_ids_dev, 4) ||
+      !aligned(top_logp_dev, 4))
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ws(ws_dev, ws_bytes, logprobs_ws_bytes(shape)));
+  int nsm = 0;
+  MOE_TRY(device_sm_count(&nsm));
+  return done(launch_logprobs(shape, logits_dev, stride, tokens_dev, logp_dev, entropy_dev,
+                              top_ids_dev, top_logp_dev, static_cast<uint8_t*>(ws_dev), nsm,
+                              (cudaStream_t)stream),
+              "log probabilities launch");
 }
 
 }  // extern "C"

@@ -168,4 +168,66 @@ __device__ __forceinline__ constexpr float lift() {
   return F16 ? 6.0f : 0.0f;
 }
 
+#ifdef __CUDACC__
+// v / l to four 16-bit elements, 0 where l is (a row that sees nothing), even
+// if what was summed for it is not finite; a NaN sum stays one
+template <bool F16>
+__device__ __forceinline__ void store4(uint16_t* to, const float4& v, float l) {
+  const float inv = 1.0f / l;
+  *reinterpret_cast<uint2*>(to) =
+      l == 0.0f ? make_uint2(0u, 0u)
+                : make_uint2(pack2<F16>(v.x * inv, v.y * inv), pack2<F16>(v.z * inv, v.w * inv));
+}
+
+// Joins parts 0 .. n - 1 in order, each batch of up to kBatch fetched as a
+// whole: part k has m at p, l at p + l_at and O at p + o_at for its p.
+struct Joined {
+  float M, L;
+  float4 o;
+};
+struct PartRef {
+  const float* p;
+  int l_at, o_at;
+};
+template <int kBatch, typename At>
+__device__ __forceinline__ void join_parts(Joined& j, int n, At at) {
+  for (int c0 = 0; c0 < n; c0 += kBatch) {
+    float m[kBatch], l[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      m[k] = -INFINITY;
+      l[k] = 0.0f;
+      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (c0 + k < n) {
+        const PartRef r = at(c0 + k);
+        m[k] = __ldcg(r.p);
+        l[k] = __ldcg(r.p + r.l_at);
+        v[k] = __ldcg(reinterpret_cast<const float4*>(r.p + r.o_at));
+      }
+    }
+    float nM = j.M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) nM = fmaxf(nM, m[k]);
+    const float U = nM == -INFINITY ? 0.0f : nM;
+    const float f = ex2(j.M - U);
+    j.L *= f;
+    j.o.x *= f;
+    j.o.y *= f;
+    j.o.z *= f;
+    j.o.w *= f;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float w = ex2(m[k] - U);
+      j.L = fmaf(l[k], w, j.L);
+      j.o.x = fmaf(v[k].x, w, j.o.x);
+      j.o.y = fmaf(v[k].y, w, j.o.y);
+      j.o.z = fmaf(v[k].z, w, j.o.z);
+      j.o.w = fmaf(v[k].w, w, j.o.w);
+    }
+    j.M = nM;
+  }
+}
+#endif
+
 }  // namespace moe

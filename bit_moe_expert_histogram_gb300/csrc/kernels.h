@@ -244,6 +244,27 @@ size_t attn_batch_ws_bytes(const moe_attn_batch_shape_t* s);
 cudaError_t launch_attn_batch(const moe_attn_batch_shape_t* s, const CUtensorMap& tk,
                               const CUtensorMap& tv, AttnBatchArgs a, uint8_t* ws, int nsm,
                               cudaStream_t stream);
+// Rows of a cache in 4 bits (cache_q4.cu) and attention over them (attn_q4.cu).
+struct AttnQ4Args;
+bool cache_q4_supported(const moe_cache_shape_t* s);
+cudaError_t launch_cache_write_q4(const moe_cache_shape_t* s, const moe_cache_meta_t& meta,
+                                  const int32_t* n_new, int T, const uint16_t* k_new,
+                                  int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
+                                  bool fp16, void* k, void* v, uint8_t* ws, cudaStream_t stream);
+cudaError_t launch_cache_read_q4(const moe_cache_shape_t* s, const moe_cache_meta_t& meta,
+                                 const int32_t* first, const int32_t* n, int T, const void* k,
+                                 const void* v, void* k_out, int64_t k_stride, void* v_out,
+                                 int64_t v_stride, int dtype, uint8_t* ws, cudaStream_t stream);
+bool attn_q4_supported(const moe_attn_batch_shape_t* s);
+size_t attn_q4_ws_bytes(const moe_attn_batch_shape_t* s);
+cudaError_t launch_attn_q4(const moe_attn_batch_shape_t* s, AttnQ4Args a, uint8_t* ws, int nsm,
+                           cudaStream_t stream);
+// Log probabilities of given tokens (logprobs.cu).
+bool logprobs_supported(const moe_logprobs_shape_t* s);
+size_t logprobs_ws_bytes(const moe_logprobs_shape_t* s);
+cudaError_t launch_logprobs(const moe_logprobs_shape_t* s, const void* logits, int64_t stride,
+                            const int32_t* tokens, float* logp, float* entropy, int32_t* top_ids,
+                            float* top_logp, uint8_t* ws, int nsm, cudaStream_t stream);
 // Verification of drafted tokens (verify.cu).
 bool verify_supported(const moe_verify_shape_t* s);
 size_t verify_ws_bytes(const moe_verify_shape_t* s);

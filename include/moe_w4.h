@@ -627,6 +627,104 @@ moe_status_t moe_verify_drafts(const moe_verify_shape_t* shape, const void* p_de
                                int32_t* tokens_dev, int32_t* n_acc_dev, void* ws_dev,
                                size_t ws_bytes, moe_stream_t stream);
 
+/* ----------------------------------------------------------------------
+ * A cache held in 4 bits. A row (one position of one head, D = 64 or 128
+ * elements) is four groups of D / 4 consecutive elements x, each with
+ *   b = the largest bf16 number <= min x,
+ *   s = (max x - b) / 15 rounded to the nearest bf16 number (ties to even),
+ *   code of x = min(15, floor((x - b) / s + 1/2)), 0 where s = 0;
+ * a code stands for s * code + b. The codes are what these formulas give in
+ * exact arithmetic. In memory a row is moe_cache_q4_units(D) 16-bit units:
+ * D / 2 bytes of codes, s of the four groups, b of the four groups. Element
+ * e's code lies in byte e / 2, in its low half where e is even; with D = 64
+ * the 8 bytes of group 2 h and the 8 of group 2 h + 1 alternate, those of
+ * group 2 h first. That is 80 bytes for D = 128, 48 for D = 64.
+ *
+ * A pool is [n_phys][n_kv][64][units]: the page calls above (reserve, compact,
+ * copy_pages) move it as what it is to them, a 16-bit pool with a cache shape
+ * whose D is moe_cache_q4_units(D). The calls below take the shape with the
+ * head's own D; both shapes go with one state and one cache workspace.
+ * ---------------------------------------------------------------------- */
+
+/* 16-bit units of a row: 40 for D = 128, 24 for D = 64, else 0. */
+int32_t moe_cache_q4_units(int32_t D);
+
+/* moe_cache_write into 4-bit pools: the same arguments and errors, with
+ *  dtype  MOE_DTYPE_BF16 or MOE_DTYPE_FP16, of k_new and v_new
+ * Values have to be finite and of at most half their type's largest number; a
+ * group with others reads back as NaN or with infinities, other groups are
+ * not touched by it. */
+moe_status_t moe_cache_write_q4(const moe_cache_shape_t* shape, const moe_cache_meta_t* meta,
+                                const int32_t* n_new_dev, int32_t T, int32_t dtype,
+                                const void* k_new_dev, int64_t k_stride, const void* v_new_dev,
+                                int64_t v_stride, void* k_cache_dev, void* v_cache_dev,
+                                void* ws_dev, size_t ws_bytes, moe_stream_t stream);
+
+/* Reads rows back: token t < n[s] of slot s is position first[s] + t, written
+ * to (s, t) of k_out_dev and v_out_dev, which lie as k_new_dev does in
+ * moe_cache_write. Other tokens of the outputs stay as they were. A range
+ * that does not lie in [0, lens[s]) is recorded and its slot left out, a page
+ * number out of range likewise for its positions.
+ *  first_dev int32 [n_slots] or NULL (0); n_dev int32 [n_slots] or NULL (T)
+ *  dtype     moe_dtype_t of the outputs; strides in elements, multiples of 16
+ *            bytes, >= n_kv * D; outputs 16-byte aligned */
+moe_status_t moe_cache_read_q4(const moe_cache_shape_t* shape, const moe_cache_meta_t* meta,
+                               const int32_t* first_dev, const int32_t* n_dev, int32_t T,
+                               const void* k_cache_dev, const void* v_cache_dev, int32_t dtype,
+                               void* k_out_dev, int64_t k_stride, void* v_out_dev,
+                               int64_t v_stride, void* ws_dev, size_t ws_bytes,
+                               moe_stream_t stream);
+
+/* moe_attn_batch over 4-bit pools: the same definition, with k_j and v_j the
+ * numbers that the rows stand for, and the same treatment of bad pages,
+ * lengths and counts; without a shared prefix (shape->prefix_blocks is 0;
+ * slots that share pages have them in their tables). dtype is that of q and o.
+ * fp32 scores, sums and biases' part of the output; a softmax weight times a
+ * value's scale is rounded to fp16 (under a power of two that keeps it in
+ * range) before it multiplies the codes, whatever dtype is. Scales and biases
+ * of positions below a slot's length have to be finite; what its pages hold
+ * past it does not matter. Deterministic. The workspace (256-byte aligned) is zero-filled once
+ * (moe_workspace_init); after MOE_ERR_TIMEOUT, again. Calls of any shape can
+ * use it in turn where it is large enough, but no other call of this library.
+ * n_slots * n_kv * ceil(T * n_q / n_kv / 16) * (2 * max_blocks + 1) has to be
+ * below 2^30. */
+size_t moe_attn_batch_q4_workspace_bytes(const moe_attn_batch_shape_t* shape);
+moe_status_t moe_attn_batch_q4(const moe_attn_batch_shape_t* shape, const void* q_dev,
+                               int64_t q_stride, const void* k_cache_dev, const void* v_cache_dev,
+                               int32_t n_phys, const int32_t* table_dev, const int32_t* lens_dev,
+                               const int32_t* n_new_dev, void* o_dev, void* ws_dev,
+                               size_t ws_bytes, moe_stream_t stream);
+
+/* Log probabilities of given tokens under rows of logits x_0 .. x_{V-1}, with
+ * the rows' entropies and likeliest tokens:
+ *   logp = x_token - ln sum_v e^x_v, entropy = - sum_v p_v ln p_v (nats),
+ *   top: the k ids of the largest logits, ties to the lower id, in that order.
+ * A logit of -inf is a token that cannot be: it has no weight and is not
+ * listed; ids that are missing for that, or where V < k, are -1 with -inf.
+ * fp32 sums in a fixed order: deterministic. A row of nothing but -inf, or
+ * with NaN or +inf, gives NaN, ids of -1, and is recorded as
+ * MOE_ERR_BAD_INPUT.
+ *  logits_dev row i starts stride * i elements in; aligned to its elements
+ *  tokens_dev int32 [n_rows]; -1: none, logp 0; others outside [0, V) give NaN
+ *             and are recorded
+ *  logp_dev   fp32 [n_rows]; entropy_dev fp32 [n_rows] or NULL
+ *  top_ids_dev int32 [n_rows][k], top_logp_dev fp32 [n_rows][k], either or
+ *             both NULL
+ * The workspace (256-byte aligned) is zero-filled once (moe_workspace_init);
+ * calls of any shape can use it in turn, but no other call of this library. */
+typedef struct moe_logprobs_shape {
+  int32_t n_rows; /* 1 .. 2^20 */
+  int32_t V;      /* vocabulary, 1 .. 2^20 */
+  int32_t k;      /* 0 .. 32 */
+  int32_t dtype;  /* moe_dtype_t of the logits */
+} moe_logprobs_shape_t;
+
+size_t moe_logprobs_workspace_bytes(const moe_logprobs_shape_t* shape);
+moe_status_t moe_token_logprobs(const moe_logprobs_shape_t* shape, const void* logits_dev,
+                                int64_t stride, const int32_t* tokens_dev, float* logp_dev,
+                                float* entropy_dev, int32_t* top_ids_dev, float* top_logp_dev,
+                                void* ws_dev, size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,14 +18,25 @@
 //    of bits 4 to 7. What is lost is below 2^-34 of the row's largest.
 //  - The biases' part of the scores is one bf16 product a position tile (the
 //    queries' group sums split into three bf16 parts, 24 bits).
-//  - p s is rounded to fp16 once (2^-11 of itself: half a step), after a power
-//    of two that keeps it below 2^14 whatever the values' size: the rows'
-//    largest scale so far, joined to the softmax's running maximum. p b and the
-//    sum of p are fp32 throughout.
+//  - The softmax weights are rounded to fp16 once (half a step: 2^-11 of
+//    themselves), times a scale a second time; sums are fp32. The values'
+//    scales and biases are fp16 under a power of two of their group, the
+//    largest so far, which loses nothing but what is 2^-24 below that. The
+//    biases' part of O and the sum of the weights are one more product: its
+//    rows are the four groups' biases and a row of ones.
+//  - Scales and biases are brought into those forms by one lane a position, and
+//    exchanged through shared memory by position pairs, as the products' lanes
+//    want them. (Each lane that needs them converting them for itself, eight
+//    times over, took twice the instructions in all: 45 us at 48 slots of 8K.)
 //
-// Both products have their free dimension where it wastes least: S = Q K^T has
-// the query rows as the tile's 16, and its result is, without any exchange,
-// the second operand of O^T = V^T P^T, whose 16 are elements of V.
+// Both products have the cache as the tile's 16 rows and the queries as its
+// columns: S^T = K Q^T over positions, O^T = V^T P^T over elements. Eight rows
+// (a pair's single token with eight heads to a key head) then waste nothing,
+// and codes, which are made for each step anyway, are the operand of four
+// registers in a row (the queries there, padded to sixteen rows, cost two moves
+// a product). P goes from S^T's result to an operand by a transposition of two
+// registers for sixteen positions. With queries as columns, a lane has two of
+// them, and their maxima, factors and sums need no exchange between lanes.
 //
 // Every warp works by itself: the (slot, head, row tile) pairs' units of 32
 // positions lie on one line, warp w takes units [w per, (w + 1) per), and
@@ -40,8 +51,6 @@ namespace moe {
 
 namespace {
 constexpr int kUnit = 32;   // positions of a unit
-constexpr int kWarps = 8;
-constexpr int kQThr = kWarps * 32;
 constexpr int kMostCtas = 256;
 
 template <int D>
@@ -50,9 +59,21 @@ struct Q4 {
   static constexpr int kTile = kUnit * kRow;        // of a unit's keys (or values)
   static constexpr int kCh = D / 32;                // 16-byte pieces of codes
 };
-// stages of a warp's ring
+// Warps of a CTA and stages of a warp's ring.
+template <int NT>
+__host__ __device__ constexpr int q4_warps() { return 12; }
 template <int D, int NT>
-__host__ __device__ constexpr int ring_stages() { return D == 64 ? 6 : NT == 1 ? 4 : 3; }
+__host__ __device__ constexpr int ring_stages() { return D == 64 ? 4 : 2; }
+// Whether a warp's first piece has a place in shared memory, beside the ring;
+// with sixteen rows there is no room for it, nor for the queries in registers.
+template <int NT>
+__host__ __device__ constexpr bool piece_in_smem() { return NT == 1; }
+// bytes of a warp's queries in shared memory, [D / 32][NT][lane][4]
+template <int D, int NT>
+__host__ __device__ constexpr int query_bytes() { return NT == 1 ? 0 : D / 32 * NT * 512; }
+// A warp's scratch for a unit's scales and biases: keys'
+// scales fp32 [32][4]; then, by position pairs, values' scales, then biases fp16 [16][2][4][2].
+constexpr int kScratch = 1024;
 // A piece: rows R[kR], l[kR], O[kR][D + 4] (the pad spreads the banks)
 template <int D, int NT>
 __host__ __device__ constexpr int piece_floats() { return 2 * 8 * NT + 8 * NT * (D + 4); }
@@ -64,12 +85,43 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
+// from zero
+__device__ __forceinline__ void mma_f16_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f), "f"(0.0f), "f"(0.0f), "f"(0.0f));
+}
+// eight steps of bf16
+__device__ __forceinline__ void mma_bf16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, "
+      "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(b0));
+}
+__device__ __forceinline__ void mma_bf16_k8_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, "
+      "{%7, %8, %9, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f), "f"(0.0f), "f"(0.0f), "f"(0.0f));
+}
+// 8 x 8 of 16 bits, rows to columns
+__device__ __forceinline__ uint32_t transpose(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -110,6 +162,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// A weight is 2^(x - m + kLift): the reference m lags the running maximum by up
+// to kSlack (else nearly every unit of a pair's first hundreds moves it: of
+// eight rows one has a new maximum), which leaves fp16's 2^15 as the largest
+// weight; what is 2^-22 of it is still a normal number, 2^-32 not 0
+constexpr float kSlack = 7.0f, kLift = 8.0f;
+// biased exponents that a group's power of two can have: from 2^-100 on
+constexpr int kSigLeast = 27, kSigMost = 253;
 constexpr uint32_t kLoNib = 0x000F000Fu, kHiNib = 0x00F000F0u;
 
 // What a slot brings: its length, new tokens and units (at least one, a unit
@@ -132,44 +191,107 @@ __device__ __forceinline__ Q4Span q4_span(const AttnQ4Args& a, int s) {
   return r;
 }
 
-// A place on the line: the pair that unit f belongs to, its first unit pb.
+// A place on the line: the pair (slot, head, row tile) and its first unit pb.
 struct Place {
-  int s, h, pb;  // h: head * row tiles + row tile
+  int s, head, tile, pb;
   Q4Span sp;
   __device__ __forceinline__ void next(const AttnQ4Args& a) {
     pb += sp.units + a.pair_cost;
-    if (++h == a.n_kv * a.tiles) {
-      h = 0;
-      if (++s < a.n_slots) sp = q4_span(a, s);
-    }
+    if (++tile < a.tiles) return;
+    tile = 0;
+    if (++head < a.n_kv) return;
+    head = 0;
+    if (++s < a.n_slots) sp = q4_span(a, s);
   }
 };
 
 // a warp's piece of a pair
 struct PieceInfo {
-  int pair, pb, units;  // pair: slot * n_kv * tiles + h, -1: none
-  uint32_t at;          // shared-memory address
+  int pair, pb, units;  // pair: (slot * n_kv + head) * tiles + tile, -1: none
+  int s, head, tile;
+  const float* at;      // in shared memory, or the warp's place in the workspace
 };
+
+// V floats of a row, to 16 bits or as they are
+template <int V>
+struct Elems {
+  float v[V];
+};
+template <int V>
+__device__ __forceinline__ Elems<V> load_elems(const float* p) {  // shared memory, or this call's parts
+  Elems<V> r;
+  if (V == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    r.v[0] = x.x, r.v[1] = x.y, r.v[V - 2] = x.z, r.v[V - 1] = x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    r.v[0] = x.x, r.v[1] = x.y;
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Elems<V> load_far(const float* p) {  // from L2
+  Elems<V> r;
+  if (V == 4) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+    r.v[0] = x.x, r.v[1] = x.y, r.v[V - 2] = x.z, r.v[V - 1] = x.w;
+  } else {
+    const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+    r.v[0] = x.x, r.v[1] = x.y;
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ void store_elems(float* p, const Elems<V>& x) {
+  if (V == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(x.v[0], x.v[1], x.v[V - 2], x.v[V - 1]);
+  else
+    *reinterpret_cast<float2*>(p) = make_float2(x.v[0], x.v[1]);
+}
+// v / l, 0 where l is (a row that sees nothing), even if what was summed for it
+// is not finite
+template <bool F16, int V>
+__device__ __forceinline__ void store_out(uint16_t* p, const Elems<V>& x, float l) {
+  const float inv = 1.0f / l;
+  const uint32_t lo = l == 0.0f ? 0u : pack2<F16>(x.v[0] * inv, x.v[1] * inv);
+  if (V == 4)
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(lo, l == 0.0f ? 0u : pack2<F16>(x.v[V - 2] * inv, x.v[V - 1] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(p) = lo;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
 }  // namespace
 
 template <bool F16, int D, int NT>
-__global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
+__global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const AttnQ4Args a) {
   using C = Q4<D>;
+  constexpr int kWarps = q4_warps<NT>(), kQThr = kWarps * 32;
   constexpr int kS = ring_stages<D, NT>(), kR = 8 * NT;
   constexpr int kKS = D / 16;  // steps of the score product, and O's element tiles
-  constexpr int kNP = kUnit / 8;
   constexpr int kPiece = piece_floats<D, NT>();
   extern __shared__ __align__(128) uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t full[kWarps][kS];
   __shared__ int s_scan[kWarps];
-  __shared__ int s_start[kWarps], s_off[kWarps];
+  __shared__ Place s_start[kWarps];  // where the warps' shares start
   __shared__ PieceInfo s_piece[2 * kWarps];
-  __shared__ int s_last[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, cq = lane & 3;
   const uint32_t sbase = smem_u32(sm_raw);
   const uint32_t ring = sbase + warp * (kS * 2 * C::kTile);
-  const uint32_t extra = sbase + kWarps * (kS * 2 * C::kTile) + warp * (kPiece * 4);
+  const uint32_t scratch = sbase + kWarps * (kS * 2 * C::kTile) + warp * kScratch;
+  // the queries or the piece
+  constexpr int kQBytes = query_bytes<D, NT>(), kMore = piece_in_smem<NT>() ? kPiece * 4 : kQBytes;
+  const uint32_t more = sbase + kWarps * (kS * 2 * C::kTile + kScratch) + warp * kMore;
   const uint32_t bars = smem_u32(&full[warp][0]);
   if (lane < kS) mbar_init(bars + 8u * lane, 1);
   if (tid < 2 * kWarps) s_piece[tid].pair = -1;
@@ -178,12 +300,16 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
   pdl_trigger();
   // ---- this warp's part of the line of units
   const int ht = a.n_kv * a.tiles;  // pairs of a slot
-  int total = 0;
+  int total = 0, per;
   {
     const int chunk = (a.n_slots + kQThr - 1) / kQThr;
     const int s0 = min(tid * chunk, a.n_slots), s1 = min(s0 + chunk, a.n_slots);
     int sum = 0;
-    for (int s = s0; s < s1; ++s) sum += q4_span(a, s).units + a.pair_cost;
+    Q4Span sp{0, 0, 0};
+    for (int s = s0; s < s1; ++s) {
+      sp = q4_span(a, s);
+      sum += sp.units + a.pair_cost;
+    }
     sum *= ht;
     int incl = sum;
 #pragma unroll
@@ -198,120 +324,146 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
       total += s_scan[w];
     }
     const unsigned warps = gridDim.x * kWarps;
-    const int per = (int)(((unsigned)total + warps - 1) / warps);
-    const int c0 = min((int)blockIdx.x * kWarps * per, total);
-    // the slots that the CTA's warps start in: each is one thread's to find
-    const int run0 = incl - sum;
+    per = cut_up((unsigned)total, warps);
+    // the slots that the CTA's warps start in: each is in one thread's part
+    const int c0 = min((int)blockIdx.x * kWarps * per, total), run0 = incl - sum;
     for (int w = 0; w < kWarps; ++w) {
       const int f = c0 + w * per;
       if (f < run0 || f >= incl) continue;
-      int s = s0, run = run0;
-      for (; s < s1 - 1; ++s) {
-        const int n = (q4_span(a, s).units + a.pair_cost) * ht;
-        if (f < run + n) break;
-        run += n;
-      }
-      s_start[w] = s;
-      s_off[w] = f - run;
+      s_start[w].s = s0;
+      s_start[w].pb = run0;
+      s_start[w].sp = sp;  // of the part's last slot, its only one but in large batches
     }
     __syncthreads();
   }
-  const unsigned warps = gridDim.x * kWarps;
-  const int per = (int)(((unsigned)total + warps - 1) / warps);
   const int F0 = min((int)blockIdx.x * kWarps * per, total);  // the CTA's share
   const int F1 = min(F0 + kWarps * per, total);
   const int f0 = min(F0 + warp * per, total), f1 = min(f0 + per, total);
-  const int G = a.n_q / a.n_kv, rows = a.T * G;
+  const int G = a.group, rows = a.T * G;
+  // row / G for row < 64: the product is off by less than 1 / (2 G)
+  const float per_g = 1.0f / (float)G;
+  auto token = [&](int r) { return (int)(((float)r + 0.5f) * per_g); };
   const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(D)
   if (f0 < f1) {
-    Place at;
-    at.s = s_start[warp];
-    at.sp = q4_span(a, at.s);
-    at.h = s_off[warp] / (at.sp.units + a.pair_cost);
-    at.pb = f0 - (s_off[warp] - at.h * (at.sp.units + a.pair_cost));
-    // ---- the loader's own place on the line, kS units ahead
+    Place at = s_start[warp];
+    if (a.n_slots > kQThr) {
+      for (at.sp = q4_span(a, at.s); at.s < a.n_slots - 1; at.sp = q4_span(a, ++at.s)) {
+        const int n = (at.sp.units + a.pair_cost) * ht;
+        if (f0 < at.pb + n) break;
+        at.pb += n;
+      }
+    }
+    {
+      const unsigned each = at.sp.units + a.pair_cost, pair = cut_up((unsigned)(f0 - at.pb) + 1u, each) - 1;
+      at.head = a.tiles == 1 ? pair : cut_up(pair + 1u, a.tiles) - 1;
+      at.tile = pair - at.head * a.tiles;
+      at.pb += pair * each;
+    }
+    // ---- the loader: kS units ahead on the line, all lanes follow, lane 0 issues
     Place ld = at;
-    int lf = f0, ln = 0, base = -1, pages = -1;
-    unsigned absent = 0, phase = 0, pending = 0;  // bit per stage; pending: a copy not waited for
-    bool dead = false;                            // a wait ran out: nothing more is fetched
+    int lu = f0 - at.pb;                        // the pair's next unit
+    int le = min(f1 - at.pb, at.sp.units);      // and how many of them are the warp's
+    int lst = 0, ln = 0, base = -1, pages = -1; // pages: of blocks base + lane
+    unsigned absent = 0;                        // bit per stage: nothing was fetched for it
+    bool dead = false;                          // a wait ran out: nothing more is fetched
     const uint64_t pol = policy_evict_first();
+    const int page_bytes = a.n_kv * kBlk * C::kRow;
     auto load_next = [&] {
-      while (lf < f1 && lf - ld.pb >= ld.sp.units) {
+      if (dead) return;
+      while (lu >= le) {
+        if (ld.pb + ld.sp.units + a.pair_cost >= f1) return;
         ld.next(a);
-        lf = ld.pb;
+        lu = 0;
+        le = min(f1 - ld.pb, ld.sp.units);
         base = -1;
       }
-      if (lf >= f1) return;
-      const int u = lf - ld.pb, block = u >> 1, st = ln % kS;
+      const int block = lu >> 1;
       if ((block & ~31) != base) {
         base = block & ~31;
         pages = base + lane < a.max_blocks ? __ldg(a.table + (int64_t)ld.s * a.max_blocks + base + lane) : -1;
       }
       const int page = __shfl_sync(0xFFFFFFFFu, pages, block & 31);
-      const int n = ld.sp.n_new == 0 ? 0 : min(kUnit, ld.sp.len - u * kUnit);
-      const bool bad = n > 0 && (page < 0 || page >= a.n_phys);
-      if (bad && lane == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_ATTNB, ld.s);
-      if (n <= 0 || bad || dead) {
-        absent |= 1u << st;
-      } else {
-        absent &= ~(1u << st);
-        pending |= 1u << st;
-        if (lane == 0) {
-          const int64_t row = ((int64_t)page * a.n_kv + ld.h / a.tiles) * kBlk + (u & 1) * kUnit;
-          const uint32_t sk = ring + st * 2 * C::kTile, bytes = n * C::kRow;
-          mbar_arrive_expect_tx(bars + 8u * st, 2 * bytes);
-          bulk_load(sk, a.k + row * C::kRow, bytes, bars + 8u * st, pol);
-          bulk_load(sk + C::kTile, a.v + row * C::kRow, bytes, bars + 8u * st, pol);
+      const int n = min(kUnit, ld.sp.len - lu * kUnit);
+      const bool none = ld.sp.n_new == 0 || n <= 0;
+      const bool bad = !none && (unsigned)page >= (unsigned)a.n_phys;
+      absent = (absent & ~(1u << lst)) | (none || bad ? 1u << lst : 0u);
+      if (lane == 0) {
+        const uint32_t bar = bars + 8u * lst;
+        if (absent >> lst & 1u) {
+          if (bad) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_ATTNB, ld.s);
+          mbar_arrive(bar);
+        } else {
+          const int64_t from = (int64_t)page * page_bytes + (ld.head * kBlk + (lu & 1) * kUnit) * C::kRow;
+          const uint32_t sk = ring + lst * 2 * C::kTile, bytes = n * C::kRow;
+          mbar_arrive_expect_tx(bar, 2 * bytes);
+          bulk_load(sk, a.k + from, bytes, bar, pol);
+          bulk_load(sk + C::kTile, a.v + from, bytes, bar, pol);
         }
       }
-      ++lf;
+      ++lu;
       ++ln;
+      lst = lst + 1 == kS ? 0 : lst + 1;
     };
+    // a row's 16-bit elements as this lane's products want them, per piece c:
+    // D = 128: 32 c + 8 cq .. + 7; D = 64: 32 c + 4 cq .. + 3 and 16 on
+    uint32_t raw[NT][C::kCh][4];
+    auto fetch_q = [&] {
+      const int first = at.sp.len - at.sp.n_new;  // may be negative
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const int r = at.tile * 16 + gq + 8 * i, t = r < rows ? token(r) : a.T;
+        const bool sees = t < at.sp.n_new && first + t >= 0;
+        const uint16_t* q = a.q + ((int64_t)at.s * a.T + t) * a.q_stride + (at.head * G + r - t * G) * D;
+#pragma unroll
+        for (int c = 0; c < C::kCh; ++c) {
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (sees) {
+            if (D == 128) {
+              w = __ldg(reinterpret_cast<const uint4*>(q + 32 * c + 8 * cq));
+            } else {
+              const uint2 x = __ldg(reinterpret_cast<const uint2*>(q + 32 * c + 4 * cq));
+              const uint2 y = __ldg(reinterpret_cast<const uint2*>(q + 32 * c + 16 + 4 * cq));
+              w = make_uint4(x.x, x.y, y.x, y.y);
+            }
+          }
+          raw[i][c][0] = w.x, raw[i][c][1] = w.y, raw[i][c][2] = w.z, raw[i][c][3] = w.w;
+        }
+      }
+    };
+    if (f0 - at.pb < at.sp.units) fetch_q();
     for (int i = 0; i < kS; ++i) load_next();
 
-    int f = f0, it = 0;
+    int f = f0, st = 0, done = 0;
+    uint32_t parity = 0;
     while (f < f1) {
-      if (f - at.pb >= at.sp.units) {
+      if (f - at.pb >= at.sp.units) {  // this warp starts in a pair's cost
         at.next(a);
         f = at.pb;
+        if (f < f1) fetch_q();
         continue;
       }
       const int fe = min(f1, at.pb + at.sp.units);
       const bool whole = f == at.pb && fe == at.pb + at.sp.units;
-      const int head = at.h / a.tiles, mt = at.h - head * a.tiles;
       const int basep = at.sp.len - at.sp.n_new;  // may be negative
       // ---- the rows: queries as fp16, their scale, their groups' sums
-      int lim[NT];        // last position that row gq + 8 i sees, -1: none
-      float cq2[NT];      // scores = cq2 * (products of codes) + biases' part
-      uint32_t qa[kKS][2 * NT], qs[2 * NT];
+      // per query column 2 cq + e of eight: its last visible position (-1: none),
+      // and scores = cf * (products of codes) + biases' part
+      int lim[NT][2];
+      float cf[NT][2];
+      uint32_t qa[kKS][2 * NT], qs[2 * NT];  // with sixteen rows qa lies in shared memory
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const int r = mt * 16 + gq + 8 * i, t = r < rows ? r / G : a.T;
-        lim[i] = t < at.sp.n_new ? max(basep + t, -1) : -1;
+        // steps 2 c and 2 c + 1 of piece c take elements 0 4 1 5 and 2 6 3 7 of
+        // the lane's eight, with D = 64 0 2 1 3 of each four
         float v[kKS][4];
-        // step 2 c and 2 c + 1 of piece c take this lane's elements
-        // D = 128: 32 c + 8 cq + {0, 4, 1, 5} and {2, 6, 3, 7}
-        // D = 64: 32 c + 4 cq + {0, 2, 1, 3}, and those of the second group
-        const uint16_t* q = a.q + ((int64_t)at.s * a.T + t) * a.q_stride + (head * G + r - t * G) * D;
         float top = 0.0f;
 #pragma unroll
         for (int c = 0; c < C::kCh; ++c) {
-          uint32_t w[4] = {0u, 0u, 0u, 0u};
-          if (lim[i] >= 0) {
-            if (D == 128) {
-              const uint4 x = __ldg(reinterpret_cast<const uint4*>(q + 32 * c + 8 * cq));
-              w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-            } else {
-              const uint2 x = __ldg(reinterpret_cast<const uint2*>(q + 32 * c + 4 * cq));
-              const uint2 y = __ldg(reinterpret_cast<const uint2*>(q + 32 * c + 16 + 4 * cq));
-              w[0] = x.x, w[1] = x.y, w[2] = y.x, w[3] = y.y;
-            }
-          }
           float e[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            e[2 * k] = unpack_lo<F16>(w[k]);
-            e[2 * k + 1] = unpack_hi<F16>(w[k]);
+            e[2 * k] = unpack_lo<F16>(raw[i][c][k]);
+            e[2 * k + 1] = unpack_hi<F16>(raw[i][c][k]);
             top = fmaxf(top, fmaxf(fabsf(e[2 * k]), fabsf(e[2 * k + 1])));
           }
           if (D == 128) {
@@ -327,7 +479,13 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
         // 2^e with top 2^e in [2^14, 2^15)
         const int ex = min(max(127 + 14 - (int)(__float_as_uint(top) >> 23), -100), 100);
         const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
-        cq2[i] = sl2 * __uint_as_float((uint32_t)(127 + 24 - ex) << 23);
+        const float back = sl2 * __uint_as_float((uint32_t)(127 + 24 - ex) << 23);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          cf[i][e] = __shfl_sync(0xFFFFFFFFu, back, 8 * cq + 4 * e);
+          const int r = at.tile * 16 + 8 * i + 2 * cq + e, t = r < rows ? token(r) : a.T;
+          lim[i][e] = t < at.sp.n_new ? max(basep + t, -1) : -1;
+        }
         float sum[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) sum[g] = 0.0f;
@@ -354,159 +512,240 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
         qs[i] = cq == 0 ? h01 : cq == 1 ? h23 : cq == 2 ? m01 : m23;
         qs[NT + i] = cq == 0 ? l01 : cq == 1 ? l23 : 0u;
       }
-      float m[NT], ref[NT], l[NT], ob[NT][4], o[kKS][NT][4];
-      float ls = -80.0f;  // log2 of a power of two that no scale of the values is above
+      // o: O^T, element tiles by rows; sb: rows 0 .. 3 the biases' part by
+      // groups, row 4 the sum of the weights
+      if (kQBytes > 0) {
+#pragma unroll
+        for (int c = 0; c < C::kCh; ++c)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            sts128(more + (c * NT + i) * 512 + lane * 16, qa[2 * c][i], qa[2 * c][NT + i], qa[2 * c + 1][i],
+                   qa[2 * c + 1][NT + i]);
+      }
+      float m[NT][2], sb[NT][4], o[kKS][NT][4];
+      int sg[4];  // biased exponents of the groups' powers of two
+#pragma unroll
+      for (int g = 0; g < 4; ++g) sg[g] = kSigLeast;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        m[i] = ref[i] = -INFINITY;
-        l[i] = 0.0f;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) ob[i][g] = 0.0f;
+        m[i][0] = m[i][1] = -INFINITY;
+        sb[i][0] = sb[i][1] = sb[i][2] = sb[i][3] = 0.0f;
 #pragma unroll
         for (int j = 0; j < kKS; ++j) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.0f;
       }
-      for (; f < fe; ++f, ++it) {
-        const int st = it % kS;
-        if (!(absent >> st & 1u) && !dead) {
+      for (; f < fe; ++f) {
+        if (!dead) {
           volatile int never = 0;
-          const bool ok = mbar_wait(bars + 8u * st, phase >> st & 1u, &never);
+          const bool ok = mbar_wait(bars + 8u * st, parity, &never);
           dead = !__all_sync(0xFFFFFFFFu, ok);
-          if (dead && lane == 0) set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, at.s);
+          if (dead) {
+            if (lane == 0) set_error(a.ctrl, MOE_ERR_TIMEOUT, KID_ATTNB, at.s);
+          } else {
+            ++done;
+          }
         }
-        if (!(absent >> st & 1u) && !dead) {
-          phase ^= 1u << st;
-          pending &= ~(1u << st);
+        if (!dead && !(absent >> st & 1u)) {
           const uint32_t sk = ring + st * 2 * C::kTile, sv = sk + C::kTile;
           const int pos0 = (f - at.pb) * kUnit, n_here = at.sp.len - pos0;
-          // ---- scores, in powers of two
-          float x[kNP][2 * NT];
-          uint32_t kc[4];  // codes of a tile's rows; D = 64: of two tiles'
+          // ---- scales and biases, a position a lane; values' rows past the slot's
+          // end hold anything and count as nothing (keys' are masked)
+          {
+            const uint32_t at = D / 2 + lane * C::kRow;
+            const uint2 wk = lds64(sk + at);
+            sts128(scratch + lane * 16, wk.x << 16, wk.x & 0xFFFF0000u, wk.y << 16, wk.y & 0xFFFF0000u);
+            uint4 wv = lds128(sv + at);
+            if (lane >= n_here) wv = make_uint4(0u, 0u, 0u, 0u);
+            const float s4[4] = {bf_lo(wv.x), bf_hi(wv.x), bf_lo(wv.y), bf_hi(wv.y)};
+            const float b4[4] = {bf_lo(wv.z), bf_hi(wv.z), bf_lo(wv.w), bf_hi(wv.w)};
+            bool grown = false;
+            int was[4];
+            float inv[4];
 #pragma unroll
-          for (int n = 0; n < kNP; ++n) {
-            const uint32_t bw = lds32(sk + (8 * n + gq) * C::kRow + D / 2 + 8 + 4 * (cq & 1));
-            float sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma_bf16(sb, qs[0], NT > 1 ? qs[1] : 0u, qs[NT], NT > 1 ? qs[NT + 1] : 0u, bw, bw);
-            if (D == 128)
-              ldsm4(sk + (8 * n + (lane & 7)) * C::kRow + (lane >> 3) * 16, kc);
-            else if (n % 2 == 0)
-              ldsm4(sk + (8 * n + (lane & 7) + (lane >> 4) * 8) * C::kRow + (lane >> 3 & 1) * 16, kc);
-            const uint2 s0 = lds64(sk + (8 * n + 2 * cq) * C::kRow + D / 2);
-            const uint2 s1 = lds64(sk + (8 * n + 2 * cq + 1) * C::kRow + D / 2);
-            float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            float acc[4];
+            for (int g = 0; g < 4; ++g) {
+              // positive numbers order as whole numbers
+              const uint32_t big = __reduce_max_sync(
+                  0xFFFFFFFFu, __float_as_uint(fmaxf(16.0f * s4[g], fabsf(b4[g]))));
+              was[g] = sg[g];
+              sg[g] = min(max(sg[g], (int)(big >> 23) + 1), kSigMost);
+              grown |= sg[g] != was[g];
+              inv[g] = __uint_as_float((uint32_t)(254 - sg[g]) << 23);
+            }
+            if (grown) {  // the same for all lanes
 #pragma unroll
-            for (int ks = 0; ks < kKS; ++ks) {
-              const int g = D == 128 ? ks >> 1 : ks;
-              const uint32_t word = D == 128 ? kc[ks >> 1] : kc[(n & 1) * 2 + (ks >> 1)];
-              const uint32_t w = ks & 1 ? word >> 8 : word;
-              if (D == 64 || (ks & 1) == 0) acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-              mma_f16(acc, qa[ks][0], NT > 1 ? qa[ks][1] : 0u, qa[ks][NT], NT > 1 ? qa[ks][NT + 1] : 0u,
-                      w & kLoNib, w & kHiNib);
-              if (D == 64 || (ks & 1)) {
-                const uint32_t u0 = g < 2 ? s0.x : s0.y, u1 = g < 2 ? s1.x : s1.y;
-                const float f0s = g & 1 ? bf_hi(u0) : bf_lo(u0), f1s = g & 1 ? bf_hi(u1) : bf_lo(u1);
+              for (int g = 0; g < 4; ++g) {
+                const float cut = sg[g] == was[g] ? 1.0f : ex2((float)(was[g] - sg[g]));
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                  t[2 * i] = fmaf(f0s, acc[2 * i], t[2 * i]);
-                  t[2 * i + 1] = fmaf(f1s, acc[2 * i + 1], t[2 * i + 1]);
+#pragma unroll
+                  for (int j = g * (kKS / 4); j < (g + 1) * (kKS / 4); ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[j][i][e] *= cut;
+                  if (gq == g) {
+                    sb[i][0] *= cut;
+                    sb[i][1] *= cut;
+                  }
                 }
               }
             }
+            // this lane's position as the low or high half of its pair: even
+            // lanes take groups 0 and 1 of both, odd lanes 2 and 3
+            const bool odd = lane & 1;
+            const uint32_t sa = pack2<true>(16.0f * s4[0] * inv[0], 16.0f * s4[1] * inv[1]);
+            const uint32_t sc = pack2<true>(16.0f * s4[2] * inv[2], 16.0f * s4[3] * inv[3]);
+            const uint32_t ba = pack2<true>(b4[0] * inv[0], b4[1] * inv[1]);
+            const uint32_t bc = pack2<true>(b4[2] * inv[2], b4[3] * inv[3]);
+            const uint32_t xs = __shfl_xor_sync(0xFFFFFFFFu, odd ? sa : sc, 1);
+            const uint32_t xb = __shfl_xor_sync(0xFFFFFFFFu, odd ? ba : bc, 1);
+            const uint32_t ls = odd ? xs : sa, hs = odd ? sc : xs;
+            const uint32_t lb = odd ? xb : ba, hb = odd ? bc : xb;
+            const uint32_t tv = scratch + 512 + (lane >> 1) * 32 + odd * 8;
+            sts64(tv, __byte_perm(ls, hs, 0x5410), __byte_perm(ls, hs, 0x7632));
+            sts64(tv + 16, __byte_perm(lb, hb, 0x5410), __byte_perm(lb, hb, 0x7632));
+          }
+          __syncwarp();
+          // ---- scores, in powers of two, of positions 16 h + gq and 8 on, and of
+          // two queries a number pair
+          uint64_t x[kUnit / 16][2][NT];
+          float t[kUnit / 16][NT][4];
+#pragma unroll
+          for (int c = 0; c < C::kCh; c += 2) {
+            if (kQBytes > 0) {
+#pragma unroll
+              for (int k = c; k < c + 2; ++k)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                  const uint4 q = lds128(more + (k * NT + i) * 512 + lane * 16);
+                  qa[2 * k][i] = q.x, qa[2 * k][NT + i] = q.y;
+                  qa[2 * k + 1][i] = q.z, qa[2 * k + 1][NT + i] = q.w;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < kUnit / 16; ++h) {
+              const uint4 s0 = lds128(scratch + (16 * h + gq) * 16), s1 = lds128(scratch + (16 * h + gq + 8) * 16);
+              const float s[2][4] = {{__uint_as_float(s0.x), __uint_as_float(s0.y), __uint_as_float(s0.z), __uint_as_float(s0.w)},
+                                     {__uint_as_float(s1.x), __uint_as_float(s1.y), __uint_as_float(s1.z), __uint_as_float(s1.w)}};
+              uint32_t kc[4];  // words of pieces c and c + 1 of positions gq, gq + 8
+              ldsm4(sk + (16 * h + (lane & 15)) * C::kRow + (c + (lane >> 4)) * 16, kc);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float acc[NT][4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int ks = 2 * (c + k) + e, g = D == 128 ? ks >> 1 : ks;
+                  const uint32_t w0 = e ? kc[2 * k] >> 8 : kc[2 * k];
+                  const uint32_t w1 = e ? kc[2 * k + 1] >> 8 : kc[2 * k + 1];
+#pragma unroll
+                  for (int i = 0; i < NT; ++i) {
+                    if (D == 64 || e == 0)
+                      mma_f16_0(acc[i], w0 & kLoNib, w1 & kLoNib, w0 & kHiNib, w1 & kHiNib, qa[ks][i], qa[ks][NT + i]);
+                    else
+                      mma_f16(acc[i], w0 & kLoNib, w1 & kLoNib, w0 & kHiNib, w1 & kHiNib, qa[ks][i], qa[ks][NT + i]);
+                    if (D == 64 || e == 1)
+#pragma unroll
+                      for (int z = 0; z < 4; ++z)
+                        t[h][i][z] = g == 0 ? s[z >> 1][0] * acc[i][z] : fmaf(s[z >> 1][g], acc[i][z], t[h][i][z]);
+                  }
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < kUnit / 16; ++h) {
+            const uint32_t r0 = sk + (16 * h + gq) * C::kRow + D / 2 + 8 + 4 * (cq & 1);
+            const uint32_t bw0 = lds32(r0), bw1 = lds32(r0 + 8 * C::kRow);
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-              x[n][2 * i] = fmaf(t[2 * i], cq2[i], sb[2 * i]);
-              x[n][2 * i + 1] = fmaf(t[2 * i + 1], cq2[i], sb[2 * i + 1]);
+              float xb[4];
+              mma_bf16_k8_0(xb, bw0, bw1, qs[i]);
+              mma_bf16_k8(xb, bw0, bw1, qs[NT + i]);
+              const uint64_t f2 = pair2(__float_as_uint(cf[i][0]), __float_as_uint(cf[i][1]));
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                x[h][y][i] = fma2(pair2(__float_as_uint(t[h][i][2 * y]), __float_as_uint(t[h][i][2 * y + 1])), f2,
+                                  pair2(__float_as_uint(xb[2 * y]), __float_as_uint(xb[2 * y + 1])));
             }
           }
-          // every row that is in use sees positions up to basep
+          // every query that is in use sees positions up to basep
           if (pos0 + kUnit - 1 > basep) {
 #pragma unroll
-            for (int n = 0; n < kNP; ++n)
-#pragma unroll
-              for (int i = 0; i < 2 * NT; ++i)
-                if (pos0 + 8 * n + 2 * cq + (i & 1) > lim[i >> 1]) x[n][i] = -INFINITY;
-          } else {
-#pragma unroll
             for (int i = 0; i < NT; ++i)
-              if (lim[i] < 0) {
 #pragma unroll
-                for (int n = 0; n < kNP; ++n) x[n][2 * i] = x[n][2 * i + 1] = -INFINITY;
+              for (int h = 0; h < kUnit / 8; ++h) {
+                float x0, x1;
+                unpair2(x[h >> 1][h & 1][i], x0, x1);
+                if (pos0 + 8 * h + gq > lim[i][0]) x0 = -INFINITY;
+                if (pos0 + 8 * h + gq > lim[i][1]) x1 = -INFINITY;
+                x[h >> 1][h & 1][i] = pair2(__float_as_uint(x0), __float_as_uint(x1));
               }
           }
-          // ---- the values' largest scale: positive bf16 numbers order as whole numbers
-          {
-            uint32_t big = 0u;
-            if (lane < n_here) {
-              const uint2 w = lds64(sv + lane * C::kRow + D / 2);
-              big = max(max(w.x >> 16, w.x & 0xFFFFu), max(w.y >> 16, w.y & 0xFFFFu));
-            }
-            big = __reduce_max_sync(0xFFFFFFFFu, big);
-            ls = fmaxf(ls, (float)((int)(big >> 7 & 255u) - 126));
-          }
-          // ---- running maximum, and what was summed up to it
+          // ---- the reference m follows the running maximum when that is kSlack
+          // ahead of it; what was summed up to then follows
+          float mx[NT][2];
           bool moved = false;
-          float cut[NT], u[NT];
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
-            float mx = -INFINITY;
+            mx[i][0] = mx[i][1] = -INFINITY;
 #pragma unroll
-            for (int n = 0; n < kNP; ++n) mx = fmaxf(mx, fmaxf(x[n][2 * i], x[n][2 * i + 1]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-            m[i] = fmaxf(m[i], mx);
-            // nothing seen so far: everything stays 0 (no inf - inf)
-            const float now = m[i] == -INFINITY ? -INFINITY : m[i] + ls;
-            u[i] = now == -INFINITY ? 0.0f : now;
-            cut[i] = ex2(ref[i] - u[i]);
-            moved |= now != ref[i];
-            ref[i] = now;
+            for (int h = 0; h < kUnit / 8; ++h) {
+              float x0, x1;
+              unpair2(x[h >> 1][h & 1][i], x0, x1);
+              mx[i][0] = fmaxf(mx[i][0], x0);
+              mx[i][1] = fmaxf(mx[i][1], x1);
+            }
+            moved |= mx[i][0] > m[i][0] + kSlack || mx[i][1] > m[i][1] + kSlack;
           }
           if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              l[i] *= cut[i];
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-              for (int g = 0; g < 4; ++g) ob[i][g] *= cut[i];
-              // O has the rows as columns: 2 cq and 2 cq + 1
-              const float c0 = __shfl_sync(0xFFFFFFFFu, cut[i], 8 * cq);
-              const float c1 = __shfl_sync(0xFFFFFFFFu, cut[i], 8 * cq + 4);
+              for (int e = 0; e < 2; ++e) {
+                float now = mx[i][e];
 #pragma unroll
-              for (int j = 0; j < kKS; ++j) {
-                o[j][i][0] *= c0;
-                o[j][i][1] *= c1;
-                o[j][i][2] *= c0;
-                o[j][i][3] *= c1;
+                for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, d));
+                now = fmaxf(now, m[i][e]);
+                // nothing seen so far: everything stays 0 (no inf - inf)
+                const float cut = ex2(m[i][e] - (now == -INFINITY ? 0.0f : now));
+                m[i][e] = now;
+                sb[i][e] *= cut;
+#pragma unroll
+                for (int j = 0; j < kKS; ++j) {
+                  o[j][i][e] *= cut;
+                  o[j][i][2 + e] *= cut;
+                }
               }
-            }
           }
+          uint64_t up[NT];
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            up[i] = pair2(__float_as_uint(kLift - (m[i][0] == -INFINITY ? 0.0f : m[i][0])),
+                          __float_as_uint(kLift - (m[i][1] == -INFINITY ? 0.0f : m[i][1])));
           // ---- weights and the second product, sixteen positions a step
 #pragma unroll
           for (int kp = 0; kp < kUnit / 16; ++kp) {
-            uint32_t pw[NT][4][2];  // p s as operands: [row half][group][position half]
+            // p and p s as operands, two positions of query gq a register:
+            // [group][position half]
+            uint32_t p[NT][2], pw[NT][4][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int n = 2 * kp + h;
-              uint4 w0 = lds128(sv + (8 * n + 2 * cq) * C::kRow + D / 2);
-              uint4 w1 = lds128(sv + (8 * n + 2 * cq + 1) * C::kRow + D / 2);
-              if (n_here < kUnit) {  // rows past the slot's end hold anything
-                if (8 * n + 2 * cq >= n_here) w0 = make_uint4(0u, 0u, 0u, 0u);
-                if (8 * n + 2 * cq + 1 >= n_here) w1 = make_uint4(0u, 0u, 0u, 0u);
-              }
+              const uint4 s4 = lds128(scratch + 512 + (4 * n + cq) * 32);
 #pragma unroll
               for (int i = 0; i < NT; ++i) {
-                const float p0 = ex2(x[n][2 * i] + (14.0f - u[i]));
-                const float p1 = ex2(x[n][2 * i + 1] + (14.0f - u[i]));
-                l[i] += p0 + p1;
-                pw[i][0][h] = pack2<true>(p0 * bf_lo(w0.x), p1 * bf_lo(w1.x));
-                pw[i][1][h] = pack2<true>(p0 * bf_hi(w0.x), p1 * bf_hi(w1.x));
-                pw[i][2][h] = pack2<true>(p0 * bf_lo(w0.y), p1 * bf_lo(w1.y));
-                pw[i][3][h] = pack2<true>(p0 * bf_hi(w0.y), p1 * bf_hi(w1.y));
-                ob[i][0] = fmaf(p1, bf_lo(w1.z), fmaf(p0, bf_lo(w0.z), ob[i][0]));
-                ob[i][1] = fmaf(p1, bf_hi(w1.z), fmaf(p0, bf_hi(w0.z), ob[i][1]));
-                ob[i][2] = fmaf(p1, bf_lo(w1.w), fmaf(p0, bf_lo(w0.w), ob[i][2]));
-                ob[i][3] = fmaf(p1, bf_hi(w1.w), fmaf(p0, bf_hi(w0.w), ob[i][3]));
+                float x0, x1;
+                unpair2(add2(x[kp][h][i], up[i]), x0, x1);
+                p[i][h] = transpose(pack2<true>(ex2(x0), ex2(x1)));
+                pw[i][0][h] = mul_h2(p[i][h], s4.x);
+                pw[i][1][h] = mul_h2(p[i][h], s4.y);
+                pw[i][2][h] = mul_h2(p[i][h], s4.z);
+                pw[i][3][h] = mul_h2(p[i][h], s4.w);
               }
             }
+            // rows 0 .. 3: the groups' biases, 4: ones; the others' results go nowhere
+            const uint32_t ab = scratch + 512 + (8 * kp + cq) * 32 + 16 + (gq & 3) * 4;
+            const uint32_t a0 = gq < 4 ? lds32(ab) : 0x3C003C00u, a2 = gq < 4 ? lds32(ab + 128) : 0x3C003C00u;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+              mma_f16(sb[i], a0, a0, a2, a2, p[i][0], p[i][1]);
 #pragma unroll
             for (int c = 0; c < C::kCh; c += 2) {
               uint32_t vc[4];  // pieces c and c + 1 of positions 0..7, 8..15
@@ -530,71 +769,69 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
           __syncwarp();
         }
         load_next();
+        st = st + 1 == kS ? 0 : st + 1;
+        parity ^= st == 0;
       }
-      // ---- the pair's end: sums over the lanes that share a row
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          ob[i][g] += __shfl_xor_sync(0xFFFFFFFFu, ob[i][g], 1);
-          ob[i][g] += __shfl_xor_sync(0xFFFFFFFFu, ob[i][g], 2);
-        }
-      }
+      // ---- the pair's end
       // a cut pair's piece: the first goes to a place of its own, as units
       // after it are on their way into the ring; the last goes to the ring
       const int which = at.pb < f0 ? 0 : 1;
-      const uint32_t piece = which == 0 ? extra : ring;
-      if (!whole && lane == 0)
-        s_piece[2 * warp + which] = PieceInfo{at.s * ht + at.h, at.pb, at.sp.units, piece};
-      float* pf = reinterpret_cast<float*>(sm_raw + (piece - sbase));
-      if (!whole && cq == 0) {
+      float sig[4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          pf[gq + 8 * i] = ref[i];
-          pf[kR + gq + 8 * i] = l[i];
-        }
-      }
+      for (int g = 0; g < 4; ++g) sig[g] = __uint_as_float((uint32_t)sg[g] << 23);
+      float* pf = reinterpret_cast<float*>(sm_raw + (ring - sbase));
+      if (which == 0)
+        pf = piece_in_smem<NT>() ? reinterpret_cast<float*>(sm_raw + (more - sbase))
+                                 : a.pieces + ((int64_t)blockIdx.x * kWarps + warp) * kPiece;
+      if (!whole && lane == 0)
+        s_piece[2 * warp + which] = PieceInfo{(at.s * a.n_kv + at.head) * a.tiles + at.tile, at.pb, at.sp.units,
+                                              at.s, at.head, at.tile, pf};
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // row 2 cq + e of the eight: its sums are with lane 4 (2 cq + e)
-          const int src = 4 * (2 * cq + e), r = 8 * i + 2 * cq + e;
-          const float lr = __shfl_sync(0xFFFFFFFFu, l[i], src);
+          // row 2 cq + e of the eight: its sum and biases' part are with lanes
+          // 16 + cq and 4 g + cq
+          const int r = 8 * i + 2 * cq + e;
+          const float sum = __shfl_sync(0xFFFFFFFFu, sb[i][e], 16 + cq);
+          // rows that see nothing weigh nothing, whatever was summed for them
+          const float lr = lim[i][e] >= 0 ? sum : 0.0f;
+          if (!whole && gq == 0) {
+            pf[r] = lim[i][e] >= 0 ? m[i][e] : -INFINITY;
+            pf[kR + r] = lr;
+          }
           float b[4];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) b[g] = __shfl_sync(0xFFFFFFFFu, ob[i][g], src);
-          const int R = mt * 16 + r, t = R / G;
-          const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;
-          uint16_t* out = a.o + (((int64_t)at.s * a.T + t) * a.n_q + head * G + R - t * G) * D;
+          for (int g = 0; g < 4; ++g) b[g] = __shfl_sync(0xFFFFFFFFu, sb[i][e], 4 * g + cq) * sig[g];
+          const int R = at.tile * 16 + r, t = token(R);
+          uint16_t* out = a.o + (((int64_t)at.s * a.T + t) * a.n_q + at.head * G + R - t * G) * D;
 #pragma unroll
           for (int c = 0; c < C::kCh; ++c) {
             // D = 128: elements 32 c + 4 gq + {0, 1, 2, 3}; D = 64: 32 c + 2 gq +
             // {0, 1} and 16 on
             const int g0 = D == 128 ? c : 2 * c, g1 = D == 128 ? c : 2 * c + 1;
-            float y[4] = {fmaf(o[2 * c][i][e], 0x1p24f, b[g0]), fmaf(o[2 * c][i][2 + e], 0x1p20f, b[g0]),
-                          fmaf(o[2 * c + 1][i][e], 0x1p24f, b[g1]), fmaf(o[2 * c + 1][i][2 + e], 0x1p20f, b[g1])};
+            float y[4] = {fmaf(o[2 * c][i][e] * 0x1p20f, sig[g0], b[g0]),
+                          fmaf(o[2 * c][i][2 + e] * 0x1p16f, sig[g0], b[g0]),
+                          fmaf(o[2 * c + 1][i][e] * 0x1p20f, sig[g1], b[g1]),
+                          fmaf(o[2 * c + 1][i][2 + e] * 0x1p16f, sig[g1], b[g1])};
+            const Elems<2> y0{y[0], y[1]}, y1{y[2], y[3]};
+            const Elems<4> y4{y[0], y[1], y[2], y[3]};
             if (whole) {
               if (R < rows) {
-                // a row that sees nothing is 0, whatever was summed for it
-                const uint32_t lo = lr == 0.0f ? 0u : pack2<F16>(y[0] * inv, y[1] * inv);
-                const uint32_t hi = lr == 0.0f ? 0u : pack2<F16>(y[2] * inv, y[3] * inv);
                 if (D == 128) {
-                  *reinterpret_cast<uint2*>(out + 32 * c + 4 * gq) = make_uint2(lo, hi);
+                  store_out<F16>(out + 32 * c + 4 * gq, y4, lr);
                 } else {
-                  *reinterpret_cast<uint32_t*>(out + 32 * c + 2 * gq) = lo;
-                  *reinterpret_cast<uint32_t*>(out + 32 * c + 16 + 2 * gq) = hi;
+                  store_out<F16>(out + 32 * c + 2 * gq, y0, lr);
+                  store_out<F16>(out + 32 * c + 16 + 2 * gq, y1, lr);
                 }
               }
             } else {
               float* to = pf + 2 * kR + r * (D + 4);
               if (D == 128) {
-                *reinterpret_cast<float4*>(to + 32 * c + 4 * gq) = make_float4(y[0], y[1], y[2], y[3]);
+                store_elems(to + 32 * c + 4 * gq, y4);
               } else {
-                *reinterpret_cast<float2*>(to + 32 * c + 2 * gq) = make_float2(y[0], y[1]);
-                *reinterpret_cast<float2*>(to + 32 * c + 16 + 2 * gq) = make_float2(y[2], y[3]);
+                store_elems(to + 32 * c + 2 * gq, y0);
+                store_elems(to + 32 * c + 16 + 2 * gq, y1);
               }
             }
           }
@@ -602,114 +839,138 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
       if (f < f1) {
         at.next(a);
         f = at.pb;
+        if (f < f1) fetch_q();
       }
     }
     // after a wait that ran out, what is in flight lands before the CTA goes
     if (dead && lane == 0) {
       volatile int never = 0;
-      for (int st = 0; st < kS; ++st)
-        if (pending >> st & 1u) mbar_wait(bars + 8u * st, phase >> st & 1u, &never);
+      for (; done < ln; ++done) mbar_wait(bars + 8u * (done % kS), (uint32_t)(done / kS) & 1u, &never);
     }
   }
   __syncthreads();
-  // ---- the CTA's pieces, pair by pair in the line's order; what its ends cut
-  // goes to the workspace: place 0 for a pair that starts before, 1 for one
-  // that starts here
-  constexpr int kItems = kR * D / 4;
-  int cut_pb[2] = {0, 0}, cut_units[2] = {0, 0}, cut_pair[2] = {-1, -1};
-  for (int i = 0; i < 2 * kWarps;) {
-    const PieceInfo p = s_piece[i];
-    int n = i + 1;  // pieces i .. n - 1, those of no warp left out
-    if (p.pair >= 0) {
-      while (n < 2 * kWarps && (s_piece[n].pair < 0 || s_piece[n].pair == p.pair)) ++n;
-      const bool own = p.pb >= F0 && p.pb + p.units <= F1;
-      const int place = p.pb < F0 ? 0 : 1;
-      if (!own) {
-        cut_pb[place] = p.pb;
-        cut_units[place] = p.units;
-        cut_pair[place] = p.pair;
-      }
-      const int s = p.pair / ht, h = p.pair - s * ht, head = h / a.tiles, mt = h - head * a.tiles;
-      float* part = a.part + (int64_t)(2 * blockIdx.x + place) * kPiece;
-      for (int item = tid; item < kItems; item += kQThr) {
-        const int r = item / (D / 4), d = item % (D / 4);
-        float M = -INFINITY;
-        for (int k = i; k < n; ++k)
-          if (s_piece[k].pair >= 0)
-            M = fmaxf(M, reinterpret_cast<const float*>(sm_raw + (s_piece[k].at - sbase))[r]);
-        const float U = M == -INFINITY ? 0.0f : M;
-        float L = 0.0f;
-        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int k = i; k < n; ++k) {
-          if (s_piece[k].pair < 0) continue;
-          const float* q = reinterpret_cast<const float*>(sm_raw + (s_piece[k].at - sbase));
-          const float w = ex2(q[r] - U);
-          const float4 v = *reinterpret_cast<const float4*>(q + 2 * kR + r * (D + 4) + 4 * d);
-          L = fmaf(q[kR + r], w, L);
-          y.x = fmaf(v.x, w, y.x);
-          y.y = fmaf(v.y, w, y.y);
-          y.z = fmaf(v.z, w, y.z);
-          y.w = fmaf(v.w, w, y.w);
-        }
-        const int R = mt * 16 + r, t = R / G;
-        if (own) {
-          if (R < rows)
-            store4<F16>(a.o + (((int64_t)s * a.T + t) * a.n_q + head * G + R - t * G) * D + 4 * d, y, L);
-        } else {
-          *reinterpret_cast<float4*>(part + 2 * kR + r * (D + 4) + 4 * d) = y;
-          if (d == 0) {
-            part[r] = M;
-            part[kR + r] = L;
-          }
-        }
-      }
-    }
-    i = n;
-  }
-  if (cut_pair[0] < 0 && cut_pair[1] < 0) return;
-  __threadfence();
-  __syncthreads();
+  // ---- the CTA's pieces, pair by pair in the line's order, a warp a row, a
+  // lane kV elements. First every row of a pair that lies in the CTA goes to the
+  // output and of one that does not to the workspace, place 0 of the CTA's two
+  // where the pair starts before it; then the latter are counted, and the last
+  // warp to arrive at a row joins it. Rows do not wait for one another.
+  constexpr int kV = D / 32;
+  const int pair_of = lane < 2 * kWarps ? s_piece[lane].pair : -1;
   const int share = kWarps * per;
-  if (tid < 2 && cut_pair[tid] >= 0) {
-    // the pair's CTAs; the counter is the one of the first, whose end cuts this
-    // pair and no other
-    const int c0 = cut_pb[tid] / share, c1 = (cut_pb[tid] + cut_units[tid] - 1) / share;
-    unsigned* cnt = a.count + c0;
-    s_last[tid] = atomicAdd(cnt, 1u) == (unsigned)(c1 - c0);
-    if (s_last[tid]) *cnt = 0u;  // ready for the next call
+  auto store_row = [&](const PieceInfo& p, int r, const Elems<kV>& y, float l) {
+    const int R = p.tile * 16 + r, t = token(R);
+    store_out<F16>(a.o + (((int64_t)p.s * a.T + t) * a.n_q + p.head * G + R - t * G) * D + kV * lane, y, l);
+  };
+  int tasks = 0, first_cta = 0, ctas = 0, row = 0, piece = 0;  // lane j: the warp's j-th cut row
+  int skip = 0;  // rows of the pairs before, modulo the warps
+  for (unsigned rest = __ballot_sync(0xFFFFFFFFu, pair_of >= 0); rest;) {
+    const int i = __ffs(rest) - 1;
+    const PieceInfo p = s_piece[i];
+    const unsigned mine = __ballot_sync(0xFFFFFFFFu, pair_of == p.pair);
+    rest &= ~mine;
+    const int last = 31 - __clz(mine), here = min(kR, rows - p.tile * 16);
+    const bool own = p.pb >= F0 && p.pb + p.units <= F1;
+    const float* from = mine >> lane & 1u ? s_piece[lane].at : p.at;
+    for (int r = warp < skip ? warp + kWarps - skip : warp - skip; r < here; r += kWarps) {
+      const float m = mine >> lane & 1u ? from[r] : -INFINITY, l = from[kR + r];
+      const float M = warp_max(m), w = ex2(m - (M == -INFINITY ? 0.0f : M)), L = warp_sum(w * l);
+      Elems<kV> y{};
+#pragma unroll 4
+      for (int k = i; k <= last; ++k) {
+        const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+        const float* pk = mine >> k & 1u ? s_piece[k].at : p.at;
+        const Elems<kV> x = load_elems<kV>(pk + 2 * kR + r * (D + 4) + kV * lane);
+#pragma unroll
+        for (int e = 0; e < kV; ++e) y.v[e] = fmaf(x.v[e], wk, y.v[e]);
+      }
+      if (own) {
+        store_row(p, r, y, L);
+      } else {
+        float* part = a.part + (int64_t)(2 * blockIdx.x + (p.pb < F0 ? 0 : 1)) * kPiece + r;
+        store_elems(part + 2 * kR + r * (D + 3) + kV * lane, y);
+        if (lane == 0) {
+          part[0] = M;
+          part[kR] = L;
+        }
+        if (lane == tasks) {
+          first_cta = cut_up((unsigned)p.pb + 1u, share) - 1;
+          ctas = cut_up((unsigned)(p.pb + p.units), share) - first_cta;
+          row = r;
+          piece = i;
+        }
+        ++tasks;
+      }
+    }
+    skip = (skip + here) % kWarps;
+  }
+  if (tasks == 0) return;
+  __threadfence();
+  __syncwarp();
+  bool last = false;
+  if (lane < tasks) {
+    // the counters are those of the pair's first CTA, whose end cuts this pair
+    // and no other
+    unsigned* cnt = a.count + first_cta * 16 + row;
+    last = atomicAdd(cnt, 1u) == (unsigned)(ctas - 1);
+    if (last) *cnt = 0u;  // ready for the next call
     __threadfence();
   }
-  __syncthreads();
-  for (int k = 0; k < 2; ++k) {
-    if (cut_pair[k] < 0 || !s_last[k]) continue;
-    const int c0 = cut_pb[k] / share, c1 = (cut_pb[k] + cut_units[k] - 1) / share;
-    const int s = cut_pair[k] / ht, h = cut_pair[k] - s * ht, head = h / a.tiles, mt = h - head * a.tiles;
-    for (int item = tid; item < kItems; item += kQThr) {
-      const int r = item / (D / 4), d = item % (D / 4);
-      Joined j{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-      join_parts<8>(j, c1 - c0 + 1, [&](int c) {
-        const float* p = a.part + (int64_t)(2 * (c0 + c) + (c == 0)) * kPiece;
-        return PartRef{p + r, kR, 2 * kR + r * (D + 4) + 4 * d - r};
-      });
-      const int R = mt * 16 + r, t = R / G;
-      if (R < rows)
-        store4<F16>(a.o + (((int64_t)s * a.T + t) * a.n_q + head * G + R - t * G) * D + 4 * d, j.o, j.L);
+  for (unsigned todo = __ballot_sync(0xFFFFFFFFu, last); todo; todo &= todo - 1) {
+    const int j = __ffs(todo) - 1;
+    const int n = __shfl_sync(0xFFFFFFFFu, ctas, j), r = __shfl_sync(0xFFFFFFFFu, row, j);
+    const PieceInfo p = s_piece[__shfl_sync(0xFFFFFFFFu, piece, j)];
+    // part c of the pair: the first CTA's is its place 1, the others' place 0
+    const float* parts = a.part + (int64_t)(2 * __shfl_sync(0xFFFFFFFFu, first_cta, j)) * kPiece + r;
+    auto place = [&](int c) { return parts + (int64_t)(2 * c + (c == 0)) * kPiece; };
+    float M = -INFINITY, L = 0.0f;
+    Elems<kV> y{};
+    for (int b = 0; b < n; b += 32) {
+      const int here = min(32, n - b);
+      const float* q = place(b + min(lane, here - 1));
+      const float mb = lane < here ? __ldcg(q) : -INFINITY, lb = __ldcg(q + kR);
+      float wb = 0.0f;
+      for (int c = 0; c < here; c += 4) {
+        Elems<kV> x[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          x[d] = load_far<kV>(place(b + min(c + d, here - 1)) + 2 * kR + r * (D + 3) + kV * lane);
+        if (c == 0) {  // after the first loads are on their way
+          const float now = fmaxf(M, warp_max(mb)), U = now == -INFINITY ? 0.0f : now;
+          const float old = ex2(M - U);
+          wb = ex2(mb - U);
+          L = L * old + warp_sum(wb * lb);
+          M = now;
+#pragma unroll
+          for (int e = 0; e < kV; ++e) y.v[e] *= old;
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const float wk = __shfl_sync(0xFFFFFFFFu, wb, (c + d) & 31);
+#pragma unroll
+          for (int e = 0; e < kV; ++e) y.v[e] = c + d < here ? fmaf(x[d].v[e], wk, y.v[e]) : y.v[e];
+        }
+      }
     }
+    store_row(p, r, y, L);
   }
 }
 
 namespace {
 int row_tiles(const moe_attn_batch_shape_t* s) { return (s->T * (s->n_q / s->n_kv) + 15) / 16; }
 constexpr int kPairCost = 1;
-constexpr size_t kCountAt = 256, kPartAt = kCountAt + kMostCtas * 4;
+constexpr int kMostWarps = q4_warps<2>();
+constexpr size_t part_floats(int D) { return 2 * 16 + 16 * (D + 4); }
+constexpr size_t kCountAt = 256, kPartAt = kCountAt + kMostCtas * 16 * 4;
 
 template <bool F16, int D, int NT>
 cudaError_t launch(const AttnQ4Args& a, int ctas, cudaStream_t stream) {
-  const size_t smem = (size_t)kWarps * (ring_stages<D, NT>() * 2 * Q4<D>::kTile + piece_floats<D, NT>() * 4);
+  const size_t smem = (size_t)q4_warps<NT>() *
+                      (ring_stages<D, NT>() * 2 * Q4<D>::kTile + kScratch +
+                       (piece_in_smem<NT>() ? piece_floats<D, NT>() * 4 : query_bytes<D, NT>()));
   const cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<F16, D, NT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_q4_kernel<F16, D, NT>, dim3(ctas), dim3(kQThr), smem, stream, a);
+  return launch_pdl(attn_q4_kernel<F16, D, NT>, dim3(ctas), dim3(q4_warps<NT>() * 32), smem, stream, a);
 }
 }  // namespace
 
@@ -719,12 +980,12 @@ bool attn_q4_supported(const moe_attn_batch_shape_t* s) {
   return (int64_t)s->n_slots * s->n_kv * row_tiles(s) * (2 * s->max_blocks + kPairCost) < (1 << 30);
 }
 
-// status, the CTAs' counters, their two places for parts. The counters are
+// status, the CTAs' counters (a row each), their two places for parts, the
+// warps' places for pieces. The counters are
 // all that one call leaves to the next (zeros), and nothing lies elsewhere for
 // another shape.
 size_t attn_q4_ws_bytes(const moe_attn_batch_shape_t* s) {
-  const size_t piece = 2 * 16 + 16 * (s->D + 4);
-  return kPartAt + 2 * (size_t)kMostCtas * piece * 4;
+  return kPartAt + (2 + kMostWarps) * (size_t)kMostCtas * part_floats(s->D) * 4;
 }
 
 cudaError_t launch_attn_q4(const moe_attn_batch_shape_t* s, AttnQ4Args a, uint8_t* ws, int nsm,
@@ -732,10 +993,12 @@ cudaError_t launch_attn_q4(const moe_attn_batch_shape_t* s, AttnQ4Args a, uint8_
   a.ctrl = reinterpret_cast<Ctrl*>(ws);
   a.count = reinterpret_cast<unsigned*>(ws + kCountAt);
   a.part = reinterpret_cast<float*>(ws + kPartAt);
+  a.pieces = a.part + 2 * (size_t)kMostCtas * part_floats(s->D);
   a.n_slots = s->n_slots;
   a.T = s->T;
   a.n_q = s->n_q;
   a.n_kv = s->n_kv;
+  a.group = s->n_q / s->n_kv;
   a.max_blocks = s->max_blocks;
   a.tiles = row_tiles(s);
   a.pair_cost = kPairCost;

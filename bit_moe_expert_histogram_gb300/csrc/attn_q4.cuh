@@ -28,11 +28,13 @@ struct AttnQ4Args {
   const int32_t* lens;
   const int32_t* n_new;  // [n_slots] or null: T
   int n_slots, T, n_q, n_kv, max_blocks, n_phys;
+  int group;          // n_q / n_kv
   int tiles;          // of 16 rows that a pair's rows make (one of 8 where they fit)
   int pair_cost;      // units of the line that a pair counts beside its own
   uint16_t* o;        // [n_slots][T][n_q][D]
   float* part;        // [CTA][2]: what the CTA's ends cut
-  unsigned* count;    // [CTA]: arrivals at the pair that the CTA's end cuts
+  float* pieces;      // [CTA][warp]: what a warp's start cuts, where shared memory has no room
+  unsigned* count;    // [CTA][16]: arrivals at a row of the pair that the CTA's end cuts
   Ctrl* ctrl;
 };
 

@@ -50,31 +50,29 @@
 namespace moe {
 
 namespace {
-constexpr int kUnit = 32;   // positions of a unit
 constexpr int kMostCtas = 256;
+constexpr int kMostRows = 16;    // of a tile
+constexpr int kMostChunks = 16;  // of 32 items of a pair's output
 
-template <int D>
+constexpr int kWarps = 8;   // of a CTA
+constexpr int kQThr = kWarps * 32;
+constexpr int kS = 2;       // stages of a warp's ring
+// A unit of work is a page of one head.
+template <int D, int NT>
 struct Q4 {
-  static constexpr int kRow = q4_units(D) * 2;      // bytes of a row
-  static constexpr int kTile = kUnit * kRow;        // of a unit's keys (or values)
-  static constexpr int kCh = D / 32;                // 16-byte pieces of codes
+  static constexpr int kRow = q4_units(D) * 2;  // bytes of a row
+  static constexpr int kTile = kBlk * kRow;     // of a unit's keys (or values)
+  static constexpr int kCh = D / 32;            // 16-byte pieces of codes
+  // sixteen rows' queries lie in shared memory, [D / 32][NT][lane][4]
+  static constexpr int kQBytes = NT == 1 ? 0 : D / 32 * NT * 512;
+  // whether a warp's first piece does, too (there is no room beside everything else)
+  static constexpr bool kPieceHere = NT == 1 || D == 64;
 };
-// Warps of a CTA and stages of a warp's ring.
-template <int NT>
-__host__ __device__ constexpr int q4_warps() { return 12; }
-template <int D, int NT>
-__host__ __device__ constexpr int ring_stages() { return D == 64 ? 4 : 2; }
-// Whether a warp's first piece has a place in shared memory, beside the ring;
-// with sixteen rows there is no room for it, nor for the queries in registers.
-template <int NT>
-__host__ __device__ constexpr bool piece_in_smem() { return NT == 1; }
-// bytes of a warp's queries in shared memory, [D / 32][NT][lane][4]
-template <int D, int NT>
-__host__ __device__ constexpr int query_bytes() { return NT == 1 ? 0 : D / 32 * NT * 512; }
-// A warp's scratch for a unit's scales and biases: keys'
-// scales fp32 [32][4]; then, by position pairs, values' scales, then biases fp16 [16][2][4][2].
-constexpr int kScratch = 1024;
-// A piece: rows R[kR], l[kR], O[kR][D + 4] (the pad spreads the banks)
+// A warp's scratch for a unit's scales and biases: keys' scales fp32
+// [position][4]; then, by position pairs, values' scales and biases fp16
+// [pair][2][4][2].
+constexpr int kVal = kBlk * 16, kScratch = kBlk * 32;
+// A piece or part: R[kR], l[kR], O[kR][D + 4] (the pad spreads the banks)
 template <int D, int NT>
 __host__ __device__ constexpr int piece_floats() { return 2 * 8 * NT + 8 * NT * (D + 4); }
 
@@ -186,7 +184,7 @@ __device__ __forceinline__ Q4Span q4_span(const AttnQ4Args& a, int s) {
     r.len = min(max(r.len, 0), most);
     r.n_new = min(max(r.n_new, 0), a.T);
   }
-  const int n = (r.len + kUnit - 1) / kUnit;
+  const int n = (r.len + kBlk - 1) / kBlk;
   r.units = r.n_new == 0 || n < 1 ? 1 : n;
   return r;
 }
@@ -218,30 +216,6 @@ struct Elems {
   float v[V];
 };
 template <int V>
-__device__ __forceinline__ Elems<V> load_elems(const float* p) {  // shared memory, or this call's parts
-  Elems<V> r;
-  if (V == 4) {
-    const float4 x = *reinterpret_cast<const float4*>(p);
-    r.v[0] = x.x, r.v[1] = x.y, r.v[V - 2] = x.z, r.v[V - 1] = x.w;
-  } else {
-    const float2 x = *reinterpret_cast<const float2*>(p);
-    r.v[0] = x.x, r.v[1] = x.y;
-  }
-  return r;
-}
-template <int V>
-__device__ __forceinline__ Elems<V> load_far(const float* p) {  // from L2
-  Elems<V> r;
-  if (V == 4) {
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
-    r.v[0] = x.x, r.v[1] = x.y, r.v[V - 2] = x.z, r.v[V - 1] = x.w;
-  } else {
-    const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
-    r.v[0] = x.x, r.v[1] = x.y;
-  }
-  return r;
-}
-template <int V>
 __device__ __forceinline__ void store_elems(float* p, const Elems<V>& x) {
   if (V == 4)
     *reinterpret_cast<float4*>(p) = make_float4(x.v[0], x.v[1], x.v[V - 2], x.v[V - 1]);
@@ -260,23 +234,26 @@ __device__ __forceinline__ void store_out(uint16_t* p, const Elems<V>& x, float 
   else
     *reinterpret_cast<uint32_t*>(p) = lo;
 }
-__device__ __forceinline__ float warp_max(float v) {
+// four more parts
+__device__ __forceinline__ void join4(Joined& j, const float (&m)[4], const float (&l)[4], const float4 (&v)[4]) {
+  const float M = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), j.M), U = M == -INFINITY ? 0.0f : M;
+  const float f = ex2(j.M - U);
+  j.L *= f;
+  j.o = make_float4(j.o.x * f, j.o.y * f, j.o.z * f, j.o.w * f);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
-  return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  return v;
+  for (int k = 0; k < 4; ++k) {
+    const float w = ex2(m[k] - U);
+    j.L = fmaf(l[k], w, j.L);
+    j.o = make_float4(fmaf(v[k].x, w, j.o.x), fmaf(v[k].y, w, j.o.y), fmaf(v[k].z, w, j.o.z), fmaf(v[k].w, w, j.o.w));
+  }
+  j.M = M;
 }
 }  // namespace
 
 template <bool F16, int D, int NT>
-__global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const AttnQ4Args a) {
-  using C = Q4<D>;
-  constexpr int kWarps = q4_warps<NT>(), kQThr = kWarps * 32;
-  constexpr int kS = ring_stages<D, NT>(), kR = 8 * NT;
+__global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
+  using C = Q4<D, NT>;
+  constexpr int kR = 8 * NT;
   constexpr int kKS = D / 16;  // steps of the score product, and O's element tiles
   constexpr int kPiece = piece_floats<D, NT>();
   extern __shared__ __align__(128) uint8_t sm_raw[];
@@ -289,9 +266,8 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
   const uint32_t sbase = smem_u32(sm_raw);
   const uint32_t ring = sbase + warp * (kS * 2 * C::kTile);
   const uint32_t scratch = sbase + kWarps * (kS * 2 * C::kTile) + warp * kScratch;
-  // the queries or the piece
-  constexpr int kQBytes = query_bytes<D, NT>(), kMore = piece_in_smem<NT>() ? kPiece * 4 : kQBytes;
-  const uint32_t more = sbase + kWarps * (kS * 2 * C::kTile + kScratch) + warp * kMore;
+  constexpr int kMore = C::kQBytes + (C::kPieceHere ? kPiece * 4 : 0);
+  const uint32_t queries = sbase + kWarps * (kS * 2 * C::kTile + kScratch) + warp * kMore;
   const uint32_t bars = smem_u32(&full[warp][0]);
   if (lane < kS) mbar_init(bars + 8u * lane, 1);
   if (tid < 2 * kWarps) s_piece[tid].pair = -1;
@@ -367,7 +343,7 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
     unsigned absent = 0;                        // bit per stage: nothing was fetched for it
     bool dead = false;                          // a wait ran out: nothing more is fetched
     const uint64_t pol = policy_evict_first();
-    const int page_bytes = a.n_kv * kBlk * C::kRow;
+    const int page_bytes = a.n_kv * C::kTile;
     auto load_next = [&] {
       if (dead) return;
       while (lu >= le) {
@@ -377,13 +353,12 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
         le = min(f1 - ld.pb, ld.sp.units);
         base = -1;
       }
-      const int block = lu >> 1;
-      if ((block & ~31) != base) {
-        base = block & ~31;
+      if ((lu & ~31) != base) {
+        base = lu & ~31;
         pages = base + lane < a.max_blocks ? __ldg(a.table + (int64_t)ld.s * a.max_blocks + base + lane) : -1;
       }
-      const int page = __shfl_sync(0xFFFFFFFFu, pages, block & 31);
-      const int n = min(kUnit, ld.sp.len - lu * kUnit);
+      const int page = __shfl_sync(0xFFFFFFFFu, pages, lu & 31);
+      const int n = min(kBlk, ld.sp.len - lu * kBlk);
       const bool none = ld.sp.n_new == 0 || n <= 0;
       const bool bad = !none && (unsigned)page >= (unsigned)a.n_phys;
       absent = (absent & ~(1u << lst)) | (none || bad ? 1u << lst : 0u);
@@ -393,7 +368,7 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
           if (bad) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_ATTNB, ld.s);
           mbar_arrive(bar);
         } else {
-          const int64_t from = (int64_t)page * page_bytes + (ld.head * kBlk + (lu & 1) * kUnit) * C::kRow;
+          const int64_t from = (int64_t)page * page_bytes + ld.head * C::kTile;
           const uint32_t sk = ring + lst * 2 * C::kTile, bytes = n * C::kRow;
           mbar_arrive_expect_tx(bar, 2 * bytes);
           bulk_load(sk, a.k + from, bytes, bar, pol);
@@ -411,7 +386,7 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
       const int first = at.sp.len - at.sp.n_new;  // may be negative
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const int r = at.tile * 16 + gq + 8 * i, t = r < rows ? token(r) : a.T;
+        const int r = at.tile * kR + gq + 8 * i, t = r < rows ? token(r) : a.T;
         const bool sees = t < at.sp.n_new && first + t >= 0;
         const uint16_t* q = a.q + ((int64_t)at.s * a.T + t) * a.q_stride + (at.head * G + r - t * G) * D;
 #pragma unroll
@@ -483,7 +458,7 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           cf[i][e] = __shfl_sync(0xFFFFFFFFu, back, 8 * cq + 4 * e);
-          const int r = at.tile * 16 + 8 * i + 2 * cq + e, t = r < rows ? token(r) : a.T;
+          const int r = at.tile * kR + 8 * i + 2 * cq + e, t = r < rows ? token(r) : a.T;
           lim[i][e] = t < at.sp.n_new ? max(basep + t, -1) : -1;
         }
         float sum[4];
@@ -514,12 +489,12 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
       }
       // o: O^T, element tiles by rows; sb: rows 0 .. 3 the biases' part by
       // groups, row 4 the sum of the weights
-      if (kQBytes > 0) {
+      if (C::kQBytes > 0) {
 #pragma unroll
         for (int c = 0; c < C::kCh; ++c)
 #pragma unroll
           for (int i = 0; i < NT; ++i)
-            sts128(more + (c * NT + i) * 512 + lane * 16, qa[2 * c][i], qa[2 * c][NT + i], qa[2 * c + 1][i],
+            sts128(queries + (c * NT + i) * 512 + lane * 16, qa[2 * c][i], qa[2 * c][NT + i], qa[2 * c + 1][i],
                    qa[2 * c + 1][NT + i]);
       }
       float m[NT][2], sb[NT][4], o[kKS][NT][4];
@@ -546,27 +521,35 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
         }
         if (!dead && !(absent >> st & 1u)) {
           const uint32_t sk = ring + st * 2 * C::kTile, sv = sk + C::kTile;
-          const int pos0 = (f - at.pb) * kUnit, n_here = at.sp.len - pos0;
+          const int pos0 = (f - at.pb) * kBlk, n_here = at.sp.len - pos0;
           // ---- scales and biases, a position a lane; values' rows past the slot's
           // end hold anything and count as nothing (keys' are masked)
           {
-            const uint32_t at = D / 2 + lane * C::kRow;
-            const uint2 wk = lds64(sk + at);
-            sts128(scratch + lane * 16, wk.x << 16, wk.x & 0xFFFF0000u, wk.y << 16, wk.y & 0xFFFF0000u);
-            uint4 wv = lds128(sv + at);
-            if (lane >= n_here) wv = make_uint4(0u, 0u, 0u, 0u);
-            const float s4[4] = {bf_lo(wv.x), bf_hi(wv.x), bf_lo(wv.y), bf_hi(wv.y)};
-            const float b4[4] = {bf_lo(wv.z), bf_hi(wv.z), bf_lo(wv.w), bf_hi(wv.w)};
+            constexpr int kOf = kBlk / 32;  // positions of a lane
+            float s4[kOf][4], b4[kOf][4], big[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int v = 0; v < kOf; ++v) {
+              const int pos = lane + 32 * v;
+              const uint32_t at = D / 2 + pos * C::kRow;
+              const uint2 wk = lds64(sk + at);
+              sts128(scratch + pos * 16, wk.x << 16, wk.x & 0xFFFF0000u, wk.y << 16, wk.y & 0xFFFF0000u);
+              uint4 wv = lds128(sv + at);
+              if (pos >= n_here) wv = make_uint4(0u, 0u, 0u, 0u);
+              s4[v][0] = 16.0f * bf_lo(wv.x), s4[v][1] = 16.0f * bf_hi(wv.x);
+              s4[v][2] = 16.0f * bf_lo(wv.y), s4[v][3] = 16.0f * bf_hi(wv.y);
+              b4[v][0] = bf_lo(wv.z), b4[v][1] = bf_hi(wv.z), b4[v][2] = bf_lo(wv.w), b4[v][3] = bf_hi(wv.w);
+#pragma unroll
+              for (int g = 0; g < 4; ++g) big[g] = fmaxf(big[g], fmaxf(s4[v][g], fabsf(b4[v][g])));
+            }
             bool grown = false;
             int was[4];
             float inv[4];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               // positive numbers order as whole numbers
-              const uint32_t big = __reduce_max_sync(
-                  0xFFFFFFFFu, __float_as_uint(fmaxf(16.0f * s4[g], fabsf(b4[g]))));
+              const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big[g]));
               was[g] = sg[g];
-              sg[g] = min(max(sg[g], (int)(big >> 23) + 1), kSigMost);
+              sg[g] = min(max(sg[g], (int)(top >> 23) + 1), kSigMost);
               grown |= sg[g] != was[g];
               inv[g] = __uint_as_float((uint32_t)(254 - sg[g]) << 23);
             }
@@ -590,87 +573,93 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
             // this lane's position as the low or high half of its pair: even
             // lanes take groups 0 and 1 of both, odd lanes 2 and 3
             const bool odd = lane & 1;
-            const uint32_t sa = pack2<true>(16.0f * s4[0] * inv[0], 16.0f * s4[1] * inv[1]);
-            const uint32_t sc = pack2<true>(16.0f * s4[2] * inv[2], 16.0f * s4[3] * inv[3]);
-            const uint32_t ba = pack2<true>(b4[0] * inv[0], b4[1] * inv[1]);
-            const uint32_t bc = pack2<true>(b4[2] * inv[2], b4[3] * inv[3]);
-            const uint32_t xs = __shfl_xor_sync(0xFFFFFFFFu, odd ? sa : sc, 1);
-            const uint32_t xb = __shfl_xor_sync(0xFFFFFFFFu, odd ? ba : bc, 1);
-            const uint32_t ls = odd ? xs : sa, hs = odd ? sc : xs;
-            const uint32_t lb = odd ? xb : ba, hb = odd ? bc : xb;
-            const uint32_t tv = scratch + 512 + (lane >> 1) * 32 + odd * 8;
-            sts64(tv, __byte_perm(ls, hs, 0x5410), __byte_perm(ls, hs, 0x7632));
-            sts64(tv + 16, __byte_perm(lb, hb, 0x5410), __byte_perm(lb, hb, 0x7632));
+#pragma unroll
+            for (int v = 0; v < kOf; ++v) {
+              const uint32_t sa = pack2<true>(s4[v][0] * inv[0], s4[v][1] * inv[1]);
+              const uint32_t sc = pack2<true>(s4[v][2] * inv[2], s4[v][3] * inv[3]);
+              const uint32_t ba = pack2<true>(b4[v][0] * inv[0], b4[v][1] * inv[1]);
+              const uint32_t bc = pack2<true>(b4[v][2] * inv[2], b4[v][3] * inv[3]);
+              const uint32_t xs = __shfl_xor_sync(0xFFFFFFFFu, odd ? sa : sc, 1);
+              const uint32_t xb = __shfl_xor_sync(0xFFFFFFFFu, odd ? ba : bc, 1);
+              const uint32_t ls = odd ? xs : sa, hs = odd ? sc : xs;
+              const uint32_t lb = odd ? xb : ba, hb = odd ? bc : xb;
+              const uint32_t tv = scratch + kVal + ((lane >> 1) + 16 * v) * 32 + odd * 8;
+              sts64(tv, __byte_perm(ls, hs, 0x5410), __byte_perm(ls, hs, 0x7632));
+              sts64(tv + 16, __byte_perm(lb, hb, 0x5410), __byte_perm(lb, hb, 0x7632));
+            }
           }
           __syncwarp();
           // ---- scores, in powers of two, of positions 16 h + gq and 8 on, and of
           // two queries a number pair
-          uint64_t x[kUnit / 16][2][NT];
-          float t[kUnit / 16][NT][4];
+          uint64_t x[kBlk / 16][2][NT];
 #pragma unroll
-          for (int c = 0; c < C::kCh; c += 2) {
-            if (kQBytes > 0) {
+          for (int v = 0; v < kBlk / 32; ++v) {
+            float t[2][NT][4];
 #pragma unroll
-              for (int k = c; k < c + 2; ++k)
+            for (int c = 0; c < C::kCh; c += 2) {
+              if (C::kQBytes > 0) {
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                  const uint4 q = lds128(more + (k * NT + i) * 512 + lane * 16);
-                  qa[2 * k][i] = q.x, qa[2 * k][NT + i] = q.y;
-                  qa[2 * k + 1][i] = q.z, qa[2 * k + 1][NT + i] = q.w;
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < kUnit / 16; ++h) {
-              const uint4 s0 = lds128(scratch + (16 * h + gq) * 16), s1 = lds128(scratch + (16 * h + gq + 8) * 16);
-              const float s[2][4] = {{__uint_as_float(s0.x), __uint_as_float(s0.y), __uint_as_float(s0.z), __uint_as_float(s0.w)},
-                                     {__uint_as_float(s1.x), __uint_as_float(s1.y), __uint_as_float(s1.z), __uint_as_float(s1.w)}};
-              uint32_t kc[4];  // words of pieces c and c + 1 of positions gq, gq + 8
-              ldsm4(sk + (16 * h + (lane & 15)) * C::kRow + (c + (lane >> 4)) * 16, kc);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float acc[NT][4];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int ks = 2 * (c + k) + e, g = D == 128 ? ks >> 1 : ks;
-                  const uint32_t w0 = e ? kc[2 * k] >> 8 : kc[2 * k];
-                  const uint32_t w1 = e ? kc[2 * k + 1] >> 8 : kc[2 * k + 1];
+                for (int k = c; k < c + 2; ++k)
 #pragma unroll
                   for (int i = 0; i < NT; ++i) {
-                    if (D == 64 || e == 0)
-                      mma_f16_0(acc[i], w0 & kLoNib, w1 & kLoNib, w0 & kHiNib, w1 & kHiNib, qa[ks][i], qa[ks][NT + i]);
-                    else
-                      mma_f16(acc[i], w0 & kLoNib, w1 & kLoNib, w0 & kHiNib, w1 & kHiNib, qa[ks][i], qa[ks][NT + i]);
-                    if (D == 64 || e == 1)
+                    const uint4 q = lds128(queries + (k * NT + i) * 512 + lane * 16);
+                    qa[2 * k][i] = q.x, qa[2 * k][NT + i] = q.y;
+                    qa[2 * k + 1][i] = q.z, qa[2 * k + 1][NT + i] = q.w;
+                  }
+              }
 #pragma unroll
-                      for (int z = 0; z < 4; ++z)
-                        t[h][i][z] = g == 0 ? s[z >> 1][0] * acc[i][z] : fmaf(s[z >> 1][g], acc[i][z], t[h][i][z]);
+              for (int h = 0; h < 2; ++h) {
+                const uint4 s0 = lds128(scratch + (16 * (2 * v + h) + gq) * 16), s1 = lds128(scratch + (16 * (2 * v + h) + gq + 8) * 16);
+                const float s[2][4] = {{__uint_as_float(s0.x), __uint_as_float(s0.y), __uint_as_float(s0.z), __uint_as_float(s0.w)},
+                                       {__uint_as_float(s1.x), __uint_as_float(s1.y), __uint_as_float(s1.z), __uint_as_float(s1.w)}};
+                uint32_t kc[4];  // words of pieces c and c + 1 of positions gq, gq + 8
+                ldsm4(sk + (16 * (2 * v + h) + (lane & 15)) * C::kRow + (c + (lane >> 4)) * 16, kc);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  float acc[NT][4];
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int ks = 2 * (c + k) + e, g = D == 128 ? ks >> 1 : ks;
+                    const uint32_t w0 = e ? kc[2 * k] >> 8 : kc[2 * k];
+                    const uint32_t w1 = e ? kc[2 * k + 1] >> 8 : kc[2 * k + 1];
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                      if (D == 64 || e == 0)
+                        mma_f16_0(acc[i], w0 & kLoNib, w1 & kLoNib, w0 & kHiNib, w1 & kHiNib, qa[ks][i], qa[ks][NT + i]);
+                      else
+                        mma_f16(acc[i], w0 & kLoNib, w1 & kLoNib, w0 & kHiNib, w1 & kHiNib, qa[ks][i], qa[ks][NT + i]);
+                      if (D == 64 || e == 1)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                          t[h][i][z] = g == 0 ? s[z >> 1][0] * acc[i][z] : fmaf(s[z >> 1][g], acc[i][z], t[h][i][z]);
+                    }
                   }
                 }
               }
             }
-          }
 #pragma unroll
-          for (int h = 0; h < kUnit / 16; ++h) {
-            const uint32_t r0 = sk + (16 * h + gq) * C::kRow + D / 2 + 8 + 4 * (cq & 1);
-            const uint32_t bw0 = lds32(r0), bw1 = lds32(r0 + 8 * C::kRow);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t r0 = sk + (16 * (2 * v + h) + gq) * C::kRow + D / 2 + 8 + 4 * (cq & 1);
+              const uint32_t bw0 = lds32(r0), bw1 = lds32(r0 + 8 * C::kRow);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              float xb[4];
-              mma_bf16_k8_0(xb, bw0, bw1, qs[i]);
-              mma_bf16_k8(xb, bw0, bw1, qs[NT + i]);
-              const uint64_t f2 = pair2(__float_as_uint(cf[i][0]), __float_as_uint(cf[i][1]));
+              for (int i = 0; i < NT; ++i) {
+                float xb[4];
+                mma_bf16_k8_0(xb, bw0, bw1, qs[i]);
+                mma_bf16_k8(xb, bw0, bw1, qs[NT + i]);
+                const uint64_t f2 = pair2(__float_as_uint(cf[i][0]), __float_as_uint(cf[i][1]));
 #pragma unroll
-              for (int y = 0; y < 2; ++y)
-                x[h][y][i] = fma2(pair2(__float_as_uint(t[h][i][2 * y]), __float_as_uint(t[h][i][2 * y + 1])), f2,
-                                  pair2(__float_as_uint(xb[2 * y]), __float_as_uint(xb[2 * y + 1])));
+                for (int y = 0; y < 2; ++y)
+                  x[2 * v + h][y][i] = fma2(pair2(__float_as_uint(t[h][i][2 * y]), __float_as_uint(t[h][i][2 * y + 1])), f2,
+                                    pair2(__float_as_uint(xb[2 * y]), __float_as_uint(xb[2 * y + 1])));
+              }
             }
           }
           // every query that is in use sees positions up to basep
-          if (pos0 + kUnit - 1 > basep) {
+          if (pos0 + kBlk - 1 > basep) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-              for (int h = 0; h < kUnit / 8; ++h) {
+              for (int h = 0; h < kBlk / 8; ++h) {
                 float x0, x1;
                 unpair2(x[h >> 1][h & 1][i], x0, x1);
                 if (pos0 + 8 * h + gq > lim[i][0]) x0 = -INFINITY;
@@ -686,7 +675,7 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
           for (int i = 0; i < NT; ++i) {
             mx[i][0] = mx[i][1] = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < kUnit / 8; ++h) {
+            for (int h = 0; h < kBlk / 8; ++h) {
               float x0, x1;
               unpair2(x[h >> 1][h & 1][i], x0, x1);
               mx[i][0] = fmaxf(mx[i][0], x0);
@@ -721,27 +710,22 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
                           __float_as_uint(kLift - (m[i][1] == -INFINITY ? 0.0f : m[i][1])));
           // ---- weights and the second product, sixteen positions a step
 #pragma unroll
-          for (int kp = 0; kp < kUnit / 16; ++kp) {
-            // p and p s as operands, two positions of query gq a register:
-            // [group][position half]
-            uint32_t p[NT][2], pw[NT][4][2];
+          for (int kp = 0; kp < kBlk / 16; ++kp) {
+            uint32_t p[NT][2];  // weights as an operand: two positions of query gq a register
+            uint32_t s4[2][4];  // the values' scales of the same positions, by groups
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const int n = 2 * kp + h;
-              const uint4 s4 = lds128(scratch + 512 + (4 * n + cq) * 32);
+              const uint4 w = lds128(scratch + kVal + (8 * kp + 4 * h + cq) * 32);
+              s4[h][0] = w.x, s4[h][1] = w.y, s4[h][2] = w.z, s4[h][3] = w.w;
 #pragma unroll
               for (int i = 0; i < NT; ++i) {
                 float x0, x1;
                 unpair2(add2(x[kp][h][i], up[i]), x0, x1);
                 p[i][h] = transpose(pack2<true>(ex2(x0), ex2(x1)));
-                pw[i][0][h] = mul_h2(p[i][h], s4.x);
-                pw[i][1][h] = mul_h2(p[i][h], s4.y);
-                pw[i][2][h] = mul_h2(p[i][h], s4.z);
-                pw[i][3][h] = mul_h2(p[i][h], s4.w);
               }
             }
             // rows 0 .. 3: the groups' biases, 4: ones; the others' results go nowhere
-            const uint32_t ab = scratch + 512 + (8 * kp + cq) * 32 + 16 + (gq & 3) * 4;
+            const uint32_t ab = scratch + kVal + (8 * kp + cq) * 32 + 16 + (gq & 3) * 4;
             const uint32_t a0 = gq < 4 ? lds32(ab) : 0x3C003C00u, a2 = gq < 4 ? lds32(ab + 128) : 0x3C003C00u;
 #pragma unroll
             for (int i = 0; i < NT; ++i)
@@ -751,17 +735,23 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
               uint32_t vc[4];  // pieces c and c + 1 of positions 0..7, 8..15
               ldsm4_t(sv + (16 * kp + (lane & 15)) * C::kRow + (c + (lane >> 4)) * 16, vc);
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
+              for (int k = 0; k < 2; ++k) {
+                uint32_t ps[NT][2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const int j = 2 * (c + k) + e, g = D == 128 ? j >> 1 : j;
                   const uint32_t x0 = e ? vc[2 * k] >> 8 : vc[2 * k];
                   const uint32_t x1 = e ? vc[2 * k + 1] >> 8 : vc[2 * k + 1];
 #pragma unroll
-                  for (int i = 0; i < NT; ++i)
-                    mma_f16(o[j][i], x0 & kLoNib, x0 & kHiNib, x1 & kLoNib, x1 & kHiNib,
-                            pw[i][g][0], pw[i][g][1]);
+                  for (int i = 0; i < NT; ++i) {
+                    if (D == 64 || e == 0) {
+                      ps[i][0] = mul_h2(p[i][0], s4[0][g]);
+                      ps[i][1] = mul_h2(p[i][1], s4[1][g]);
+                    }
+                    mma_f16(o[j][i], x0 & kLoNib, x0 & kHiNib, x1 & kLoNib, x1 & kHiNib, ps[i][0], ps[i][1]);
+                  }
                 }
+              }
             }
           }
           // the stage is the loader's again
@@ -781,8 +771,8 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
       for (int g = 0; g < 4; ++g) sig[g] = __uint_as_float((uint32_t)sg[g] << 23);
       float* pf = reinterpret_cast<float*>(sm_raw + (ring - sbase));
       if (which == 0)
-        pf = piece_in_smem<NT>() ? reinterpret_cast<float*>(sm_raw + (more - sbase))
-                                 : a.pieces + ((int64_t)blockIdx.x * kWarps + warp) * kPiece;
+        pf = C::kPieceHere ? reinterpret_cast<float*>(sm_raw + (queries + C::kQBytes - sbase))
+                           : a.pieces + ((int64_t)blockIdx.x * kWarps + warp) * kPiece;
       if (!whole && lane == 0)
         s_piece[2 * warp + which] = PieceInfo{(at.s * a.n_kv + at.head) * a.tiles + at.tile, at.pb, at.sp.units,
                                               at.s, at.head, at.tile, pf};
@@ -803,7 +793,7 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
           float b[4];
 #pragma unroll
           for (int g = 0; g < 4; ++g) b[g] = __shfl_sync(0xFFFFFFFFu, sb[i][e], 4 * g + cq) * sig[g];
-          const int R = at.tile * 16 + r, t = token(R);
+          const int R = at.tile * kR + r, t = token(R);
           uint16_t* out = a.o + (((int64_t)at.s * a.T + t) * a.n_q + at.head * G + R - t * G) * D;
 #pragma unroll
           for (int c = 0; c < C::kCh; ++c) {
@@ -849,143 +839,129 @@ __global__ void __launch_bounds__(q4_warps<NT>() * 32, 1) attn_q4_kernel(const A
     }
   }
   __syncthreads();
-  // ---- the CTA's pieces, pair by pair in the line's order, a warp a row, a
-  // lane kV elements. First every row of a pair that lies in the CTA goes to the
-  // output and of one that does not to the workspace, place 0 of the CTA's two
-  // where the pair starts before it; then the latter are counted, and the last
-  // warp to arrive at a row joins it. Rows do not wait for one another.
-  constexpr int kV = D / 32;
+  // ---- the CTA's pieces, pair by pair in the line's order, a thread for four
+  // elements of a row, a warp for 32 such items. What a pair that lies in the CTA
+  // has goes to the output, what one that does not has to the workspace, place 0
+  // of the CTA's two where it starts before the CTA. Then a warp counts itself
+  // in at the cut pairs, for its items alone, and the last to arrive joins them.
+  constexpr int kItems = kR * D / 4, kPasses = (kItems + kQThr - 1) / kQThr;
   const int pair_of = lane < 2 * kWarps ? s_piece[lane].pair : -1;
+  const unsigned pieces = __ballot_sync(0xFFFFFFFFu, pair_of >= 0);
   const int share = kWarps * per;
-  auto store_row = [&](const PieceInfo& p, int r, const Elems<kV>& y, float l) {
-    const int R = p.tile * 16 + r, t = token(R);
-    store_out<F16>(a.o + (((int64_t)p.s * a.T + t) * a.n_q + p.head * G + R - t * G) * D + kV * lane, y, l);
+  auto store = [&](const PieceInfo& p, int r, int d, const float4& y, float l) {
+    const int R = p.tile * kR + r, t = token(R);
+    if (R < rows) store4<F16>(a.o + (((int64_t)p.s * a.T + t) * a.n_q + p.head * G + R - t * G) * D + 4 * d, y, l);
   };
-  int tasks = 0, first_cta = 0, ctas = 0, row = 0, piece = 0;  // lane j: the warp's j-th cut row
-  int skip = 0;  // rows of the pairs before, modulo the warps
-  for (unsigned rest = __ballot_sync(0xFFFFFFFFu, pair_of >= 0); rest;) {
+  bool cut = false;
+  for (unsigned rest = pieces; rest;) {
     const int i = __ffs(rest) - 1;
     const PieceInfo p = s_piece[i];
     const unsigned mine = __ballot_sync(0xFFFFFFFFu, pair_of == p.pair);
     rest &= ~mine;
-    const int last = 31 - __clz(mine), here = min(kR, rows - p.tile * 16);
     const bool own = p.pb >= F0 && p.pb + p.units <= F1;
-    const float* from = mine >> lane & 1u ? s_piece[lane].at : p.at;
-    for (int r = warp < skip ? warp + kWarps - skip : warp - skip; r < here; r += kWarps) {
-      const float m = mine >> lane & 1u ? from[r] : -INFINITY, l = from[kR + r];
-      const float M = warp_max(m), w = ex2(m - (M == -INFINITY ? 0.0f : M)), L = warp_sum(w * l);
-      Elems<kV> y{};
-#pragma unroll 4
-      for (int k = i; k <= last; ++k) {
-        const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
-        const float* pk = mine >> k & 1u ? s_piece[k].at : p.at;
-        const Elems<kV> x = load_elems<kV>(pk + 2 * kR + r * (D + 4) + kV * lane);
+    cut |= !own;
+#pragma unroll 1
+    for (int item = tid; item < kItems; item += kQThr) {
+      const int r = item / (D / 4), d = item % (D / 4);
+      Joined j{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+      unsigned left = mine;
+#pragma unroll 1
+      while (left) {  // four pieces at once
+        float m[4], l[4];
+        float4 v[4];
 #pragma unroll
-        for (int e = 0; e < kV; ++e) y.v[e] = fmaf(x.v[e], wk, y.v[e]);
+        for (int k = 0; k < 4; ++k) {
+          const float* q = s_piece[left ? __ffs(left) - 1 : i].at;
+          m[k] = left ? q[r] : -INFINITY;
+          l[k] = q[kR + r];
+          v[k] = *reinterpret_cast<const float4*>(q + 2 * kR + r * (D + 4) + 4 * d);
+          left &= left - 1;
+        }
+        join4(j, m, l, v);
       }
       if (own) {
-        store_row(p, r, y, L);
+        store(p, r, d, j.o, j.L);
       } else {
-        float* part = a.part + (int64_t)(2 * blockIdx.x + (p.pb < F0 ? 0 : 1)) * kPiece + r;
-        store_elems(part + 2 * kR + r * (D + 3) + kV * lane, y);
-        if (lane == 0) {
-          part[0] = M;
-          part[kR] = L;
+        float* part = a.part + (int64_t)(2 * blockIdx.x + (p.pb < F0 ? 0 : 1)) * kPiece;
+        *reinterpret_cast<float4*>(part + 2 * kR + r * (D + 4) + 4 * d) = j.o;
+        if (d == 0) {
+          part[r] = j.M;
+          part[kR + r] = j.L;
         }
-        if (lane == tasks) {
-          first_cta = cut_up((unsigned)p.pb + 1u, share) - 1;
-          ctas = cut_up((unsigned)(p.pb + p.units), share) - first_cta;
-          row = r;
-          piece = i;
-        }
-        ++tasks;
       }
     }
-    skip = (skip + here) % kWarps;
   }
-  if (tasks == 0) return;
-  __threadfence();
+  if (!cut) return;
   __syncwarp();
+  // lane c + 2 k: the warp's k-th items of the pair that is cut at the CTA's
+  // start (c = 0, the first piece's) or at its end (the last piece's)
+  int c0 = 0, n = 0;
   bool last = false;
-  if (lane < tasks) {
-    // the counters are those of the pair's first CTA, whose end cuts this pair
-    // and no other
-    unsigned* cnt = a.count + first_cta * 16 + row;
-    last = atomicAdd(cnt, 1u) == (unsigned)(ctas - 1);
-    if (last) *cnt = 0u;  // ready for the next call
-    __threadfence();
+  if (lane < 2 * kPasses && warp * 32 + (lane >> 1) * kQThr < kItems) {
+    const PieceInfo& p = s_piece[lane & 1 ? 31 - __clz(pieces) : __ffs(pieces) - 1];
+    if (lane & 1 ? p.pb >= F0 && p.pb + p.units > F1 : p.pb < F0) {
+      c0 = cut_up((unsigned)p.pb + 1u, share) - 1;
+      n = cut_up((unsigned)(p.pb + p.units), share) - c0;
+      // the counters are those of the pair's first CTA, whose end cuts this pair
+      // and no other
+      unsigned* cnt = a.count + c0 * kMostChunks + warp + (lane >> 1) * kWarps;
+      __threadfence();
+      last = atomicAdd(cnt, 1u) == (unsigned)(n - 1);
+      if (last) *cnt = 0u;  // ready for the next call
+      __threadfence();
+    }
   }
   for (unsigned todo = __ballot_sync(0xFFFFFFFFu, last); todo; todo &= todo - 1) {
-    const int j = __ffs(todo) - 1;
-    const int n = __shfl_sync(0xFFFFFFFFu, ctas, j), r = __shfl_sync(0xFFFFFFFFu, row, j);
-    const PieceInfo p = s_piece[__shfl_sync(0xFFFFFFFFu, piece, j)];
+    const int k = __ffs(todo) - 1, parts = __shfl_sync(0xFFFFFFFFu, n, k);
+    const PieceInfo p = s_piece[k & 1 ? 31 - __clz(pieces) : __ffs(pieces) - 1];
+    const int item = tid + (k >> 1) * kQThr, r = item / (D / 4), d = item % (D / 4);
+    const float* from = a.part + (int64_t)(2 * __shfl_sync(0xFFFFFFFFu, c0, k)) * kPiece + r;
+    Joined j{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
     // part c of the pair: the first CTA's is its place 1, the others' place 0
-    const float* parts = a.part + (int64_t)(2 * __shfl_sync(0xFFFFFFFFu, first_cta, j)) * kPiece + r;
-    auto place = [&](int c) { return parts + (int64_t)(2 * c + (c == 0)) * kPiece; };
-    float M = -INFINITY, L = 0.0f;
-    Elems<kV> y{};
-    for (int b = 0; b < n; b += 32) {
-      const int here = min(32, n - b);
-      const float* q = place(b + min(lane, here - 1));
-      const float mb = lane < here ? __ldcg(q) : -INFINITY, lb = __ldcg(q + kR);
-      float wb = 0.0f;
-      for (int c = 0; c < here; c += 4) {
-        Elems<kV> x[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
-          x[d] = load_far<kV>(place(b + min(c + d, here - 1)) + 2 * kR + r * (D + 3) + kV * lane);
-        if (c == 0) {  // after the first loads are on their way
-          const float now = fmaxf(M, warp_max(mb)), U = now == -INFINITY ? 0.0f : now;
-          const float old = ex2(M - U);
-          wb = ex2(mb - U);
-          L = L * old + warp_sum(wb * lb);
-          M = now;
-#pragma unroll
-          for (int e = 0; e < kV; ++e) y.v[e] *= old;
-        }
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const float wk = __shfl_sync(0xFFFFFFFFu, wb, (c + d) & 31);
-#pragma unroll
-          for (int e = 0; e < kV; ++e) y.v[e] = c + d < here ? fmaf(x[d].v[e], wk, y.v[e]) : y.v[e];
-        }
-      }
-    }
-    store_row(p, r, y, L);
+    join_parts<6>(j, parts, [&](int c) {
+      return PartRef{from + (int64_t)(2 * c + (c == 0)) * kPiece, kR, 2 * kR + r * (D + 3) + 4 * d};
+    });
+    store(p, r, d, j.o, j.L);
   }
 }
 
 namespace {
-int row_tiles(const moe_attn_batch_shape_t* s) { return (s->T * (s->n_q / s->n_kv) + 15) / 16; }
+int row_tiles(const moe_attn_batch_shape_t* s) {
+  return (s->T * (s->n_q / s->n_kv) + kMostRows - 1) / kMostRows;
+}
 constexpr int kPairCost = 1;
-constexpr int kMostWarps = q4_warps<2>();
-constexpr size_t part_floats(int D) { return 2 * 16 + 16 * (D + 4); }
-constexpr size_t kCountAt = 256, kPartAt = kCountAt + kMostCtas * 16 * 4;
+constexpr size_t part_floats(int D) { return 2 * kMostRows + kMostRows * (D + 4); }
+constexpr size_t kCountAt = 256, kPartAt = kCountAt + kMostCtas * kMostChunks * 4;
 
 template <bool F16, int D, int NT>
 cudaError_t launch(const AttnQ4Args& a, int ctas, cudaStream_t stream) {
-  const size_t smem = (size_t)q4_warps<NT>() *
-                      (ring_stages<D, NT>() * 2 * Q4<D>::kTile + kScratch +
-                       (piece_in_smem<NT>() ? piece_floats<D, NT>() * 4 : query_bytes<D, NT>()));
+  using C = Q4<D, NT>;
+  const size_t smem = (size_t)kWarps * (kS * 2 * C::kTile + kScratch + C::kQBytes +
+                                        (C::kPieceHere ? piece_floats<D, NT>() * 4 : 0));
   const cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<F16, D, NT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_q4_kernel<F16, D, NT>, dim3(ctas), dim3(q4_warps<NT>() * 32), smem, stream, a);
+  return launch_pdl(attn_q4_kernel<F16, D, NT>, dim3(ctas), dim3(kQThr), smem, stream, a);
+}
+// tiles of 8 or 16 rows
+template <bool F16, int D>
+cudaError_t launch_rows(const AttnQ4Args& a, int ctas, cudaStream_t stream) {
+  return a.T * a.group <= 8 ? launch<F16, D, 1>(a, ctas, stream) : launch<F16, D, 2>(a, ctas, stream);
 }
 }  // namespace
 
 bool attn_q4_supported(const moe_attn_batch_shape_t* s) {
   if (!attn_batch_supported(s) || s->prefix_blocks != 0) return false;
   // the line of units is counted in 32 bits
-  return (int64_t)s->n_slots * s->n_kv * row_tiles(s) * (2 * s->max_blocks + kPairCost) < (1 << 30);
+  return (int64_t)s->n_slots * s->n_kv * row_tiles(s) * (s->max_blocks + kPairCost) < (1 << 30);
 }
 
-// status, the CTAs' counters (a row each), their two places for parts, the
+// status, the CTAs' counters (one for 32 items), their two places for parts, the
 // warps' places for pieces. The counters are
 // all that one call leaves to the next (zeros), and nothing lies elsewhere for
 // another shape.
 size_t attn_q4_ws_bytes(const moe_attn_batch_shape_t* s) {
-  return kPartAt + (2 + kMostWarps) * (size_t)kMostCtas * part_floats(s->D) * 4;
+  return kPartAt + (2 + kWarps) * (size_t)kMostCtas * part_floats(s->D) * 4;
 }
 
 cudaError_t launch_attn_q4(const moe_attn_batch_shape_t* s, AttnQ4Args a, uint8_t* ws, int nsm,
@@ -1003,13 +979,9 @@ cudaError_t launch_attn_q4(const moe_attn_batch_shape_t* s, AttnQ4Args a, uint8_
   a.tiles = row_tiles(s);
   a.pair_cost = kPairCost;
   const int ctas = nsm < kMostCtas ? nsm : kMostCtas;
-  const bool one = s->T * (s->n_q / s->n_kv) <= 8;
-  if (s->dtype == MOE_DTYPE_FP16) {
-    if (s->D == 64) return one ? launch<true, 64, 1>(a, ctas, stream) : launch<true, 64, 2>(a, ctas, stream);
-    return one ? launch<true, 128, 1>(a, ctas, stream) : launch<true, 128, 2>(a, ctas, stream);
-  }
-  if (s->D == 64) return one ? launch<false, 64, 1>(a, ctas, stream) : launch<false, 64, 2>(a, ctas, stream);
-  return one ? launch<false, 128, 1>(a, ctas, stream) : launch<false, 128, 2>(a, ctas, stream);
+  if (s->dtype == MOE_DTYPE_FP16)
+    return s->D == 64 ? launch_rows<true, 64>(a, ctas, stream) : launch_rows<true, 128>(a, ctas, stream);
+  return s->D == 64 ? launch_rows<false, 64>(a, ctas, stream) : launch_rows<false, 128>(a, ctas, stream);
 }
 
 }  // namespace moe

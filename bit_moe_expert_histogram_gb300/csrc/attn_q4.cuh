@@ -34,7 +34,7 @@ struct AttnQ4Args {
   uint16_t* o;        // [n_slots][T][n_q][D]
   float* part;        // [CTA][2]: what the CTA's ends cut
   float* pieces;      // [CTA][warp]: what a warp's start cuts, where shared memory has no room
-  unsigned* count;    // [CTA][16]: arrivals at a row of the pair that the CTA's end cuts
+  unsigned* count;    // [CTA][16]: arrivals at 32 items of the pair that the CTA's end cuts
   Ctrl* ctrl;
 };
 

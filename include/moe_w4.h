@@ -686,7 +686,7 @@ moe_status_t moe_cache_read_q4(const moe_cache_shape_t* shape, const moe_cache_m
  * past it does not matter. Deterministic. The workspace (256-byte aligned) is zero-filled once
  * (moe_workspace_init); after MOE_ERR_TIMEOUT, again. Calls of any shape can
  * use it in turn where it is large enough, but no other call of this library.
- * n_slots * n_kv * ceil(T * n_q / n_kv / 16) * (2 * max_blocks + 1) has to be
+ * n_slots * n_kv * ceil(T * n_q / n_kv / 16) * (max_blocks + 1) has to be
  * below 2^30. */
 size_t moe_attn_batch_q4_workspace_bytes(const moe_attn_batch_shape_t* shape);
 moe_status_t moe_attn_batch_q4(const moe_attn_batch_shape_t* shape, const void* q_dev,

@@ -72,7 +72,7 @@ def test_attention_refusals(lib):
     assert call(s=None) == m.MOE_ERR_UNSUPPORTED_SHAPE
     for bad in (dict(n_slots=0), dict(n_slots=4097), dict(T=0), dict(T=9), dict(n_q=15), dict(n_kv=0),
                 dict(D=96), dict(D=256), dict(block=32), dict(max_blocks=0), dict(prefix_blocks=1),
-                dict(dtype=2), dict(n_slots=4096, n_kv=16, max_blocks=1 << 13, T=1)):
+                dict(dtype=2), dict(n_slots=4096, n_kv=16, max_blocks=1 << 13, T=32)):
         t = m.AttnBatchShape(**{**ok, **bad})
         assert lib.moe_attn_batch_q4_workspace_bytes(C.byref(t)) == 0, bad
         assert call(s=t) == m.MOE_ERR_UNSUPPORTED_SHAPE, bad

@@ -11,29 +11,38 @@
 //
 // The k likeliest, ties to the lower id. Of the first chunk that a CTA reads
 // (16 bytes a thread and vector, held in registers) the k-th largest of the
-// maxima of 128 groups of threads is a number that at least k elements reach,
+// maxima of 64 groups of threads is a number that at least k elements reach,
 // and few do: those are listed, ordered by counting, and the k-th of them is
 // the bar for what follows, where only a larger number can still enter (an
-// equal one has a higher id). Chunks that bring more than the list holds
-// (sorted logits, or many equal ones) are taken up again from the registers:
-// first what is above the groups' bar, then, in id order, as many of its
-// equals as are missing; and where even that is too much, one by one.
+// equal one has a higher id). Where more reach the groups' bar than the list
+// holds (many equal logits), those above it are listed and then, in id order,
+// as many of its equals as are missing. After 2, 4, 8 .. chunks the list is put
+// in order and the bar raised, so that some k elements enter in between and
+// the CTA's warps need not meet at every chunk (meeting at each, with chunks
+// of twice the size, took 203 us for 2048 rows of 128001). If more enter than
+// the list holds (rising logits), the CTA's stretch is read again, once for
+// each of the k.
 //
-// Bound by HBM: a logit costs some five instructions and one exponential.
+// Bound by HBM: a logit costs some seven instructions, one of them an
+// exponential; pairs of fp32 numbers share what they can.
+#include <cfloat>
+
 #include "attn_batch.cuh"
 
 namespace moe {
 
 namespace {
-constexpr int kLThr = 512;
+constexpr int kLThr = 256;
+constexpr int kLCtas = 5;       // an SM
 constexpr int kLWarps = kLThr / 32;
 constexpr int kVec = 4;         // 16-byte vectors a thread and chunk
 constexpr int kCap = 1024;      // entries of the list
 constexpr int kMostTop = 32;
-constexpr int kMostParts = 512; // (row, stretch) pairs where rows are cut
+constexpr int kMostCuts = kCap / kMostTop;  // stretches of a row, whose entries one list holds
+constexpr int kMostParts = 1024;            // (row, stretch) pairs where rows are cut
 constexpr int kLGroups = kLThr / 4;
 constexpr size_t kLCountAt = 256, kLPartAt = kLCountAt + kMostParts * 4;
-constexpr int kLPart = 4 + 2 * kMostTop;  // floats of a part: m, Z, A, entries, values, ids
+constexpr int kLPart = 4 + 2 * kMostTop;  // floats of a part: m, Z, A, how many entries, those
 
 struct LogpArgs {
   const char* x;
@@ -53,7 +62,10 @@ template <int DT>
 struct El {
   static constexpr int kE = DT == MOE_DTYPE_FP32 ? 4 : 2;  // bytes
   static constexpr int kN = 16 / kE;                       // of a vector
+  static constexpr int kChunk = kLThr * kVec * kN;         // elements
+  // -inf, and the least finite number, as a word
   static constexpr uint32_t kNone = DT == MOE_DTYPE_FP32 ? 0xFF800000u : DT == MOE_DTYPE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+  static constexpr uint32_t kLeast = DT == MOE_DTYPE_FP32 ? 0xFF7FFFFFu : DT == MOE_DTYPE_BF16 ? 0xFF7FFF7Fu : 0xFBFFFBFFu;
 };
 template <int DT>
 __device__ __forceinline__ float el_at(const uint4& v, int i) {
@@ -62,16 +74,20 @@ __device__ __forceinline__ float el_at(const uint4& v, int i) {
   constexpr bool kF16 = DT == MOE_DTYPE_FP16;
   return i & 1 ? unpack_hi<kF16>(w[i / 2]) : unpack_lo<kF16>(w[i / 2]);
 }
-// the largest, of those that are numbers
 template <int DT>
-__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {  // NaN if either is
   uint32_t r;
   if (DT == MOE_DTYPE_FP32)
-    r = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    asm("max.NaN.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   else if (DT == MOE_DTYPE_BF16)
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   else
-    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 template <int DT>
@@ -82,7 +98,7 @@ __device__ __forceinline__ float max_of(const uint4 (&v)[kVec]) {
     w = max_word<DT>(w, max_word<DT>(max_word<DT>(v[j].x, v[j].y), max_word<DT>(v[j].z, v[j].w)));
   if (DT == MOE_DTYPE_FP32) return __uint_as_float(w);
   constexpr bool kF16 = DT == MOE_DTYPE_FP16;
-  return fmaxf(unpack_lo<kF16>(w), unpack_hi<kF16>(w));
+  return max_nan(unpack_lo<kF16>(w), unpack_hi<kF16>(w));
 }
 __device__ __forceinline__ uint4 load_stream(const void* p) {
   uint4 v;
@@ -91,59 +107,122 @@ __device__ __forceinline__ uint4 load_stream(const void* p) {
                : "l"(p));
   return v;
 }
-
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t both(float a) { return pair2(__float_as_uint(a), __float_as_uint(a)); }
 
 struct Sums {
   float m, Z, A;
 };
-__device__ __forceinline__ void raise(Sums& s, float m) {  // m >= s.m
-  if (m == s.m) return;
-  if (s.Z != 0.0f) {
-    const float d = s.m - m, f = expf(d);
-    s.A = (s.A + d * s.Z) * f;
-    s.Z *= f;
+// the same sums from another maximum, M >= s.m
+__device__ __forceinline__ Sums from(const Sums& s, float M) {
+  const float d = s.m - M, f = ex2(d * 1.4426950408889634f);
+  // nothing so far: no inf * 0
+  return s.Z == 0.0f ? Sums{M, 0.0f, 0.0f} : Sums{M, s.Z * f, fmaf(d, s.Z, s.A) * f};
+}
+// the sums of `n` lanes (a power of two), by each of them
+__device__ __forceinline__ Sums join(const Sums& s, int n) {
+  float M = s.m;
+  for (int o = n / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  Sums r = from(s, M);
+  for (int o = n / 2; o > 0; o >>= 1) {
+    r.Z += __shfl_xor_sync(0xFFFFFFFFu, r.Z, o);
+    r.A += __shfl_xor_sync(0xFFFFFFFFu, r.A, o);
   }
-  s.m = m;
+  return r;
 }
-__device__ __forceinline__ void join(Sums& a, Sums b) {
-  const float m = fmaxf(a.m, b.m);
-  raise(a, m);
-  raise(b, m);
-  a.Z += b.Z;
-  a.A += b.A;
+// the least fp32 number above x (x is not NaN or +inf)
+__device__ __forceinline__ float next_up(float x) {
+  const int u = __float_as_int(x);
+  return x == 0.0f ? __int_as_float(1) : __int_as_float(u + (u < 0 ? -1 : 1));
+}
+// adds a thread's vectors, whose largest element is `top`, to its sums
+template <int DT>
+__device__ __forceinline__ void add_chunk(Sums& s, const uint4 (&v)[kVec], float top) {
+  if (top > s.m) s = from(s, top);
+  if (top != top) s.Z = top;
+  if (s.m < (DT == MOE_DTYPE_FP16 ? -65000.0f : -1e38f)) {
+    // nothing but -inf, or what a mask of the least number leaves, which weighs
+    // something beside nothing else: -inf is told from it
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+#pragma unroll
+      for (int i = 0; i < El<DT>::kN; ++i) {
+        const float x = el_at<DT>(v[j], i);
+        if (x == -INFINITY) continue;
+        const float d = fmaxf(x - s.m, -200.0f), e = ex2(d * 1.4426950408889634f);
+        s.Z += e;
+        s.A = fmaf(e, d, s.A);
+      }
+    return;
+  }
+  uint64_t Z = pair2(__float_as_uint(s.Z), 0u), A = pair2(__float_as_uint(s.A), 0u);
+  const uint64_t nm = both(-s.m), l2 = both(1.4426950408889634f);
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) {
+    const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+    for (int i = 0; i < El<DT>::kN / 2; ++i) {
+      // -inf as the least finite number: its weight is 0, and 0 times d, too
+      uint64_t x;
+      if (DT == MOE_DTYPE_FP32) {
+        x = pair2(max_word<DT>(w[2 * (i & 1)], El<DT>::kLeast), max_word<DT>(w[2 * (i & 1) + 1], El<DT>::kLeast));
+      } else {
+        const uint32_t c = max_word<DT>(w[i & 3], El<DT>::kLeast);
+        x = pair2(__float_as_uint(unpack_lo<DT == MOE_DTYPE_FP16>(c)), __float_as_uint(unpack_hi<DT == MOE_DTYPE_FP16>(c)));
+      }
+      const uint64_t d = add2(x, nm);
+      float y0, y1;
+      unpair2(mul2(d, l2), y0, y1);
+      const uint64_t e = pair2(__float_as_uint(ex2(y0)), __float_as_uint(ex2(y1)));
+      Z = add2(Z, e);
+      A = fma2(e, d, A);
+    }
+  }
+  float z0, z1, a0, a1;
+  unpair2(Z, z0, z1);
+  unpair2(A, a0, a1);
+  s.Z = z0 + z1;
+  s.A = a0 + a1;
 }
 
-struct Entry {
-  float v;
-  int id;
-};
-__device__ __forceinline__ bool before(const Entry& a, const Entry& b) {
-  return a.v > b.v || (a.v == b.v && a.id < b.id);
+// An entry as a whole number that is larger the earlier it comes: the logit in
+// an order-keeping form (-0 is 0), below it the id, lower ones larger. 0: none.
+// (Two comparisons with a branch between them took 42 ns an entry compared.)
+__device__ __forceinline__ uint64_t entry(float x, int id) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return (uint64_t)(u & 0x80000000u ? ~u : u | 0x80000000u) << 32 | (uint32_t)~id;
 }
-
-// The first k of n entries (n <= kCap) in order, in place: each entry's rank
-// is the number of those before it. Called by the whole CTA; returns how many
-// there are.
+__device__ __forceinline__ int entry_id(uint64_t e) { return (int)~(uint32_t)e; }
+__device__ __forceinline__ float entry_x(uint64_t e) {
+  const uint32_t u = (uint32_t)(e >> 32);
+  return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
 struct TopList {
-  Entry e[kCap];
-  Entry best[kMostTop];
+  uint64_t e[kCap];
+  uint64_t best[kMostTop];
   int n;
 };
-__device__ __forceinline__ int keep_best(TopList& t, int n, int k) {
-  __syncthreads();
+// how many of n entries are before this one
+__device__ __forceinline__ int rank_of(const TopList& t, int n, uint64_t x) {
+  int rank = 0;
+#pragma unroll 8
+  for (int j = 0; j < n; ++j) rank += t.e[j] > x;
+  return rank;
+}
+// Puts the first k of the list's entries in order, in place. By the whole CTA,
+// which has met since the last entry came; returns how many there are.
+__device__ __forceinline__ int keep_best(TopList& t, int k) {
+  const int n = t.n, m = n < k ? n : k;
   for (int i = threadIdx.x; i < n; i += kLThr) {
-    const Entry x = t.e[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += before(t.e[j], x);
+    const uint64_t x = t.e[i];
+    const int rank = rank_of(t, n, x);
     if (rank < k) t.best[rank] = x;
   }
   __syncthreads();
-  const int m = n < k ? n : k;
   if ((int)threadIdx.x < m) t.e[threadIdx.x] = t.best[threadIdx.x];
   if (threadIdx.x == 0) t.n = m;
   __syncthreads();
@@ -152,14 +231,15 @@ __device__ __forceinline__ int keep_best(TopList& t, int n, int k) {
 }  // namespace
 
 template <int DT, bool TOP>
-__global__ void __launch_bounds__(kLThr, 2) logprobs_kernel(const LogpArgs a) {
+__global__ void __launch_bounds__(kLThr, kLCtas) logprobs_kernel(const LogpArgs a) {
   using E = El<DT>;
   __shared__ TopList list;
-  __shared__ float s_group[kLGroups];
+  __shared__ __align__(16) float s_group[kLGroups];
   __shared__ float s_bar, s_w[3][kLWarps];
   __shared__ int s_scan[kLWarps], s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / a.S, cut = blockIdx.x - row * a.S;
+  if (TOP && tid == 0) list.n = 0;
   pdl_wait();
   pdl_trigger();
   const char* x0 = a.x + (int64_t)row * a.stride;
@@ -171,15 +251,20 @@ __global__ void __launch_bounds__(kLThr, 2) logprobs_kernel(const LogpArgs a) {
   // vectors lie on 16-byte borders; elements before the row's first and past
   // its last are left out
   const int shift = (int)(reinterpret_cast<uintptr_t>(x0) & 15u) / E::kE;
-  const char* base = x0 - shift * E::kE;
   const int n_vec = (a.V + shift + E::kN - 1) / E::kN;
   auto first_of = [&](int chunk, int j) { return ((chunk * kVec + j) * kLThr + tid) * E::kN - shift; };
   auto load = [&](int chunk, uint4 (&v)[kVec]) {
+    const char* p = x0 + (int64_t)first_of(chunk, 0) * E::kE;
+    if (chunk * E::kChunk >= shift && (chunk + 1) * E::kChunk - shift <= a.V) {  // all of it inside
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[j] = load_stream(p + j * (kLThr * 16));
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       const int e0 = first_of(chunk, j);
       if (e0 >= 0 && e0 + E::kN <= a.V) {
-        v[j] = load_stream(x0 + (int64_t)e0 * E::kE);
+        v[j] = load_stream(p + j * (kLThr * 16));
         continue;
       }
       uint32_t w[4] = {E::kNone, E::kNone, E::kNone, E::kNone};
@@ -188,7 +273,7 @@ __global__ void __launch_bounds__(kLThr, 2) logprobs_kernel(const LogpArgs a) {
         for (int i = 0; i < E::kN; ++i) {
           if (e0 + i < 0 || e0 + i >= a.V) continue;
           if (DT == MOE_DTYPE_FP32) {
-            w[i] = __ldg(reinterpret_cast<const uint32_t*>(x0) + e0 + i);
+            w[i & 3] = __ldg(reinterpret_cast<const uint32_t*>(x0) + e0 + i);
           } else {
             const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(x0) + e0 + i);
             w[i / 2] = i & 1 ? (w[i / 2] & 0xFFFFu) | h << 16 : (w[i / 2] & 0xFFFF0000u) | h;
@@ -198,190 +283,191 @@ __global__ void __launch_bounds__(kLThr, 2) logprobs_kernel(const LogpArgs a) {
       v[j] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   };
-  const int c0 = cut * a.per, c1 = min(c0 + a.per, (n_vec + kLThr * kVec - 1) / (kLThr * kVec));
+  auto element = [&](int id) {
+    if (DT == MOE_DTYPE_FP32) return __ldg(reinterpret_cast<const float*>(x0) + id);
+    return unpack_lo<DT == MOE_DTYPE_FP16>(__ldg(reinterpret_cast<const uint16_t*>(x0) + id));
+  };
+  constexpr int kChunkVecs = kLThr * kVec;
+  const int c0 = cut * a.per, c1 = min(c0 + a.per, (n_vec + kChunkVecs - 1) / kChunkVecs);
   Sums s{-INFINITY, 0.0f, 0.0f};
-  float bar = -INFINITY;  // what a further element has to be above
-  int n_list = 0;         // entries of the list at the last count
-  bool full = false;      // k of them are known: the bar holds for what follows
-  if (TOP && tid == 0) list.n = 0;
-  if (TOP) __syncthreads();
-  uint4 v[kVec], nv[kVec];
+  float bar = -FLT_MAX;   // what a further element has to reach
+  bool over = false;      // more came than the list holds
+  uint4 v[kVec];
   if (c0 < c1) load(c0, v);
   for (int c = c0; c < c1; ++c) {
-    if (c + 1 < c1) load(c + 1, nv);
     const float top = max_of<DT>(v);
-    if (top > s.m) raise(s, top);
-    if (s.m > -INFINITY) {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-#pragma unroll
-        for (int i = 0; i < E::kN; ++i) {
-          // e^-200 is 0, and 0 times it, too, where x is -inf
-          const float d = max_nan(el_at<DT>(v[j], i) - s.m, -200.0f);
-          const float e = ex2(d * 1.4426950408889634f);
-          s.Z += e;
-          s.A = fmaf(e, d, s.A);
-        }
-    }
-    if (TOP) {
-      // lists what `want` takes; the place of this thread's last one, or -1
-      auto push = [&](auto want) {
-        int at = -1;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-#pragma unroll
-          for (int i = 0; i < E::kN; ++i) {
-            const float x = el_at<DT>(v[j], i);
-            if (!want(x)) continue;
-            at = atomicAdd(&list.n, 1);
-            if (at < kCap) list.e[at] = Entry{x, first_of(c, j) + i};
-          }
-        return at;
-      };
-      bool over = !full;
-      if (full) {
-        int at = -1;
-        if (top > bar) at = push([&](float x) { return x > bar; });
-        if (__syncthreads_or(at >= kCap / 2)) {
-          over = __syncthreads_or(at >= kCap);
-          if (over) {  // only what was there before this chunk is whole
-            const int begin = c * kVec * kLThr * E::kN - shift;
-            for (int i = tid; i < kCap; i += kLThr)
-              if (list.e[i].id >= begin) list.e[i].v = -INFINITY;
-          }
-          n_list = keep_best(list, over ? kCap : list.n, a.k);
-          bar = list.e[a.k - 1].v;
-        }
-      }
-      if (over) {
-        // the bar that at least k of this chunk reach
+    add_chunk<DT>(s, v, top);
+    if (!TOP) {
+      if (c + 1 < c1) load(c + 1, v);
+    } else {
+      const bool begin = c == c0;
+      float low = -INFINITY;
+      if (begin) {
+        // the number that at least k of this chunk reach, NaN aside: of the 64
+        // groups' maxima the k-th, each group ranked by its four threads
         float g = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 2));
-        if ((tid & 3) == 0) s_group[tid >> 2] = g;
-        if (tid == 0) {
-          s_bar = -INFINITY;
-          list.n = n_list;
-        }
+        g = g != g ? -INFINITY : g;
+        const int mine = tid >> 2, q = tid & 3;
+        if (q == 0) s_group[mine] = g;
+        if (tid == 0) s_bar = -INFINITY;
         __syncthreads();
-        if (tid < kLGroups) {
-          const float mine = s_group[tid];
-          int rank = 0;
-          for (int j = 0; j < kLGroups; ++j)
-            rank += s_group[j] > mine || (s_group[j] == mine && j < tid);
-          if (rank == a.k - 1) s_bar = mine;
+        int rank = 0;
+#pragma unroll
+        for (int j = 4 * q; j < kLGroups; j += 16) {
+          const float4 o = *reinterpret_cast<const float4*>(s_group + j);
+          rank += (o.x > g || (o.x == g && j < mine)) + (o.y > g || (o.y == g && j + 1 < mine)) +
+                  (o.z > g || (o.z == g && j + 2 < mine)) + (o.w > g || (o.w == g && j + 3 < mine));
         }
+        rank += __shfl_xor_sync(0xFFFFFFFFu, rank, 1);
+        rank += __shfl_xor_sync(0xFFFFFFFFu, rank, 2);
+        if (q == 0 && rank == a.k - 1) s_bar = g;
         __syncthreads();
-        // equals of an earlier chunk's bar have lower ids
-        const float low = fmaxf(s_bar, bar);
-        const bool strict = full && low == bar;
-        auto above = [&](float x) { return x > low; };
-        auto reach = [&](float x) { return x >= low && x > -INFINITY; };
-        int at = -1;
-        if (strict ? top > low : top >= low) at = strict ? push(above) : push(reach);
-        if (__syncthreads_or(at >= kCap)) {
-          // too many: those above the bar, then the first of its equals
-          if (tid == 0) list.n = n_list;
-          __syncthreads();
-          at = top > low ? push(above) : -1;
-          if (__syncthreads_or(at >= kCap)) {
-            // still too many: the best k one after the other
-            if (tid == 0) list.n = n_list;
-            Entry last{INFINITY, -1};
-            for (int r = 0; r < a.k; ++r) {
-              Entry mine{-INFINITY, 0x7FFFFFFF};
+        low = s_bar;
+        bar = fmaxf(low, -FLT_MAX);
+      }
+      const int seen = c - c0 + 1;
+      const bool meet = begin || ((seen & (seen - 1)) == 0 && c + 1 < c1);  // the list is put in order
+      bool equals = false;
+#pragma unroll 1
+      for (;;) {
+        // which of the thread's elements reach the bar (few threads have one),
+        // then the next chunk's loads, then those elements from memory
+        uint32_t mask = 0;
+        if (!(top < bar)) {
 #pragma unroll
-              for (int j = 0; j < kVec; ++j)
+          for (int j = 0; j < kVec; ++j)
 #pragma unroll
-                for (int i = 0; i < E::kN; ++i) {
-                  const Entry x{el_at<DT>(v[j], i), first_of(c, j) + i};
-                  if (before(last, x) && before(x, mine)) mine = x;
-                }
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) {
-                const Entry y{__shfl_xor_sync(0xFFFFFFFFu, mine.v, o), __shfl_xor_sync(0xFFFFFFFFu, mine.id, o)};
-                if (before(y, mine)) mine = y;
-              }
-              __syncthreads();
-              if (lane == 0) list.best[warp] = mine;
-              __syncthreads();
-              last = list.best[0];
-              for (int w = 1; w < kLWarps; ++w)
-                if (before(list.best[w], last)) last = list.best[w];
-              if (tid == 0 && last.v > -INFINITY) list.e[list.n++] = last;
-            }
-          } else if (!strict && list.n - n_list < a.k && low > -INFINITY) {
-            int need = a.k - (list.n - n_list), have = list.n;  // the same for all
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-              int n = 0;
-#pragma unroll
-              for (int i = 0; i < E::kN; ++i) n += el_at<DT>(v[j], i) == low;
-              int incl = n;
-#pragma unroll
-              for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if (lane >= o) incl += y;
-              }
-              __syncthreads();
-              if (lane == 31) s_scan[warp] = incl;
-              __syncthreads();
-              int all = 0, start = incl - n;
-              for (int w = 0; w < kLWarps; ++w) {
-                if (w < warp) start += s_scan[w];
-                all += s_scan[w];
-              }
-#pragma unroll
-              for (int i = 0; i < E::kN; ++i)
-                if (el_at<DT>(v[j], i) == low) {
-                  if (start < need) list.e[have + start] = Entry{low, first_of(c, j) + i};
-                  ++start;
-                }
-              const int took = min(all, need);
-              have += took;
-              need -= took;
-            }
-            __syncthreads();
-            if (tid == 0) list.n = have;
+            for (int i = 0; i < E::kN; ++i) mask |= el_at<DT>(v[j], i) >= bar ? 1u << (j * E::kN + i) : 0u;
+        }
+        if (c + 1 < c1) load(c + 1, v);
+        {
+#pragma unroll 1
+          for (; mask; mask &= mask - 1) {
+            const int b = __ffs(mask) - 1, id = first_of(c, b / E::kN) + b % E::kN;
+            const int at = atomicAdd(&list.n, 1);
+            if (at < kCap) list.e[at] = entry(element(id), id);
           }
         }
+        if (!meet || over) break;
         __syncthreads();
-        n_list = keep_best(list, list.n, a.k);
-        full = n_list == a.k;
-        bar = full ? list.e[a.k - 1].v : -INFINITY;
+        if (list.n <= kCap) break;
+        // too many: of the first chunk those above the groups' bar and then the
+        // first of its equals, once
+        over = !begin || equals;
+        equals = true;
+        __syncthreads();
+        if (over) break;
+        if (tid == 0) list.n = 0;
+        bar = next_up(low);
+        load(c, v);
+        __syncthreads();
       }
-    }
+      if (equals && !over && low > -INFINITY) {
+        load(c, v);
+        int have = list.n, need = have < a.k ? a.k - have : 0;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) v[j] = nv[j];
+        for (int j = 0; j < kVec; ++j) {
+          if (need == 0) break;  // the same for all
+          int n = 0;
+#pragma unroll
+          for (int i = 0; i < E::kN; ++i) n += el_at<DT>(v[j], i) == low;
+          int incl = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += y;
+          }
+          __syncthreads();
+          if (lane == 31) s_scan[warp] = incl;
+          __syncthreads();
+          int all = 0, start = incl - n;
+          for (int w = 0; w < kLWarps; ++w) {
+            if (w < warp) start += s_scan[w];
+            all += s_scan[w];
+          }
+#pragma unroll
+          for (int i = 0; i < E::kN; ++i)
+            if (el_at<DT>(v[j], i) == low) {
+              if (start < need) list.e[have + start] = entry(low, first_of(c, j) + i);
+              ++start;
+            }
+          const int took = min(all, need);
+          have += took;
+          need -= took;
+        }
+        __syncthreads();
+        if (tid == 0) list.n = have;
+        __syncthreads();
+        if (c + 1 < c1) load(c + 1, v);
+      }
+      if (over)
+        bar = INFINITY;
+      else if (meet && c + 1 < c1)
+        // equals of the k-th have higher ids from here on
+        bar = keep_best(list, a.k) == a.k ? next_up(entry_x(list.e[a.k - 1])) : -FLT_MAX;
+    }
   }
   if (TOP) {
     __syncthreads();
-    n_list = keep_best(list, list.n, a.k);
+    over |= list.n > kCap;
+    if (over) {
+      // the best k one after the other, each found by reading the stretch again
+      __syncthreads();
+      if (tid == 0) list.n = 0;
+      uint64_t last = ~0ull;
+      for (int r = 0; r < a.k; ++r) {
+        uint64_t mine = 0;
+        for (int c = c0; c < c1; ++c) {
+          load(c, v);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j)
+#pragma unroll
+            for (int i = 0; i < E::kN; ++i) {
+              const float x = el_at<DT>(v[j], i);
+              const uint64_t e = x > -INFINITY ? entry(x, first_of(c, j) + i) : 0;
+              if (e < last && e > mine) mine = e;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const uint64_t y = __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+          mine = y > mine ? y : mine;
+        }
+        __syncthreads();
+        if (lane == 0) list.best[warp] = mine;
+        __syncthreads();
+        last = 0;
+        for (int w = 0; w < kLWarps; ++w) last = list.best[w] > last ? list.best[w] : last;
+        if (tid == 0 && last != 0) list.e[list.n++] = last;
+      }
+    }
   }
   // ---- the CTA's sums, in a fixed order
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    join(s, Sums{__shfl_xor_sync(0xFFFFFFFFu, s.m, o), __shfl_xor_sync(0xFFFFFFFFu, s.Z, o),
-                 __shfl_xor_sync(0xFFFFFFFFu, s.A, o)});
+  s = join(s, 32);
   if (lane == 0) {
     s_w[0][warp] = s.m;
     s_w[1][warp] = s.Z;
     s_w[2][warp] = s.A;
   }
   __syncthreads();
-  s = Sums{s_w[0][0], s_w[1][0], s_w[2][0]};
-  for (int w = 1; w < kLWarps; ++w) join(s, Sums{s_w[0][w], s_w[1][w], s_w[2][w]});
+  s = Sums{s_w[0][lane % kLWarps], s_w[1][lane % kLWarps], s_w[2][lane % kLWarps]};
+  s = join(s, kLWarps);
   if (a.S > 1) {
     float* part = a.part + (int64_t)blockIdx.x * kLPart;
     if (tid == 0) {
       part[0] = s.m;
       part[1] = s.Z;
       part[2] = s.A;
-      part[3] = __int_as_float(n_list);
+      part[3] = __int_as_float(TOP ? min(list.n, a.k) : 0);
     }
-    if (tid < n_list) {
-      part[4 + tid] = list.e[tid].v;
-      part[4 + kMostTop + tid] = __int_as_float(list.e[tid].id);
+    if (TOP) {
+      const int n = list.n;
+      for (int i = tid; i < n; i += kLThr) {
+        const uint64_t x = list.e[i];
+        const int rank = rank_of(list, n, x);
+        if (rank < a.k) reinterpret_cast<uint64_t*>(part + 4)[rank] = x;
+      }
     }
     __threadfence();
     __syncthreads();
@@ -400,23 +486,16 @@ __global__ void __launch_bounds__(kLThr, 2) logprobs_kernel(const LogpArgs a) {
       const float* p = parts + lane * kLPart;
       s = Sums{__ldcg(p), __ldcg(p + 1), __ldcg(p + 2)};
     }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-      join(s, Sums{__shfl_xor_sync(0xFFFFFFFFu, s.m, o), __shfl_xor_sync(0xFFFFFFFFu, s.Z, o),
-                   __shfl_xor_sync(0xFFFFFFFFu, s.A, o)});
     if (TOP) {
       for (int i = tid; i < a.S * kMostTop; i += kLThr) {
         const float* p = parts + i / kMostTop * kLPart;
         const int j = i % kMostTop;
-        const float x = __ldcg(p + 4 + j), id = __ldcg(p + 4 + kMostTop + j);
-        if (j < __float_as_int(__ldcg(p + 3)))
-          list.e[atomicAdd(&list.n, 1)] = Entry{x, __float_as_int(id)};
+        const uint64_t x = __ldcg(reinterpret_cast<const unsigned long long*>(p + 4) + j);
+        if (j < __float_as_int(__ldcg(p + 3))) list.e[atomicAdd(&list.n, 1)] = x;
       }
     }
-    if (TOP) {
-      __syncthreads();
-      n_list = keep_best(list, list.n, a.k);
-    }
+    s = join(s, 32);
+    __syncthreads();
   }
   // nothing but -inf, or a number that is none: no distribution
   const bool ok = s.m > -INFINITY && s.m < INFINITY && s.Z > 0.0f && s.Z < INFINITY;
@@ -433,11 +512,19 @@ __global__ void __launch_bounds__(kLThr, 2) logprobs_kernel(const LogpArgs a) {
     a.logp[row] = r;
     if (a.entropy) a.entropy[row] = ok ? lz - s.A / s.Z : nan;
   }
-  if (TOP && tid < a.k) {
-    const bool here = ok && tid < n_list;
-    const int64_t at = (int64_t)row * a.k + tid;
-    if (a.top_ids) a.top_ids[at] = here ? list.e[tid].id : -1;
-    if (a.top_logp) a.top_logp[at] = here ? (list.e[tid].v - s.m) - lz : -INFINITY;
+  if (TOP) {
+    const int n = list.n;
+    auto put = [&](int rank, int id, float v) {
+      const int64_t at = (int64_t)row * a.k + rank;
+      if (a.top_ids) a.top_ids[at] = id;
+      if (a.top_logp) a.top_logp[at] = v;
+    };
+    for (int i = tid; i < n; i += kLThr) {
+      const uint64_t x = list.e[i];
+      const int rank = rank_of(list, n, x);
+      if (rank < a.k) put(rank, ok ? entry_id(x) : -1, ok ? (entry_x(x) - s.m) - lz : -INFINITY);
+    }
+    if (tid >= n && tid < a.k) put(tid, -1, -INFINITY);  // missing
   }
 }
 
@@ -471,10 +558,10 @@ cudaError_t launch_logprobs(const moe_logprobs_shape_t* s, const void* logits, i
   const bool even = (reinterpret_cast<uintptr_t>(logits) & 15u) == 0 && a.stride % 16 == 0;
   const int vecs = (s->V * e + 15) / 16 + (even ? 0 : 1), chunk = kLThr * kVec;
   const int chunks = (vecs + chunk - 1) / chunk;
-  // rows are cut where there are fewer than CTAs that fit at once, two an SM
-  int most = 2 * nsm < kMostParts ? 2 * nsm : kMostParts;
+  // rows are cut where there are fewer than CTAs that fit at once
+  int most = kLCtas * nsm < kMostParts ? kLCtas * nsm : kMostParts;
   most /= s->n_rows;
-  if (most > kCap / kMostTop) most = kCap / kMostTop;  // whose entries one list holds
+  if (most > kMostCuts) most = kMostCuts;
   const int cuts = most < 1 ? 1 : most < chunks ? most : chunks;
   a.per = (chunks + cuts - 1) / cuts;
   a.S = (chunks + a.per - 1) / a.per;

@@ -7,11 +7,17 @@
 // a code stands for s * code + b. Rounding b down keeps every x - b >= 0, so
 // that the 16 codes cover the whole group; it is exact for bf16 rows.
 //
-// Codes and scales are decided as the formulas say, not as roundings fall:
-// fp32 finds the code, and where it comes within its own error of a border
-// (2^-16 of a step, once in some ten thousand elements) the sign of
-// x - b - (c + 1/2) s is taken without error. Two machines, or this kernel and
-// a reference in 64 bits, so write the same cache.
+// Codes and scales are decided as the formulas say, not as roundings fall, so
+// two machines, or this kernel and a reference in 64 bits, write the same cache.
+// (x - b) / s meets borders c + 1/2 exactly quite often, as 16-bit numbers have
+// few digits. But what is not on a border is not near it either: x - b and
+// (c + 1/2) s are multiples of q, the least of x's, b's and s / 2's last places,
+// so that the quotient misses by q / s, which is 2^-16 or more unless x or b is
+// tiny beside s. So fp32 with a factor of 1 + 2^-21 (+-2^-22, all roundings
+// counted) takes every border upwards and nothing else: the quotient below 15.1
+// moves by less than 2^-16.4. A tiny x lies next to -b / s; where that is next to
+// a border, or b is tiny, or s so small that its reciprocal is not a normal
+// number, each code is taken from the sign of x - b - (c + 1/2) s without error.
 //
 // Layout of a row, 16-bit units: D / 4 units of codes, s[4], b[4]: 80 bytes
 // for D = 128, 48 for D = 64. Element e's code is nibble e % 2 of byte e / 2;
@@ -20,6 +26,11 @@
 // matrix products then has one scale whatever D is. Rows of 80 and 48 bytes
 // also spread over the shared-memory banks as they are (eight rows' 16-byte
 // pieces never meet in one), so pages are copied as they lie.
+//
+// Bound: both by HBM. A thread has sixteen elements of a row, whose group it
+// shares with one other (D = 128) or has alone, so that a row's bookkeeping and
+// a group's scale are paid once for as many; fp32 pairs share instructions, no
+// element branches, and nothing divides.
 #include "attn_q4.cuh"
 
 namespace moe {
@@ -27,7 +38,7 @@ namespace moe {
 namespace {
 constexpr int kPage = 64;  // positions per page
 constexpr int kThr = 256;
-constexpr int kRows = 4;   // rows a thread has a piece of
+constexpr int kRows = 2;   // rows a thread has a piece of
 
 template <bool F16>
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // NaN if either is
@@ -47,14 +58,7 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-template <bool F16>
-__device__ __forceinline__ float lo_of(uint32_t v) {
-  return F16 ? half_bits_to_float(v & 0xFFFFu) : bf_lo(v);
-}
-template <bool F16>
-__device__ __forceinline__ float hi_of(uint32_t v) {
-  return F16 ? half_bits_to_float(v >> 16) : bf_hi(v);
-}
+__device__ __forceinline__ uint64_t both(float a) { return pair2(__float_as_uint(a), __float_as_uint(a)); }
 // what a - b leaves over, a - b = d + rest, d = fl(a - b)
 __device__ __forceinline__ float sub_rest(float a, float b, float d) {
   const float z = __fsub_rn(d, a);
@@ -66,93 +70,145 @@ __device__ __forceinline__ uint32_t floor_bf16(float v) {
   if (v != v) return 0x7FC0u;
   return (v < 0.0f ? u + 0xFFFFu : u) >> 16;
 }
-// bits of the bf16 number nearest to (hi - b) / 15, ties to even. The fp32
-// quotient can only be wrong about the side of a midpoint by being one (a
-// midpoint and its multiple by 15 are fp32 numbers, and rounding keeps order).
+// Bits of the bf16 number nearest to (hi - b) / 15, ties to even. An fp32
+// product with 1/15 is off by less than two of its last places; near a midpoint
+// of bf16 numbers the sign of hi - b - 15 midpoint says it without error.
 __device__ __forceinline__ uint32_t scale_bits(float hi, float b) {
-  const float d = __fsub_rn(hi, b), q = __fdiv_rn(d, 15.0f);
+  const float d = __fsub_rn(hi, b), q = d * (1.0f / 15.0f);
   const uint32_t u = __float_as_uint(q), low = u & 0xFFFFu;
   if (q != q) return 0x7FC0u;
-  bool up = low > 0x8000u;
-  if (low == 0x8000u) {
-    const float over = __fadd_rn(fmaf(-15.0f, q, d), sub_rest(hi, b, d));
-    up = over > 0.0f || (over == 0.0f && (u & 0x10000u));
+  uint32_t r = u + 0x8000u;  // no ties away from a midpoint
+  if (low - 0x7FF8u <= 16u) {
+    const uint32_t at = (u & 0xFFFF0000u) | 0x8000u;
+    const float mid = __uint_as_float(at);
+    // 15 mid has 13 bits; what it leaves of d is exact, as d is next to it
+    const float over = __fadd_rn(fmaf(-15.0f, mid, d), sub_rest(hi, b, d));
+    const bool up = over > 0.0f || (over == 0.0f && (at & 0x10000u));
+    r = at + (up ? 0x8000u : 0u);
   }
-  return (u >> 16) + up;
+  return r >> 16;
 }
 
-// the code of x where fp32 cannot tell: the border next to x is (c + 1/2) s
-__device__ __noinline__ uint32_t code_exact(float x, float b, float s, float f) {
-  const float c = floorf(f);
+// the code of x: the borders around f are (c + 1/2) s
+__device__ __forceinline__ uint32_t code_exact(float x, float b, float s, float f) {
+  const float c = floorf(fminf(f, 15.0f));
   if (!(c >= 0.0f) || c >= 15.0f) return c >= 15.0f ? 15u : 0u;
   const float d = __fsub_rn(x, b);
   // (c + 1/2) s has 13 bits, and d is next to it: both steps are exact
   const float over = __fadd_rn(__fsub_rn(d, __fmul_rn(c + 0.5f, s)), sub_rest(x, b, d));
   return (uint32_t)c + (over >= 0.0f);
 }
-// eight elements' codes, the first in the lowest bits
 template <bool F16>
-__device__ __forceinline__ uint32_t codes8(const uint4& v, float b, float s) {
-  if (!(s > 0.0f)) return 0u;
-  // 1 / s is a normal number from 2^-126 to 2^126; smaller scales (bf16 has
-  // seven binades of them) go through 2^20 s
+__device__ __noinline__ uint32_t codes_exact(uint4 v, float b, float s) {
+  // 1 / s is a normal number down to 2^-126; smaller scales (bf16 has seven
+  // binades of them) go through 2^20 s
   const float up = s < 0x1p-120f ? 0x1p20f : 1.0f, inv = 1.0f / (s * up);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t r = 0;
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < 8; ++i) {
-    const float x = i & 1 ? hi_of<F16>(w[i / 2]) : lo_of<F16>(w[i / 2]);
-    const float f = fminf((x - b) * up * inv, 15.0f);
-    const float t = f + 0x1.8p23f;  // the nearest whole number in the low bits
-    uint32_t c = __float_as_uint(t) & 15u;
-    // f is off by less than 2^-18 (three roundings of 2^-24 below 16)
-    if (fabsf(f - (t - 0x1.8p23f)) > 0.5f - 0x1p-16f) c = code_exact(x, b, s, f);
-    r |= c << (4 * i);
+    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    const float x = i & 1 ? unpack_hi<F16>(w) : unpack_lo<F16>(w);
+    r |= code_exact(x, b, s, (x - b) * up * inv) << (4 * i);
   }
   return r;
 }
+// Eight elements' codes, the first in the lowest bits; up = (1 + 2^-21) / s.
+template <bool F16>
+__device__ __forceinline__ uint32_t codes8(const uint4& v, float b, float up) {
+  const uint64_t nb = both(-b), f2 = both(up), magic = both(0x1.8p23f);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  // 1.5 2^23 + c is 0x4B400000 + c: of the sum of 16^i times that, the constant
+  uint32_t r = 0u - 0x3F400000u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t x = pair2(__float_as_uint(unpack_lo<F16>(w[i])), __float_as_uint(unpack_hi<F16>(w[i])));
+    const uint64_t c = fma2(add2(x, nb), f2, magic);
+    r += (uint32_t)c << (8 * i);
+    r += (uint32_t)(c >> 32) << (8 * i + 4);
+  }
+  return r;
+}
+// Whether the codes of these elements want codes_exact. tiny: below how many s
+// an x has a last place below 2^-16 s.
+template <bool F16>
+__device__ __forceinline__ bool in_doubt(const uint4 (&v)[2], float b, float s, float up) {
+  constexpr float kTiny = F16 ? 0x1p-5f : 0x1p-8f;
+  const float fb = fabsf(b) * up + 0.5f;  // a whole number on a border
+  const bool border = fabsf(fb - rintf(fb)) < kTiny + 0x1p-14f;
+  if (!border && fabsf(b) >= s * kTiny && s >= 0x1p-120f) return false;
+  if (s < 0x1p-120f || (b != 0.0f && fabsf(b) < s * kTiny)) return true;
+  bool found = false;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x0 = fabsf(unpack_lo<F16>(w[i])), x1 = fabsf(unpack_hi<F16>(w[i]));
+      found |= (x0 > 0.0f && x0 < s * kTiny) || (x1 > 0.0f && x1 < s * kTiny);
+    }
+  }
+  return border && found;
+}
+
+// Where a call's rows lie: a CTA has 2^log_t tokens of some slots a pass, and
+// its passes go on along the tokens (chunks > 0: how many CTAs a slot has) or
+// along the slots.
+struct RowsPlan {
+  int log_t, chunks;
+};
+template <int D>
+struct RowOf {
+  int s, t;
+};
+template <int D>
+__device__ __forceinline__ RowOf<D> row_of(const RowsPlan& p, int k) {
+  constexpr int kStep = kThr / (D / 16);  // rows of a pass
+  const int r = threadIdx.x / (D / 16), t = r & ((1 << p.log_t) - 1);
+  if (p.chunks > 0) {
+    const int s = blockIdx.x / (unsigned)p.chunks;
+    return RowOf<D>{s, ((int)blockIdx.x - s * p.chunks) * (kStep * kRows) + k * kStep + t};
+  }
+  return RowOf<D>{(((int)blockIdx.x * kRows + k) * kStep + r) >> p.log_t, t};
+}
 }  // namespace
 
-// A thread has eight elements of kRows rows: of tokens one after the other, of
-// one head and tensor (blockIdx.y), so that a CTA reads whole lines and writes
-// a stretch of a page.
+// A thread has sixteen elements of kRows rows of one head and tensor
+// (blockIdx.y), a CTA tokens one after the other: it reads whole lines and
+// writes a stretch of a page.
 template <bool F16, int D>
 __global__ void __launch_bounds__(kThr)
-    cache_write_q4_kernel(const CacheQ4Args a, const uint16_t* __restrict__ k_new, int64_t k_stride,
-                          const uint16_t* __restrict__ v_new, int64_t v_stride) {
-  constexpr int kLanes = D / 8;          // threads of a row
-  constexpr int kStep = kThr / kLanes;   // rows of a pass
+    cache_write_q4_kernel(const CacheQ4Args a, const RowsPlan plan, const uint16_t* __restrict__ k_new,
+                          int64_t k_stride, const uint16_t* __restrict__ v_new, int64_t v_stride) {
+  constexpr int kLanes = D / 16;         // threads of a row
   constexpr int kUnits = q4_units(D);
-  const int part = threadIdx.x % kLanes, g = part * 8 / (D / 4);
-  const int head = blockIdx.y >> 1;
+  const int part = threadIdx.x % kLanes, head = blockIdx.y >> 1;
   const bool is_v = blockIdx.y & 1;
-  const uint16_t* from = (is_v ? v_new : k_new) + head * D + part * 8;
+  const uint16_t* from = (is_v ? v_new : k_new) + head * D + part * 16;
   const int64_t stride = is_v ? v_stride : k_stride;
   uint16_t* pool = static_cast<uint16_t*>(is_v ? a.v : a.k) + (int64_t)head * kPage * kUnits;
   pdl_wait();
   pdl_trigger();
-  const int64_t all = (int64_t)a.n_slots * a.T;
-  const int64_t tok0 = (int64_t)blockIdx.x * (kStep * kRows) + threadIdx.x / kLanes;
-  uint4 x[kRows];
+  uint4 x[kRows][2];
   int64_t at[kRows];  // the row's place in the pool, -1: nothing to write
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    const int64_t tok = tok0 + k * kStep;
+    const RowOf<D> row = row_of<D>(plan, k);
     at[k] = -1;
-    x[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (tok >= all) continue;
-    const int s = (int)(tok / a.T), t = (int)(tok - (int64_t)s * a.T);
-    const int n = a.n ? __ldg(a.n + s) : a.T, len = __ldg(a.lens + s);
+    x[k][0] = x[k][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (row.s >= a.n_slots || row.t >= a.T) continue;
+    const int n = a.n ? __ldg(a.n + row.s) : a.T, len = __ldg(a.lens + row.s);
     if (n < 0 || n > a.T || len < n || len > a.max_blocks * kPage) {
-      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
+      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, row.s);
       continue;
     }
-    if (t >= n) continue;
-    const int pos = len - n + t;
-    x[k] = __ldg(reinterpret_cast<const uint4*>(from + tok * stride));
-    const int page = __ldg(a.table + (int64_t)s * a.max_blocks + pos / kPage);
+    if (row.t >= n) continue;
+    const int pos = len - n + row.t;
+    const uint4* p = reinterpret_cast<const uint4*>(from + ((int64_t)row.s * a.T + row.t) * stride);
+    x[k][0] = __ldg(p);
+    x[k][1] = __ldg(p + 1);
+    const int page = __ldg(a.table + (int64_t)row.s * a.max_blocks + pos / kPage);
     if (page < 0 || page >= a.n_phys) {
-      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
+      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, row.s);
       continue;
     }
     at[k] = ((int64_t)page * a.n_kv * kPage + pos % kPage) * kUnits;
@@ -160,119 +216,163 @@ __global__ void __launch_bounds__(kThr)
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     // all lanes take part in the exchanges, rows that are not there as zeros
-    uint32_t lo = min2<F16>(min2<F16>(x[k].x, x[k].y), min2<F16>(x[k].z, x[k].w));
-    uint32_t hi = max2<F16>(max2<F16>(x[k].x, x[k].y), max2<F16>(x[k].z, x[k].w));
-#pragma unroll
-    for (int d = 1; d < D / 32; d <<= 1) {
-      lo = min2<F16>(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, d));
-      hi = max2<F16>(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, d));
+    const uint4 &y = x[k][0], &z = x[k][1];
+    uint32_t lo = min2<F16>(min2<F16>(min2<F16>(y.x, y.y), min2<F16>(y.z, y.w)),
+                            min2<F16>(min2<F16>(z.x, z.y), min2<F16>(z.z, z.w)));
+    uint32_t hi = max2<F16>(max2<F16>(max2<F16>(y.x, y.y), max2<F16>(y.z, y.w)),
+                            max2<F16>(max2<F16>(z.x, z.y), max2<F16>(z.z, z.w)));
+    if (D == 128) {  // two threads a group
+      lo = min2<F16>(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, 1));
+      hi = max2<F16>(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, 1));
     }
     lo = min2<F16>(lo, lo >> 16 | lo << 16);
     hi = max2<F16>(hi, hi >> 16 | hi << 16);
-    const uint32_t bb = floor_bf16(lo_of<F16>(lo));
+    const uint32_t bb = floor_bf16(unpack_lo<F16>(lo));
     const float b = __uint_as_float(bb << 16);
-    const uint32_t sb = scale_bits(lo_of<F16>(hi), b);
-    uint32_t w = codes8<F16>(x[k], b, __uint_as_float(sb << 16));
-    int word = part;
-    if (D == 64) {  // bytes of groups 2 h and 2 h + 1 alternate
-      const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 2);
-      w = part & 2 ? __byte_perm(o, w, 0x7362) : __byte_perm(w, o, 0x5140);
-      word = (part & 4) + (part & 1) * 2 + (part >> 1 & 1);
+    const uint32_t sb = scale_bits(unpack_lo<F16>(hi), b);
+    const float s = __uint_as_float(sb << 16);
+    float up;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(up) : "f"(s));  // within 2^-23
+    up *= 1.0f + 0x1p-21f;
+    uint32_t w0 = codes8<F16>(y, b, up), w1 = codes8<F16>(z, b, up);
+    if (in_doubt<F16>(x[k], b, s, up)) {
+      w0 = s > 0.0f ? codes_exact<F16>(y, b, s) : 0u;
+      w1 = s > 0.0f ? codes_exact<F16>(z, b, s) : 0u;
+    }
+    int word = 2 * part;
+    if (D == 64) {
+      // bytes of groups 2 h (this thread's or its neighbour's) and 2 h + 1 alternate
+      const bool odd = part & 1;
+      const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, odd ? w0 : w1, 1);
+      const uint32_t p = odd ? o : w0, q = odd ? w1 : o;
+      w0 = __byte_perm(p, q, 0x5140);
+      w1 = __byte_perm(p, q, 0x7362);
     }
     if (at[k] < 0) continue;
     uint16_t* row = pool + at[k];
-    reinterpret_cast<uint32_t*>(row)[word] = w;
-    if (part % (D / 32) == 0) {
+    *reinterpret_cast<uint2*>(row + 2 * word) = make_uint2(w0, w1);
+    if (D == 64 || part % 2 == 0) {
+      const int g = D == 64 ? part : part / 2;
       row[D / 4 + g] = (uint16_t)sb;
       row[D / 4 + 4 + g] = (uint16_t)bb;
     }
   }
 }
 
-// The same arrangement the other way. DT: moe_dtype_t of what comes out, each
-// value rounded once.
+// Eight codes of a word as numbers s c + b, each rounded once: to four words of
+// 16-bit pairs or eight of fp32. D = 64: nibbles 2, 3, 6 and 7 are of the second
+// group (s1, b1), and pairs come as 0 1, 4 5, 2 3, 6 7: each group's together.
+template <int DT, int D>
+__device__ __forceinline__ void values8(uint32_t w, uint32_t s0, uint32_t b0, uint32_t s1, uint32_t b1,
+                                        uint32_t (&o)[DT == MOE_DTYPE_FP32 ? 8 : 4]) {
+  if (DT == MOE_DTYPE_BF16) {
+    uint32_t p[4];  // nibbles i and i + 4
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool second = D == 64 && i >= 2;
+      p[i] = affine_pair(nibble_pair_128(w >> (4 * i)), second ? s1 : s0, second ? b1 : b0);
+    }
+    o[0] = __byte_perm(p[0], p[1], 0x5410);
+    o[D == 64 ? 2 : 1] = __byte_perm(p[2], p[3], 0x5410);
+    o[D == 64 ? 1 : 2] = __byte_perm(p[0], p[1], 0x7632);
+    o[3] = __byte_perm(p[2], p[3], 0x7632);
+    return;
+  }
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool second = D == 64 && (i & 2);
+    // 2^23 + c, less 2^23
+    const float c = __uint_as_float((w >> (4 * i) & 15u) | 0x4B000000u) - 0x1p23f;
+    v[i] = fmaf(c, bf_lo(second ? s1 : s0), bf_lo(second ? b1 : b0));
+  }
+  constexpr int to[4] = {0, D == 64 ? 2 : 1, D == 64 ? 1 : 2, 3};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (DT == MOE_DTYPE_FP32) {
+      o[2 * to[i]] = __float_as_uint(v[2 * i]);
+      o[2 * to[i] + 1] = __float_as_uint(v[2 * i + 1]);
+    } else {
+      o[to[i]] = pack2<true>(v[2 * i], v[2 * i + 1]);
+    }
+  }
+}
+
+// The same arrangement the other way. DT: moe_dtype_t of what comes out.
 template <int DT, int D>
 __global__ void __launch_bounds__(kThr)
-    cache_read_q4_kernel(const CacheQ4Args a, const int32_t* __restrict__ first,
+    cache_read_q4_kernel(const CacheQ4Args a, const RowsPlan plan, const int32_t* __restrict__ first,
                          void* __restrict__ k_out, int64_t k_stride, void* __restrict__ v_out,
                          int64_t v_stride) {
-  constexpr int kLanes = D / 8, kStep = kThr / kLanes, kUnits = q4_units(D);
-  constexpr int kE = DT == MOE_DTYPE_FP32 ? 4 : 2;
-  const int part = threadIdx.x % kLanes;
-  const int head = blockIdx.y >> 1;
+  constexpr int kLanes = D / 16, kUnits = q4_units(D);
+  constexpr int kE = DT == MOE_DTYPE_FP32 ? 4 : 2, kW = DT == MOE_DTYPE_FP32 ? 8 : 4;
+  const int part = threadIdx.x % kLanes, head = blockIdx.y >> 1;
   const bool is_v = blockIdx.y & 1;
   char* to = static_cast<char*>(is_v ? v_out : k_out) + (int64_t)head * D * kE;
   const int64_t stride = is_v ? v_stride : k_stride;
   const uint16_t* pool = static_cast<const uint16_t*>(is_v ? a.v : a.k) + (int64_t)head * kPage * kUnits;
   pdl_wait();
   pdl_trigger();
-  const int64_t all = (int64_t)a.n_slots * a.T;
-  const int64_t tok0 = (int64_t)blockIdx.x * (kStep * kRows) + threadIdx.x / kLanes;
-  // D = 64: a word holds four elements of group 2 h and four of 2 h + 1
-  const int ga = D == 128 ? part / 4 : part / 4 * 2, gb = D == 128 ? ga : ga + 1;
-  uint32_t w[kRows], sb[kRows][2], bb[kRows][2];
-  bool there[kRows];
+  // D = 128: two words of a group; D = 64: two words of half a row, each with
+  // four elements of group 2 h and four of 2 h + 1
+  const int ga = D == 128 ? part / 2 : part / 2 * 2, gb = D == 128 ? ga : ga + 1;
+  uint2 w[kRows];
+  uint32_t sa[kRows], ba[kRows], sb[kRows], bb[kRows];
+  int64_t at[kRows];  // the token, -1: not there
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    const int64_t tok = tok0 + k * kStep;
-    there[k] = false;
-    if (tok >= all) continue;
-    const int s = (int)(tok / a.T), t = (int)(tok - (int64_t)s * a.T);
-    const int n = a.n ? __ldg(a.n + s) : a.T, len = __ldg(a.lens + s);
-    const int f = first ? __ldg(first + s) : 0;
+    const RowOf<D> row = row_of<D>(plan, k);
+    at[k] = -1;
+    if (row.s >= a.n_slots || row.t >= a.T) continue;
+    const int n = a.n ? __ldg(a.n + row.s) : a.T, len = __ldg(a.lens + row.s);
+    const int f = first ? __ldg(first + row.s) : 0;
     if (n < 0 || n > a.T || len < 0 || len > a.max_blocks * kPage || (n > 0 && (f < 0 || f > len - n))) {
-      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
+      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, row.s);
       continue;
     }
-    if (t >= n) continue;
-    const int pos = f + t;
-    const int page = __ldg(a.table + (int64_t)s * a.max_blocks + pos / kPage);
+    if (row.t >= n) continue;
+    const int pos = f + row.t;
+    const int page = __ldg(a.table + (int64_t)row.s * a.max_blocks + pos / kPage);
     if (page < 0 || page >= a.n_phys) {
-      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
+      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, row.s);
       continue;
     }
-    const uint16_t* row = pool + ((int64_t)page * a.n_kv * kPage + pos % kPage) * kUnits;
-    w[k] = __ldg(reinterpret_cast<const uint32_t*>(row) + part);
-    sb[k][0] = __ldg(row + D / 4 + ga);
-    bb[k][0] = __ldg(row + D / 4 + 4 + ga);
-    if (D == 64) {
-      sb[k][1] = __ldg(row + D / 4 + gb);
-      bb[k][1] = __ldg(row + D / 4 + 4 + gb);
-    }
-    there[k] = true;
+    const uint16_t* q = pool + ((int64_t)page * a.n_kv * kPage + pos % kPage) * kUnits;
+    w[k] = __ldg(reinterpret_cast<const uint2*>(q) + part);
+    sa[k] = __ldg(q + D / 4 + ga);
+    ba[k] = __ldg(q + D / 4 + 4 + ga);
+    sb[k] = D == 64 ? __ldg(q + D / 4 + gb) : 0u;
+    bb[k] = D == 64 ? __ldg(q + D / 4 + 4 + gb) : 0u;
+    at[k] = (int64_t)row.s * a.T + row.t;
   }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    if (!there[k]) continue;
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int p = D == 64 ? i >> 1 & 1 : 0;  // D = 64: nibbles 2, 3, 6, 7 are of the second group
-      v[i] = fmaf((float)(w[k] >> (4 * i) & 15u), __uint_as_float(sb[k][p] << 16),
-                  __uint_as_float(bb[k][p] << 16));
-    }
-    uint32_t o[8];
-    if (DT == MOE_DTYPE_FP32) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(v[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = pack2<DT == MOE_DTYPE_FP16>(v[2 * i], v[2 * i + 1]);
-    }
-    const int64_t tok = tok0 + k * kStep;
+    if (at[k] < 0) continue;
+    const uint32_t s0 = dup_lo(sa[k]), b0 = dup_lo(ba[k]), s1 = dup_lo(sb[k]), b1 = dup_lo(bb[k]);
+    uint32_t o[2][kW];
+    values8<DT, D>(w[k].x, s0, b0, s1, b1, o[0]);
+    values8<DT, D>(w[k].y, s0, b0, s1, b1, o[1]);
     if (D == 128) {
-      uint4* p = reinterpret_cast<uint4*>(to + (tok * stride + part * 8) * kE);
-      p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      if (DT == MOE_DTYPE_FP32) p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      uint4* p = reinterpret_cast<uint4*>(to + (at[k] * stride + part * 16) * kE);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < kW; i += 4)
+          p[(j * kW + i) / 4] = make_uint4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]);
     } else {
-      char* p = to + (tok * stride + (part >> 2) * 32 + (part & 3) * 4) * kE;
-      if (DT == MOE_DTYPE_FP32) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[4], o[5]);
-        *reinterpret_cast<uint4*>(p + 16 * kE) = make_uint4(o[2], o[3], o[6], o[7]);
-      } else {
-        *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[2]);
-        *reinterpret_cast<uint2*>(p + 16 * kE) = make_uint2(o[1], o[3]);
-      }
+      // elements 8 (part % 2) .. + 7 of group 2 h, then of the next
+      char* p = to + (at[k] * stride + (part >> 1) * 32 + (part & 1) * 8) * kE;
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int i = 0; i < kW; i += 4) {
+          const int j = g * (kW / 2);
+          uint4* q = reinterpret_cast<uint4*>(p + g * 16 * kE + i * 4);
+          if (DT == MOE_DTYPE_FP32)
+            *q = make_uint4(o[i / 4][j], o[i / 4][j + 1], o[i / 4][j + 2], o[i / 4][j + 3]);
+          else
+            *q = make_uint4(o[0][j], o[0][j + 1], o[1][j], o[1][j + 1]);
+        }
     }
   }
 }
@@ -298,10 +398,20 @@ CacheQ4Args args_of(const moe_cache_shape_t* s, const moe_cache_meta_t& meta, co
   a.ctrl = reinterpret_cast<Ctrl*>(ws);
   return a;
 }
-// tokens of a CTA: kThr / (D / 8) * kRows
-dim3 grid_of(const moe_cache_shape_t* s, int T) {
-  const int64_t per = (int64_t)kThr / (s->D / 8) * kRows, n = (int64_t)s->n_slots * T;
-  return dim3((unsigned)((n + per - 1) / per), 2 * s->n_kv);
+RowsPlan plan_of(const moe_cache_shape_t* s, int T, dim3* grid) {
+  const int step = kThr / (s->D / 16);
+  RowsPlan p{0, 0};
+  while (1 << p.log_t < T && 1 << p.log_t < step) ++p.log_t;
+  int x;
+  if (T > step) {
+    p.chunks = (T + step * kRows - 1) / (step * kRows);
+    x = s->n_slots * p.chunks;  // below 2^12 * 2^13
+  } else {
+    const int slots = (step >> p.log_t) * kRows;
+    x = (s->n_slots + slots - 1) / slots;
+  }
+  *grid = dim3(x, 2 * s->n_kv);
+  return p;
 }
 }  // namespace
 
@@ -310,8 +420,10 @@ cudaError_t launch_cache_write_q4(const moe_cache_shape_t* s, const moe_cache_me
                                   int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
                                   bool fp16, void* k, void* v, uint8_t* ws, cudaStream_t stream) {
   const CacheQ4Args a = args_of(s, meta, n_new, T, k, v, ws);
+  dim3 grid;
+  const RowsPlan plan = plan_of(s, T, &grid);
   auto go = [&](auto kern) {
-    return launch_pdl(kern, grid_of(s, T), dim3(kThr), 0, stream, a, k_new, k_stride, v_new, v_stride);
+    return launch_pdl(kern, grid, dim3(kThr), 0, stream, a, plan, k_new, k_stride, v_new, v_stride);
   };
   if (s->D == 64) return fp16 ? go(cache_write_q4_kernel<true, 64>) : go(cache_write_q4_kernel<false, 64>);
   return fp16 ? go(cache_write_q4_kernel<true, 128>) : go(cache_write_q4_kernel<false, 128>);
@@ -322,8 +434,10 @@ cudaError_t launch_cache_read_q4(const moe_cache_shape_t* s, const moe_cache_met
                                  const void* v, void* k_out, int64_t k_stride, void* v_out,
                                  int64_t v_stride, int dtype, uint8_t* ws, cudaStream_t stream) {
   const CacheQ4Args a = args_of(s, meta, n, T, const_cast<void*>(k), const_cast<void*>(v), ws);
+  dim3 grid;
+  const RowsPlan plan = plan_of(s, T, &grid);
   auto go = [&](auto kern) {
-    return launch_pdl(kern, grid_of(s, T), dim3(kThr), 0, stream, a, first, k_out, k_stride, v_out, v_stride);
+    return launch_pdl(kern, grid, dim3(kThr), 0, stream, a, plan, first, k_out, k_stride, v_out, v_stride);
   };
   if (s->D == 64) {
     if (dtype == MOE_DTYPE_FP32) return go(cache_read_q4_kernel<MOE_DTYPE_FP32, 64>);

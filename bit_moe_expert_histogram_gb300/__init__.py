@@ -617,11 +617,17 @@ def moe_verify_drafts(shape, p, q, draft, n_draft, u, tokens, n_acc, ws, stream=
 
 
 # --------------------------------------------------- a cache held in 4 bits --
+_Q4_UNITS = {}  # by D, as the library gives them
+
+
 def moe_cache_q4_units(D):
     """16-bit units of a head's 4-bit row: 40 for D = 128, 24 for D = 64."""
-    n = (_lib or load()).moe_cache_q4_units(D)
-    if n == 0:
-        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_cache_q4_units")
+    n = _Q4_UNITS.get(D)
+    if n is None:
+        n = load().moe_cache_q4_units(D)
+        if n == 0:
+            raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_cache_q4_units")
+        _Q4_UNITS[D] = n
     return n
 
 

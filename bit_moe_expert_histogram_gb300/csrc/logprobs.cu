@@ -36,7 +36,8 @@ constexpr int kLThr = 256;
 constexpr int kLCtas = 5;       // an SM
 constexpr int kLWarps = kLThr / 32;
 constexpr int kVec = 4;         // 16-byte vectors a thread and chunk
-constexpr int kCap = 1024;      // entries of the list
+constexpr int kCap = 1024;      // entries of the list, when stretches are joined
+constexpr int kMost = 256;      // that one stretch may bring: ordering takes their square
 constexpr int kMostTop = 32;
 constexpr int kMostCuts = kCap / kMostTop;  // stretches of a row, whose entries one list holds
 constexpr int kMostParts = 1024;            // (row, stretch) pairs where rows are cut
@@ -346,12 +347,12 @@ __global__ void __launch_bounds__(kLThr, kLCtas) logprobs_kernel(const LogpArgs 
           for (; mask; mask &= mask - 1) {
             const int b = __ffs(mask) - 1, id = first_of(c, b / E::kN) + b % E::kN;
             const int at = atomicAdd(&list.n, 1);
-            if (at < kCap) list.e[at] = entry(element(id), id);
+            if (at < kMost) list.e[at] = entry(element(id), id);
           }
         }
         if (!meet || over) break;
         __syncthreads();
-        if (list.n <= kCap) break;
+        if (list.n <= kMost) break;
         // too many: of the first chunk those above the groups' bar and then the
         // first of its equals, once
         over = !begin || equals;
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(kLThr, kLCtas) logprobs_kernel(const LogpArgs 
   }
   if (TOP) {
     __syncthreads();
-    over |= list.n > kCap;
+    over |= list.n > kMost;
     if (over) {
       // the best k one after the other, each found by reading the stretch again
       __syncthreads();
@@ -487,11 +488,20 @@ __global__ void __launch_bounds__(kLThr, kLCtas) logprobs_kernel(const LogpArgs 
       s = Sums{__ldcg(p), __ldcg(p + 1), __ldcg(p + 2)};
     }
     if (TOP) {
+      // nothing below a stretch's k-th can be among the first k
+      uint64_t least = 0;
+      if (lane < a.S && __float_as_int(__ldcg(parts + lane * kLPart + 3)) == a.k)
+        least = __ldcg(reinterpret_cast<const unsigned long long*>(parts + lane * kLPart + 4) + a.k - 1);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t y = __shfl_xor_sync(0xFFFFFFFFu, least, o);
+        least = y > least ? y : least;
+      }
       for (int i = tid; i < a.S * kMostTop; i += kLThr) {
         const float* p = parts + i / kMostTop * kLPart;
         const int j = i % kMostTop;
         const uint64_t x = __ldcg(reinterpret_cast<const unsigned long long*>(p + 4) + j);
-        if (j < __float_as_int(__ldcg(p + 3))) list.e[atomicAdd(&list.n, 1)] = x;
+        if (j < __float_as_int(__ldcg(p + 3)) && x >= least) list.e[atomicAdd(&list.n, 1)] = x;
       }
     }
     s = join(s, 32);

@@ -169,10 +169,12 @@ constexpr float kSlack = 7.0f, kLift = 8.0f;
 constexpr int kSigLeast = 27, kSigMost = 253;
 constexpr uint32_t kLoNib = 0x000F000Fu, kHiNib = 0x00F000F0u;
 
-// What a slot brings: its length, new tokens and units (at least one, a unit
-// of nothing where it has none, so that each slot's rows get written).
+// What a slot brings: its length, new tokens, row tiles with a token in them,
+// and the units of such a tile's pair (at least one, a unit of nothing where it
+// has none, so that each slot's rows get written; a tile without a token has
+// one, too).
 struct Q4Span {
-  int len, n_new, units;
+  int len, n_new, used, units;
 };
 __device__ __forceinline__ Q4Span q4_span(const AttnQ4Args& a, int s) {
   Q4Span r;
@@ -185,16 +187,22 @@ __device__ __forceinline__ Q4Span q4_span(const AttnQ4Args& a, int s) {
     r.n_new = min(max(r.n_new, 0), a.T);
   }
   const int n = (r.len + kBlk - 1) / kBlk;
-  r.units = r.n_new == 0 || n < 1 ? 1 : n;
+  r.used = a.tiles == 1 ? r.n_new > 0 : (r.n_new * a.group + kMostRows - 1) / kMostRows;
+  r.units = n < 1 ? 1 : n;
   return r;
+}
+// on the line: what a slot's heads take each
+__device__ __forceinline__ int head_units(const AttnQ4Args& a, const Q4Span& sp) {
+  return sp.used * (sp.units + a.pair_cost) + (a.tiles - sp.used) * (1 + a.pair_cost);
 }
 
 // A place on the line: the pair (slot, head, row tile) and its first unit pb.
 struct Place {
   int s, head, tile, pb;
   Q4Span sp;
+  __device__ __forceinline__ int units() const { return tile < sp.used ? sp.units : 1; }
   __device__ __forceinline__ void next(const AttnQ4Args& a) {
-    pb += sp.units + a.pair_cost;
+    pb += units() + a.pair_cost;
     if (++tile < a.tiles) return;
     tile = 0;
     if (++head < a.n_kv) return;
@@ -275,18 +283,17 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
   pdl_wait();
   pdl_trigger();
   // ---- this warp's part of the line of units
-  const int ht = a.n_kv * a.tiles;  // pairs of a slot
   int total = 0, per;
   {
     const int chunk = (a.n_slots + kQThr - 1) / kQThr;
     const int s0 = min(tid * chunk, a.n_slots), s1 = min(s0 + chunk, a.n_slots);
     int sum = 0;
-    Q4Span sp{0, 0, 0};
+    Q4Span sp{0, 0, 0, 0};
     for (int s = s0; s < s1; ++s) {
       sp = q4_span(a, s);
-      sum += sp.units + a.pair_cost;
+      sum += head_units(a, sp);
     }
-    sum *= ht;
+    sum *= a.n_kv;
     int incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -324,21 +331,29 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
     Place at = s_start[warp];
     if (a.n_slots > kQThr) {
       for (at.sp = q4_span(a, at.s); at.s < a.n_slots - 1; at.sp = q4_span(a, ++at.s)) {
-        const int n = (at.sp.units + a.pair_cost) * ht;
+        const int n = head_units(a, at.sp) * a.n_kv;
         if (f0 < at.pb + n) break;
         at.pb += n;
       }
     }
     {
-      const unsigned each = at.sp.units + a.pair_cost, pair = cut_up((unsigned)(f0 - at.pb) + 1u, each) - 1;
-      at.head = a.tiles == 1 ? pair : cut_up(pair + 1u, a.tiles) - 1;
-      at.tile = pair - at.head * a.tiles;
-      at.pb += pair * each;
+      const int all = head_units(a, at.sp), each = at.sp.units + a.pair_cost, rest = 1 + a.pair_cost;
+      at.head = a.n_kv == 1 ? 0 : cut_up((unsigned)(f0 - at.pb) + 1u, all) - 1;
+      at.pb += at.head * all;
+      int in = f0 - at.pb;  // of the head's units
+      at.tile = min(a.tiles == 1 ? 0 : cut_up((unsigned)in + 1u, each) - 1, at.sp.used);
+      at.pb += at.tile * each;
+      in -= at.tile * each;
+      if (at.tile == at.sp.used) {
+        const int more = cut_up((unsigned)in + 1u, rest) - 1;
+        at.tile += more;
+        at.pb += more * rest;
+      }
     }
     // ---- the loader: kS units ahead on the line, all lanes follow, lane 0 issues
     Place ld = at;
     int lu = f0 - at.pb;                        // the pair's next unit
-    int le = min(f1 - at.pb, at.sp.units);      // and how many of them are the warp's
+    int le = min(f1 - at.pb, at.units());      // and how many of them are the warp's
     int lst = 0, ln = 0, base = -1, pages = -1; // pages: of blocks base + lane
     unsigned absent = 0;                        // bit per stage: nothing was fetched for it
     bool dead = false;                          // a wait ran out: nothing more is fetched
@@ -347,10 +362,10 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
     auto load_next = [&] {
       if (dead) return;
       while (lu >= le) {
-        if (ld.pb + ld.sp.units + a.pair_cost >= f1) return;
+        if (ld.pb + ld.units() + a.pair_cost >= f1) return;
         ld.next(a);
         lu = 0;
-        le = min(f1 - ld.pb, ld.sp.units);
+        le = min(f1 - ld.pb, ld.units());
         base = -1;
       }
       if ((lu & ~31) != base) {
@@ -359,7 +374,7 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
       }
       const int page = __shfl_sync(0xFFFFFFFFu, pages, lu & 31);
       const int n = min(kBlk, ld.sp.len - lu * kBlk);
-      const bool none = ld.sp.n_new == 0 || n <= 0;
+      const bool none = ld.tile >= ld.sp.used || n <= 0;
       const bool bad = !none && (unsigned)page >= (unsigned)a.n_phys;
       absent = (absent & ~(1u << lst)) | (none || bad ? 1u << lst : 0u);
       if (lane == 0) {
@@ -405,20 +420,21 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
         }
       }
     };
-    if (f0 - at.pb < at.sp.units) fetch_q();
+    if (f0 - at.pb < at.units()) fetch_q();
     for (int i = 0; i < kS; ++i) load_next();
 
     int f = f0, st = 0, done = 0;
     uint32_t parity = 0;
     while (f < f1) {
-      if (f - at.pb >= at.sp.units) {  // this warp starts in a pair's cost
+      const int units = at.units();
+      if (f - at.pb >= units) {  // this warp starts in a pair's cost
         at.next(a);
         f = at.pb;
         if (f < f1) fetch_q();
         continue;
       }
-      const int fe = min(f1, at.pb + at.sp.units);
-      const bool whole = f == at.pb && fe == at.pb + at.sp.units;
+      const int fe = min(f1, at.pb + units);
+      const bool whole = f == at.pb && fe == at.pb + units;
       const int basep = at.sp.len - at.sp.n_new;  // may be negative
       // ---- the rows: queries as fp16, their scale, their groups' sums
       // per query column 2 cq + e of eight: its last visible position (-1: none),
@@ -774,7 +790,7 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
         pf = C::kPieceHere ? reinterpret_cast<float*>(sm_raw + (queries + C::kQBytes - sbase))
                            : a.pieces + ((int64_t)blockIdx.x * kWarps + warp) * kPiece;
       if (!whole && lane == 0)
-        s_piece[2 * warp + which] = PieceInfo{(at.s * a.n_kv + at.head) * a.tiles + at.tile, at.pb, at.sp.units,
+        s_piece[2 * warp + which] = PieceInfo{(at.s * a.n_kv + at.head) * a.tiles + at.tile, at.pb, units,
                                               at.s, at.head, at.tile, pf};
 #pragma unroll
       for (int i = 0; i < NT; ++i)

@@ -1,6 +1,6 @@
 """A batch of requests over one page pool, decoded with drafted tokens.
 
-    python examples/speculative_serving.py [--requests 8] [--new 48] [--temperature 0.0]
+    python examples/speculative_serving.py [--requests 8] [--new 48] [--temperature 0.0] [--cache 4]
 
 One prompt is read once into a slot's pages and forked to every request
 (moe_cache_fork), so its pages are shared; each step then takes room for the
@@ -11,6 +11,10 @@ drafts against the model's probabilities (moe_verify_drafts) and gives the
 rejected tail back (moe_cache_fork with `keep`). The model is a small
 random-weight one: 2 layers of 8 query heads on 2 key/value heads of 64, 16
 experts. Drafts are what followed the current token the last time it came up.
+With --cache 4 keys and values are held in 4 bits: the same steps with
+moe_cache_write_q4 and moe_attn_batch_q4, where the prompt's pages are shared
+through the slots' tables. The answers' log probabilities come from
+moe_token_logprobs.
 
 With temperature 0 the probabilities are one-hot, and every token has to be the
 likeliest one when the same text is read one token at a time (up to the
@@ -77,13 +81,19 @@ class Model:
 class Server:
     """Slots, their pages and the calls of a step."""
 
-    def __init__(self, model, n_slots, max_len, n_phys):
+    def __init__(self, model, n_slots, max_len, n_phys, bits=16):
         self.model, self.B, dev = model, n_slots, model.dev
+        self.bits = bits
         self.width = -(-max_len // BLOCK)
         self.shape = m.make_cache_shape(n_slots, self.width, n_phys, N_KV, D)
+        # what the page calls move: pages of 16-bit rows, or of 4-bit ones
+        self.page_shape = m.q4_page_shape(self.shape) if bits == 4 else self.shape
         self.cache_ws = m.alloc_cache_workspace(self.shape, dev)
         self.meta, self.spare = m.CacheMeta.empty(self.shape, dev), m.CacheMeta.empty(self.shape, dev)
-        pool = lambda: torch.empty((n_phys, N_KV, BLOCK, D), dtype=torch.bfloat16, device=dev)  # noqa: E731
+        if bits == 4:
+            pool = lambda: m.alloc_q4_pool(self.shape, dev)  # noqa: E731
+        else:
+            pool = lambda: torch.empty((n_phys, N_KV, BLOCK, D), dtype=torch.bfloat16, device=dev)  # noqa: E731
         self.k, self.v = [pool() for _ in range(LAYERS)], [pool() for _ in range(LAYERS)]
         self.pools = m.pool_table(self.k + self.v)
         self.granted = torch.empty(n_slots, dtype=torch.int32, device=dev)
@@ -91,23 +101,25 @@ class Server:
         self.prefix = None
 
     def fork(self, parent, keep=None):
-        m.moe_cache_fork(self.shape, self.meta, parent, self.spare, self.cache_ws, keep=keep)
+        m.moe_cache_fork(self.page_shape, self.meta, parent, self.spare, self.cache_ws, keep=keep)
         self.meta, self.spare = self.spare, self.meta
 
     def share_prefix(self, slot, blocks):
         """The first `blocks` pages of `slot` are every slot's from here on."""
-        self.prefix = self.meta.table[slot, :blocks].clone() if blocks else None
+        if self.bits == 16:
+            self.prefix = self.meta.table[slot, :blocks].clone() if blocks else None
 
     def step(self, tokens, n_new):
         """tokens int32 [B][T], n_new int32 [B]: their logits [B][T][VOCAB]."""
         B, T = tokens.shape
-        m.moe_cache_reserve(self.shape, self.meta, n_new, self.spare, self.granted, self.pools,
+        m.moe_cache_reserve(self.page_shape, self.meta, n_new, self.spare, self.granted, self.pools,
                             self.cache_ws)
         self.meta, self.spare = self.spare, self.meta
         P = 0 if self.prefix is None else len(self.prefix)
         if (T, P) not in self.attn:
             shape = m.make_attn_batch_shape(B, T, N_Q, N_KV, D, self.width, P)
-            self.attn[T, P] = (shape, m.alloc_attn_batch_workspace(shape, self.model.dev),
+            alloc = m.alloc_attn_batch_q4_workspace if self.bits == 4 else m.alloc_attn_batch_workspace
+            self.attn[T, P] = (shape, alloc(shape, self.model.dev),
                                torch.empty((B, T, N_Q, D), dtype=torch.bfloat16,
                                            device=self.model.dev))
         shape, ws, o = self.attn[T, P]
@@ -115,10 +127,15 @@ class Server:
         for layer in range(LAYERS):
             qkv = (self.model.norm(x) @ self.model.qkv[layer]).view(B, T, N_Q + 2 * N_KV, D)
             q, k, v = qkv[:, :, :N_Q], qkv[:, :, N_Q:N_Q + N_KV], qkv[:, :, N_Q + N_KV:]
-            m.moe_cache_write(self.shape, self.meta, self.granted, k, v, self.k[layer],
-                              self.v[layer], self.cache_ws)
-            m.moe_attn_batch(shape, q, self.k[layer], self.v[layer], self.meta.table,
-                             self.meta.lens, o, ws, n_new=self.granted, prefix=self.prefix)
+            pools = self.k[layer], self.v[layer]
+            if self.bits == 4:
+                m.moe_cache_write_q4(self.shape, self.meta, self.granted, k, v, *pools, self.cache_ws)
+                m.moe_attn_batch_q4(shape, q, *pools, self.meta.table, self.meta.lens, o, ws,
+                                    n_new=self.granted)
+            else:
+                m.moe_cache_write(self.shape, self.meta, self.granted, k, v, *pools, self.cache_ws)
+                m.moe_attn_batch(shape, q, *pools, self.meta.table, self.meta.lens, o, ws,
+                                 n_new=self.granted, prefix=self.prefix)
             x = x + o.view(B * T, -1) @ self.model.out[layer]
             x = x + self.model.experts(layer, self.model.norm(x))
         return (self.model.norm(x) @ self.model.head).float().view(B, T, VOCAB)
@@ -138,12 +155,14 @@ def look_up(history, n):
     return []
 
 
-def decode(model, prompt, requests, new, drafts, temperature=0.0, seed=0):
-    """Token lists of every request and how many steps they took."""
+def decode(model, prompt, requests, new, drafts, temperature=0.0, seed=0, bits=16, logps=None):
+    """Token lists of every request, how many steps they took and how many pages
+    were held. logps: a list that takes the tokens' log probabilities (of the
+    model as it is, whatever the temperature), a list a request."""
     dev = model.dev
     max_len = len(prompt) + new + drafts + BLOCK
     per_slot = -(-(new + drafts + BLOCK) // BLOCK) + 1
-    server = Server(model, requests, max_len, -(-len(prompt) // BLOCK) + requests * per_slot)
+    server = Server(model, requests, max_len, -(-len(prompt) // BLOCK) + requests * per_slot, bits)
     ints = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
     # the prompt, sixteen tokens at a time, into slot 0; its last token starts
     # every request
@@ -162,6 +181,9 @@ def decode(model, prompt, requests, new, drafts, temperature=0.0, seed=0):
     everyone = ints(list(range(requests)))
     g = torch.Generator(device=dev).manual_seed(seed)
     history = [list(prompt) for _ in range(requests)]
+    lshape = m.make_logprobs_shape(requests * T, VOCAB)
+    lws, logp = m.alloc_logprobs_workspace(lshape, dev), torch.empty(requests * T, device=dev)
+    said = [[] for _ in range(requests)]
     steps = 0
     while min(len(h) for h in history) < len(prompt) + new:
         tokens = torch.zeros((requests, T), dtype=torch.int32, device=dev)
@@ -175,29 +197,36 @@ def decode(model, prompt, requests, new, drafts, temperature=0.0, seed=0):
                 draft[b, :len(d)] = ints(d)
         n_draft = ints(counts)
         lens = server.meta.lens.clone()
-        p = probabilities(server.step(tokens, n_draft + 1), temperature)
+        logits = server.step(tokens, n_draft + 1)
+        p = probabilities(logits, temperature)
         if drafts == 0:  # verification wants room for one draft
             p = torch.cat([p, p], 1).contiguous()
         u = torch.rand(out.shape, generator=g, device=dev)
         m.moe_verify_drafts(shape, p, None, draft, n_draft, u, out, n_acc, ws)
         server.fork(everyone, keep=lens + 1 + n_acc)  # what was rejected goes back
         steps += 1
-        for h, row in zip(history, out.tolist()):
+        # row t of a request's logits is what its t-th token here was drawn from
+        m.moe_token_logprobs(lshape, logits.view(requests * T, VOCAB), out[:, :T].contiguous().view(-1),
+                             logp, lws)
+        for h, s, row, lp in zip(history, said, out.tolist(), logp.view(requests, T).tolist()):
             h += [t for t in row if t >= 0]
-    for w in (server.cache_ws, ws, *[a[1] for a in server.attn.values()]):
+            s += [x for x, t in zip(lp, row) if t >= 0]
+    for w in (server.cache_ws, ws, lws, *[a[1] for a in server.attn.values()]):
         status = m.moe_query_device_status(w)
         if status != 0:
             raise RuntimeError("device status %d" % status)
+    if logps is not None:
+        logps += [s[:new] for s in said]
     held = int((server.meta.refs > 0).sum())
     return [h[len(prompt):len(prompt) + new] for h in history], steps, held
 
 
-def shortfall(model, prompt, text):
+def shortfall(model, prompt, text, bits=16):
     """For every token of `text` after `prompt`, read one token at a time: the
     largest logit less the token's own."""
     ints = lambda a: torch.tensor(a, dtype=torch.int32, device=model.dev)  # noqa: E731
     tokens = list(prompt) + list(text)
-    server = Server(model, 1, len(tokens), -(-len(tokens) // BLOCK) + 1)
+    server = Server(model, 1, len(tokens), -(-len(tokens) // BLOCK) + 1, bits)
     gaps = []
     for i, t in enumerate(tokens[:-1]):
         logits = server.step(ints([[t]]), ints([1]))[0, 0]
@@ -213,14 +242,18 @@ def main():
     ap.add_argument("--drafts", type=int, default=3)
     ap.add_argument("--prompt", type=int, default=300)
     ap.add_argument("--temperature", type=float, default=0.0)
+    ap.add_argument("--cache", type=int, choices=(16, 4), default=16, help="bits of keys and values")
     args = ap.parse_args()
     m.load()
     model = Model()
     prompt = np.random.default_rng(0).integers(0, VOCAB, args.prompt).tolist()
-    got, steps, held = decode(model, prompt, args.requests, args.new, args.drafts, args.temperature)
-    print("%d requests x %d tokens in %d steps, %d pages held" % (args.requests, args.new, steps, held))
+    logps = []
+    got, steps, held = decode(model, prompt, args.requests, args.new, args.drafts, args.temperature,
+                              bits=args.cache, logps=logps)
+    print("%d requests x %d tokens in %d steps, %d pages held, %.2f nats a token" % (
+        args.requests, args.new, steps, held, -np.mean(logps)))
     if args.temperature == 0:
-        gaps = shortfall(model, prompt, got[0])
+        gaps = shortfall(model, prompt, got[0], args.cache)
         print("read one at a time: %d of %d tokens the likeliest, the others short by up to %.3f" % (
             sum(x <= 0 for x in gaps), len(gaps), max(gaps)))
 

@@ -26,6 +26,7 @@
 // Bound by HBM: a logit costs some seven instructions, one of them an
 // exponential; pairs of fp32 numbers share what they can.
 #include <cfloat>
+#include <type_traits>
 
 #include "attn_batch.cuh"
 
@@ -33,7 +34,10 @@ namespace moe {
 
 namespace {
 constexpr int kLThr = 256;
-constexpr int kLCtas = 5;       // an SM
+// CTAs an SM: many rows want loads in flight, a few want the shorter path that
+// more registers give (64 rows of 131072, twenty alternatives: 14.5 us with 4,
+// 16.4 with 5; 2048 rows of 128001: 107.5 and 102.7).
+constexpr int kLMany = 5, kLFew = 4;
 constexpr int kLWarps = kLThr / 32;
 constexpr int kVec = 4;         // 16-byte vectors a thread and chunk
 constexpr int kCap = 1024;      // entries of the list, when stretches are joined
@@ -231,8 +235,8 @@ __device__ __forceinline__ int keep_best(TopList& t, int k) {
 }
 }  // namespace
 
-template <int DT, bool TOP>
-__global__ void __launch_bounds__(kLThr, kLCtas) logprobs_kernel(const LogpArgs a) {
+template <int DT, bool TOP, int kCtas>
+__global__ void __launch_bounds__(kLThr, kCtas) logprobs_kernel(const LogpArgs a) {
   using E = El<DT>;
   __shared__ TopList list;
   __shared__ __align__(16) float s_group[kLGroups];
@@ -569,7 +573,7 @@ cudaError_t launch_logprobs(const moe_logprobs_shape_t* s, const void* logits, i
   const int vecs = (s->V * e + 15) / 16 + (even ? 0 : 1), chunk = kLThr * kVec;
   const int chunks = (vecs + chunk - 1) / chunk;
   // rows are cut where there are fewer than CTAs that fit at once
-  int most = kLCtas * nsm < kMostParts ? kLCtas * nsm : kMostParts;
+  int most = kLFew * nsm < kMostParts ? kLFew * nsm : kMostParts;
   most /= s->n_rows;
   if (most > kMostCuts) most = kMostCuts;
   const int cuts = most < 1 ? 1 : most < chunks ? most : chunks;
@@ -579,11 +583,14 @@ cudaError_t launch_logprobs(const moe_logprobs_shape_t* s, const void* logits, i
     return launch_pdl(kern, dim3((unsigned)s->n_rows * a.S), dim3(kLThr), 0, stream, a);
   };
   const bool top = s->k > 0 && (top_ids || top_logp);
-  if (s->dtype == MOE_DTYPE_FP32)
-    return top ? go(logprobs_kernel<MOE_DTYPE_FP32, true>) : go(logprobs_kernel<MOE_DTYPE_FP32, false>);
-  if (s->dtype == MOE_DTYPE_FP16)
-    return top ? go(logprobs_kernel<MOE_DTYPE_FP16, true>) : go(logprobs_kernel<MOE_DTYPE_FP16, false>);
-  return top ? go(logprobs_kernel<MOE_DTYPE_BF16, true>) : go(logprobs_kernel<MOE_DTYPE_BF16, false>);
+  auto pick = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (a.S > 1) return top ? go(logprobs_kernel<DT, true, kLFew>) : go(logprobs_kernel<DT, false, kLFew>);
+    return top ? go(logprobs_kernel<DT, true, kLMany>) : go(logprobs_kernel<DT, false, kLMany>);
+  };
+  if (s->dtype == MOE_DTYPE_FP32) return pick(std::integral_constant<int, MOE_DTYPE_FP32>());
+  if (s->dtype == MOE_DTYPE_FP16) return pick(std::integral_constant<int, MOE_DTYPE_FP16>());
+  return pick(std::integral_constant<int, MOE_DTYPE_BF16>());
 }
 
 }  // namespace moe

@@ -538,71 +538,17 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
         if (!dead && !(absent >> st & 1u)) {
           const uint32_t sk = ring + st * 2 * C::kTile, sv = sk + C::kTile;
           const int pos0 = (f - at.pb) * kBlk, n_here = at.sp.len - pos0;
-          // ---- scales and biases, a position a lane; values' rows past the slot's
-          // end hold anything and count as nothing (keys' are masked)
-          {
-            constexpr int kOf = kBlk / 32;  // positions of a lane
-            float s4[kOf][4], b4[kOf][4], big[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          // ---- keys' scales, a position a lane; rows past the slot's end hold
+          // anything and are masked, values' count as nothing
+          constexpr int kOf = kBlk / 32;  // positions of a lane
+          uint4 wv[kOf];
 #pragma unroll
-            for (int v = 0; v < kOf; ++v) {
-              const int pos = lane + 32 * v;
-              const uint32_t at = D / 2 + pos * C::kRow;
-              const uint2 wk = lds64(sk + at);
-              sts128(scratch + pos * 16, wk.x << 16, wk.x & 0xFFFF0000u, wk.y << 16, wk.y & 0xFFFF0000u);
-              uint4 wv = lds128(sv + at);
-              if (pos >= n_here) wv = make_uint4(0u, 0u, 0u, 0u);
-              s4[v][0] = 16.0f * bf_lo(wv.x), s4[v][1] = 16.0f * bf_hi(wv.x);
-              s4[v][2] = 16.0f * bf_lo(wv.y), s4[v][3] = 16.0f * bf_hi(wv.y);
-              b4[v][0] = bf_lo(wv.z), b4[v][1] = bf_hi(wv.z), b4[v][2] = bf_lo(wv.w), b4[v][3] = bf_hi(wv.w);
-#pragma unroll
-              for (int g = 0; g < 4; ++g) big[g] = fmaxf(big[g], fmaxf(s4[v][g], fabsf(b4[v][g])));
-            }
-            bool grown = false;
-            int was[4];
-            float inv[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              // positive numbers order as whole numbers
-              const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big[g]));
-              was[g] = sg[g];
-              sg[g] = min(max(sg[g], (int)(top >> 23) + 1), kSigMost);
-              grown |= sg[g] != was[g];
-              inv[g] = __uint_as_float((uint32_t)(254 - sg[g]) << 23);
-            }
-            if (grown) {  // the same for all lanes
-#pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const float cut = sg[g] == was[g] ? 1.0f : ex2((float)(was[g] - sg[g]));
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-#pragma unroll
-                  for (int j = g * (kKS / 4); j < (g + 1) * (kKS / 4); ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[j][i][e] *= cut;
-                  if (gq == g) {
-                    sb[i][0] *= cut;
-                    sb[i][1] *= cut;
-                  }
-                }
-              }
-            }
-            // this lane's position as the low or high half of its pair: even
-            // lanes take groups 0 and 1 of both, odd lanes 2 and 3
-            const bool odd = lane & 1;
-#pragma unroll
-            for (int v = 0; v < kOf; ++v) {
-              const uint32_t sa = pack2<true>(s4[v][0] * inv[0], s4[v][1] * inv[1]);
-              const uint32_t sc = pack2<true>(s4[v][2] * inv[2], s4[v][3] * inv[3]);
-              const uint32_t ba = pack2<true>(b4[v][0] * inv[0], b4[v][1] * inv[1]);
-              const uint32_t bc = pack2<true>(b4[v][2] * inv[2], b4[v][3] * inv[3]);
-              const uint32_t xs = __shfl_xor_sync(0xFFFFFFFFu, odd ? sa : sc, 1);
-              const uint32_t xb = __shfl_xor_sync(0xFFFFFFFFu, odd ? ba : bc, 1);
-              const uint32_t ls = odd ? xs : sa, hs = odd ? sc : xs;
-              const uint32_t lb = odd ? xb : ba, hb = odd ? bc : xb;
-              const uint32_t tv = scratch + kVal + ((lane >> 1) + 16 * v) * 32 + odd * 8;
-              sts64(tv, __byte_perm(ls, hs, 0x5410), __byte_perm(ls, hs, 0x7632));
-              sts64(tv + 16, __byte_perm(lb, hb, 0x5410), __byte_perm(lb, hb, 0x7632));
-            }
+          for (int v = 0; v < kOf; ++v) {
+            const int pos = lane + 32 * v;
+            const uint32_t at = D / 2 + pos * C::kRow;
+            const uint2 wk = lds64(sk + at);
+            wv[v] = lds128(sv + at);
+            sts128(scratch + pos * 16, wk.x << 16, wk.x & 0xFFFF0000u, wk.y << 16, wk.y & 0xFFFF0000u);
           }
           __syncwarp();
           // ---- scores, in powers of two, of positions 16 h + gq and 8 on, and of
@@ -683,6 +629,66 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
                 x[h >> 1][h & 1][i] = pair2(__float_as_uint(x0), __float_as_uint(x1));
               }
           }
+          // ---- values' scales and biases, while the products run
+          {
+            float s4[kOf][4], b4[kOf][4], big[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int v = 0; v < kOf; ++v) {
+              uint4 w = wv[v];
+              if (lane + 32 * v >= n_here) w = make_uint4(0u, 0u, 0u, 0u);
+              s4[v][0] = 16.0f * bf_lo(w.x), s4[v][1] = 16.0f * bf_hi(w.x);
+              s4[v][2] = 16.0f * bf_lo(w.y), s4[v][3] = 16.0f * bf_hi(w.y);
+              b4[v][0] = bf_lo(w.z), b4[v][1] = bf_hi(w.z), b4[v][2] = bf_lo(w.w), b4[v][3] = bf_hi(w.w);
+#pragma unroll
+              for (int g = 0; g < 4; ++g) big[g] = fmaxf(big[g], fmaxf(s4[v][g], fabsf(b4[v][g])));
+            }
+            bool grown = false;
+            int was[4];
+            float inv[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              // positive numbers order as whole numbers
+              const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big[g]));
+              was[g] = sg[g];
+              sg[g] = min(max(sg[g], (int)(top >> 23) + 1), kSigMost);
+              grown |= sg[g] != was[g];
+              inv[g] = __uint_as_float((uint32_t)(254 - sg[g]) << 23);
+            }
+            if (grown) {  // the same for all lanes
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const float cut = sg[g] == was[g] ? 1.0f : ex2((float)(was[g] - sg[g]));
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+#pragma unroll
+                  for (int j = g * (kKS / 4); j < (g + 1) * (kKS / 4); ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[j][i][e] *= cut;
+                  if (gq == g) {
+                    sb[i][0] *= cut;
+                    sb[i][1] *= cut;
+                  }
+                }
+              }
+            }
+            // this lane's position as the low or high half of its pair: even
+            // lanes take groups 0 and 1 of both, odd lanes 2 and 3
+            const bool odd = lane & 1;
+#pragma unroll
+            for (int v = 0; v < kOf; ++v) {
+              const uint32_t sa = pack2<true>(s4[v][0] * inv[0], s4[v][1] * inv[1]);
+              const uint32_t sc = pack2<true>(s4[v][2] * inv[2], s4[v][3] * inv[3]);
+              const uint32_t ba = pack2<true>(b4[v][0] * inv[0], b4[v][1] * inv[1]);
+              const uint32_t bc = pack2<true>(b4[v][2] * inv[2], b4[v][3] * inv[3]);
+              const uint32_t xs = __shfl_xor_sync(0xFFFFFFFFu, odd ? sa : sc, 1);
+              const uint32_t xb = __shfl_xor_sync(0xFFFFFFFFu, odd ? ba : bc, 1);
+              const uint32_t ls = odd ? xs : sa, hs = odd ? sc : xs;
+              const uint32_t lb = odd ? xb : ba, hb = odd ? bc : xb;
+              const uint32_t tv = scratch + kVal + ((lane >> 1) + 16 * v) * 32 + odd * 8;
+              sts64(tv, __byte_perm(ls, hs, 0x5410), __byte_perm(ls, hs, 0x7632));
+              sts64(tv + 16, __byte_perm(lb, hb, 0x5410), __byte_perm(lb, hb, 0x7632));
+            }
+          }
           // ---- the reference m follows the running maximum when that is kSlack
           // ahead of it; what was summed up to then follows
           float mx[NT][2];
@@ -724,6 +730,7 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
           for (int i = 0; i < NT; ++i)
             up[i] = pair2(__float_as_uint(kLift - (m[i][0] == -INFINITY ? 0.0f : m[i][0])),
                           __float_as_uint(kLift - (m[i][1] == -INFINITY ? 0.0f : m[i][1])));
+          __syncwarp();
           // ---- weights and the second product, sixteen positions a step
 #pragma unroll
           for (int kp = 0; kp < kBlk / 16; ++kp) {

@@ -38,13 +38,25 @@
 // registers for sixteen positions. With queries as columns, a lane has two of
 // them, and their maxima, factors and sums need no exchange between lanes.
 //
-// Every warp works by itself: the (slot, head, row tile) pairs' units of 32
-// positions lie on one line, warp w takes units [w per, (w + 1) per), and
-// fetches them through a ring of its own (one bulk copy of keys, one of values
-// a unit: rows of a head lie together in a page). A pair that lies within a
-// warp's share goes straight to the output; what a share's ends cut is left in
+// Every warp works by itself: the pages of the (slot, head, row tile) pairs lie
+// on one line, warp w takes units (a page of one head) [w per, (w + 1) per), and
+// fetches them through a ring of its own, one bulk copy of keys and one of
+// values a unit: rows of a head lie together in a page. A pair that lies within
+// a warp's share goes straight to the output; what a share's ends cut is left in
 // shared memory, joined by the CTA, and where the CTA's ends cut it, left in
 // the workspace and joined by the last of its CTAs to arrive, in CTA order.
+//
+// Measured on one GB300, 16 query heads on 2 of 128, in us a call:
+//  - 48 slots of some 8.4K, 123 MB: 29.3, of which the pages take 20 (6 TB/s,
+//    0.9 of a plain copy's rate), the lengths, tables and first pages 4, joining
+//    4; 8 slots of some 112K, 250 MB: 50.3, 5.0 TB/s. HBM bounds both. Twelve
+//    warps with half a page a unit took 33.7 and 56.0: a unit's fixed work (two
+//    copies, a wait, scales exchanged, maxima compared) then weighs twice.
+//  - 256 slots of up to 16K and 4 tokens, 513 MB read for two tiles of 16 rows:
+//    208, bound by instruction latency: two warps a scheduler (queries, O and
+//    scores of 16 rows take all registers) issue in 46 cycles of a hundred, the
+//    tensor pipe is busy in 42. Tiles of 32 rows (spills) took 330, 12 warps
+//    of half pages 296.
 #include "attn_q4.cuh"
 
 namespace moe {
@@ -119,7 +131,8 @@ __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -150,6 +163,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "r"(a)
                : "memory");
   return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  const uint4 v = lds128(a);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ float elem4(const float4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ uint64_t pair_f(float a, float b) {
+  return pair2(__float_as_uint(a), __float_as_uint(b));
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
                                           uint64_t policy) {
@@ -243,8 +266,10 @@ __device__ __forceinline__ void store_out(uint16_t* p, const Elems<V>& x, float 
     *reinterpret_cast<uint32_t*>(p) = lo;
 }
 // four more parts
-__device__ __forceinline__ void join4(Joined& j, const float (&m)[4], const float (&l)[4], const float4 (&v)[4]) {
-  const float M = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), j.M), U = M == -INFINITY ? 0.0f : M;
+__device__ __forceinline__ void join4(Joined& j, const float (&m)[4], const float (&l)[4],
+                                      const float4 (&v)[4]) {
+  const float M = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), j.M);
+  const float U = M == -INFINITY ? 0.0f : M;
   const float f = ex2(j.M - U);
   j.L *= f;
   j.o = make_float4(j.o.x * f, j.o.y * f, j.o.z * f, j.o.w * f);
@@ -252,7 +277,8 @@ __device__ __forceinline__ void join4(Joined& j, const float (&m)[4], const floa
   for (int k = 0; k < 4; ++k) {
     const float w = ex2(m[k] - U);
     j.L = fmaf(l[k], w, j.L);
-    j.o = make_float4(fmaf(v[k].x, w, j.o.x), fmaf(v[k].y, w, j.o.y), fmaf(v[k].z, w, j.o.z), fmaf(v[k].w, w, j.o.w));
+    j.o = make_float4(fmaf(v[k].x, w, j.o.x), fmaf(v[k].y, w, j.o.y), fmaf(v[k].z, w, j.o.z),
+                      fmaf(v[k].w, w, j.o.w));
   }
   j.M = M;
 }
@@ -370,7 +396,8 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
       }
       if ((lu & ~31) != base) {
         base = lu & ~31;
-        pages = base + lane < a.max_blocks ? __ldg(a.table + (int64_t)ld.s * a.max_blocks + base + lane) : -1;
+        const int64_t at = (int64_t)ld.s * a.max_blocks + base + lane;
+        pages = base + lane < a.max_blocks ? __ldg(a.table + at) : -1;
       }
       const int page = __shfl_sync(0xFFFFFFFFu, pages, lu & 31);
       const int n = min(kBlk, ld.sp.len - lu * kBlk);
@@ -510,8 +537,8 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
         for (int c = 0; c < C::kCh; ++c)
 #pragma unroll
           for (int i = 0; i < NT; ++i)
-            sts128(queries + (c * NT + i) * 512 + lane * 16, qa[2 * c][i], qa[2 * c][NT + i], qa[2 * c + 1][i],
-                   qa[2 * c + 1][NT + i]);
+            sts128(queries + (c * NT + i) * 512 + lane * 16, qa[2 * c][i], qa[2 * c][NT + i],
+                   qa[2 * c + 1][i], qa[2 * c + 1][NT + i]);
       }
       float m[NT][2], sb[NT][4], o[kKS][NT][4];
       int sg[4];  // biased exponents of the groups' powers of two
@@ -571,9 +598,8 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
               }
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint4 s0 = lds128(scratch + (16 * (2 * v + h) + gq) * 16), s1 = lds128(scratch + (16 * (2 * v + h) + gq + 8) * 16);
-                const float s[2][4] = {{__uint_as_float(s0.x), __uint_as_float(s0.y), __uint_as_float(s0.z), __uint_as_float(s0.w)},
-                                       {__uint_as_float(s1.x), __uint_as_float(s1.y), __uint_as_float(s1.z), __uint_as_float(s1.w)}};
+                const uint32_t at = scratch + (16 * (2 * v + h) + gq) * 16;
+                const float4 s[2] = {lds_f4(at), lds_f4(at + 128)};
                 uint32_t kc[4];  // words of pieces c and c + 1 of positions gq, gq + 8
                 ldsm4(sk + (16 * (2 * v + h) + (lane & 15)) * C::kRow + (c + (lane >> 4)) * 16, kc);
 #pragma unroll
@@ -587,13 +613,16 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                       if (D == 64 || e == 0)
-                        mma_f16_0(acc[i], w0 & kLoNib, w1 & kLoNib, w0 & kHiNib, w1 & kHiNib, qa[ks][i], qa[ks][NT + i]);
+                        mma_f16_0(acc[i], w0 & kLoNib, w1 & kLoNib, w0 & kHiNib, w1 & kHiNib, qa[ks][i],
+                                  qa[ks][NT + i]);
                       else
-                        mma_f16(acc[i], w0 & kLoNib, w1 & kLoNib, w0 & kHiNib, w1 & kHiNib, qa[ks][i], qa[ks][NT + i]);
+                        mma_f16(acc[i], w0 & kLoNib, w1 & kLoNib, w0 & kHiNib, w1 & kHiNib, qa[ks][i],
+                                qa[ks][NT + i]);
                       if (D == 64 || e == 1)
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
-                          t[h][i][z] = g == 0 ? s[z >> 1][0] * acc[i][z] : fmaf(s[z >> 1][g], acc[i][z], t[h][i][z]);
+                          t[h][i][z] = g == 0 ? s[z >> 1].x * acc[i][z]
+                                              : fmaf(elem4(s[z >> 1], g), acc[i][z], t[h][i][z]);
                     }
                   }
                 }
@@ -608,11 +637,11 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
                 float xb[4];
                 mma_bf16_k8_0(xb, bw0, bw1, qs[i]);
                 mma_bf16_k8(xb, bw0, bw1, qs[NT + i]);
-                const uint64_t f2 = pair2(__float_as_uint(cf[i][0]), __float_as_uint(cf[i][1]));
+                const uint64_t f2 = pair_f(cf[i][0], cf[i][1]);
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                  x[2 * v + h][y][i] = fma2(pair2(__float_as_uint(t[h][i][2 * y]), __float_as_uint(t[h][i][2 * y + 1])), f2,
-                                    pair2(__float_as_uint(xb[2 * y]), __float_as_uint(xb[2 * y + 1])));
+                  x[2 * v + h][y][i] = fma2(pair_f(t[h][i][2 * y], t[h][i][2 * y + 1]), f2,
+                                            pair_f(xb[2 * y], xb[2 * y + 1]));
               }
             }
           }
@@ -626,7 +655,7 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
                 unpair2(x[h >> 1][h & 1][i], x0, x1);
                 if (pos0 + 8 * h + gq > lim[i][0]) x0 = -INFINITY;
                 if (pos0 + 8 * h + gq > lim[i][1]) x1 = -INFINITY;
-                x[h >> 1][h & 1][i] = pair2(__float_as_uint(x0), __float_as_uint(x1));
+                x[h >> 1][h & 1][i] = pair_f(x0, x1);
               }
           }
           // ---- values' scales and biases, while the products run
@@ -728,8 +757,8 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
           uint64_t up[NT];
 #pragma unroll
           for (int i = 0; i < NT; ++i)
-            up[i] = pair2(__float_as_uint(kLift - (m[i][0] == -INFINITY ? 0.0f : m[i][0])),
-                          __float_as_uint(kLift - (m[i][1] == -INFINITY ? 0.0f : m[i][1])));
+            up[i] = pair_f(kLift - (m[i][0] == -INFINITY ? 0.0f : m[i][0]),
+                           kLift - (m[i][1] == -INFINITY ? 0.0f : m[i][1]));
           __syncwarp();
           // ---- weights and the second product, sixteen positions a step
 #pragma unroll
@@ -873,7 +902,8 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
   const int share = kWarps * per;
   auto store = [&](const PieceInfo& p, int r, int d, const float4& y, float l) {
     const int R = p.tile * kR + r, t = token(R);
-    if (R < rows) store4<F16>(a.o + (((int64_t)p.s * a.T + t) * a.n_q + p.head * G + R - t * G) * D + 4 * d, y, l);
+    uint16_t* to = a.o + (((int64_t)p.s * a.T + t) * a.n_q + p.head * G + R - t * G) * D + 4 * d;
+    if (R < rows) store4<F16>(to, y, l);
   };
   bool cut = false;
   for (unsigned rest = pieces; rest;) {
@@ -952,6 +982,8 @@ namespace {
 int row_tiles(const moe_attn_batch_shape_t* s) {
   return (s->T * (s->n_q / s->n_kv) + kMostRows - 1) / kMostRows;
 }
+// the start and end of a pair against a unit: 31.6 us without, 29.5 with one and
+// 31.7 with two for 48 slots of 8K, 27, 23.4 and 23.2 for 33 ragged ones
 constexpr int kPairCost = 1;
 constexpr size_t part_floats(int D) { return 2 * kMostRows + kMostRows * (D + 4); }
 constexpr size_t kCountAt = 256, kPartAt = kCountAt + kMostCtas * kMostChunks * 4;
@@ -980,9 +1012,8 @@ bool attn_q4_supported(const moe_attn_batch_shape_t* s) {
 }
 
 // status, the CTAs' counters (one for 32 items), their two places for parts, the
-// warps' places for pieces. The counters are
-// all that one call leaves to the next (zeros), and nothing lies elsewhere for
-// another shape.
+// warps' places for pieces. The counters are all that one call leaves to the
+// next (zeros), and their place and extent are the same for every shape.
 size_t attn_q4_ws_bytes(const moe_attn_batch_shape_t* s) {
   return kPartAt + (2 + kWarps) * (size_t)kMostCtas * part_floats(s->D) * 4;
 }

@@ -31,11 +31,13 @@
 // shares with one other (D = 128) or has alone, so that a row's bookkeeping and
 // a group's scale are paid once for as many; fp32 pairs share instructions, no
 // element branches, and nothing divides. 111 thousand positions of 2 heads of
-// 128 written, 148 MB, take 38 us, 3.9 TB/s (150 instructions a thread and row:
-// the integer pipe is busy in 63 cycles of a hundred), and read back 27 us, 5.4
+// 128 written, 148 MB, take 35 us, 4.2 TB/s (120 instructions a thread and row:
+// the integer pipe is busy in 60 cycles of a hundred), and read back 26 us, 5.6
 // TB/s. (Eight elements a thread, a division a group and each code checked for a
 // border by itself took 78 and 50; borders checked by how near fp32 comes to
 // them 61, as 16-bit numbers meet borders in most warps.)
+#include <type_traits>
+
 #include "attn_q4.cuh"
 
 namespace moe {
@@ -155,34 +157,55 @@ __device__ __forceinline__ bool in_doubt(const uint4 (&v)[2], float b, float s, 
   return border && found;
 }
 
-// Where a call's rows lie: a CTA has 2^log_t tokens of some slots a pass, and
-// its passes go on along the tokens (chunks > 0: how many CTAs a slot has) or
-// along the slots.
-struct RowsPlan {
-  int log_t, chunks;
-};
-template <int D>
-struct RowOf {
-  int s, t;
-};
-template <int D>
-__device__ __forceinline__ RowOf<D> row_of(const RowsPlan& p, int k) {
-  constexpr int kStep = kThr / (D / 16);  // rows of a pass
-  const int r = threadIdx.x / (D / 16), t = r & ((1 << p.log_t) - 1);
-  if (p.chunks > 0) {
-    const int s = blockIdx.x / (unsigned)p.chunks;
-    return RowOf<D>{s, ((int)blockIdx.x - s * p.chunks) * (kStep * kRows) + k * kStep + t};
+// Where a call's rows lie. LONG: a CTA has one slot's tokens, its passes go on
+// along them (n: how many CTAs a slot has); else 2^n tokens of some slots a
+// pass, and its passes go on along the slots.
+template <int D, bool LONG>
+struct Rows {
+  static constexpr int kStep = kThr / (D / 16);  // rows of a pass
+  int s0, t0, n;
+  __device__ __forceinline__ explicit Rows(int n_) : n(n_) {
+    const int r = threadIdx.x / (D / 16);
+    if (LONG) {
+      s0 = blockIdx.x / (unsigned)n;
+      t0 = ((int)blockIdx.x - s0 * n) * (kStep * kRows) + r;
+    } else {
+      s0 = ((int)blockIdx.x * (kRows * kStep) + r) >> n;
+      t0 = r & ((1 << n) - 1);
+    }
   }
-  return RowOf<D>{(((int)blockIdx.x * kRows + k) * kStep + r) >> p.log_t, t};
+  __device__ __forceinline__ int slot(int k) const { return LONG ? s0 : s0 + (k * kStep >> n); }
+  __device__ __forceinline__ int token(int k) const { return LONG ? t0 + k * kStep : t0; }
+};
+// A slot's new rows (write) or rows to read: the first one's position and how
+// many, 0 where the numbers are out of range.
+struct Span {
+  int pos, n;
+};
+__device__ __forceinline__ Span span_of(const CacheQ4Args& a, const int32_t* first, bool read, int s) {
+  const int n = a.n ? __ldg(a.n + s) : a.T, len = __ldg(a.lens + s);
+  const int pos = read ? (first ? __ldg(first + s) : 0) : len - n;
+  if (n < 0 || n > a.T || len < 0 || len > a.max_blocks * kPage || (n > 0 && (pos < 0 || pos > len - n))) {
+    set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
+    return Span{0, 0};
+  }
+  return Span{pos, n};
+}
+// The page of a position, -1 where there is none.
+__device__ __forceinline__ int page_of(const CacheQ4Args& a, int s, int pos) {
+  const int page = __ldg(a.table + (int64_t)s * a.max_blocks + pos / kPage);
+  if ((unsigned)page < (unsigned)a.n_phys) return page;
+  set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, s);
+  return -1;
 }
 }  // namespace
 
 // A thread has sixteen elements of kRows rows of one head and tensor
 // (blockIdx.y), a CTA tokens one after the other: it reads whole lines and
 // writes a stretch of a page.
-template <bool F16, int D>
+template <bool F16, int D, bool LONG>
 __global__ void __launch_bounds__(kThr)
-    cache_write_q4_kernel(const CacheQ4Args a, const RowsPlan plan, const uint16_t* __restrict__ k_new,
+    cache_write_q4_kernel(const CacheQ4Args a, int plan, const uint16_t* __restrict__ k_new,
                           int64_t k_stride, const uint16_t* __restrict__ v_new, int64_t v_stride) {
   constexpr int kLanes = D / 16;         // threads of a row
   constexpr int kUnits = q4_units(D);
@@ -195,28 +218,24 @@ __global__ void __launch_bounds__(kThr)
   pdl_trigger();
   uint4 x[kRows][2];
   int64_t at[kRows];  // the row's place in the pool, -1: nothing to write
+  const Rows<D, LONG> rows(plan);
+  Span sp{0, 0};
+  if (LONG) {
+    sp = span_of(a, nullptr, false, rows.s0);
+    if (rows.t0 - (int)threadIdx.x / kLanes >= sp.n) return;  // the whole CTA
+  }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    const RowOf<D> row = row_of<D>(plan, k);
+    const int s = rows.slot(k), tok = rows.token(k);
     at[k] = -1;
     x[k][0] = x[k][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (row.s >= a.n_slots || row.t >= a.T) continue;
-    const int n = a.n ? __ldg(a.n + row.s) : a.T, len = __ldg(a.lens + row.s);
-    if (n < 0 || n > a.T || len < n || len > a.max_blocks * kPage) {
-      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, row.s);
-      continue;
-    }
-    if (row.t >= n) continue;
-    const int pos = len - n + row.t;
-    const uint4* p = reinterpret_cast<const uint4*>(from + ((int64_t)row.s * a.T + row.t) * stride);
+    if (!LONG) sp = s < a.n_slots ? span_of(a, nullptr, false, s) : Span{0, 0};
+    if (tok >= sp.n) continue;
+    const uint4* p = reinterpret_cast<const uint4*>(from + ((int64_t)s * a.T + tok) * stride);
     x[k][0] = __ldg(p);
     x[k][1] = __ldg(p + 1);
-    const int page = __ldg(a.table + (int64_t)row.s * a.max_blocks + pos / kPage);
-    if (page < 0 || page >= a.n_phys) {
-      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, row.s);
-      continue;
-    }
-    at[k] = ((int64_t)page * a.n_kv * kPage + pos % kPage) * kUnits;
+    const int pos = sp.pos + tok, page = page_of(a, s, pos);
+    if (page >= 0) at[k] = ((int64_t)page * a.n_kv * kPage + pos % kPage) * kUnits;
   }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
@@ -304,9 +323,9 @@ __device__ __forceinline__ void values8(uint32_t w, uint32_t s0, uint32_t b0, ui
 }
 
 // The same arrangement the other way. DT: moe_dtype_t of what comes out.
-template <int DT, int D>
+template <int DT, int D, bool LONG>
 __global__ void __launch_bounds__(kThr)
-    cache_read_q4_kernel(const CacheQ4Args a, const RowsPlan plan, const int32_t* __restrict__ first,
+    cache_read_q4_kernel(const CacheQ4Args a, int plan, const int32_t* __restrict__ first,
                          void* __restrict__ k_out, int64_t k_stride, void* __restrict__ v_out,
                          int64_t v_stride) {
   constexpr int kLanes = D / 16, kUnits = q4_units(D);
@@ -324,31 +343,27 @@ __global__ void __launch_bounds__(kThr)
   uint2 w[kRows];
   uint32_t sa[kRows], ba[kRows], sb[kRows], bb[kRows];
   int64_t at[kRows];  // the token, -1: not there
+  const Rows<D, LONG> rows(plan);
+  Span sp{0, 0};
+  if (LONG) {
+    sp = span_of(a, first, true, rows.s0);
+    if (rows.t0 - (int)threadIdx.x / kLanes >= sp.n) return;  // the whole CTA
+  }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    const RowOf<D> row = row_of<D>(plan, k);
+    const int s = rows.slot(k), tok = rows.token(k);
     at[k] = -1;
-    if (row.s >= a.n_slots || row.t >= a.T) continue;
-    const int n = a.n ? __ldg(a.n + row.s) : a.T, len = __ldg(a.lens + row.s);
-    const int f = first ? __ldg(first + row.s) : 0;
-    if (n < 0 || n > a.T || len < 0 || len > a.max_blocks * kPage || (n > 0 && (f < 0 || f > len - n))) {
-      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, row.s);
-      continue;
-    }
-    if (row.t >= n) continue;
-    const int pos = f + row.t;
-    const int page = __ldg(a.table + (int64_t)row.s * a.max_blocks + pos / kPage);
-    if (page < 0 || page >= a.n_phys) {
-      if (part == 0) set_error(a.ctrl, MOE_ERR_BAD_INPUT, KID_CACHE, row.s);
-      continue;
-    }
+    if (!LONG) sp = s < a.n_slots ? span_of(a, first, true, s) : Span{0, 0};
+    if (tok >= sp.n) continue;
+    const int pos = sp.pos + tok, page = page_of(a, s, pos);
+    if (page < 0) continue;
     const uint16_t* q = pool + ((int64_t)page * a.n_kv * kPage + pos % kPage) * kUnits;
     w[k] = __ldg(reinterpret_cast<const uint2*>(q) + part);
     sa[k] = __ldg(q + D / 4 + ga);
     ba[k] = __ldg(q + D / 4 + 4 + ga);
     sb[k] = D == 64 ? __ldg(q + D / 4 + gb) : 0u;
     bb[k] = D == 64 ? __ldg(q + D / 4 + 4 + gb) : 0u;
-    at[k] = (int64_t)row.s * a.T + row.t;
+    at[k] = (int64_t)s * a.T + tok;
   }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
@@ -387,6 +402,9 @@ bool cache_q4_supported(const moe_cache_shape_t* s) {
 }
 
 namespace {
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 CacheQ4Args args_of(const moe_cache_shape_t* s, const moe_cache_meta_t& meta, const int32_t* n,
                     int T, void* k, void* v, uint8_t* ws) {
   CacheQ4Args a;
@@ -403,20 +421,20 @@ CacheQ4Args args_of(const moe_cache_shape_t* s, const moe_cache_meta_t& meta, co
   a.ctrl = reinterpret_cast<Ctrl*>(ws);
   return a;
 }
-RowsPlan plan_of(const moe_cache_shape_t* s, int T, dim3* grid) {
+// Rows' n, and whether slots have more tokens than a pass (LONG).
+int plan_of(const moe_cache_shape_t* s, int T, bool* along, dim3* grid) {
   const int step = kThr / (s->D / 16);
-  RowsPlan p{0, 0};
-  while (1 << p.log_t < T && 1 << p.log_t < step) ++p.log_t;
-  int x;
-  if (T > step) {
-    p.chunks = (T + step * kRows - 1) / (step * kRows);
-    x = s->n_slots * p.chunks;  // below 2^12 * 2^13
-  } else {
-    const int slots = (step >> p.log_t) * kRows;
-    x = (s->n_slots + slots - 1) / slots;
+  *along = T > step;
+  if (*along) {
+    const int ctas = (T + step * kRows - 1) / (step * kRows);
+    *grid = dim3(s->n_slots * ctas, 2 * s->n_kv);  // below 2^12 * 2^13
+    return ctas;
   }
-  *grid = dim3(x, 2 * s->n_kv);
-  return p;
+  int log_t = 0;
+  while (1 << log_t < T) ++log_t;
+  const int slots = (step >> log_t) * kRows;
+  *grid = dim3((s->n_slots + slots - 1) / slots, 2 * s->n_kv);
+  return log_t;
 }
 }  // namespace
 
@@ -426,12 +444,16 @@ cudaError_t launch_cache_write_q4(const moe_cache_shape_t* s, const moe_cache_me
                                   bool fp16, void* k, void* v, uint8_t* ws, cudaStream_t stream) {
   const CacheQ4Args a = args_of(s, meta, n_new, T, k, v, ws);
   dim3 grid;
-  const RowsPlan plan = plan_of(s, T, &grid);
-  auto go = [&](auto kern) {
+  bool along;
+  const int plan = plan_of(s, T, &along, &grid);
+  auto go = [&](auto d, auto f) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool F16 = decltype(f)::value;
+    auto* kern = along ? cache_write_q4_kernel<F16, D, true> : cache_write_q4_kernel<F16, D, false>;
     return launch_pdl(kern, grid, dim3(kThr), 0, stream, a, plan, k_new, k_stride, v_new, v_stride);
   };
-  if (s->D == 64) return fp16 ? go(cache_write_q4_kernel<true, 64>) : go(cache_write_q4_kernel<false, 64>);
-  return fp16 ? go(cache_write_q4_kernel<true, 128>) : go(cache_write_q4_kernel<false, 128>);
+  if (s->D == 64) return fp16 ? go(Int<64>(), std::true_type()) : go(Int<64>(), std::false_type());
+  return fp16 ? go(Int<128>(), std::true_type()) : go(Int<128>(), std::false_type());
 }
 
 cudaError_t launch_cache_read_q4(const moe_cache_shape_t* s, const moe_cache_meta_t& meta,
@@ -440,18 +462,18 @@ cudaError_t launch_cache_read_q4(const moe_cache_shape_t* s, const moe_cache_met
                                  int64_t v_stride, int dtype, uint8_t* ws, cudaStream_t stream) {
   const CacheQ4Args a = args_of(s, meta, n, T, const_cast<void*>(k), const_cast<void*>(v), ws);
   dim3 grid;
-  const RowsPlan plan = plan_of(s, T, &grid);
-  auto go = [&](auto kern) {
+  bool along;
+  const int plan = plan_of(s, T, &along, &grid);
+  auto go = [&](auto d, auto dt) {
+    constexpr int D = decltype(d)::value, DT = decltype(dt)::value;
+    auto* kern = along ? cache_read_q4_kernel<DT, D, true> : cache_read_q4_kernel<DT, D, false>;
     return launch_pdl(kern, grid, dim3(kThr), 0, stream, a, plan, first, k_out, k_stride, v_out, v_stride);
   };
-  if (s->D == 64) {
-    if (dtype == MOE_DTYPE_FP32) return go(cache_read_q4_kernel<MOE_DTYPE_FP32, 64>);
-    return dtype == MOE_DTYPE_FP16 ? go(cache_read_q4_kernel<MOE_DTYPE_FP16, 64>)
-                                   : go(cache_read_q4_kernel<MOE_DTYPE_BF16, 64>);
-  }
-  if (dtype == MOE_DTYPE_FP32) return go(cache_read_q4_kernel<MOE_DTYPE_FP32, 128>);
-  return dtype == MOE_DTYPE_FP16 ? go(cache_read_q4_kernel<MOE_DTYPE_FP16, 128>)
-                                 : go(cache_read_q4_kernel<MOE_DTYPE_BF16, 128>);
+  auto type = [&](auto d) {
+    if (dtype == MOE_DTYPE_FP32) return go(d, Int<MOE_DTYPE_FP32>());
+    return dtype == MOE_DTYPE_FP16 ? go(d, Int<MOE_DTYPE_FP16>()) : go(d, Int<MOE_DTYPE_BF16>());
+  };
+  return s->D == 64 ? type(Int<64>()) : type(Int<128>());
 }
 
 }  // namespace moe

@@ -17,18 +17,18 @@
 // equal one has a higher id). Where more reach the groups' bar than the list
 // holds (many equal logits), those above it are listed and then, in id order,
 // as many of its equals as are missing. After 2, 4, 8 .. chunks the list is put
-// in order and the bar raised, so that some k elements enter in between and
+// in order and the bar raised, where more than one follows, so that some k elements enter in between and
 // the CTA's warps need not meet at every chunk (meeting at each, with chunks
 // of twice the size, took 203 us for 2048 rows of 128001). If more enter than
 // the list holds (rising logits), the CTA's stretch is read again, once for
 // each of the k.
 //
-// Many rows are bound by HBM: 2048 rows of 128001 bf16 logits, 524 MB, take 103
-// us, 5.1 TB/s, 0.75 of a plain copy's rate (ten instructions a logit, one of
+// Many rows are bound by HBM: 2048 rows of 128001 bf16 logits, 524 MB, take 102
+// us, 5.15 TB/s, 0.75 of a plain copy's rate (ten instructions a logit, one of
 // them an exponential; pairs of fp32 numbers share what they can). Few rows are
-// a chain of waits: 64 rows of 131072 with twenty alternatives, 17 MB, take 14.4
-// us - logits 2, sums 0.6, the bar 0.8, the list 2.5, the second chunk 2, the
-// part and the arrival 2.5, joining and ordering eight stretches' lists 3.
+// a chain of waits: 64 rows of 131072 with twenty alternatives, 17 MB, take 14.0
+// us - logits 2, sums 0.5, the bar 1, the list 1.2, the second chunk 1.6, the
+// part and the arrival 2, joining and ordering eight stretches' lists 3.
 #include <cfloat>
 #include <type_traits>
 
@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kLThr, kCtas) logprobs_kernel(const LogpArgs a
   Sums s{-INFINITY, 0.0f, 0.0f};
   float bar = -FLT_MAX;   // what a further element has to reach
   bool over = false;      // more came than the list holds
+  bool spilled = false;   // an entry of this thread found it full
   uint4 v[kVec];
   if (c0 < c1) load(c0, v);
   for (int c = c0; c < c1; ++c) {
@@ -367,12 +368,16 @@ __global__ void __launch_bounds__(kLThr, kCtas) logprobs_kernel(const LogpArgs a
           for (; mask; mask &= mask - 1) {
             const int b = __ffs(mask) - 1, id = first_of(c, b / E::kN) + b % E::kN;
             const int at = atomicAdd(&list.n, 1);
-            if (at < kMost) list.e[at] = entry(own(b), id);
+            if (at < kMost)
+              list.e[at] = entry(own(b), id);
+            else
+              spilled = true;
           }
         }
         if (!meet || over) break;
-        __syncthreads();
-        if (list.n <= kMost) break;
+        // the same answer for all: list.n may grow as soon as one thread goes on
+        if (!__syncthreads_or(spilled)) break;
+        spilled = false;
         // too many: of the first chunk those above the groups' bar and then the
         // first of its equals, once
         over = !begin || equals;

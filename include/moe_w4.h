@@ -682,8 +682,10 @@ moe_status_t moe_cache_read_q4(const moe_cache_shape_t* shape, const moe_cache_m
  * fp32 scores, sums and biases' part of the output; a softmax weight times a
  * value's scale is rounded to fp16 (under a power of two that keeps it in
  * range) before it multiplies the codes, whatever dtype is. Scales and biases
- * of positions below a slot's length have to be finite; what its pages hold
- * past it does not matter. Deterministic. The workspace (256-byte aligned) is zero-filled once
+ * of positions below a slot's length have to be finite, those of values of at
+ * most 2^80 (sums of weights times values are kept in fp32 and divided at the
+ * end; 2^-100 counts as nothing); what its pages hold past it does not matter.
+ * Deterministic. The workspace (256-byte aligned) is zero-filled once
  * (moe_workspace_init); after MOE_ERR_TIMEOUT, again. Calls of any shape can
  * use it in turn where it is large enough, but no other call of this library.
  * n_slots * n_kv * ceil(T * n_q / n_kv / 16) * (max_blocks + 1) has to be

@@ -211,3 +211,28 @@ def test_rows_past_32_bits_of_bytes():
     lp, ent, ids, top = call(x, [3] * n, 4)
     check(x[some], [3] * 4, 4, (lp[some], ent[some], ids[some], top[some]))
     assert ids[2].tolist() == [0, 1, 2, 3]
+
+
+@pytest.mark.parametrize("dtype,vec", [("bf16", 8), ("fp32", 4)])
+@pytest.mark.parametrize("first,more", [(256, 0), (256, 1), (255, 1), (250, 40), (256, 300), (257, 5)])
+@pytest.mark.parametrize("chunks", [2, 3])
+@pytest.mark.parametrize("n", [3, 900])
+def test_a_list_that_is_about_full(dtype, vec, first, more, chunks, n):
+    # the first chunk (1024 vectors) brings as many as the list holds or nearly,
+    # in all of the 64 groups of four threads that the bar comes from; what
+    # follows overfills it
+    chunk = 1024 * vec
+    x = torch.full((n, chunks * chunk), -3.0)
+    at = torch.arange(first)
+    x[:, (at % 64) * 4 * vec + at // 64 % 4 * vec + at // 256] = 5.0
+    for c in range(1, chunks):
+        x[:, c * chunk + 7 * torch.arange(more)] = 5.0 + c
+    x = x.to(TYPES[dtype]).to(DEV)
+    tokens = [(i * 7919) % x.shape[1] for i in range(n)]
+    if n <= 3:
+        check(x, tokens, 32)
+        return
+    lp, ent, ids, top = call(x, tokens, 32)
+    _, _, wids, _ = ref.logprobs(x[:1].cpu().double().numpy(), tokens[:1], 32)
+    assert torch.equal(ids, torch.from_numpy(wids).to(ids).expand_as(ids))
+    assert torch.equal(top, top[:1].expand_as(top)) and torch.equal(ent, ent[:1].expand_as(ent))

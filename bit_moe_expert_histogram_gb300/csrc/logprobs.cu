@@ -17,14 +17,14 @@
 // equal one has a higher id). Where more reach the groups' bar than the list
 // holds (many equal logits), those above it are listed and then, in id order,
 // as many of its equals as are missing. After 2, 4, 8 .. chunks the list is put
-// in order and the bar raised, where more than one follows, so that some k elements enter in between and
-// the CTA's warps need not meet at every chunk (meeting at each, with chunks
-// of twice the size, took 203 us for 2048 rows of 128001). If more enter than
-// the list holds (rising logits), the CTA's stretch is read again, once for
-// each of the k.
+// in order and the bar raised, where more than one follows, so that some k
+// elements enter in between and the CTA's warps need not meet at every chunk
+// (meeting at each, with chunks of twice the size, took 203 us for 2048 rows of
+// 128001). If more enter than the list holds (rising logits), the CTA's stretch
+// is read again, once for each of the k.
 //
 // Many rows are bound by HBM: 2048 rows of 128001 bf16 logits, 524 MB, take 102
-// us, 5.15 TB/s, 0.75 of a plain copy's rate (ten instructions a logit, one of
+// us, 5.15 TB/s, 0.76 of a plain copy's rate (ten instructions a logit, one of
 // them an exponential; pairs of fp32 numbers share what they can). Few rows are
 // a chain of waits: 64 rows of 131072 with twenty alternatives, 17 MB, take 14.0
 // us - logits 2, sums 0.5, the bar 1, the list 1.2, the second chunk 1.6, the

@@ -133,8 +133,8 @@ struct Sums {
 // the same sums from another maximum, M >= s.m
 __device__ __forceinline__ Sums from(const Sums& s, float M) {
   const float d = s.m - M, f = ex2(d * 1.4426950408889634f);
-  // nothing so far: no inf * 0
-  return s.Z == 0.0f ? Sums{M, 0.0f, 0.0f} : Sums{M, s.Z * f, fmaf(d, s.Z, s.A) * f};
+  // nothing so far, or far below (the lowest number as a mask): no inf * 0
+  return s.Z == 0.0f ? Sums{M, 0.0f, 0.0f} : Sums{M, s.Z * f, f == 0.0f ? 0.0f : fmaf(d, s.Z, s.A) * f};
 }
 // the sums of `n` lanes (a power of two), by each of them
 __device__ __forceinline__ Sums join(const Sums& s, int n) {

@@ -701,8 +701,8 @@ moe_status_t moe_attn_batch_q4(const moe_attn_batch_shape_t* shape, const void* 
  * the rows' entropies and likeliest tokens:
  *   logp = x_token - ln sum_v e^x_v, entropy = - sum_v p_v ln p_v (nats),
  *   top: the k ids of the largest logits, ties to the lower id, in that order.
- * A logit of -inf is a token that cannot be: it has no weight and is not
- * listed; ids that are missing for that, or where V < k, are -1 with -inf.
+ * Logits are -inf, the type's lowest number or of at most 2^100. One of -inf
+ * is a token that cannot be: it has no weight and is not listed; ids that are missing for that, or where V < k, are -1 with -inf.
  * fp32 sums in a fixed order: deterministic. A row of nothing but -inf, or
  * with NaN or +inf, gives NaN, ids of -1, and is recorded as
  * MOE_ERR_BAD_INPUT.

@@ -123,9 +123,8 @@ def logprobs(x, tokens, k):
     """x float64 [n][V]: logp, entropy, top ids, top logp."""
     n, V = x.shape
     m = x.max(-1, keepdims=True)
-    e = np.exp(x - m)
-    lse = m[:, 0] + np.log(e.sum(-1))
-    lp = x - lse[:, None]
+    d = x - m
+    lp = d - np.log(np.exp(d).sum(-1, keepdims=True))
     p = np.exp(lp)
     ent = -(p * np.where(p > 0, lp, 0.0)).sum(-1)
     got = np.array([lp[i, t] if t >= 0 else 0.0 for i, t in enumerate(tokens)])

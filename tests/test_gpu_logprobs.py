@@ -236,3 +236,22 @@ def test_a_list_that_is_about_full(dtype, vec, first, more, chunks, n):
     _, _, wids, _ = ref.logprobs(x[:1].cpu().double().numpy(), tokens[:1], 32)
     assert torch.equal(ids, torch.from_numpy(wids).to(ids).expand_as(ids))
     assert torch.equal(top, top[:1].expand_as(top)) and torch.equal(ent, ent[:1].expand_as(ent))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("n,V", [(6, 9000), (6, 70001), (700, 9000)])
+def test_masks_of_the_lowest_number(dtype, n, V):
+    """Rows of which whole threads', warps' and stretches' shares are the
+    type's lowest number, alone or beside -inf: it weighs nothing beside an
+    ordinary logit, but it is listed, and alone it is a distribution."""
+    low = torch.finfo(TYPES[dtype]).min
+    x = logits(10, n, V, dtype)
+    x[0, 100:] = low
+    x[1, :] = low
+    x[2, :], x[2, 1::2] = low, -float("inf")
+    x[3, :], x[3, V - 1] = low, -3.0
+    x[4, :V // 2], x[4, V // 2:] = -float("inf"), low
+    x[5, :-5] = low
+    tokens = [(i * 7919) % V for i in range(n)]
+    got = call(x, tokens, 8)
+    check(x[:6], tokens[:6], 8, [y[:6] for y in got])

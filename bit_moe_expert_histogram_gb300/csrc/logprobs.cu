@@ -12,16 +12,17 @@
 // The k likeliest, ties to the lower id. Of the first chunk that a CTA reads
 // (16 bytes a thread and vector, held in registers) the k-th largest of the
 // maxima of 64 groups of threads is a number that at least k elements reach,
-// and few do: those are listed, ordered by counting, and the k-th of them is
-// the bar for what follows, where only a larger number can still enter (an
-// equal one has a higher id). Where more reach the groups' bar than the list
-// holds (many equal logits), those above it are listed and then, in id order,
-// as many of its equals as are missing. After 2, 4, 8 .. chunks the list is put
-// in order and the bar raised, where more than one follows, so that some k
-// elements enter in between and the CTA's warps need not meet at every chunk
-// (meeting at each, with chunks of twice the size, took 203 us for 2048 rows of
-// 128001). If more enter than the list holds (rising logits), the CTA's stretch
-// is read again, once for each of the k.
+// and few do (where fewer groups have anything, the k-th of the threads'): those
+// are listed, ordered by counting, and the k-th of them is the bar for what
+// follows, where only a larger number can still enter (an equal one has a higher
+// id). Where more reach the first bar than the list holds (many equal logits),
+// those above it are listed and then, in id order, as many of its equals as are
+// missing. After 2, 4, 8 .. chunks the list is put in order and the bar raised,
+// where more than one follows, so that some k elements enter in between and the
+// CTA's warps need not meet at every chunk (meeting at each, with chunks of
+// twice the size, took 203 us for 2048 rows of 128001). If more enter than the
+// list holds (rising logits), the CTA's stretch is read again, once for each of
+// the k.
 //
 // Many rows are bound by HBM: 2048 rows of 128001 bf16 logits, 524 MB, take 102
 // us, 5.15 TB/s, 0.76 of a plain copy's rate (ten instructions a logit, one of
@@ -216,8 +217,29 @@ __device__ __forceinline__ float entry_x(uint64_t e) {
   const uint32_t u = (uint32_t)(e >> 32);
   return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
 }
+// A maximum among `n` (a power of two): in an order-keeping form that ends in
+// as many zeros as the number, whose last places are the index, lower ones
+// larger; and the number back, or the one below it whose last places are zeros.
+__device__ __forceinline__ uint32_t place(float x, int i, int n) {
+  const uint32_t u = __float_as_uint(x + 0.0f), c = u & 0x80000000u ? 0u - u : u | 0x80000000u;
+  return (c & (uint32_t)-n) | (uint32_t)(n - 1 - i);
+}
+__device__ __forceinline__ float placed(uint32_t p, int n) {
+  const uint32_t c = p & (uint32_t)-n;
+  return __uint_as_float(c & 0x80000000u ? c & 0x7FFFFFFFu : 0u - c);
+}
+// how many of t[from], four each `step`, below t[n], are before p
+__device__ __forceinline__ int before(const uint32_t* t, int from, int step, int n, uint32_t p) {
+  int r = 0;
+#pragma unroll 4
+  for (int j = from; j < n; j += step) {
+    const uint4 o = *reinterpret_cast<const uint4*>(t + j);
+    r += (o.x > p) + (o.y > p) + (o.z > p) + (o.w > p);
+  }
+  return r;
+}
 struct TopList {
-  uint64_t e[kCap];
+  alignas(16) uint64_t e[kCap];
   uint64_t best[kMostTop];
   int n;
 };
@@ -250,7 +272,7 @@ __global__ void __launch_bounds__(kLThr, kCtas) logprobs_kernel(const LogpArgs a
   using E = El<DT>;
   __shared__ TopList list;
   __shared__ uint4 s_vec[TOP ? kLThr : 1][kVec];
-  __shared__ __align__(16) float s_group[kLGroups];
+  __shared__ __align__(16) uint32_t s_group[kLGroups];
   __shared__ float s_bar, s_w[3][kLWarps];
   __shared__ int s_scan[kLWarps], s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -325,22 +347,30 @@ __global__ void __launch_bounds__(kLThr, kCtas) logprobs_kernel(const LogpArgs a
         float g = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 2));
         g = g != g ? -INFINITY : g;
-        const int mine = tid >> 2, q = tid & 3;
-        if (q == 0) s_group[mine] = g;
+        const int q = tid & 3;
+        uint32_t mine = place(g, tid >> 2, kLGroups);
+        if (q == 0) s_group[tid >> 2] = mine;
         if (tid == 0) s_bar = -INFINITY;
         __syncthreads();
-        int rank = 0;
-#pragma unroll
-        for (int j = 4 * q; j < kLGroups; j += 16) {
-          const float4 o = *reinterpret_cast<const float4*>(s_group + j);
-          rank += (o.x > g || (o.x == g && j < mine)) + (o.y > g || (o.y == g && j + 1 < mine)) +
-                  (o.z > g || (o.z == g && j + 2 < mine)) + (o.w > g || (o.w == g && j + 3 < mine));
-        }
+        int rank = before(s_group, 4 * q, 16, kLGroups, mine);
         rank += __shfl_xor_sync(0xFFFFFFFFu, rank, 1);
         rank += __shfl_xor_sync(0xFFFFFFFFu, rank, 2);
-        if (q == 0 && rank == a.k - 1) s_bar = g;
+        if (q == 0 && rank == a.k - 1) s_bar = placed(mine, kLGroups);
         __syncthreads();
         low = s_bar;
+        if (low == -INFINITY) {
+          // fewer groups have anything (a short row, or most of it masked): the
+          // k-th of the threads' maxima (1160 rows of 952, the first 32: 244 us
+          // without, as all of a row then overfills the list, 16.7 with)
+          uint32_t* one = reinterpret_cast<uint32_t*>(list.e);
+          g = top != top ? -INFINITY : top;
+          mine = place(g, tid, kLThr);
+          one[tid] = mine;
+          __syncthreads();
+          if (g > -INFINITY && before(one, 0, 4, kLThr, mine) == a.k - 1) s_bar = placed(mine, kLThr);
+          __syncthreads();
+          low = s_bar;
+        }
         bar = fmaxf(low, -FLT_MAX);
       }
       const int seen = c - c0 + 1;

@@ -46,6 +46,7 @@ namespace {
 constexpr int kPage = 64;  // positions per page
 constexpr int kThr = 256;
 constexpr int kRows = 2;   // rows a thread has a piece of
+constexpr int kMostCtas = 4096;  // where slots have more tokens than a pass, or a CTA a slot
 
 template <bool F16>
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // NaN if either is
@@ -158,8 +159,9 @@ __device__ __forceinline__ bool in_doubt(const uint4 (&v)[2], float b, float s, 
 }
 
 // Where a call's rows lie. LONG: a CTA has one slot's tokens, its passes go on
-// along them (n: how many CTAs a slot has); else 2^n tokens of some slots a
-// pass, and its passes go on along the slots.
+// along them, and where the slot has more than its n CTAs take at once the CTA
+// goes on n times as far; else 2^n tokens of some slots a pass, and its passes go
+// on along the slots.
 template <int D, bool LONG>
 struct Rows {
   static constexpr int kStep = kThr / (D / 16);  // rows of a pass
@@ -176,6 +178,11 @@ struct Rows {
   }
   __device__ __forceinline__ int slot(int k) const { return LONG ? s0 : s0 + (k * kStep >> n); }
   __device__ __forceinline__ int token(int k) const { return LONG ? t0 + k * kStep : t0; }
+  // goes on along the slot, false (for the whole CTA) behind its last token
+  __device__ __forceinline__ bool next(int tokens) {
+    t0 += n * (kStep * kRows);
+    return LONG && t0 - (int)threadIdx.x / (D / 16) < tokens;
+  }
 };
 // A slot's new rows (write) or rows to read: the first one's position and how
 // many, 0 where the numbers are out of range.
@@ -216,71 +223,73 @@ __global__ void __launch_bounds__(kThr)
   uint16_t* pool = static_cast<uint16_t*>(is_v ? a.v : a.k) + (int64_t)head * kPage * kUnits;
   pdl_wait();
   pdl_trigger();
-  uint4 x[kRows][2];
-  int64_t at[kRows];  // the row's place in the pool, -1: nothing to write
-  const Rows<D, LONG> rows(plan);
+  Rows<D, LONG> rows(plan);
   Span sp{0, 0};
   if (LONG) {
     sp = span_of(a, nullptr, false, rows.s0);
     if (rows.t0 - (int)threadIdx.x / kLanes >= sp.n) return;  // the whole CTA
   }
+  do {
+    uint4 x[kRows][2];
+    int64_t at[kRows];  // the row's place in the pool, -1: nothing to write
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const int s = rows.slot(k), tok = rows.token(k);
-    at[k] = -1;
-    x[k][0] = x[k][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (!LONG) sp = s < a.n_slots ? span_of(a, nullptr, false, s) : Span{0, 0};
-    if (tok >= sp.n) continue;
-    const uint4* p = reinterpret_cast<const uint4*>(from + ((int64_t)s * a.T + tok) * stride);
-    x[k][0] = __ldg(p);
-    x[k][1] = __ldg(p + 1);
-    const int pos = sp.pos + tok, page = page_of(a, s, pos);
-    if (page >= 0) at[k] = ((int64_t)page * a.n_kv * kPage + pos % kPage) * kUnits;
-  }
+    for (int k = 0; k < kRows; ++k) {
+      const int s = rows.slot(k), tok = rows.token(k);
+      at[k] = -1;
+      x[k][0] = x[k][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (!LONG) sp = s < a.n_slots ? span_of(a, nullptr, false, s) : Span{0, 0};
+      if (tok >= sp.n) continue;
+      const uint4* p = reinterpret_cast<const uint4*>(from + ((int64_t)s * a.T + tok) * stride);
+      x[k][0] = __ldg(p);
+      x[k][1] = __ldg(p + 1);
+      const int pos = sp.pos + tok, page = page_of(a, s, pos);
+      if (page >= 0) at[k] = ((int64_t)page * a.n_kv * kPage + pos % kPage) * kUnits;
+    }
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    // all lanes take part in the exchanges, rows that are not there as zeros
-    const uint4 &y = x[k][0], &z = x[k][1];
-    uint32_t lo = min2<F16>(min2<F16>(min2<F16>(y.x, y.y), min2<F16>(y.z, y.w)),
-                            min2<F16>(min2<F16>(z.x, z.y), min2<F16>(z.z, z.w)));
-    uint32_t hi = max2<F16>(max2<F16>(max2<F16>(y.x, y.y), max2<F16>(y.z, y.w)),
-                            max2<F16>(max2<F16>(z.x, z.y), max2<F16>(z.z, z.w)));
-    if (D == 128) {  // two threads a group
-      lo = min2<F16>(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, 1));
-      hi = max2<F16>(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, 1));
+    for (int k = 0; k < kRows; ++k) {
+      // all lanes take part in the exchanges, rows that are not there as zeros
+      const uint4 &y = x[k][0], &z = x[k][1];
+      uint32_t lo = min2<F16>(min2<F16>(min2<F16>(y.x, y.y), min2<F16>(y.z, y.w)),
+                              min2<F16>(min2<F16>(z.x, z.y), min2<F16>(z.z, z.w)));
+      uint32_t hi = max2<F16>(max2<F16>(max2<F16>(y.x, y.y), max2<F16>(y.z, y.w)),
+                              max2<F16>(max2<F16>(z.x, z.y), max2<F16>(z.z, z.w)));
+      if (D == 128) {  // two threads a group
+        lo = min2<F16>(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, 1));
+        hi = max2<F16>(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, 1));
+      }
+      lo = min2<F16>(lo, lo >> 16 | lo << 16);
+      hi = max2<F16>(hi, hi >> 16 | hi << 16);
+      const uint32_t bb = floor_bf16(unpack_lo<F16>(lo));
+      const float b = __uint_as_float(bb << 16);
+      const uint32_t sb = scale_bits(unpack_lo<F16>(hi), b);
+      const float s = __uint_as_float(sb << 16);
+      float up;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(up) : "f"(s));  // within 2^-23
+      up *= 1.0f + 0x1p-21f;
+      uint32_t w0 = codes8<F16>(y, b, up), w1 = codes8<F16>(z, b, up);
+      if (in_doubt<F16>(x[k], b, s, up)) {
+        w0 = s > 0.0f ? codes_exact<F16>(y, b, s) : 0u;
+        w1 = s > 0.0f ? codes_exact<F16>(z, b, s) : 0u;
+      }
+      int word = 2 * part;
+      if (D == 64) {
+        // bytes of groups 2 h (this thread's or its neighbour's) and 2 h + 1 alternate
+        const bool odd = part & 1;
+        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, odd ? w0 : w1, 1);
+        const uint32_t p = odd ? o : w0, q = odd ? w1 : o;
+        w0 = __byte_perm(p, q, 0x5140);
+        w1 = __byte_perm(p, q, 0x7362);
+      }
+      if (at[k] < 0) continue;
+      uint16_t* row = pool + at[k];
+      *reinterpret_cast<uint2*>(row + 2 * word) = make_uint2(w0, w1);
+      if (D == 64 || part % 2 == 0) {
+        const int g = D == 64 ? part : part / 2;
+        row[D / 4 + g] = (uint16_t)sb;
+        row[D / 4 + 4 + g] = (uint16_t)bb;
+      }
     }
-    lo = min2<F16>(lo, lo >> 16 | lo << 16);
-    hi = max2<F16>(hi, hi >> 16 | hi << 16);
-    const uint32_t bb = floor_bf16(unpack_lo<F16>(lo));
-    const float b = __uint_as_float(bb << 16);
-    const uint32_t sb = scale_bits(unpack_lo<F16>(hi), b);
-    const float s = __uint_as_float(sb << 16);
-    float up;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(up) : "f"(s));  // within 2^-23
-    up *= 1.0f + 0x1p-21f;
-    uint32_t w0 = codes8<F16>(y, b, up), w1 = codes8<F16>(z, b, up);
-    if (in_doubt<F16>(x[k], b, s, up)) {
-      w0 = s > 0.0f ? codes_exact<F16>(y, b, s) : 0u;
-      w1 = s > 0.0f ? codes_exact<F16>(z, b, s) : 0u;
-    }
-    int word = 2 * part;
-    if (D == 64) {
-      // bytes of groups 2 h (this thread's or its neighbour's) and 2 h + 1 alternate
-      const bool odd = part & 1;
-      const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, odd ? w0 : w1, 1);
-      const uint32_t p = odd ? o : w0, q = odd ? w1 : o;
-      w0 = __byte_perm(p, q, 0x5140);
-      w1 = __byte_perm(p, q, 0x7362);
-    }
-    if (at[k] < 0) continue;
-    uint16_t* row = pool + at[k];
-    *reinterpret_cast<uint2*>(row + 2 * word) = make_uint2(w0, w1);
-    if (D == 64 || part % 2 == 0) {
-      const int g = D == 64 ? part : part / 2;
-      row[D / 4 + g] = (uint16_t)sb;
-      row[D / 4 + 4 + g] = (uint16_t)bb;
-    }
-  }
+  } while (rows.next(sp.n));
 }
 
 // Eight codes of a word as numbers s c + b, each rounded once: to four words of
@@ -340,61 +349,63 @@ __global__ void __launch_bounds__(kThr)
   // D = 128: two words of a group; D = 64: two words of half a row, each with
   // four elements of group 2 h and four of 2 h + 1
   const int ga = D == 128 ? part / 2 : part / 2 * 2, gb = D == 128 ? ga : ga + 1;
-  uint2 w[kRows];
-  uint32_t sa[kRows], ba[kRows], sb[kRows], bb[kRows];
-  int64_t at[kRows];  // the token, -1: not there
-  const Rows<D, LONG> rows(plan);
+  Rows<D, LONG> rows(plan);
   Span sp{0, 0};
   if (LONG) {
     sp = span_of(a, first, true, rows.s0);
     if (rows.t0 - (int)threadIdx.x / kLanes >= sp.n) return;  // the whole CTA
   }
+  do {
+    uint2 w[kRows];
+    uint32_t sa[kRows], ba[kRows], sb[kRows], bb[kRows];
+    int64_t at[kRows];  // the token, -1: not there
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const int s = rows.slot(k), tok = rows.token(k);
-    at[k] = -1;
-    if (!LONG) sp = s < a.n_slots ? span_of(a, first, true, s) : Span{0, 0};
-    if (tok >= sp.n) continue;
-    const int pos = sp.pos + tok, page = page_of(a, s, pos);
-    if (page < 0) continue;
-    const uint16_t* q = pool + ((int64_t)page * a.n_kv * kPage + pos % kPage) * kUnits;
-    w[k] = __ldg(reinterpret_cast<const uint2*>(q) + part);
-    sa[k] = __ldg(q + D / 4 + ga);
-    ba[k] = __ldg(q + D / 4 + 4 + ga);
-    sb[k] = D == 64 ? __ldg(q + D / 4 + gb) : 0u;
-    bb[k] = D == 64 ? __ldg(q + D / 4 + 4 + gb) : 0u;
-    at[k] = (int64_t)s * a.T + tok;
-  }
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    if (at[k] < 0) continue;
-    const uint32_t s0 = dup_lo(sa[k]), b0 = dup_lo(ba[k]), s1 = dup_lo(sb[k]), b1 = dup_lo(bb[k]);
-    uint32_t o[2][kW];
-    values8<DT, D>(w[k].x, s0, b0, s1, b1, o[0]);
-    values8<DT, D>(w[k].y, s0, b0, s1, b1, o[1]);
-    if (D == 128) {
-      uint4* p = reinterpret_cast<uint4*>(to + (at[k] * stride + part * 16) * kE);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < kW; i += 4)
-          p[(j * kW + i) / 4] = make_uint4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]);
-    } else {
-      // elements 8 (part % 2) .. + 7 of group 2 h, then of the next
-      char* p = to + (at[k] * stride + (part >> 1) * 32 + (part & 1) * 8) * kE;
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int i = 0; i < kW; i += 4) {
-          const int j = g * (kW / 2);
-          uint4* q = reinterpret_cast<uint4*>(p + g * 16 * kE + i * 4);
-          if (DT == MOE_DTYPE_FP32)
-            *q = make_uint4(o[i / 4][j], o[i / 4][j + 1], o[i / 4][j + 2], o[i / 4][j + 3]);
-          else
-            *q = make_uint4(o[0][j], o[0][j + 1], o[1][j], o[1][j + 1]);
-        }
+    for (int k = 0; k < kRows; ++k) {
+      const int s = rows.slot(k), tok = rows.token(k);
+      at[k] = -1;
+      if (!LONG) sp = s < a.n_slots ? span_of(a, first, true, s) : Span{0, 0};
+      if (tok >= sp.n) continue;
+      const int pos = sp.pos + tok, page = page_of(a, s, pos);
+      if (page < 0) continue;
+      const uint16_t* q = pool + ((int64_t)page * a.n_kv * kPage + pos % kPage) * kUnits;
+      w[k] = __ldg(reinterpret_cast<const uint2*>(q) + part);
+      sa[k] = __ldg(q + D / 4 + ga);
+      ba[k] = __ldg(q + D / 4 + 4 + ga);
+      sb[k] = D == 64 ? __ldg(q + D / 4 + gb) : 0u;
+      bb[k] = D == 64 ? __ldg(q + D / 4 + 4 + gb) : 0u;
+      at[k] = (int64_t)s * a.T + tok;
     }
-  }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (at[k] < 0) continue;
+      const uint32_t s0 = dup_lo(sa[k]), b0 = dup_lo(ba[k]), s1 = dup_lo(sb[k]), b1 = dup_lo(bb[k]);
+      uint32_t o[2][kW];
+      values8<DT, D>(w[k].x, s0, b0, s1, b1, o[0]);
+      values8<DT, D>(w[k].y, s0, b0, s1, b1, o[1]);
+      if (D == 128) {
+        uint4* p = reinterpret_cast<uint4*>(to + (at[k] * stride + part * 16) * kE);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < kW; i += 4)
+            p[(j * kW + i) / 4] = make_uint4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]);
+      } else {
+        // elements 8 (part % 2) .. + 7 of group 2 h, then of the next
+        char* p = to + (at[k] * stride + (part >> 1) * 32 + (part & 1) * 8) * kE;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int i = 0; i < kW; i += 4) {
+            const int j = g * (kW / 2);
+            uint4* q = reinterpret_cast<uint4*>(p + g * 16 * kE + i * 4);
+            if (DT == MOE_DTYPE_FP32)
+              *q = make_uint4(o[i / 4][j], o[i / 4][j + 1], o[i / 4][j + 2], o[i / 4][j + 3]);
+            else
+              *q = make_uint4(o[0][j], o[0][j + 1], o[1][j], o[1][j + 1]);
+          }
+      }
+    }
+  } while (rows.next(sp.n));
 }
 
 bool cache_q4_supported(const moe_cache_shape_t* s) {
@@ -426,8 +437,13 @@ int plan_of(const moe_cache_shape_t* s, int T, bool* along, dim3* grid) {
   const int step = kThr / (s->D / 16);
   *along = T > step;
   if (*along) {
-    const int ctas = (T + step * kRows - 1) / (step * kRows);
-    *grid = dim3(s->n_slots * ctas, 2 * s->n_kv);  // below 2^12 * 2^13
+    // T may be far above what most slots have, and CTAs without a token cost their
+    // start: 39 slots of up to 1119 positions of 8 heads, T 8049, were read in 82
+    // us with a CTA for each stretch of T, in 18.7 with 4096 in all (18.2 with
+    // 8192, 21.5 with 2048); 16 prompts written and read back 62.3 and 63.7.
+    const int all = (T + step * kRows - 1) / (step * kRows), some = kMostCtas / (2 * s->n_slots * s->n_kv);
+    const int ctas = some < 1 ? 1 : some < all ? some : all;
+    *grid = dim3(s->n_slots * ctas, 2 * s->n_kv);
     return ctas;
   }
   int log_t = 0;

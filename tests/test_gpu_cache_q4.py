@@ -297,3 +297,26 @@ def test_captured_calls_take_new_numbers():
             err = (out[0][i, :c].cpu().double() - want[i, :c]).abs()
             assert (err <= 2.0**-8 * want[i, :c].abs() + 2.0**-25).all()
             assert (out[0][i, c:] == 5).all()
+
+
+@pytest.mark.parametrize("D,dtype,lens,T", [(128, "bf16", [500, 449, 385, 384, 5], 500),
+                                            (64, "fp16", [1000, 769, 768, 130], 1000)])
+def test_slots_of_very_different_length(D, dtype, lens, T):
+    """A CTA goes on along its slot where there are too few for one a stretch
+    (40 slots of 8 heads have six each)."""
+    lens = lens + [1] * (40 - len(lens))
+    st = State(D, lens, 8, D)
+    n = st.lens.copy()
+    k, v = rows(st.rng, (40, T, 8, D), dtype), rows(st.rng, (40, T, 8, D), dtype)
+    m.moe_cache_write_q4(st.shape, st.meta(), ints(n), k.to(DEV), v.to(DEV), st.k, st.v, st.ws)
+    assert m.moe_query_device_status(st.ws) == 0
+    for pool, old, x in ((st.k, st.k0, k), (st.v, st.v0, v)):
+        np.testing.assert_array_equal(pool.cpu().numpy(), st.written(old, x.double().numpy(), 0 * n, n))
+    out = [torch.full((40, T, 8, D), 7.0, device=DEV) for _ in range(2)]
+    m.moe_cache_read_q4(st.shape, st.meta(), None, ints(n), st.k, st.v, *out, st.ws)
+    assert m.moe_query_device_status(st.ws) == 0
+    for x, got in zip((k, v), out):
+        for s in range(40):
+            want = ref.values(ref.pack(*ref.quantise(x[s, :n[s]].double().numpy())), D)
+            np.testing.assert_array_equal(got[s, :n[s]].cpu().numpy(), want.astype(np.float32))
+            assert (got[s, n[s]:] == 7.0).all()

@@ -815,14 +815,15 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
         parity ^= st == 0;
       }
       // ---- the pair's end
-      // a cut pair's piece: the first goes to a place of its own, as units
-      // after it are on their way into the ring; the last goes to the ring
+      // a cut pair's piece: the warp's last goes to the ring, which nothing is on
+      // its way into any more; a first one before other pairs to a place of its own
       const int which = at.pb < f0 ? 0 : 1;
+      const bool more = fe == at.pb + units && fe + a.pair_cost < f1;
       float sig[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) sig[g] = __uint_as_float((uint32_t)sg[g] << 23);
       float* pf = reinterpret_cast<float*>(sm_raw + (ring - sbase));
-      if (which == 0)
+      if (more)
         pf = C::kPieceHere ? reinterpret_cast<float*>(sm_raw + (queries + C::kQBytes - sbase))
                            : a.pieces + ((int64_t)blockIdx.x * kWarps + warp) * kPiece;
       if (!whole && lane == 0)

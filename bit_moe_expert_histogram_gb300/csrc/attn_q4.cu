@@ -63,7 +63,7 @@ namespace moe {
 
 namespace {
 constexpr int kMostCtas = 256;
-constexpr int kMostRows = 16;    // of a tile
+constexpr int kMostRows = 16;    // of a tile, the others have 8
 constexpr int kMostChunks = 16;  // of 32 items of a pair's output
 
 constexpr int kWarps = 8;   // of a CTA
@@ -210,7 +210,7 @@ __device__ __forceinline__ Q4Span q4_span(const AttnQ4Args& a, int s) {
     r.n_new = min(max(r.n_new, 0), a.T);
   }
   const int n = (r.len + kBlk - 1) / kBlk;
-  r.used = a.tiles == 1 ? r.n_new > 0 : (r.n_new * a.group + kMostRows - 1) / kMostRows;
+  r.used = (r.n_new * a.group + (1 << a.row_shift) - 1) >> a.row_shift;
   r.units = n < 1 ? 1 : n;
   return r;
 }
@@ -980,8 +980,20 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
 }
 
 namespace {
-int row_tiles(const moe_attn_batch_shape_t* s) {
-  return (s->T * (s->n_q / s->n_kv) + kMostRows - 1) / kMostRows;
+// Rows of a tile, as a power of two. Tiles of sixteen take every page of a pair
+// half as often, but a unit of theirs takes 2.7 us from start to end, one of eight
+// 1.7 (they spill, too, where D is 128): eight are better until the work is so much
+// that there is always something to do. Units a warp has at most, as far as the
+// shape says, against us with sixteen and eight rows:
+//  D = 128: 0.1 12.0 8.4, 2 14.3 10.0, 14.7 33.4 27.5, 20 40.5 35.1, 30 43.2 42.3,
+//   40 56.5 51.7, 54 73.8 70.6, 62 68.2 73.8, 107 133 141, 214 208 240
+//  D = 64: 0.8 10.2 8.6, 2.4 10.7 10.5 and 12.7 10.7, 4.9 12.9 14.0 and 15.1 14.0,
+//   10 16.9 17.8, 39 33.7 41.8, 47 49.5 53.9
+int row_shift(const moe_attn_batch_shape_t* s, int ctas) {
+  const int rows = s->T * (s->n_q / s->n_kv), warps = ctas * kWarps;
+  if (rows <= 8) return 3;
+  const int64_t units = (int64_t)s->n_slots * s->n_kv * ((rows + 15) / 16) * s->max_blocks;
+  return units <= (int64_t)warps * (s->D == 128 ? 48 : 4) ? 3 : 4;
 }
 // the start and end of a pair against a unit: 31.6 us without, 29.5 with one and
 // 31.7 with two for 48 slots of 8K, 27, 23.4 and 23.2 for 33 ragged ones
@@ -999,17 +1011,17 @@ cudaError_t launch(const AttnQ4Args& a, int ctas, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_q4_kernel<F16, D, NT>, dim3(ctas), dim3(kQThr), smem, stream, a);
 }
-// tiles of 8 or 16 rows
 template <bool F16, int D>
 cudaError_t launch_rows(const AttnQ4Args& a, int ctas, cudaStream_t stream) {
-  return a.T * a.group <= 8 ? launch<F16, D, 1>(a, ctas, stream) : launch<F16, D, 2>(a, ctas, stream);
+  return a.row_shift == 3 ? launch<F16, D, 1>(a, ctas, stream) : launch<F16, D, 2>(a, ctas, stream);
 }
 }  // namespace
 
 bool attn_q4_supported(const moe_attn_batch_shape_t* s) {
   if (!attn_batch_supported(s) || s->prefix_blocks != 0) return false;
   // the line of units is counted in 32 bits
-  return (int64_t)s->n_slots * s->n_kv * row_tiles(s) * (s->max_blocks + kPairCost) < (1 << 30);
+  const int tiles = (s->T * (s->n_q / s->n_kv) + kMostRows - 1) / kMostRows;
+  return (int64_t)s->n_slots * s->n_kv * tiles * (s->max_blocks + kPairCost) < (1 << 30);
 }
 
 // status, the CTAs' counters (one for 32 items), their two places for parts, the
@@ -1031,9 +1043,10 @@ cudaError_t launch_attn_q4(const moe_attn_batch_shape_t* s, AttnQ4Args a, uint8_
   a.n_kv = s->n_kv;
   a.group = s->n_q / s->n_kv;
   a.max_blocks = s->max_blocks;
-  a.tiles = row_tiles(s);
   a.pair_cost = kPairCost;
   const int ctas = nsm < kMostCtas ? nsm : kMostCtas;
+  a.row_shift = row_shift(s, ctas);
+  a.tiles = (s->T * a.group + (1 << a.row_shift) - 1) >> a.row_shift;
   if (s->dtype == MOE_DTYPE_FP16)
     return s->D == 64 ? launch_rows<true, 64>(a, ctas, stream) : launch_rows<true, 128>(a, ctas, stream);
   return s->D == 64 ? launch_rows<false, 64>(a, ctas, stream) : launch_rows<false, 128>(a, ctas, stream);

@@ -29,7 +29,8 @@ struct AttnQ4Args {
   const int32_t* n_new;  // [n_slots] or null: T
   int n_slots, T, n_q, n_kv, max_blocks, n_phys;
   int group;          // n_q / n_kv
-  int tiles;          // of 16 rows that a pair's rows make (one of 8 where they fit)
+  int row_shift;      // rows of a tile: 8 or 16
+  int tiles;          // that a pair's rows make
   int pair_cost;      // units of the line that a pair counts beside its own
   uint16_t* o;        // [n_slots][T][n_q][D]
   float* part;        // [CTA][2]: what the CTA's ends cut

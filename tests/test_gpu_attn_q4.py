@@ -284,3 +284,60 @@ def test_as_the_16_bit_attention_over_the_same_numbers():
     # < 8, which move weights by as much: 4 (2 + 8) 2^-9 + 4 2^-9 < 0.09
     assert (o4.float() - o16.float()).abs().max() < 0.09
     assert (o4.float() - o16.float()).abs().mean() < 0.004
+
+
+def wide(c):
+    """Tables so wide that tiles have sixteen rows: more blocks than are ever read."""
+    B, T, n_q, n_kv, D = c.dims
+    tiles = -(-T * n_q // n_kv // 16)
+    warps = 8 * torch.cuda.get_device_properties(0).multi_processor_count
+    blocks = warps * (48 if D == 128 else 4) // (B * n_kv * tiles) + 1
+    table = np.full((B, max(blocks, c.table.shape[1])), 1 << 20, np.int32)
+    table[:, :c.table.shape[1]] = c.table
+    c.table = table
+    return c
+
+
+@pytest.mark.parametrize("name", [n for n, (_, T, n_q, n_kv, *_) in CASES.items() if T * n_q // n_kv > 8])
+def test_tiles_of_sixteen_rows(name):
+    slots, T, n_q, n_kv, D, dtype = CASES[name]
+    got = wide(Case(len(name), slots, T, n_q, n_kv, D, dtype, k_std=0.3)).check()
+    for s, (L, n) in enumerate(slots):  # what sees nothing is 0
+        assert not got[s, n:].any()
+        assert not got[s, :max(0, n - L)].any()
+
+
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "fp16"), (128, "fp16")])
+@pytest.mark.parametrize("k_std,v_std,v_spread", [(3.0, 1.0, 0.5), (1.0, 1e-4, 2.0), (1.0, 5.0, 2.0)])
+def test_sizes_in_tiles_of_sixteen(D, dtype, k_std, v_std, v_spread):
+    wide(Case(35, [(700, 4), (64, 1), (129, 3)], 4, 8, 2, D, dtype, k_std, v_std, v_spread)).check()
+
+
+def test_sixteen_rows_over_many_units():
+    """Shares of several pairs, first pieces before other pairs among them."""
+    rng = np.random.default_rng(36)
+    c = wide(Case(37, some(rng, 150, 1500, 4), 4, 16, 2, 128, "bf16", 0.5))
+    first = c.call()
+    c.check(o=first)
+    for _ in range(3):
+        assert torch.equal(c.call(ws=c.ws), first)
+    c = wide(Case(38, some(rng, 90, 1500, 3), 3, 12, 4, 64, "fp16", 0.5))
+    c.check()
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_slots_that_share_pages(T):
+    """Forked slots: one table's pages in several, cut at different lengths."""
+    c = Case(39, [(700, T)] * 6, T, 16, 2, 128, "bf16", 0.5)
+    c.table[1:] = c.table[0]
+    c.lens = np.array([700, 640, 641, 64, 699, 5], np.int32)
+    for s in range(6):  # pages past a slot's end are another's
+        c.new[s] = min(T, c.lens[s])
+    c.check()
+
+
+def test_a_page_that_is_none_in_tiles_of_sixteen():
+    c = wide(Case(40, [(300, 2), (200, 1), (64, 1)], 2, 16, 2, 128))
+    c.table[0, 1], c.table[1, 0], c.table[2, 0] = -1, c.k.shape[0], 1 << 30
+    got = c.check(status=m.MOE_ERR_BAD_INPUT)
+    assert not got[2].any()

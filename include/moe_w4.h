@@ -679,9 +679,11 @@ moe_status_t moe_cache_read_q4(const moe_cache_shape_t* shape, const moe_cache_m
  * numbers that the rows stand for, and the same treatment of bad pages,
  * lengths and counts; without a shared prefix (shape->prefix_blocks is 0;
  * slots that share pages have them in their tables). dtype is that of q and o.
- * fp32 scores, sums and biases' part of the output; a softmax weight times a
- * value's scale is rounded to fp16 (under a power of two that keeps it in
- * range) before it multiplies the codes, whatever dtype is. Scales and biases
+ * fp32 scores and sums; a softmax weight is rounded to fp16 (for numerator and
+ * denominator alike), and a second time with a value's scale before it
+ * multiplies the codes, whatever dtype is. Scales and biases of values are fp16
+ * under a power of two of their group of elements, that of the largest so far:
+ * what is 2^-24 below it counts as nothing. Scales and biases
  * of positions below a slot's length have to be finite, those of values of at
  * most 2^80 (sums of weights times values are kept in fp32 and divided at the
  * end; 2^-100 counts as nothing); what its pages hold past it does not matter.

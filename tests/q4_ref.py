@@ -82,10 +82,19 @@ def attention(q, k, v, table, lens, n_new):
     """(o, bound per output but for o's own rounding): q float64
     [B][T][n_q][D], pools int16 [n_phys][n_kv][64][units]. Positions on pages
     that are none are left out. The bound counts the roundings that the
-    call's documentation allows: p s to fp16 (half a step, 2^-11 of it); the
-    scores' fp32 sums (up to 136 terms, 2^-23 each) in the exponent, twice for
-    numerator and denominator; and fp32 sums over the positions, sixteen a
-    step and some ten steps more for joining."""
+    call's documentation allows, e = 2^-11 being half a step of fp16:
+    - weights p (1 + d), |d| <= e, the same in numerator and denominator:
+      sum p (1 + d) v / sum p (1 + d) - o = sum p d (v - o) / sum p (1 + d), at
+      most (1 + 2 e) e sum p |v - o|;
+    - their products with the scales, e of sum p s c, a second time;
+    - below 2^-14 fp16 is off by half its least number, 2^-25: scales and biases
+      under the group's power of two 2^g, 2^-25 2^g each; products and weights,
+      of which there are n beside a sum of 2^8 or more, n 2^-33 2^g and n 2^-33
+      |v - o|. 2^g is at most twice the largest of 16 s and |b|, and so |v| is at
+      most 2^g, |v - o| twice that;
+    - the scores' fp32 sums (up to 136 terms, 2^-23 each) in the exponent, twice
+      for numerator and denominator; fp32 sums over the positions, sixteen a step
+      and some ten steps more for joining."""
     B, T, n_q, D = q.shape
     n_phys, n_kv = k.shape[:2]
     G = n_q // n_kv
@@ -111,11 +120,15 @@ def attention(q, k, v, table, lens, n_new):
                 mag = np.abs(x) @ (kc * np.abs(ks) + np.abs(kb))[see].T / np.sqrt(D)
                 p = np.exp(sc - sc.max(-1, keepdims=True))
                 p /= p.sum(-1, keepdims=True)
-                o[s, t, h * G:(h + 1) * G] = p @ (vc * vs + vb)[see]
+                val = (vc * vs + vb)[see]
+                o[s, t, h * G:(h + 1) * G] = p @ val
+                off = np.stack([p[i] @ np.abs(val - o[s, t, h * G + i]) for i in range(G)])
+                big = np.maximum(16 * vs, np.abs(vb))[:L][there].max(0)
                 w = p @ (vc * vs)[see]
                 a = w + p @ np.abs(vb)[see]
                 far = 2 * 136 * 2.0**-23 * mag.max(-1, keepdims=True) + (see.sum() / 16 + 32) * 2.0**-23
-                tol[s, t, h * G:(h + 1) * G] = 2.0**-11 * w + far * a
+                least = 2 * big * (2 * 2.0**-25 + 3 * see.sum() * 2.0**-33)
+                tol[s, t, h * G:(h + 1) * G] = 2.0**-11 * (1 + 2.0**-9) * (w + off) + least + far * a
     return o, tol
 
 

@@ -44,7 +44,8 @@
 // values a unit: rows of a head lie together in a page. A pair that lies within
 // a warp's share goes straight to the output; what a share's ends cut is left in
 // shared memory, joined by the CTA, and where the CTA's ends cut it, left in
-// the workspace and joined by the last of its CTAs to arrive, in CTA order.
+// the workspace and joined by the last of its CTAs to arrive, in CTA order. (A few
+// short pairs have a CTA each instead.)
 //
 // Measured on one GB300, 16 query heads on 2 of 128, in us a call:
 //  - 48 slots of some 8.4K, 123 MB: 29.3, of which the pages take 20 (6 TB/s,
@@ -69,6 +70,11 @@ constexpr int kMostChunks = 16;  // of 32 items of a pair's output
 constexpr int kWarps = 8;   // of a CTA
 constexpr int kQThr = kWarps * 32;
 constexpr int kS = 2;       // stages of a warp's ring
+// Units a warp may have where every pair gets a CTA of its own, which saves the
+// joining across CTAs, some 2 us: 2 slots of 300 positions 8.4 -> 6.1 us, 60 of
+// up to 400 10.0 -> 6.6, of up to 1000 10.1 -> 8.6; with four, 8 of up to 2000
+// took 11.7 against 9.6.
+constexpr int kAloneMost = 2;
 // A unit of work is a page of one head.
 template <int D, int NT>
 struct Q4 {
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
   constexpr int kPiece = piece_floats<D, NT>();
   extern __shared__ __align__(128) uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t full[kWarps][kS];
-  __shared__ int s_scan[kWarps];
+  __shared__ int s_scan[kWarps], s_most[kWarps];
   __shared__ Place s_start[kWarps];  // where the warps' shares start
   __shared__ PieceInfo s_piece[2 * kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -310,15 +316,18 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
   pdl_trigger();
   // ---- this warp's part of the line of units
   int total = 0, per;
+  bool alone = false;  // every CTA has a pair of its own
   {
     const int chunk = (a.n_slots + kQThr - 1) / kQThr;
     const int s0 = min(tid * chunk, a.n_slots), s1 = min(s0 + chunk, a.n_slots);
-    int sum = 0;
+    int sum = 0, most = 0;
     Q4Span sp{0, 0, 0, 0};
     for (int s = s0; s < s1; ++s) {
       sp = q4_span(a, s);
       sum += head_units(a, sp);
+      most = max(most, sp.units);
     }
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
     sum *= a.n_kv;
     int incl = sum;
 #pragma unroll
@@ -327,53 +336,73 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
       if (lane >= d) incl += o;
     }
     if (lane == 31) s_scan[warp] = incl;
+    if (lane == 0) s_most[warp] = most;
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) incl += s_scan[w];
       total += s_scan[w];
+      most = max(most, s_most[w]);
     }
-    const unsigned warps = gridDim.x * kWarps;
-    per = cut_up((unsigned)total, warps);
-    // the slots that the CTA's warps start in: each is in one thread's part
-    const int c0 = min((int)blockIdx.x * kWarps * per, total), run0 = incl - sum;
-    for (int w = 0; w < kWarps; ++w) {
-      const int f = c0 + w * per;
-      if (f < run0 || f >= incl) continue;
-      s_start[w].s = s0;
-      s_start[w].pb = run0;
-      s_start[w].sp = sp;  // of the part's last slot, its only one but in large batches
+    if (a.pairs <= (int)gridDim.x && most <= kAloneMost * kWarps) {
+      // a few short pairs: a CTA each, so that nothing is joined across CTAs
+      per = (most + kWarps - 1) / kWarps;
+      total = a.pairs * per * kWarps;
+      alone = true;
+    } else {
+      per = cut_up((unsigned)total, gridDim.x * kWarps);
+      // the slots that the CTA's warps start in: each is in one thread's part
+      const int c0 = min((int)blockIdx.x * kWarps * per, total), run0 = incl - sum;
+      for (int w = 0; w < kWarps; ++w) {
+        const int f = c0 + w * per;
+        if (f < run0 || f >= incl) continue;
+        s_start[w].s = s0;
+        s_start[w].pb = run0;
+        s_start[w].sp = sp;  // of the part's last slot, its only one but in large batches
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
   const int F0 = min((int)blockIdx.x * kWarps * per, total);  // the CTA's share
   const int F1 = min(F0 + kWarps * per, total);
-  const int f0 = min(F0 + warp * per, total), f1 = min(f0 + per, total);
+  const int f0 = min(F0 + warp * per, total);
+  int f1 = min(f0 + per, total);
   const int G = a.group, rows = a.T * G;
   // row / G for row < 64: the product is off by less than 1 / (2 G)
   const float per_g = 1.0f / (float)G;
   auto token = [&](int r) { return (int)(((float)r + 0.5f) * per_g); };
   const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(D)
   if (f0 < f1) {
-    Place at = s_start[warp];
-    if (a.n_slots > kQThr) {
-      for (at.sp = q4_span(a, at.s); at.s < a.n_slots - 1; at.sp = q4_span(a, ++at.s)) {
-        const int n = head_units(a, at.sp) * a.n_kv;
-        if (f0 < at.pb + n) break;
-        at.pb += n;
+    Place at;
+    if (alone) {
+      const int head = (int)blockIdx.x / a.tiles;
+      at.s = head / a.n_kv;
+      at.head = head - at.s * a.n_kv;
+      at.tile = (int)blockIdx.x - head * a.tiles;
+      at.pb = F0;
+      at.sp = q4_span(a, at.s);
+      f1 = min(f1, F0 + at.units());
+    } else {
+      at = s_start[warp];
+      if (a.n_slots > kQThr) {
+        for (at.sp = q4_span(a, at.s); at.s < a.n_slots - 1; at.sp = q4_span(a, ++at.s)) {
+          const int n = head_units(a, at.sp) * a.n_kv;
+          if (f0 < at.pb + n) break;
+          at.pb += n;
+        }
       }
-    }
-    {
-      const int all = head_units(a, at.sp), each = at.sp.units + a.pair_cost, rest = 1 + a.pair_cost;
-      at.head = a.n_kv == 1 ? 0 : cut_up((unsigned)(f0 - at.pb) + 1u, all) - 1;
-      at.pb += at.head * all;
-      int in = f0 - at.pb;  // of the head's units
-      at.tile = min(a.tiles == 1 ? 0 : cut_up((unsigned)in + 1u, each) - 1, at.sp.used);
-      at.pb += at.tile * each;
-      in -= at.tile * each;
-      if (at.tile == at.sp.used) {
-        const int more = cut_up((unsigned)in + 1u, rest) - 1;
-        at.tile += more;
-        at.pb += more * rest;
+      {
+        const int all = head_units(a, at.sp), each = at.sp.units + a.pair_cost, rest = 1 + a.pair_cost;
+        at.head = a.n_kv == 1 ? 0 : cut_up((unsigned)(f0 - at.pb) + 1u, all) - 1;
+        at.pb += at.head * all;
+        int in = f0 - at.pb;  // of the head's units
+        at.tile = min(a.tiles == 1 ? 0 : cut_up((unsigned)in + 1u, each) - 1, at.sp.used);
+        at.pb += at.tile * each;
+        in -= at.tile * each;
+        if (at.tile == at.sp.used) {
+          const int more = cut_up((unsigned)in + 1u, rest) - 1;
+          at.tile += more;
+          at.pb += more * rest;
+        }
       }
     }
     // ---- the loader: kS units ahead on the line, all lanes follow, lane 0 issues
@@ -1047,6 +1076,7 @@ cudaError_t launch_attn_q4(const moe_attn_batch_shape_t* s, AttnQ4Args a, uint8_
   const int ctas = nsm < kMostCtas ? nsm : kMostCtas;
   a.row_shift = row_shift(s, ctas);
   a.tiles = (s->T * a.group + (1 << a.row_shift) - 1) >> a.row_shift;
+  a.pairs = a.n_slots * a.n_kv * a.tiles;
   if (s->dtype == MOE_DTYPE_FP16)
     return s->D == 64 ? launch_rows<true, 64>(a, ctas, stream) : launch_rows<true, 128>(a, ctas, stream);
   return s->D == 64 ? launch_rows<false, 64>(a, ctas, stream) : launch_rows<false, 128>(a, ctas, stream);

@@ -30,7 +30,8 @@ struct AttnQ4Args {
   int n_slots, T, n_q, n_kv, max_blocks, n_phys;
   int group;          // n_q / n_kv
   int row_shift;      // rows of a tile: 8 or 16
-  int tiles;          // that a pair's rows make
+  int tiles;          // that a slot's and head's rows make
+  int pairs;          // slots, heads and tiles
   int pair_cost;      // units of the line that a pair counts beside its own
   uint16_t* o;        // [n_slots][T][n_q][D]
   float* part;        // [CTA][2]: what the CTA's ends cut

@@ -54,7 +54,7 @@
 //    warps with half a page a unit took 33.7 and 56.0: a unit's fixed work (two
 //    copies, a wait, scales exchanged, maxima compared) then weighs twice.
 //  - 256 slots of up to 16K and 4 tokens, 513 MB read for two tiles of 16 rows:
-//    208, bound by instruction latency: two warps a scheduler (queries, O and
+//    202, bound by instruction latency: two warps a scheduler (queries, O and
 //    scores of 16 rows take all registers) issue in 46 cycles of a hundred, the
 //    tensor pipe is busy in 42. Tiles of 32 rows (spills) took 330, 12 warps
 //    of half pages 296.
@@ -176,6 +176,11 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
 }
 __device__ __forceinline__ float elem4(const float4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ uint64_t pair_f(float a, float b) {
   return pair2(__float_as_uint(a), __float_as_uint(b));
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
           uint64_t x[kBlk / 16][2][NT];
 #pragma unroll
           for (int v = 0; v < kBlk / 32; ++v) {
-            float t[2][NT][4];
+            uint64_t t[2][NT][2];
 #pragma unroll
             for (int c = 0; c < C::kCh; c += 2) {
               if (C::kQBytes > 0) {
@@ -649,9 +654,11 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
                                 qa[ks][NT + i]);
                       if (D == 64 || e == 1)
 #pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                          t[h][i][z] = g == 0 ? s[z >> 1].x * acc[i][z]
-                                              : fmaf(elem4(s[z >> 1], g), acc[i][z], t[h][i][z]);
+                        for (int y = 0; y < 2; ++y) {
+                          const float sy = elem4(s[y], g);
+                          const uint64_t a2 = pair_f(acc[i][2 * y], acc[i][2 * y + 1]), s2 = pair_f(sy, sy);
+                          t[h][i][y] = g == 0 ? mul2(s2, a2) : fma2(s2, a2, t[h][i][y]);
+                        }
                     }
                   }
                 }
@@ -669,7 +676,7 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
                 const uint64_t f2 = pair_f(cf[i][0], cf[i][1]);
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                  x[2 * v + h][y][i] = fma2(pair_f(t[h][i][2 * y], t[h][i][2 * y + 1]), f2,
+                  x[2 * v + h][y][i] = fma2(t[h][i][y], f2,
                                             pair_f(xb[2 * y], xb[2 * y + 1]));
               }
             }
@@ -1015,7 +1022,7 @@ namespace {
 // that there is always something to do. Units a warp has at most, as far as the
 // shape says, against us with sixteen and eight rows:
 //  D = 128: 0.1 12.0 8.4, 2 14.3 10.0, 14.7 33.4 27.5, 20 40.5 35.1, 30 43.2 42.3,
-//   40 56.5 51.7, 54 73.8 70.6, 62 68.2 73.8, 107 133 141, 214 208 240
+//   40 56.5 51.7, 54 73.8 70.6, 62 68.2 73.8, 107 133 141, 214 206 240
 //  D = 64: 0.8 10.2 8.6, 2.4 10.7 10.5 and 12.7 10.7, 4.9 12.9 14.0 and 15.1 14.0,
 //   10 16.9 17.8, 39 33.7 41.8, 47 49.5 53.9
 int row_shift(const moe_attn_batch_shape_t* s, int ctas) {

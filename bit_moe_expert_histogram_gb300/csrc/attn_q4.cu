@@ -500,7 +500,10 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
       // ---- the rows: queries as fp16, their scale, their groups' sums
       // per query column 2 cq + e of eight: its last visible position (-1: none),
       // and scores = cf * (products of codes) + biases' part
-      int lim[NT][2];
+      auto lim_of = [&](int i, int e) {  // little used, and registers are scarce
+        const int r = at.tile * kR + 8 * i + 2 * cq + e, t = r < rows ? token(r) : a.T;
+        return t < at.sp.n_new ? max(basep + t, -1) : -1;
+      };
       float cf[NT][2];
       uint32_t qa[kKS][2 * NT], qs[2 * NT];  // with sixteen rows qa lies in shared memory
 #pragma unroll
@@ -535,8 +538,6 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           cf[i][e] = __shfl_sync(0xFFFFFFFFu, back, 8 * cq + 4 * e);
-          const int r = at.tile * kR + 8 * i + 2 * cq + e, t = r < rows ? token(r) : a.T;
-          lim[i][e] = t < at.sp.n_new ? max(basep + t, -1) : -1;
         }
         float sum[4];
 #pragma unroll
@@ -684,15 +685,17 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
           // every query that is in use sees positions up to basep
           if (pos0 + kBlk - 1 > basep) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i) {
+              const int lim0 = lim_of(i, 0), lim1 = lim_of(i, 1);
 #pragma unroll
               for (int h = 0; h < kBlk / 8; ++h) {
                 float x0, x1;
                 unpair2(x[h >> 1][h & 1][i], x0, x1);
-                if (pos0 + 8 * h + gq > lim[i][0]) x0 = -INFINITY;
-                if (pos0 + 8 * h + gq > lim[i][1]) x1 = -INFINITY;
+                if (pos0 + 8 * h + gq > lim0) x0 = -INFINITY;
+                if (pos0 + 8 * h + gq > lim1) x1 = -INFINITY;
                 x[h >> 1][h & 1][i] = pair_f(x0, x1);
               }
+            }
           }
           // ---- values' scales and biases, while the products run
           {
@@ -874,9 +877,10 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
           const int r = 8 * i + 2 * cq + e;
           const float sum = __shfl_sync(0xFFFFFFFFu, sb[i][e], 16 + cq);
           // rows that see nothing weigh nothing, whatever was summed for them
-          const float lr = lim[i][e] >= 0 ? sum : 0.0f;
+          const bool used = lim_of(i, e) >= 0;
+          const float lr = used ? sum : 0.0f;
           if (!whole && gq == 0) {
-            pf[r] = lim[i][e] >= 0 ? m[i][e] : -INFINITY;
+            pf[r] = used ? m[i][e] : -INFINITY;
             pf[kR + r] = lr;
           }
           float b[4];

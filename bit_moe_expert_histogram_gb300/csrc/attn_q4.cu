@@ -48,15 +48,15 @@
 // short pairs have a CTA each instead.)
 //
 // Measured on one GB300, 16 query heads on 2 of 128, in us a call:
-//  - 48 slots of some 8.4K, 123 MB: 29.3, of which the pages take 20 (6 TB/s,
+//  - 48 slots of some 8.4K, 123 MB: 29.0, of which the pages take 20 (6 TB/s,
 //    0.9 of a plain copy's rate), the lengths, tables and first pages 4, joining
-//    4; 8 slots of some 112K, 250 MB: 50.3, 5.0 TB/s. HBM bounds both. Twelve
+//    4; 8 slots of some 112K, 250 MB: 49.7, 5.0 TB/s. HBM bounds both. Twelve
 //    warps with half a page a unit took 33.7 and 56.0: a unit's fixed work (two
 //    copies, a wait, scales exchanged, maxima compared) then weighs twice.
 //  - 256 slots of up to 16K and 4 tokens, 513 MB read for two tiles of 16 rows:
-//    202, bound by instruction latency: two warps a scheduler (queries, O and
-//    scores of 16 rows take all registers) issue in 46 cycles of a hundred, the
-//    tensor pipe is busy in 42. Tiles of 32 rows (spills) took 330, 12 warps
+//    200, bound by instruction latency: two warps a scheduler (queries, O and
+//    scores of 16 rows take all registers) issue in 45 cycles of a hundred, the
+//    tensor pipe is busy in 44. Tiles of 32 rows (spills) took 330, 12 warps
 //    of half pages 296.
 #include "attn_q4.cuh"
 

@@ -21,8 +21,10 @@
 // where more than one follows, so that some k elements enter in between and the
 // CTA's warps need not meet at every chunk (meeting at each, with chunks of
 // twice the size, took 203 us for 2048 rows of 128001). If more enter than the
-// list holds (rising logits), the CTA's stretch is read again, once for each of
-// the k.
+// list holds (sorted or smooth rows), the CTA's stretch is read again, for every
+// thread's maximum and for what reaches the k-th of these (2048 sorted rows of
+// 128001, the first 32: 278 us); if that is still too much (a thousand equals of
+// it), once for each of the k (5.3 ms).
 //
 // Many rows are bound by HBM: 2048 rows of 128001 bf16 logits, 524 MB, take 102
 // us, 5.15 TB/s, 0.76 of a plain copy's rate (ten instructions a logit, one of
@@ -469,8 +471,48 @@ __global__ void __launch_bounds__(kLThr, kCtas) logprobs_kernel(const LogpArgs a
     __syncthreads();
     over |= list.n > kMost;
     if (over) {
-      // the best k one after the other, each found by reading the stretch again
+      // Large numbers that lie together, or came late. The stretch is read again,
+      // for the threads' maxima, whose k-th is a bar (a thread has eight of what
+      // lies together where a group has 32), and for what reaches it.
+      uint32_t* one = reinterpret_cast<uint32_t*>(s_vec);
+      float g = -INFINITY;
+#pragma unroll 1
+      for (int c = c0; c < c1; ++c) {
+        load(c, v);
+        const float top = max_of<DT>(v);
+        g = fmaxf(g, top != top ? -INFINITY : top);
+      }
       __syncthreads();
+      const uint32_t mine = place(g, tid, kLThr);
+      one[tid] = mine;
+      if (tid == 0) {
+        s_bar = -INFINITY;
+        list.n = 0;
+      }
+      __syncthreads();
+      if (g > -INFINITY && before(one, 0, 4, kLThr, mine) == a.k - 1) s_bar = placed(mine, kLThr);
+      __syncthreads();
+      bar = fmaxf(s_bar, -FLT_MAX);
+#pragma unroll 1
+      for (int c = c0; c < c1; ++c) {
+        load(c, v);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+#pragma unroll
+          for (int i = 0; i < E::kN; ++i) {
+            const float x = el_at<DT>(v[j], i);
+            if (!(x >= bar)) continue;
+            const int at = atomicAdd(&list.n, 1);
+            if (at < kCap) list.e[at] = entry(x, first_of(c, j) + i);
+          }
+      }
+      __syncthreads();
+      over = list.n > kCap;
+      __syncthreads();
+      if (!over) keep_best(list, a.k);
+    }
+    if (over) {
+      // the best k one after the other, each found by reading the stretch again
       if (tid == 0) list.n = 0;
       uint64_t last = ~0ull;
       for (int r = 0; r < a.k; ++r) {

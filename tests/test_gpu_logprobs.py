@@ -255,3 +255,21 @@ def test_masks_of_the_lowest_number(dtype, n, V):
     tokens = [(i * 7919) % V for i in range(n)]
     got = call(x, tokens, 8)
     check(x[:6], tokens[:6], 8, [y[:6] for y in got])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,V", [(6, 70001), (640, 20000)])
+def test_rows_whose_large_numbers_lie_together(dtype, n, V):
+    """Sorted and smooth rows, cut and uncut: the list is overfilled early, late
+    or throughout."""
+    g = torch.Generator().manual_seed(12)
+    r = torch.randn(V, generator=g)
+    at = torch.arange(V) / 900.0
+    rows = [torch.sort(r)[0], torch.sort(r, descending=True)[0], torch.sin(at), torch.sin(at) * torch.cos(7 * at),
+            torch.floor(at), torch.where(at > at[-1] / 2, torch.floor(at) % 3, torch.zeros(()))]
+    x = torch.stack([rows[i % 6] for i in range(n)]).to(TYPES[dtype]).to(DEV)
+    tokens = [(i * 7919) % V for i in range(n)]
+    for k in (1, 20, 32):
+        got = call(x, tokens, k)
+        check(x[:6], tokens[:6], k, [y[:6] for y in got])
+        assert all(torch.equal(y[6:12], y[:6]) for y in got[1:] if n > 12)

@@ -1005,6 +1005,9 @@ __global__ void __launch_bounds__(kQThr, 1) attn_q4_kernel(const AttnQ4Args a) {
       __threadfence();
     }
   }
+  // single lanes counted and fenced, the whole warp reads the other CTAs' parts:
+  // ordered by the barrier, as a vote orders no memory
+  __syncwarp();
   for (unsigned todo = __ballot_sync(0xFFFFFFFFu, last); todo; todo &= todo - 1) {
     const int k = __ffs(todo) - 1, parts = __shfl_sync(0xFFFFFFFFu, n, k);
     const PieceInfo p = s_piece[k & 1 ? 31 - __clz(pieces) : __ffs(pieces) - 1];

@@ -662,9 +662,10 @@ moe_status_t moe_cache_write_q4(const moe_cache_shape_t* shape, const moe_cache_
 
 /* Reads rows back: token t < n[s] of slot s is position first[s] + t, written
  * to (s, t) of k_out_dev and v_out_dev, which lie as k_new_dev does in
- * moe_cache_write. Other tokens of the outputs stay as they were. A range
- * that does not lie in [0, lens[s]) is recorded and its slot left out, a page
- * number out of range likewise for its positions.
+ * moe_cache_write: s * code + b rounded once, to the nearest number of the
+ * outputs' type (ties to even). Other tokens of the outputs stay as they
+ * were. A range that does not lie in [0, lens[s]) is recorded and its slot
+ * left out, a page number out of range likewise for its positions.
  *  first_dev int32 [n_slots] or NULL (0); n_dev int32 [n_slots] or NULL (T)
  *  dtype     moe_dtype_t of the outputs; strides in elements, multiples of 16
  *            bytes, >= n_kv * D; outputs 16-byte aligned */

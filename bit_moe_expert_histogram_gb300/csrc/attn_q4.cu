@@ -15,7 +15,10 @@
 //    and eight elements take five instructions.
 //  - The queries are fp16 with a power of two of their row that brings its
 //    largest element to 2^14 .. 2^15, and divided by 16 where they meet codes
-//    of bits 4 to 7. What is lost is below 2^-34 of the row's largest.
+//    of bits 4 to 7. What is lost is below 2^-34 of the row's largest. The power
+//    stays within 2^-100 and 2^100, so that its inverse and the codes' 2^24 are an
+//    fp32 number: elements are of at most 2^100, and what is lost is 2^-121 at most
+//    where the row's largest is below 2^-86.
 //  - The biases' part of the scores is one bf16 product a position tile (the
 //    queries' group sums split into three bf16 parts, 24 bits).
 //  - The softmax weights are rounded to fp16 once (half a step: 2^-11 of

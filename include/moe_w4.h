@@ -684,10 +684,12 @@ moe_status_t moe_cache_read_q4(const moe_cache_shape_t* shape, const moe_cache_m
  * denominator alike), and a second time with a value's scale before it
  * multiplies the codes, whatever dtype is. Scales and biases of values are fp16
  * under a power of two of their group of elements, that of the largest so far:
- * what is 2^-24 below it counts as nothing. Scales and biases
- * of positions below a slot's length have to be finite, those of values of at
- * most 2^80 (sums of weights times values are kept in fp32 and divided at the
- * end; 2^-100 counts as nothing); what its pages hold past it does not matter.
+ * what is 2^-24 below it counts as nothing.
+ * Elements of q have to be of at most 2^100 (2^-120 counts as nothing). Scales
+ * and biases of positions below a slot's length have to be finite, those of
+ * keys of at most 2^100, those of values of at most 2^80 (sums of weights times
+ * values are kept in fp32 and divided at the end; 2^-100 counts as nothing);
+ * what its pages hold past it does not matter.
  * Deterministic. The workspace (256-byte aligned) is zero-filled once
  * (moe_workspace_init); after MOE_ERR_TIMEOUT, again. Calls of any shape can
  * use it in turn where it is large enough, but no other call of this library.

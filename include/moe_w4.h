@@ -707,13 +707,14 @@ moe_status_t moe_attn_batch_q4(const moe_attn_batch_shape_t* shape, const void* 
  *   logp = x_token - ln sum_v e^x_v, entropy = - sum_v p_v ln p_v (nats),
  *   top: the k ids of the largest logits, ties to the lower id, in that order.
  * Logits are -inf, the type's lowest number or of at most 2^100. One of -inf
- * is a token that cannot be: it has no weight and is not listed; ids that are missing for that, or where V < k, are -1 with -inf.
- * fp32 sums in a fixed order: deterministic. A row of nothing but -inf, or
- * with NaN or +inf, gives NaN, ids of -1, and is recorded as
- * MOE_ERR_BAD_INPUT.
+ * is a token that cannot be: it has no weight and is not listed; ids that are
+ * missing for that, or where V < k, are -1 with -inf. fp32 sums in a fixed
+ * order: deterministic. A row of nothing but -inf, or with NaN or +inf, gives
+ * NaN for logp and entropy and ids of -1 with -inf, and is recorded as
+ * MOE_ERR_BAD_INPUT. A token that is neither -1 nor in [0, V) is recorded, and
+ * its logp is NaN.
  *  logits_dev row i starts stride * i elements in; aligned to its elements
- *  tokens_dev int32 [n_rows]; -1: none, logp 0; others outside [0, V) give NaN
- *             and are recorded
+ *  tokens_dev int32 [n_rows]; -1: none, logp 0 (of a bad row, too)
  *  logp_dev   fp32 [n_rows]; entropy_dev fp32 [n_rows] or NULL
  *  top_ids_dev int32 [n_rows][k], top_logp_dev fp32 [n_rows][k], either or
  *             both NULL

@@ -706,7 +706,8 @@ def alloc_attn_batch_q4_workspace(shape, device="cuda", stream=None):
 
 
 def moe_attn_batch_q4(shape, q, k_cache, v_cache, table, lens, o, ws, n_new=None, stream=None):
-    """moe_attn_batch over 4-bit pools (shape.prefix_blocks is 0)."""
+    """moe_attn_batch over 4-bit pools (shape.prefix_blocks is 0: pages that
+    slots share stand in their tables, and each slot reads them)."""
     B, T, nq, D = shape.n_slots, shape.T, shape.n_q, shape.D
     dt = torch.float16 if shape.dtype == 1 else torch.bfloat16
     if q.dtype is not dt and q.dtype is not torch.int16:

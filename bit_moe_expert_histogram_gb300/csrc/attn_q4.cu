@@ -56,6 +56,11 @@
 //    4; 8 slots of some 112K, 250 MB: 49.7, 5.0 TB/s. HBM bounds both. Twelve
 //    warps with half a page a unit took 33.7 and 56.0: a unit's fixed work (two
 //    copies, a wait, scales exchanged, maxima compared) then weighs twice.
+//  - The 16-bit call over as many positions: 64.6 us for the first, 123 for the
+//    second, 253 for the next; at 33 slots of up to 5000 with D = 64, where starting
+//    and joining are most of it, 15.1 against 17.1 here. Slots that share a long
+//    prompt's pages each walk them by themselves: 256 slots of up to 4 tokens under
+//    32K shared positions take 862 us, the 16-bit call with its shared part 147.
 //  - 256 slots of up to 16K and 4 tokens, 513 MB read for two tiles of 16 rows:
 //    200, bound by instruction latency: two warps a scheduler (queries, O and
 //    scores of 16 rows take all registers) issue in 45 cycles of a hundred, the
@@ -1035,6 +1040,9 @@ namespace {
 //   40 56.5 51.7, 54 73.8 70.6, 62 68.2 73.8, 107 133 141, 214 206 240
 //  D = 64: 0.8 10.2 8.6, 2.4 10.7 10.5 and 12.7 10.7, 4.9 12.9 14.0 and 15.1 14.0,
 //   10 16.9 17.8, 39 33.7 41.8, 47 49.5 53.9
+// The shape's units are the table's width, not the lengths: 8 slots of 2800 with 4
+// tokens take 14.0 us with a table of 44 blocks and 17.4 with one of 2048, 64 of 500
+// 16.6 and 18.2 (64 of 6000 with 2 tokens 45.4 and 39.5).
 int row_shift(const moe_attn_batch_shape_t* s, int ctas) {
   const int rows = s->T * (s->n_q / s->n_kv), warps = ctas * kWarps;
   if (rows <= 8) return 3;

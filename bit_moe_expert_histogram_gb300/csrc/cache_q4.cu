@@ -31,11 +31,15 @@
 // shares with one other (D = 128) or has alone, so that a row's bookkeeping and
 // a group's scale are paid once for as many; fp32 pairs share instructions, no
 // element branches, and nothing divides. 111 thousand positions of 2 heads of
-// 128 written, 148 MB, take 35 us, 4.2 TB/s (120 instructions a thread and row:
-// the integer pipe is busy in 60 cycles of a hundred), and read back 26 us, 5.6
-// TB/s. (Eight elements a thread, a division a group and each code checked for a
-// border by itself took 78 and 50; borders checked by how near fp32 comes to
-// them 61, as 16-bit numbers meet borders in most warps.)
+// 128 written, 148 MB, take 32 to 35 us, 4.2 to 4.7 TB/s (120 instructions a thread
+// and row), and read back 26 to 28 us, 5.3 to 5.6 TB/s. Writing fills no pipe:
+// instructions are issued in 70 cycles of a hundred, the integer pipe is busy in
+// 57, 43 warps of a hundred are there, and every pass waits for its own rows. fp16
+// rows take 54 us: what counts as tiny beside a scale is 2^-5 of it there, 2^-8 for
+// bf16, and more groups have to be looked through for it. (Eight elements a thread,
+// a division a group and each code checked for a border by itself took 78 and 50;
+// borders checked by how near fp32 comes to them 61, as 16-bit numbers meet borders
+// in most warps.)
 #include <type_traits>
 
 #include "attn_q4.cuh"
@@ -306,8 +310,8 @@ __device__ __forceinline__ float affine_odd(float c, float s, float b) {
 // with exponent e lies below 2^(e + 1) and on multiples of 2^(e - 7), so that the
 // sum has at most eb - es + 9 places where b is the larger, es - eb + 13 where s
 // is. (s, b: bits in the low half.) 16 times 4096 positions of 8 heads of 128 to
-// fp16 take 61.1 us, of 64 39.0; with all rows rounded to odd 65.9 and 41.0, with
-// none 62.3 and 35.0.
+// fp16 take 61.1 us, of 64 39.0, a call a graph; with all rows rounded to odd
+// 65.9 and 41.0, with none 62.3 and 35.0.
 __device__ __forceinline__ bool past_fp32(uint32_t s, uint32_t b) {
   const int apart = (int)(b >> 7 & 0xFFu) - (int)(s >> 7 & 0xFFu);
   return (b & 0x7FFFu) != 0u && (apart > 15 || apart < -11);
@@ -466,7 +470,10 @@ int plan_of(const moe_cache_shape_t* s, int T, bool* along, dim3* grid) {
     // T may be far above what most slots have, and CTAs without a token cost their
     // start: 39 slots of up to 1119 positions of 8 heads, T 8049, were read in 82
     // us with a CTA for each stretch of T, in 18.7 with 4096 in all (18.2 with
-    // 8192, 21.5 with 2048); 16 prompts written and read back 62.3 and 63.7.
+    // 8192, 21.5 with 2048); 16 prompts written and read back 62.3 and 63.7. The
+    // price: slots get the same number whatever they have, so one long slot among
+    // many is worked through by few. 8192 tokens beside 255 slots of one are written
+    // in 39 us with 2 heads and 140 with 8 (alone 5.2 and 10.9), read back in 31 and 100.
     const int all = (T + step * kRows - 1) / (step * kRows), some = kMostCtas / (2 * s->n_slots * s->n_kv);
     const int ctas = some < 1 ? 1 : some < all ? some : all;
     *grid = dim3(s->n_slots * ctas, 2 * s->n_kv);

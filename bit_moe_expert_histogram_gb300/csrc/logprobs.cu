@@ -24,7 +24,10 @@
 // list holds (sorted or smooth rows), the CTA's stretch is read again, for every
 // thread's maximum and for what reaches the k-th of these (2048 sorted rows of
 // 128001, the first 32: 278 us); if that is still too much (a thousand equals of
-// it), once for each of the k (5.3 ms).
+// it), once for each of the k (5.3 ms). A stretch whose first chunk has fewer than
+// k elements that are not -inf has no bar from it, what follows overfills the list,
+// and the stretch is read again like those: 2048 rows of 128001 of which the first
+// 16384 are -inf take 290 us.
 //
 // Many rows are bound by HBM: 2048 rows of 128001 bf16 logits, 524 MB, take 102
 // us, 5.15 TB/s, 0.76 of a plain copy's rate (ten instructions a logit, one of
@@ -43,7 +46,8 @@ namespace {
 constexpr int kLThr = 256;
 // CTAs an SM: many rows want loads in flight, a few want the shorter path that
 // more registers give (64 rows of 131072, twenty alternatives: 14.5 us with 4,
-// 16.4 with 5; 2048 rows of 128001: 107.5 and 102.7).
+// 16.4 with 5; 2048 rows of 128001: 107.5 and 102.7, although five leave 48
+// registers and spill 36 to 40 bytes for 16-bit logits with alternatives).
 constexpr int kLMany = 5, kLFew = 4;
 constexpr int kLWarps = kLThr / 32;
 constexpr int kVec = 4;         // 16-byte vectors a thread and chunk

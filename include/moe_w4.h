@@ -679,7 +679,9 @@ moe_status_t moe_cache_read_q4(const moe_cache_shape_t* shape, const moe_cache_m
 /* moe_attn_batch over 4-bit pools: the same definition, with k_j and v_j the
  * numbers that the rows stand for, and the same treatment of bad pages,
  * lengths and counts; without a shared prefix (shape->prefix_blocks is 0;
- * slots that share pages have them in their tables). dtype is that of q and o.
+ * slots that share pages have them in their tables, and each reads them: where
+ * many share a long prompt moe_attn_batch over 16-bit pages, which reads it once,
+ * is the faster call). dtype is that of q and o.
  * fp32 scores and sums; a softmax weight is rounded to fp16 (for numerator and
  * denominator alike), and a second time with a value's scale before it
  * multiplies the codes, whatever dtype is. Scales and biases of values are fp16
